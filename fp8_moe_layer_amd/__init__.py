@@ -80,6 +80,17 @@ _fused_forward_noalloc = _sig("moe_fused_forward_noalloc", _i32, _DP, _vp, _vp, 
                               _vp, _vp, _vp, _vp, _vp)
 _group_tokens = _sig("moe_group_tokens", _i32, _vp, _i32, _i32, _i32, _i32, _vp)
 _k_tiers = _sig("moe_k_tiers", _i32, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp)
+_i64 = C.c_int64
+_quantize_rows_i8 = _sig("moe_quantize_rows_i8", _i32, _vp, _i32, _i64, _i32, _i32, _vp, _vp, _vp)
+_matmul_i8 = _sig("moe_matmul_i8", _i32, _vp, _i64, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp,
+                  _vp)
+_gated_ffn_i8 = _sig("moe_gated_ffn_i8", _i32, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32,
+                     _i32, _vp, _vp)
+_gated_ffn = _sig("moe_gated_ffn", _i32, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp,
+                  _vp)
+_gated_bwd_ws = _sig("moe_gated_ffn_backward_workspace_bytes", C.c_size_t, _i32, _i32, _i32)
+_gated_bwd = _sig("moe_gated_ffn_backward", _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i32,
+                  _i32, _i32, _i32, _vp, _vp, _vp, _vp, C.c_size_t, _vp)
 
 N_STAGE_EVENTS = 8
 STAGES = ("route", "topk", "permute", "gate_up", "requant", "down", "combine")
@@ -345,6 +356,198 @@ def combine(dm: Dims, perm: dict, y, topk_ids, topk_w, stream=None):
     _check(_combine(C.byref(dm), perm["capacity"], _ptr(y, torch.float32), _ptr(topk_ids, torch.int32),
                     _ptr(topk_w, torch.float32), _ptr(perm["inv_pairs"]), _ptr(out), _stream(stream)))
     return out
+
+
+# --------------------------------------------------------------------------- dense feed-forward
+
+_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # MOE_T_*
+
+
+def _type(dtype, allowed=tuple(_TYPES)):
+    if dtype not in allowed:
+        raise TypeError(f"expected one of {[str(t) for t in allowed]}, got {dtype}")
+    return _TYPES[dtype]
+
+
+class _Call:
+    """One call of a dense operator: its device (that of the first tensor;
+    the others must be on it too) and its stream (default: the device's
+    current one).  New tensors are allocated for that stream, and the library
+    runs with that device current."""
+
+    def __init__(self, first: torch.Tensor, stream):
+        if not first.is_cuda:
+            raise ValueError("fp8_moe_layer_amd works on device tensors only")
+        self.dev = first.device
+        if stream is None:
+            self.stream = torch.cuda.current_stream(self.dev)
+            self.alloc = None
+        else:
+            if stream.device != self.dev:
+                raise ValueError(f"stream is on {stream.device}, tensors on {self.dev}")
+            self.stream = self.alloc = stream
+
+    def ptr(self, t: Optional[torch.Tensor], shape, dtype, name: str):
+        """Address of a contiguous tensor of that shape and type on the call's device."""
+        if t is None:
+            return None
+        if t.device != self.dev:
+            raise ValueError(f"{name} is on {t.device}, expected {self.dev}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def rows(self, t: torch.Tensor, shape, dtype, name: str):
+        """(address, row stride in elements) of a 2-D tensor whose rows are
+        contiguous; the library checks the stride."""
+        if t.device != self.dev:
+            raise ValueError(f"{name} is on {t.device}, expected {self.dev}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.stride(1) != 1 and t.shape[1] > 1:
+            raise ValueError(f"{name}: rows must be contiguous")
+        return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+    def empty(self, shape, dtype):
+        with _on(self.alloc):
+            return torch.empty(shape, dtype=dtype, device=self.dev)
+
+    def run(self, fn, *args):
+        if torch.cuda.current_device() == self.dev.index:
+            _check(fn(*args, self.stream.cuda_stream))
+        else:
+            with torch.cuda.device(self.dev):
+                _check(fn(*args, self.stream.cuda_stream))
+
+
+def _shape2(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected 2 dimensions, got {t.dim()}")
+    return t.shape
+
+
+def quantize_rows_i8(x: torch.Tensor, q: Optional[torch.Tensor] = None,
+                     scale: Optional[torch.Tensor] = None, stream=None):
+    """Per-row symmetric int8 quantisation of x [rows, cols] (fp32, bf16 or
+    fp16; rows may be strided): (codes int8 [rows, cols], fp32 scale [rows]),
+    x ~= codes * scale (moe_quantize_rows_i8).  For activations per token, for
+    weight matrices per output channel."""
+    rows, cols = _shape2(x, "x")
+    c = _Call(x, stream)
+    kind = _type(x.dtype)
+    xp, ldx = c.rows(x, x.shape, x.dtype, "x")
+    q = c.empty((rows, cols), torch.int8) if q is None else q
+    scale = c.empty((rows,), torch.float32) if scale is None else scale
+    c.run(_quantize_rows_i8, xp, kind, ldx, rows, cols, c.ptr(q, x.shape, torch.int8, "q"),
+          c.ptr(scale, x.shape[:1], torch.float32, "scale"))
+    return q, scale
+
+
+def matmul_i8(xq: torch.Tensor, sx: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor,
+              bias: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+              out_dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
+    """y = (xq @ wq.T) * sx[:, None] * sw (+ bias) from int8 codes
+    (moe_matmul_i8): xq [T, K] (rows may be strided) with a scale per token,
+    wq [N, K] with a scale per output channel, bias fp32 [N]; y [T, N] in
+    out_dtype (or out's type): fp32, bf16 or fp16."""
+    (T, K), (N, _) = _shape2(xq, "xq"), _shape2(wq, "wq")
+    c = _Call(xq, stream)
+    y = c.empty((T, N), out_dtype) if out is None else out
+    kind = _type(y.dtype)
+    xp, ldx = c.rows(xq, (T, K), torch.int8, "xq")
+    c.run(_matmul_i8, xp, ldx, c.ptr(sx, (T,), torch.float32, "sx"),
+          c.ptr(wq, (N, K), torch.int8, "wq"), c.ptr(sw, (N,), torch.float32, "sw"),
+          c.ptr(bias, (N,), torch.float32, "bias"), T, K, N, kind,
+          c.ptr(y, (T, N), y.dtype, "out"))
+    return y
+
+
+def gated_ffn_i8(xq: torch.Tensor, sx: torch.Tensor, w_gate: torch.Tensor, s_gate: torch.Tensor,
+                 w_up: torch.Tensor, s_up: torch.Tensor, out: Optional[torch.Tensor] = None,
+                 out_dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
+    """h = SiLU(g) * u with g, u the two int8 projections of xq [T, d]
+    (moe_gated_ffn_i8): w_gate, w_up int8 [f, d] with a scale per channel;
+    h [T, f] in out_dtype (or out's type)."""
+    (T, d), (f, _) = _shape2(xq, "xq"), _shape2(w_gate, "w_gate")
+    c = _Call(xq, stream)
+    h = c.empty((T, f), out_dtype) if out is None else out
+    kind = _type(h.dtype)
+    xp, ldx = c.rows(xq, (T, d), torch.int8, "xq")
+    c.run(_gated_ffn_i8, xp, ldx, c.ptr(sx, (T,), torch.float32, "sx"),
+          c.ptr(w_gate, (f, d), torch.int8, "w_gate"),
+          c.ptr(s_gate, (f,), torch.float32, "s_gate"), c.ptr(w_up, (f, d), torch.int8, "w_up"),
+          c.ptr(s_up, (f,), torch.float32, "s_up"), T, d, f, kind,
+          c.ptr(h, (T, f), h.dtype, "out"))
+    return h
+
+
+_TYPES16 = (torch.bfloat16, torch.float16)
+
+
+def _no_autograd(fn: str, *tensors):
+    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
+        raise RuntimeError(f"{fn} is not recorded by autograd: call it under torch.no_grad() "
+                           "(inside a torch.autograd.Function, say) and take the gradients from "
+                           "gated_ffn_backward")
+
+
+def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+              out: Optional[torch.Tensor] = None, save: bool = False, stream=None):
+    """h = SiLU(x w_gate^T) * (x w_up^T) in one kernel (moe_gated_ffn): x
+    [T, d] (rows may be strided), w_gate, w_up [f, d], all bf16 or all fp16.
+    Returns h [T, f]; with save=True (h, gate, up), the two products that
+    gated_ffn_backward takes.  Autograd does not see the call."""
+    (T, d), (f, _) = _shape2(x, "x"), _shape2(w_gate, "w_gate")
+    _no_autograd("gated_ffn", x, w_gate, w_up)
+    c = _Call(x, stream)
+    kind = _type(x.dtype, _TYPES16)
+    h = c.empty((T, f), x.dtype) if out is None else out
+    gate, up = (c.empty((T, f), x.dtype), c.empty((T, f), x.dtype)) if save else (None, None)
+    xp, ldx = c.rows(x, (T, d), x.dtype, "x")
+    c.run(_gated_ffn, xp, ldx, c.ptr(w_gate, (f, d), x.dtype, "w_gate"),
+          c.ptr(w_up, (f, d), x.dtype, "w_up"), kind, T, d, f, c.ptr(h, (T, f), x.dtype, "out"),
+          None if gate is None else gate.data_ptr(), None if up is None else up.data_ptr())
+    return (h, gate, up) if save else h
+
+
+def gated_ffn_backward_workspace_bytes(T: int, d: int, f: int) -> int:
+    return int(_gated_bwd_ws(T, d, f))
+
+
+def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor,
+                       w_up: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
+                       dx: Optional[torch.Tensor] = None, dw_gate: Optional[torch.Tensor] = None,
+                       dw_up: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of gated_ffn (moe_gated_ffn_backward) from dh [T, f] (rows
+    may be strided) and the gate, up that gated_ffn(save=True) returned:
+    (dx, dw_gate, dw_up) in x's type, written over whatever dx, dw_gate, dw_up
+    held.  workspace: uint8, gated_ffn_backward_workspace_bytes(T, d, f) or
+    more, 256-byte aligned; allocated here when not given."""
+    (T, d), (f, _) = _shape2(x, "x"), _shape2(w_gate, "w_gate")
+    _no_autograd("gated_ffn_backward", dh, x, w_gate, w_up, gate, up)
+    c = _Call(x, stream)
+    t16 = x.dtype
+    kind = _type(t16, _TYPES16)
+    dx = c.empty((T, d), t16) if dx is None else dx
+    dw_gate = c.empty((f, d), t16) if dw_gate is None else dw_gate
+    dw_up = c.empty((f, d), t16) if dw_up is None else dw_up
+    if workspace is None:
+        workspace = c.empty((max(gated_ffn_backward_workspace_bytes(T, d, f), 1),), torch.uint8)
+    dp, lddh = c.rows(dh, (T, f), t16, "dh")
+    xp, ldx = c.rows(x, (T, d), t16, "x")
+    c.run(_gated_bwd, dp, lddh, xp, ldx, c.ptr(w_gate, (f, d), t16, "w_gate"),
+          c.ptr(w_up, (f, d), t16, "w_up"), c.ptr(gate, (T, f), t16, "gate"),
+          c.ptr(up, (T, f), t16, "up"), kind, T, d, f, c.ptr(dx, (T, d), t16, "dx"),
+          c.ptr(dw_gate, (f, d), t16, "dw_gate"), c.ptr(dw_up, (f, d), t16, "dw_up"),
+          c.ptr(workspace, workspace.shape, torch.uint8, "workspace"), workspace.numel())
+    return dx, dw_gate, dw_up
 
 
 # --------------------------------------------------------------------------- whole layer

@@ -17,7 +17,7 @@ CSRC = HERE / "csrc"
 LIB = HERE / "libfp8moe.so"
 LIB_DEBUG = HERE / "libfp8moe_debug.so"
 SOURCES = ["kernels_route.hip", "kernels_permute.hip", "kernels_expert.hip", "kernels_persistent.hip",
-           "abi.hip", "batching.hip"]
+           "abi.hip", "batching.hip", "kernels_dense.hip", "dense.hip"]
 ARCH = os.environ.get("FP8MOE_ARCH", "gfx950")
 
 HIPCC_FLAGS = [

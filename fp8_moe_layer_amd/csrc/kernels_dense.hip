@@ -1,0 +1,486 @@
+// kernels_dense.hip -- the dense feed-forward operators: per-row int8
+// quantisation, the int8 product with token and channel scales, the gated
+// block (both projections, SiLU and product in one kernel) in int8 and in
+// 16-bit types, and the 16-bit block's backward pass.
+#include "dense.hpp"
+#include "dense_dev.hpp"
+#include "expert_dev.hpp"  // exp_neg
+
+namespace fp8moe {
+
+namespace {
+
+// ---------------------------------------------------------------- elements
+template <class T>
+struct Elem;
+template <>
+struct Elem<float> {
+  static __device__ __forceinline__ float get(float v) { return v; }
+  static __device__ __forceinline__ float put(float v) { return v; }
+};
+template <>
+struct Elem<__bf16> {
+  static __device__ __forceinline__ float get(__bf16 v) { return (float)v; }
+  static __device__ __forceinline__ __bf16 put(float v) { return (__bf16)v; }
+};
+template <>
+struct Elem<_Float16> {
+  static __device__ __forceinline__ float get(_Float16 v) { return (float)v; }
+  static __device__ __forceinline__ _Float16 put(float v) { return (_Float16)v; }
+};
+
+// CNT consecutive values to dst, rounded once to T (nearest, ties to even);
+// the first `valid` of them exist.  vec: dst's row starts and length are
+// multiples of 16 bytes.
+template <class T, int CNT>
+__device__ __forceinline__ void store_run(T *dst, const float (&v)[CNT], int valid, bool vec) {
+  if (vec && valid >= CNT) {
+    constexpr int kBytes = CNT * (int)sizeof(T);
+    constexpr int kPart = kBytes < 16 ? kBytes : 16;  // 8 or 16 bytes a store
+    T tmp[CNT];
+#pragma unroll
+    for (int i = 0; i < CNT; ++i) tmp[i] = Elem<T>::put(v[i]);
+#pragma unroll
+    for (int b = 0; b < kBytes / kPart; ++b) {
+      if constexpr (kPart == 16) {
+        v4i w;
+        __builtin_memcpy(&w, reinterpret_cast<const char *>(tmp) + b * 16, 16);
+        reinterpret_cast<v4i *>(dst)[b] = w;
+      } else {
+        v2i w;
+        __builtin_memcpy(&w, tmp, 8);
+        reinterpret_cast<v2i *>(dst)[b] = w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < CNT; ++i)
+      if (i < valid) dst[i] = Elem<T>::put(v[i]);
+  }
+}
+
+// SiLU(g) * u with the reciprocal instruction (1 ulp) for the divide.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  return g * __builtin_amdgcn_rcpf(1.0f + exp_neg(g)) * u;
+}
+
+// ---------------------------------------------------------------- epilogues
+// An epilogue takes a lane's 4*NJ consecutive channels of one token.
+// Per-channel scales are loaded once per lane, per-token scales once per token.
+template <class OUT>
+struct EpiI8 {
+  static constexpr bool kGated = false;
+  const float *sx, *sw, *bias;
+  OUT *y;
+  int32_t N, vec;
+  template <int CNT>
+  struct Chan {
+    float s[CNT], b[CNT];
+  };
+  template <int CNT>
+  __device__ __forceinline__ void load(Chan<CNT> &c, int ch) const {
+#pragma unroll
+    for (int i = 0; i < CNT; ++i) {
+      const bool in = ch + i < N;
+      c.s[i] = in ? sw[ch + i] : 0.0f;
+      c.b[i] = in && bias ? bias[ch + i] : 0.0f;
+    }
+  }
+  // The integer sum is rounded to fp32 once (it can pass 24 bits), then
+  // scaled by the token's and the channel's scale.
+  template <int CNT>
+  __device__ __forceinline__ void store(const Chan<CNT> &c, int t, int ch, const int (&a)[1][CNT]) const {
+    const float s = sx[t];
+    float v[CNT];
+#pragma unroll
+    for (int i = 0; i < CNT; ++i) v[i] = (float)a[0][i] * s * c.s[i] + c.b[i];
+    store_run<OUT, CNT>(y + (int64_t)t * N + ch, v, N - ch, vec);
+  }
+};
+
+template <class OUT>
+struct EpiI8Gated {
+  static constexpr bool kGated = true;
+  const float *sx, *sg, *su;
+  OUT *h;
+  int32_t N, vec;
+  template <int CNT>
+  struct Chan {
+    float g[CNT], u[CNT];
+  };
+  template <int CNT>
+  __device__ __forceinline__ void load(Chan<CNT> &c, int ch) const {
+#pragma unroll
+    for (int i = 0; i < CNT; ++i) {
+      const bool in = ch + i < N;
+      c.g[i] = in ? sg[ch + i] : 0.0f;
+      c.u[i] = in ? su[ch + i] : 0.0f;
+    }
+  }
+  template <int CNT>
+  __device__ __forceinline__ void store(const Chan<CNT> &c, int t, int ch, const int (&a)[2][CNT]) const {
+    const float s = sx[t];
+    float v[CNT];
+#pragma unroll
+    for (int i = 0; i < CNT; ++i)
+      v[i] = silu_mul((float)a[0][i] * s * c.g[i], (float)a[1][i] * s * c.u[i]);
+    store_run<OUT, CNT>(h + (int64_t)t * N + ch, v, N - ch, vec);
+  }
+};
+
+// h from the fp32 products; the products themselves, rounded to the
+// activations' type, only where the caller keeps them for the backward pass.
+template <class T>
+struct EpiGated {
+  static constexpr bool kGated = true;
+  T *h, *gate, *up;
+  int32_t N, vec;
+  template <int CNT>
+  struct Chan {};
+  template <int CNT>
+  __device__ __forceinline__ void load(Chan<CNT> &, int) const {}
+  template <int CNT>
+  __device__ __forceinline__ void store(const Chan<CNT> &, int t, int ch, const float (&a)[2][CNT]) const {
+    const int64_t at = (int64_t)t * N + ch;
+    float v[CNT];
+#pragma unroll
+    for (int i = 0; i < CNT; ++i) v[i] = silu_mul(a[0][i], a[1][i]);
+    store_run<T, CNT>(h + at, v, N - ch, vec);
+    if (gate) {
+      store_run<T, CNT>(gate + at, a[0], N - ch, vec);
+      store_run<T, CNT>(up + at, a[1], N - ch, vec);
+    }
+  }
+};
+
+// A plain product: rows below `split` go to y0, the others to y1.
+template <class T>
+struct EpiPlain {
+  static constexpr bool kGated = false;
+  T *y0, *y1;
+  int32_t split, N, vec;
+  template <int CNT>
+  struct Chan {};
+  template <int CNT>
+  __device__ __forceinline__ void load(Chan<CNT> &, int) const {}
+  template <int CNT>
+  __device__ __forceinline__ void store(const Chan<CNT> &, int t, int ch, const float (&a)[1][CNT]) const {
+    T *row = t < split ? y0 + (int64_t)t * N : y1 + (int64_t)(t - split) * N;
+    store_run<T, CNT>(row + ch, a[0], N - ch, vec);
+  }
+};
+
+// ---------------------------------------------------------------- product kernel
+template <class Op, int BM, int BN, int TM, int TN, class Epi>
+__global__ __launch_bounds__(TM *TN *kWave) void tile_kernel(DenseIn in, Epi epi, int tiles_m,
+                                                             int tiles_n) {
+  typedef TileShape<BM, BN, TM, TN, Epi::kGated> S;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * S::kStageBytes];
+  int tm, tn;
+  tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  const int t0 = tm * BM, n0 = tn * S::kTileChannels;
+  typename Op::Acc acc[S::NB][S::MS][S::NJ];
+  tile_product<Op, BM, BN, TM, TN, Epi::kGated>(in, t0, n0, lds, acc);
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int ch = n0 + (wave % TN) * S::CH + (lane >> 4) * 4 * S::NJ;
+  if (ch >= in.N) return;
+  typename Epi::template Chan<4 * S::NJ> chan;
+  epi.load(chan, ch);
+#pragma unroll
+  for (int m = 0; m < S::MS; ++m) {
+    const int t = t0 + (wave / TN) * S::WM + m * 16 + (lane & 15);
+    if (t >= in.M) continue;
+    typename Op::Sum a[S::NB][4 * S::NJ];
+#pragma unroll
+    for (int b = 0; b < S::NB; ++b)
+#pragma unroll
+      for (int j = 0; j < S::NJ; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[b][j * 4 + i] = acc[b][m][j][i];
+    epi.store(chan, t, ch, a);
+  }
+}
+
+template <class Op, int BM, int BN, int TM, int TN, class Epi>
+hipError_t run_tile(const DenseIn &in, const Epi &epi, hipStream_t stream) {
+  typedef TileShape<BM, BN, TM, TN, Epi::kGated> S;
+  const int64_t tm = ((int64_t)in.M + BM - 1) / BM;
+  const int64_t tn = ((int64_t)in.N + S::kTileChannels - 1) / S::kTileChannels;
+  if (tm * tn == 0) return hipSuccess;
+  if (tm * tn > 0x7fffffff) return hipErrorInvalidValue;
+  tile_kernel<Op, BM, BN, TM, TN, Epi>
+      <<<(unsigned)(tm * tn), S::kThreads, 0, stream>>>(in, epi, (int)tm, (int)tn);
+  return hipGetLastError();
+}
+
+template <class Op, class Epi>
+hipError_t run_product(const DenseIn &in, const Epi &epi, hipStream_t stream) {
+  return run_tile<Op, 64, 64, 2, 2, Epi>(in, epi, stream);
+}
+
+bool vec_ok(const void *p, int64_t row_bytes) {
+  return (uintptr_t)p % 16 == 0 && row_bytes % 16 == 0;
+}
+
+// ---------------------------------------------------------------- int8 quantisation
+// m = max(amax, 2^-100), r = fl(127/m) and s = fl(m/127) as two correctly
+// rounded fp32 divisions (the floor keeps r finite for rows of tiny values; an
+// all-zero row gets s = 1), code = round-to-nearest-even of x * r.
+// fma(x, r, 1.5 * 2^23) is that rounding itself, of the exact product and in
+// one step: the sum's last place is 1, and its low byte the code in two's
+// complement (|x * r| <= 127 * (1 + 2^-24)^2, which rounds to at most 127).
+constexpr float kI8Max = 127.0f;
+constexpr float kI8Floor = 0x1p-100f;
+constexpr float kRoundMagic = 12582912.0f;  // 1.5 * 2^23
+
+struct I8Scale {
+  float r, s;
+};
+__device__ __forceinline__ I8Scale i8_scale(float amax) {
+  const float m = fmaxf(amax, kI8Floor);
+  return I8Scale{kI8Max / m, amax == 0.0f ? 1.0f : m / kI8Max};
+}
+
+__device__ __forceinline__ uint32_t i8x4(const float *v, float r) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w |= (__float_as_uint(fmaf(v[i], r, kRoundMagic)) & 0xffu) << (8 * i);
+  return w;
+}
+
+// 16 consecutive values as floats.
+template <class T>
+__device__ __forceinline__ void load_run16(const T *p, float (&v)[16]) {
+  T tmp[16];
+#pragma unroll
+  for (int b = 0; b < (int)sizeof(T); ++b) {
+    const v4i w = load16(reinterpret_cast<const char *>(p) + b * 16);
+    __builtin_memcpy(reinterpret_cast<char *>(tmp) + b * 16, &w, 16);
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = Elem<T>::get(tmp[i]);
+}
+
+__device__ __forceinline__ float amax_run16(const float (&v)[16], float m) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    m = fmaxf(m, fabsf(v[i]));
+    if constexpr (kDebugChecks) dcheck(__builtin_isfinite(v[i]), kDbgNonFinite);
+  }
+  return m;
+}
+
+// One workgroup per row, 16 values a thread at a time; the row is read twice
+// (the second time from cache).
+template <class T>
+__global__ __launch_bounds__(256) void quantize_i8_kernel(const T *__restrict__ x, int64_t ldx,
+                                                          int cols, int8_t *__restrict__ q,
+                                                          float *__restrict__ scale) {
+  __shared__ float red[4];
+  const int64_t row = blockIdx.x;
+  const T *xr = x + row * ldx;
+  float amax = 0.0f;
+  for (int i = threadIdx.x * 16; i < cols; i += 256 * 16) {
+    float v[16];
+    load_run16(xr + i, v);
+    amax = amax_run16(v, amax);
+  }
+  amax = wave_max(amax);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = amax;
+  __syncthreads();
+  const I8Scale k = i8_scale(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
+  for (int i = threadIdx.x * 16; i < cols; i += 256 * 16) {
+    float v[16];
+    load_run16(xr + i, v);
+    v4i w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = (int)i8x4(v + 4 * j, k.r);
+    *reinterpret_cast<v4i *>(q + row * cols + i) = w;
+  }
+  if (threadIdx.x == 0) scale[row] = k.s;
+}
+
+// ---------------------------------------------------------------- backward helpers
+// dg = dh * u * s * (1 + g * (1 - s)), du = dh * g * s with s = sigmoid(g), in
+// fp32 from the kept g and u, rounded once to the operands' type: the two
+// products that follow take 16-bit operands.  Written row-major as
+// dgu [T][2f] (operand of dx) and transposed as dgu_t [2f][Tp] (operand of
+// dW; the Tp - T last columns are zero).
+template <class T>
+__global__ __launch_bounds__(256) void gate_grad_kernel(const T *__restrict__ dh, int64_t lddh,
+                                                        const T *__restrict__ gate,
+                                                        const T *__restrict__ up, int rows, int f,
+                                                        int64_t rows_p, T *__restrict__ dgu,
+                                                        T *__restrict__ dgu_t) {
+  __shared__ T tg[64][72], tu[64][72];
+  const int64_t t0 = (int64_t)blockIdx.x * 64;
+  const int c0 = blockIdx.y * 64;
+  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
+    const int c = i & 63;
+    const int64_t t = t0 + (i >> 6);
+    T a = Elem<T>::put(0.0f), b = a;
+    if (t < rows) {
+      const float g = Elem<T>::get(gate[t * f + c0 + c]), u = Elem<T>::get(up[t * f + c0 + c]);
+      const float d = Elem<T>::get(dh[t * lddh + c0 + c]);
+      const float s = __builtin_amdgcn_rcpf(1.0f + exp_neg(g));
+      a = Elem<T>::put(d * u * s * (1.0f + g * (1.0f - s)));
+      b = Elem<T>::put(d * g * s);
+      dgu[t * 2 * f + c0 + c] = a;
+      dgu[t * 2 * f + f + c0 + c] = b;
+    }
+    tg[c][i >> 6] = a;
+    tu[c][i >> 6] = b;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
+    const int64_t t = t0 + (i & 63);
+    const int c = i >> 6;
+    if (t < rows_p) {
+      dgu_t[(int64_t)(c0 + c) * rows_p + t] = tg[c][i & 63];
+      dgu_t[(int64_t)(f + c0 + c) * rows_p + t] = tu[c][i & 63];
+    }
+  }
+}
+
+// out[c][r] = in[r][c], zero for rows <= r < rows_p.
+template <class T>
+__global__ __launch_bounds__(256) void transpose_kernel(const T *__restrict__ in, int64_t ld,
+                                                        int rows, int64_t rows_p,
+                                                        T *__restrict__ out, int64_t ldo) {
+  __shared__ T tile[64][72];
+  const int64_t r0 = (int64_t)blockIdx.x * 64;
+  const int c0 = blockIdx.y * 64;
+  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
+    const int64_t r = r0 + (i >> 6);
+    tile[i & 63][i >> 6] = r < rows ? in[r * ld + c0 + (i & 63)] : Elem<T>::put(0.0f);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
+    const int64_t r = r0 + (i & 63);
+    if (r < rows_p) out[(int64_t)(c0 + (i >> 6)) * ldo + r] = tile[i >> 6][i & 63];
+  }
+}
+
+int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+struct BackwardLayout {
+  size_t dgu, dgu_t, x_t, w_t, total;
+};
+BackwardLayout backward_layout(int32_t T, int32_t d, int32_t f) {
+  BackwardLayout L{};
+  size_t o = 0;
+  auto take = [&](size_t elems) {
+    const size_t at = o;
+    o = up256(o + elems * 2);
+    return at;
+  };
+  const size_t tp = (size_t)up8(T);
+  L.dgu = take((size_t)T * 2 * f);
+  L.dgu_t = take(2 * (size_t)f * tp);
+  L.x_t = take((size_t)d * tp);
+  L.w_t = take((size_t)d * 2 * f);
+  L.total = o;
+  return L;
+}
+
+template <class OUT>
+hipError_t matmul_i8_as(const I8Product &p, hipStream_t stream) {
+  const DenseIn in{(const uint8_t *)p.xq, (const uint8_t *)p.wq, nullptr, p.ldx, p.K, p.T, p.N, p.K};
+  const EpiI8<OUT> epi{p.sx, p.sw, p.bias, (OUT *)p.y, p.N,
+                       vec_ok(p.y, (int64_t)p.N * (int64_t)sizeof(OUT))};
+  return run_product<OpI8>(in, epi, stream);
+}
+
+template <class OUT>
+hipError_t gated_i8_as(const I8Gated &p, hipStream_t stream) {
+  const DenseIn in{(const uint8_t *)p.xq, (const uint8_t *)p.w_gate, (const uint8_t *)p.w_up,
+                   p.ldx, p.d, p.T, p.f, p.d};
+  const EpiI8Gated<OUT> epi{p.sx, p.s_gate, p.s_up, (OUT *)p.h, p.f,
+                            vec_ok(p.h, (int64_t)p.f * (int64_t)sizeof(OUT))};
+  return run_product<OpI8>(in, epi, stream);
+}
+
+template <class Op, class E>
+hipError_t gated_as(const Gated16 &p, hipStream_t stream) {
+  const DenseIn in{(const uint8_t *)p.x, (const uint8_t *)p.w_gate, (const uint8_t *)p.w_up,
+                   p.ldx * 2, (int64_t)p.d * 2, p.T, p.f, (int64_t)p.d * 2};
+  const EpiGated<E> epi{(E *)p.h, (E *)p.gate, (E *)p.up, p.f, 1};
+  return run_product<Op>(in, epi, stream);
+}
+
+template <class Op, class E>
+hipError_t backward_as(const Gated16Backward &p, hipStream_t stream) {
+  const BackwardLayout L = backward_layout(p.T, p.d, p.f);
+  E *dgu = (E *)(p.workspace + L.dgu), *dgu_t = (E *)(p.workspace + L.dgu_t);
+  E *x_t = (E *)(p.workspace + L.x_t), *w_t = (E *)(p.workspace + L.w_t);
+  const int64_t tp = up8(p.T);
+  hipError_t e = hipSuccess;
+  if (p.T > 0) {
+    const unsigned tb = (unsigned)((tp + 63) / 64);
+    gate_grad_kernel<E><<<dim3(tb, p.f / 64), 256, 0, stream>>>(
+        (const E *)p.dh, p.lddh, (const E *)p.gate, (const E *)p.up, p.T, p.f, tp, dgu, dgu_t);
+    transpose_kernel<E>
+        <<<dim3(tb, p.d / 64), 256, 0, stream>>>((const E *)p.x, p.ldx, p.T, tp, x_t, tp);
+    transpose_kernel<E><<<dim3(p.f / 64, p.d / 64), 256, 0, stream>>>(
+        (const E *)p.w_gate, p.d, p.f, p.f, w_t, 2 * (int64_t)p.f);
+    transpose_kernel<E><<<dim3(p.f / 64, p.d / 64), 256, 0, stream>>>(
+        (const E *)p.w_up, p.d, p.f, p.f, w_t + p.f, 2 * (int64_t)p.f);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const int64_t k2 = (int64_t)p.f * 4;  // bytes of 2f elements
+    const DenseIn in{(const uint8_t *)dgu, (const uint8_t *)w_t, nullptr, k2, k2, p.T, p.d, k2};
+    const EpiPlain<E> epi{(E *)p.dx, nullptr, p.T, p.d, 1};
+    if ((e = run_product<Op>(in, epi, stream)) != hipSuccess) return e;
+  }
+  // no tokens: K = 0, and the weights' gradients come out as zeros
+  const DenseIn in{(const uint8_t *)dgu_t, (const uint8_t *)x_t, nullptr, tp * 2, tp * 2,
+                   2 * p.f, p.d, tp * 2};
+  const EpiPlain<E> epi{(E *)p.dw_gate, (E *)p.dw_up, p.f, p.d, 1};
+  return run_product<Op>(in, epi, stream);
+}
+
+}  // namespace
+
+hipError_t launch_quantize_i8(const void *x, int32_t type, int64_t ldx, int32_t rows, int32_t cols,
+                              int8_t *q, float *scale, hipStream_t stream) {
+  if (rows == 0) return hipSuccess;
+  if (type == kTypeF32)
+    quantize_i8_kernel<float><<<rows, 256, 0, stream>>>((const float *)x, ldx, cols, q, scale);
+  else if (type == kTypeBf16)
+    quantize_i8_kernel<__bf16><<<rows, 256, 0, stream>>>((const __bf16 *)x, ldx, cols, q, scale);
+  else
+    quantize_i8_kernel<_Float16><<<rows, 256, 0, stream>>>((const _Float16 *)x, ldx, cols, q, scale);
+  return hipGetLastError();
+}
+
+hipError_t launch_matmul_i8(const I8Product &p, hipStream_t stream) {
+  return p.out_type == kTypeF32    ? matmul_i8_as<float>(p, stream)
+         : p.out_type == kTypeBf16 ? matmul_i8_as<__bf16>(p, stream)
+                                   : matmul_i8_as<_Float16>(p, stream);
+}
+
+hipError_t launch_gated_i8(const I8Gated &p, hipStream_t stream) {
+  return p.out_type == kTypeF32    ? gated_i8_as<float>(p, stream)
+         : p.out_type == kTypeBf16 ? gated_i8_as<__bf16>(p, stream)
+                                   : gated_i8_as<_Float16>(p, stream);
+}
+
+hipError_t launch_gated(const Gated16 &p, hipStream_t stream) {
+  return p.type == kTypeBf16 ? gated_as<OpBf16, __bf16>(p, stream)
+                             : gated_as<OpF16, _Float16>(p, stream);
+}
+
+size_t gated_backward_workspace(int32_t T, int32_t d, int32_t f) {
+  return backward_layout(T, d, f).total;
+}
+
+hipError_t launch_gated_backward(const Gated16Backward &p, hipStream_t stream) {
+  return p.type == kTypeBf16 ? backward_as<OpBf16, __bf16>(p, stream)
+                             : backward_as<OpF16, _Float16>(p, stream);
+}
+
+FP8MOE_DEBUG_TAKE(dense)
+
+}  // namespace fp8moe

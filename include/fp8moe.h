@@ -307,6 +307,86 @@ moe_status moe_fused_forward_noalloc(const moe_dims *dims /*host*/, const float 
                                      int32_t *topk_ids_out, float *topk_w_out, void *stream);
 
 /* ------------------------------------------------------------------------ */
+/* Dense feed-forward operators                                              */
+/* ------------------------------------------------------------------------ */
+
+/* The gated feed-forward block of a model's dense layers, outside any
+ * routing: in 16-bit types with its backward pass, to be trained, and in int8
+ * with a scale per token row and per output channel, to be served:
+ *
+ *   training   h = moe_gated_ffn(x), gradients by moe_gated_ffn_backward
+ *   serving    moe_quantize_rows_i8(x) -> moe_gated_ffn_i8 -> h
+ *              moe_quantize_rows_i8(h) -> moe_matmul_i8 (the down projection)
+ *
+ * (int8 weights: moe_quantize_rows_i8 on the weight matrix, once.)  Weights
+ * are row-major, contiguous: [outputs][inputs].  Activations that are read may
+ * have a row stride: ldx, lddh are in ELEMENTS, at least the row length, a
+ * multiple of 16 bytes and at most 8 MiB.  Outputs are contiguous.  Every
+ * array is 16-byte aligned (scales and bias 4-byte).  An output that shares
+ * memory with an input or with another output is MOE_ERR_SHAPE.  T = 0 is
+ * valid: the arrays with T rows may then be NULL, and nothing is written but
+ * the weights' gradients, which are zeros.  Inputs are finite, as everywhere. */
+enum { MOE_T_F32 = 0, MOE_T_BF16 = 1, MOE_T_F16 = 2 }; /* element types */
+#define MOE_MAX_TOKENS (1 << 22) /* rows of one call, and outputs N of moe_matmul_i8 */
+#define MOE_MAX_I8_K 65536       /* longest int8 row: its products' sum fits 31 bits */
+
+/* Per-row symmetric int8 quantisation of x [rows][cols] (x_type, row stride
+ * ldx): with a = max |x| of the row and m = max(a, 2^-100),
+ *   r = fl(127 / m), scale = fl(m / 127) (1 for an all-zero row),
+ *   q = x * r rounded once, to nearest, ties to even (|q| <= 127),
+ * so x ~= q * scale within scale * (1/2 + 2^-15).
+ * q [rows][cols] contiguous, scale [rows].  cols: a multiple of 16 up to
+ * MOE_MAX_I8_K; rows: any. */
+moe_status moe_quantize_rows_i8(const void *x, int32_t x_type, int64_t ldx, int32_t rows,
+                                int32_t cols, int8_t *q, float *scale, void *stream);
+
+/* Matrix product of int8 codes with a scale per token and per channel:
+ *   y[t][n] = fl32(sum_k xq[t][k] * wq[n][k]) * sx[t] * sw[n] (+ bias[n])
+ * The sum is exact (32-bit integers, any codes); the rest is fp32, rounded
+ * once to y_type (fp16: past 65504 to infinity).  xq [T][K] with row stride
+ * ldx, sx [T], wq [N][K], sw [N], bias [N] fp32 or NULL, y [T][N].
+ * K: a multiple of 16 up to MOE_MAX_I8_K; T and N: any up to MOE_MAX_TOKENS. */
+moe_status moe_matmul_i8(const int8_t *xq, int64_t ldx, const float *sx, const int8_t *wq,
+                         const float *sw, const float *bias, int32_t T, int32_t K, int32_t N,
+                         int32_t y_type, void *y, void *stream);
+
+/* The gated block on int8 codes, in one kernel:
+ *   g = xq w_gate^T * sx * s_gate, u = xq w_up^T * sx * s_up, h = SiLU(g) * u
+ * xq [T][d] with row stride ldx, w_gate, w_up [f][d], s_gate, s_up [f],
+ * h [T][f] in h_type.  d, f: multiples of 64 up to MOE_MAX_HIDDEN / MOE_MAX_FFN. */
+moe_status moe_gated_ffn_i8(const int8_t *xq, int64_t ldx, const float *sx, const int8_t *w_gate,
+                            const float *s_gate, const int8_t *w_up, const float *s_up, int32_t T,
+                            int32_t d, int32_t f, int32_t h_type, void *h, void *stream);
+
+/* The gated block in bf16 or fp16 (`type`, of every array), in one kernel:
+ *   g = x w_gate^T, u = x w_up^T (fp32 sums), h = SiLU(g) * u, rounded once
+ * x [T][d] with row stride ldx, w_gate, w_up [f][d], h [T][f].  gate, up
+ * [T][f]: where g and u, rounded to `type`, are kept for the backward pass, or
+ * both NULL.  d, f: multiples of 64 up to MOE_MAX_HIDDEN / MOE_MAX_FFN. */
+moe_status moe_gated_ffn(const void *x, int64_t ldx, const void *w_gate, const void *w_up,
+                         int32_t type, int32_t T, int32_t d, int32_t f, void *h, void *gate,
+                         void *up, void *stream);
+
+/* Its backward pass, from the gradient dh [T][f] (row stride lddh) of h and
+ * the g, u kept by the forward pass: with s = sigmoid(g),
+ *   dg = dh * u * s * (1 + g * (1 - s)),  du = dh * g * s
+ * (fp32, then rounded to `type`: the products below take 16-bit operands),
+ *   dx = dg w_gate + du w_up   [T][d],
+ *   dw_gate = dg^T x, dw_up = du^T x   [f][d],
+ * fp32 sums, each output rounded once to `type` and overwritten (not added
+ * to).  Sums are taken in an order that depends on the sizes alone, so equal
+ * inputs give equal bits.  workspace: a device buffer of at least
+ * moe_gated_ffn_backward_workspace_bytes(T, d, f), 256-byte aligned, not
+ * touched by anything else while the work is in flight (the size is 0, with a
+ * text in moe_last_error(), for sizes that the call refuses). */
+size_t moe_gated_ffn_backward_workspace_bytes(int32_t T, int32_t d, int32_t f);
+moe_status moe_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, int64_t ldx,
+                                  const void *w_gate, const void *w_up, const void *gate,
+                                  const void *up, int32_t type, int32_t T, int32_t d, int32_t f,
+                                  void *dx, void *dw_gate, void *dw_up, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ */
 /* Diagnostics                                                               */
 /* ------------------------------------------------------------------------ */
 
