@@ -501,14 +501,14 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
               out: Optional[torch.Tensor] = None, save: bool = False, stream=None):
     """h = SiLU(x w_gate^T) * (x w_up^T) in one kernel (moe_gated_ffn): x
     [T, d] (rows may be strided), w_gate, w_up [f, d], all bf16 or all fp16.
-    Returns h [T, f]; with save=True (h, gate, up), the two products that
-    gated_ffn_backward takes.  Autograd does not see the call."""
+    Returns h [T, f]; with save=True (h, gate, up), the two products in fp32 as
+    gated_ffn_backward takes them.  Autograd does not see the call."""
     (T, d), (f, _) = _shape2(x, "x"), _shape2(w_gate, "w_gate")
     _no_autograd("gated_ffn", x, w_gate, w_up)
     c = _Call(x, stream)
     kind = _type(x.dtype, _TYPES16)
     h = c.empty((T, f), x.dtype) if out is None else out
-    gate, up = (c.empty((T, f), x.dtype), c.empty((T, f), x.dtype)) if save else (None, None)
+    gate, up = (c.empty((T, f), torch.float32), c.empty((T, f), torch.float32)) if save else (None, None)
     xp, ldx = c.rows(x, (T, d), x.dtype, "x")
     c.run(_gated_ffn, xp, ldx, c.ptr(w_gate, (f, d), x.dtype, "w_gate"),
           c.ptr(w_up, (f, d), x.dtype, "w_up"), kind, T, d, f, c.ptr(h, (T, f), x.dtype, "out"),
@@ -543,8 +543,8 @@ def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor,
     dp, lddh = c.rows(dh, (T, f), t16, "dh")
     xp, ldx = c.rows(x, (T, d), t16, "x")
     c.run(_gated_bwd, dp, lddh, xp, ldx, c.ptr(w_gate, (f, d), t16, "w_gate"),
-          c.ptr(w_up, (f, d), t16, "w_up"), c.ptr(gate, (T, f), t16, "gate"),
-          c.ptr(up, (T, f), t16, "up"), kind, T, d, f, c.ptr(dx, (T, d), t16, "dx"),
+          c.ptr(w_up, (f, d), t16, "w_up"), c.ptr(gate, (T, f), torch.float32, "gate"),
+          c.ptr(up, (T, f), torch.float32, "up"), kind, T, d, f, c.ptr(dx, (T, d), t16, "dx"),
           c.ptr(dw_gate, (f, d), t16, "dw_gate"), c.ptr(dw_up, (f, d), t16, "dw_up"),
           c.ptr(workspace, workspace.shape, torch.uint8, "workspace"), workspace.numel())
     return dx, dw_gate, dw_up

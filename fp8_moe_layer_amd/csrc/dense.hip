@@ -31,9 +31,9 @@ bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 int32_t type_bytes(int32_t type) { return type == MOE_T_F32 ? 4 : 2; }
 
-// Rows of an operand as the kernels' buffer descriptors address them: 256
-// rows of ld bytes each stay below 2^32 bytes.
-constexpr int64_t kMaxRowBytes = (int64_t)1 << 23;
+// Longest row stride: a tile's rows (256) stay within the kernels' buffer
+// descriptors (2^30 bytes).
+constexpr int64_t kMaxRowBytes = (int64_t)1 << 22;
 
 // A caller's array: where it starts and how many bytes it spans.
 struct Span {
@@ -167,8 +167,8 @@ moe_status moe_gated_ffn_i8(const int8_t *xq, int64_t ldx, const float *sx, cons
 }
 
 moe_status moe_gated_ffn(const void *x, int64_t ldx, const void *w_gate, const void *w_up,
-                         int32_t type, int32_t T, int32_t d, int32_t f, void *h, void *gate,
-                         void *up, void *stream) {
+                         int32_t type, int32_t T, int32_t d, int32_t f, void *h, float *gate,
+                         float *up, void *stream) {
   const char *fn = "moe_gated_ffn";
   if (type != MOE_T_BF16 && type != MOE_T_F16)
     return fail_status(MOE_ERR_UNSUPPORTED, "%s: type=%d (MOE_T_BF16 or MOE_T_F16)", fn, type);
@@ -182,7 +182,7 @@ moe_status moe_gated_ffn(const void *x, int64_t ldx, const void *w_gate, const v
   if (!all_aligned({x, w_gate, w_up, h, gate, up}, 16))
     return fail_status(MOE_ERR_ALIGN, "%s: every array must be 16-byte aligned", fn);
   const int64_t wb = (int64_t)f * d * 2, hb = (int64_t)T * f * 2;
-  const Span out[] = {{h, hb}, {gate, hb}, {up, hb}};
+  const Span out[] = {{h, hb}, {gate, 2 * hb}, {up, 2 * hb}};
   const Span in[] = {{x, span_rows(T, ldx, d, 2)}, {w_gate, wb}, {w_up, wb}};
   if (clash(out, in))
     return fail_status(MOE_ERR_SHAPE, "%s: an output overlaps an input or another output", fn);
@@ -198,8 +198,8 @@ size_t moe_gated_ffn_backward_workspace_bytes(int32_t T, int32_t d, int32_t f) {
 }
 
 moe_status moe_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, int64_t ldx,
-                                  const void *w_gate, const void *w_up, const void *gate,
-                                  const void *up, int32_t type, int32_t T, int32_t d, int32_t f,
+                                  const void *w_gate, const void *w_up, const float *gate,
+                                  const float *up, int32_t type, int32_t T, int32_t d, int32_t f,
                                   void *dx, void *dw_gate, void *dw_up, void *workspace,
                                   size_t workspace_bytes, void *stream) {
   const char *fn = "moe_gated_ffn_backward";
@@ -223,7 +223,7 @@ moe_status moe_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, i
   const Span out[] = {{dx, (int64_t)T * d * 2}, {dw_gate, wb}, {dw_up, wb},
                       {workspace, (int64_t)need}};
   const Span in[] = {{dh, span_rows(T, lddh, f, 2)}, {x, span_rows(T, ldx, d, 2)}, {w_gate, wb},
-                     {w_up, wb}, {gate, hb}, {up, hb}};
+                     {w_up, wb}, {gate, 2 * hb}, {up, 2 * hb}};
   if (clash(out, in))
     return fail_status(MOE_ERR_SHAPE,
                        "%s: an output or the workspace overlaps an input or another output", fn);

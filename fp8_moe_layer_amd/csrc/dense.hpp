@@ -42,13 +42,14 @@ struct I8Gated {
 hipError_t launch_gated_i8(const I8Gated &p, hipStream_t stream);
 
 // h = SiLU(x Wg^T) * (x Wu^T) in 16-bit types; gate, up: the two products
-// kept for the backward pass, or both NULL.
+// kept (fp32) for the backward pass, or both NULL.
 struct Gated16 {
   const void *x;
   int64_t ldx;  // elements
   const void *w_gate, *w_up;
   int32_t T, d, f, type;
-  void *h, *gate, *up;
+  void *h;
+  float *gate, *up;
 };
 hipError_t launch_gated(const Gated16 &p, hipStream_t stream);
 
@@ -57,7 +58,8 @@ struct Gated16Backward {
   int64_t lddh;
   const void *x;
   int64_t ldx;
-  const void *w_gate, *w_up, *gate, *up;
+  const void *w_gate, *w_up;
+  const float *gate, *up;
   int32_t T, d, f, type;
   void *dx, *dw_gate, *dw_up;
   char *workspace;

@@ -2,6 +2,8 @@
 // quantisation, the int8 product with token and channel scales, the gated
 // block (both projections, SiLU and product in one kernel) in int8 and in
 // 16-bit types, and the 16-bit block's backward pass.
+#include <math.h>
+
 #include "dense.hpp"
 #include "dense_dev.hpp"
 #include "expert_dev.hpp"  // exp_neg
@@ -128,12 +130,15 @@ struct EpiI8Gated {
   }
 };
 
-// h from the fp32 products; the products themselves, rounded to the
-// activations' type, only where the caller keeps them for the backward pass.
+// h from the fp32 products; the products themselves only where the caller
+// keeps them for the backward pass, and then in fp32: rounded to 16 bits they
+// alone would make the gradients' error half as large again (dg and du are
+// rounded once more for the products that follow).
 template <class T>
 struct EpiGated {
   static constexpr bool kGated = true;
-  T *h, *gate, *up;
+  T *h;
+  float *gate, *up;
   int32_t N, vec;
   template <int CNT>
   struct Chan {};
@@ -147,8 +152,8 @@ struct EpiGated {
     for (int i = 0; i < CNT; ++i) v[i] = silu_mul(a[0][i], a[1][i]);
     store_run<T, CNT>(h + at, v, N - ch, vec);
     if (gate) {
-      store_run<T, CNT>(gate + at, a[0], N - ch, vec);
-      store_run<T, CNT>(up + at, a[1], N - ch, vec);
+      store_run<float, CNT>(gate + at, a[0], N - ch, vec);
+      store_run<float, CNT>(up + at, a[1], N - ch, vec);
     }
   }
 };
@@ -171,20 +176,20 @@ struct EpiPlain {
 };
 
 // ---------------------------------------------------------------- product kernel
-template <class Op, int BM, int BN, int TM, int TN, class Epi>
-__global__ __launch_bounds__(TM *TN *kWave) void tile_kernel(DenseIn in, Epi epi, int tiles_m,
+template <class Op, int BM, int BN, int TM, int TN, int U, int KG, class Epi>
+__global__ __launch_bounds__(TM *TN *KG *kWave) void tile_kernel(DenseIn in, Epi epi, int tiles_m,
                                                              int tiles_n) {
-  typedef TileShape<BM, BN, TM, TN, Epi::kGated> S;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * S::kStageBytes];
+  typedef TileShape<BM, BN, TM, TN, U, KG, Epi::kGated> S;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLdsBytes];
   int tm, tn;
   tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
   const int t0 = tm * BM, n0 = tn * S::kTileChannels;
   typename Op::Acc acc[S::NB][S::MS][S::NJ];
-  tile_product<Op, BM, BN, TM, TN, Epi::kGated>(in, t0, n0, lds, acc);
+  tile_product<Op, BM, BN, TM, TN, U, KG, Epi::kGated>(in, t0, n0, lds, acc);
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int ch = n0 + (wave % TN) * S::CH + (lane >> 4) * 4 * S::NJ;
-  if (ch >= in.N) return;
+  if (wave >= S::kWaves || ch >= in.N) return;  // the first K group has the sums
   typename Epi::template Chan<4 * S::NJ> chan;
   epi.load(chan, ch);
 #pragma unroll
@@ -202,21 +207,134 @@ __global__ __launch_bounds__(TM *TN *kWave) void tile_kernel(DenseIn in, Epi epi
   }
 }
 
-template <class Op, int BM, int BN, int TM, int TN, class Epi>
+template <class Op, int BM, int BN, int TM, int TN, int U, int KG, class Epi>
 hipError_t run_tile(const DenseIn &in, const Epi &epi, hipStream_t stream) {
-  typedef TileShape<BM, BN, TM, TN, Epi::kGated> S;
+  typedef TileShape<BM, BN, TM, TN, U, KG, Epi::kGated> S;
   const int64_t tm = ((int64_t)in.M + BM - 1) / BM;
   const int64_t tn = ((int64_t)in.N + S::kTileChannels - 1) / S::kTileChannels;
   if (tm * tn == 0) return hipSuccess;
   if (tm * tn > 0x7fffffff) return hipErrorInvalidValue;
-  tile_kernel<Op, BM, BN, TM, TN, Epi>
+  tile_kernel<Op, BM, BN, TM, TN, U, KG, Epi>
       <<<(unsigned)(tm * tn), S::kThreads, 0, stream>>>(in, epi, (int)tm, (int)tn);
   return hipGetLastError();
 }
 
+// ---------------------------------------------------------------- few tokens
+template <class Op, int XP, int NS, int W, int R, class Epi>
+__global__ __launch_bounds__(W *kWave) void stream_kernel(DenseIn in, Epi epi, int groups) {
+  typedef StreamShape<XP, NS, W, R> S;
+  typedef typename Op::Acc Acc;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLdsBytes];
+  constexpr bool kGated = Epi::kGated;
+  constexpr int kChannels = kGated ? S::kRows / 2 : S::kRows;
+  stream_product<Op, XP, NS, W, R, kGated>(in, groups, lds, [&](int g, const uint8_t *part) {
+    const int lane = threadIdx.x & 63;
+    auto sum = [&](int block, int l) {  // of the waves' parts, in wave order
+      Acc a = *reinterpret_cast<const Acc *>(part + block * 1024 + l * 16);
+#pragma unroll
+      for (int w = 1; w < W; ++w)
+        a += *reinterpret_cast<const Acc *>(part + w * S::kPart + block * 1024 + l * 16);
+      return a;
+    };
+    const int row = (lane >> 4) * 4;
+#pragma unroll
+    for (int s = 0; s < (kGated && NS > 1 ? NS / 2 : NS); ++s) {
+      // one gated sub-tile: rows 0-7 gate, 8-15 up, so the upper lanes have no channel
+      const bool none = kGated && NS == 1 && row >= 8;
+      const int ch = g * kChannels + s * 16 + row;
+      if (none || ch >= in.N) continue;
+      typename Epi::template Chan<4> chan;
+      epi.load(chan, ch);
+#pragma unroll
+      for (int m = 0; m < S::MS; ++m) {
+        const int t = m * 16 + (lane & 15);
+        if (t >= in.M) continue;
+        typename Op::Sum a[kGated ? 2 : 1][4];
+        const Acc a0 = sum(s * S::MS + m, lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[0][i] = a0[i];
+        if constexpr (kGated) {
+          const Acc a1 = NS == 1 ? sum(m, lane + 32) : sum((s + NS / 2) * S::MS + m, lane);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[1][i] = a1[i];
+        }
+        epi.store(chan, t, ch, a);
+      }
+    }
+  });
+}
+
+template <class Op, int XP, int NS, int W, int R, class Epi>
+hipError_t run_stream(const DenseIn &in, const Epi &epi, int most, hipStream_t stream) {
+  typedef StreamShape<XP, NS, W, R> S;
+  constexpr int kChannels = Epi::kGated ? S::kRows / 2 : S::kRows;
+  const int groups = (int)(((int64_t)in.N + kChannels - 1) / kChannels);
+  stream_kernel<Op, XP, NS, W, R, Epi>
+      <<<groups < most ? groups : most, S::kThreads, 0, stream>>>(in, epi, groups);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- choice
+constexpr int kCUs = 256;  // compute units of an MI355X
+
+// Estimated time of a product in tiles, in us.  A compute unit that holds r
+// workgroups takes max(a + b*(r-1), w*r) for a K step of all of them: alone, a
+// workgroup waits for its loads and barriers (a), a few hide each other's
+// waits (b), and then the loads or the matrix instructions are the limit (w).
+// At most `cap` workgroups fit; a round of cap per compute unit also costs c
+// to start and to store.  The constants are fits to measured products of 64 to
+// 8192 tokens, K of 768 to 28672 bytes, in int8 and bf16 (the byte counts
+// decide, not the type); the estimate is within about 15 % of them.
+struct TileCost {
+  int bm, channels, cap;
+  float a, b, w, c;
+};
+double tile_time(const TileCost &t, const DenseIn &in) {
+  const int64_t tiles = (((int64_t)in.M + t.bm - 1) / t.bm) *
+                        (((int64_t)in.N + t.channels - 1) / t.channels);
+  const double steps = (double)((in.kbytes + kStepBytes - 1) / kStepBytes);
+  auto step = [&](double r) { return fmax(t.a + t.b * (r - 1), t.w * r); };
+  const int64_t full = tiles / (kCUs * t.cap), rest = tiles % (kCUs * t.cap);
+  double us = (double)full * (t.c + steps * step(t.cap));
+  if (rest > 0) us += t.c + steps * step((double)((rest + kCUs - 1) / kCUs));
+  return us;
+}
+
+// Up to 32 tokens stream the weights (stream_product), unless at 17 to 32
+// there are many channels: then small tiles, which read the tokens less often,
+// are faster (bf16, T = 32, 4096 -> 2 x 14336: 35 us in tiles, 48 us streamed;
+// 14336 -> 4096 int8: 18 us streamed, 52 us in tiles).  Eight waves a
+// workgroup where the groups leave one to a compute unit, else four and two
+// workgroups (int8, one token, 14336 -> 4096: 11.0 and 14.3 us; 4096 -> 14336:
+// 13.4 and 11.9 us).  Above, the tile with the least estimated time.
 template <class Op, class Epi>
 hipError_t run_product(const DenseIn &in, const Epi &epi, hipStream_t stream) {
-  return run_tile<Op, 64, 64, 2, 2, Epi>(in, epi, stream);
+  if (in.M == 0) return hipSuccess;
+  constexpr int nb = Epi::kGated ? 2 : 1;
+  const int64_t groups = ((int64_t)in.N * nb + 15) / 16;  // of 16 weight rows
+  if (in.M <= 8)
+    return groups <= kCUs ? run_stream<Op, 1, 1, 8, 4, Epi>(in, epi, kCUs, stream)
+                          : run_stream<Op, 1, 1, 4, 4, Epi>(in, epi, 2 * kCUs, stream);
+  if (in.M <= 16)
+    return groups <= kCUs ? run_stream<Op, 2, 1, 8, 4, Epi>(in, epi, kCUs, stream)
+                          : run_stream<Op, 2, 1, 4, 4, Epi>(in, epi, 2 * kCUs, stream);
+  if (in.M <= 32 && groups <= 4 * kCUs)
+    return run_stream<Op, 4, 2, 4, 4, Epi>(in, epi, kCUs, stream);
+  const TileCost cost[] = {{64, 64 / nb, 1, 0.27f, 0.0f, 0.0f, 2.5f},
+                           {64, 64 / nb, 5, 0.45f, 0.06f, 0.20f, 2.5f},
+                           {64, 128 / nb, 3, 0.55f, 0.12f, 0.32f, 2.5f},
+                           {128, 128 / nb, 2, 0.74f, 0.32f, 0.53f, 2.5f},
+                           {256, 256 / nb, 1, 1.50f, 0.0f, 0.0f, 2.5f}};
+  int best = 0;
+  for (int i = 1; i < 5; ++i)
+    if (tile_time(cost[i], in) < tile_time(cost[best], in)) best = i;
+  switch (best) {
+    case 0: return run_tile<Op, 64, 64, 2, 2, 4, 4, Epi>(in, epi, stream);
+    case 1: return run_tile<Op, 64, 64, 2, 2, 4, 1, Epi>(in, epi, stream);
+    case 2: return run_tile<Op, 64, 128, 2, 2, 4, 1, Epi>(in, epi, stream);
+    case 3: return run_tile<Op, 128, 128, 2, 2, 4, 1, Epi>(in, epi, stream);
+    default: return run_tile<Op, 256, 256, 2, 4, 4, 1, Epi>(in, epi, stream);
+  }
 }
 
 bool vec_ok(const void *p, int64_t row_bytes) {
@@ -310,8 +428,8 @@ __global__ __launch_bounds__(256) void quantize_i8_kernel(const T *__restrict__ 
 // dW; the Tp - T last columns are zero).
 template <class T>
 __global__ __launch_bounds__(256) void gate_grad_kernel(const T *__restrict__ dh, int64_t lddh,
-                                                        const T *__restrict__ gate,
-                                                        const T *__restrict__ up, int rows, int f,
+                                                        const float *__restrict__ gate,
+                                                        const float *__restrict__ up, int rows, int f,
                                                         int64_t rows_p, T *__restrict__ dgu,
                                                         T *__restrict__ dgu_t) {
   __shared__ T tg[64][72], tu[64][72];
@@ -322,7 +440,7 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const T *__restrict__ dh
     const int64_t t = t0 + (i >> 6);
     T a = Elem<T>::put(0.0f), b = a;
     if (t < rows) {
-      const float g = Elem<T>::get(gate[t * f + c0 + c]), u = Elem<T>::get(up[t * f + c0 + c]);
+      const float g = gate[t * f + c0 + c], u = up[t * f + c0 + c];
       const float d = Elem<T>::get(dh[t * lddh + c0 + c]);
       const float s = __builtin_amdgcn_rcpf(1.0f + exp_neg(g));
       a = Elem<T>::put(d * u * s * (1.0f + g * (1.0f - s)));
@@ -407,7 +525,7 @@ template <class Op, class E>
 hipError_t gated_as(const Gated16 &p, hipStream_t stream) {
   const DenseIn in{(const uint8_t *)p.x, (const uint8_t *)p.w_gate, (const uint8_t *)p.w_up,
                    p.ldx * 2, (int64_t)p.d * 2, p.T, p.f, (int64_t)p.d * 2};
-  const EpiGated<E> epi{(E *)p.h, (E *)p.gate, (E *)p.up, p.f, 1};
+  const EpiGated<E> epi{(E *)p.h, p.gate, p.up, p.f, 1};
   return run_product<Op>(in, epi, stream);
 }
 
@@ -421,7 +539,7 @@ hipError_t backward_as(const Gated16Backward &p, hipStream_t stream) {
   if (p.T > 0) {
     const unsigned tb = (unsigned)((tp + 63) / 64);
     gate_grad_kernel<E><<<dim3(tb, p.f / 64), 256, 0, stream>>>(
-        (const E *)p.dh, p.lddh, (const E *)p.gate, (const E *)p.up, p.T, p.f, tp, dgu, dgu_t);
+        (const E *)p.dh, p.lddh, p.gate, p.up, p.T, p.f, tp, dgu, dgu_t);
     transpose_kernel<E>
         <<<dim3(tb, p.d / 64), 256, 0, stream>>>((const E *)p.x, p.ldx, p.T, tp, x_t, tp);
     transpose_kernel<E><<<dim3(p.f / 64, p.d / 64), 256, 0, stream>>>(

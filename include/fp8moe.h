@@ -321,13 +321,13 @@ moe_status moe_fused_forward_noalloc(const moe_dims *dims /*host*/, const float 
  * (int8 weights: moe_quantize_rows_i8 on the weight matrix, once.)  Weights
  * are row-major, contiguous: [outputs][inputs].  Activations that are read may
  * have a row stride: ldx, lddh are in ELEMENTS, at least the row length, a
- * multiple of 16 bytes and at most 8 MiB.  Outputs are contiguous.  Every
+ * multiple of 16 bytes and at most 4 MiB.  Outputs are contiguous.  Every
  * array is 16-byte aligned (scales and bias 4-byte).  An output that shares
  * memory with an input or with another output is MOE_ERR_SHAPE.  T = 0 is
  * valid: the arrays with T rows may then be NULL, and nothing is written but
  * the weights' gradients, which are zeros.  Inputs are finite, as everywhere. */
 enum { MOE_T_F32 = 0, MOE_T_BF16 = 1, MOE_T_F16 = 2 }; /* element types */
-#define MOE_MAX_TOKENS (1 << 22) /* rows of one call, and outputs N of moe_matmul_i8 */
+#define MOE_MAX_TOKENS (1 << 21) /* rows of one call, and outputs N of moe_matmul_i8 */
 #define MOE_MAX_I8_K 65536       /* longest int8 row: its products' sum fits 31 bits */
 
 /* Per-row symmetric int8 quantisation of x [rows][cols] (x_type, row stride
@@ -358,14 +358,14 @@ moe_status moe_gated_ffn_i8(const int8_t *xq, int64_t ldx, const float *sx, cons
                             const float *s_gate, const int8_t *w_up, const float *s_up, int32_t T,
                             int32_t d, int32_t f, int32_t h_type, void *h, void *stream);
 
-/* The gated block in bf16 or fp16 (`type`, of every array), in one kernel:
+/* The gated block in bf16 or fp16 (`type`, of x, the weights and h), in one
+ * kernel:
  *   g = x w_gate^T, u = x w_up^T (fp32 sums), h = SiLU(g) * u, rounded once
  * x [T][d] with row stride ldx, w_gate, w_up [f][d], h [T][f].  gate, up
- * [T][f]: where g and u, rounded to `type`, are kept for the backward pass, or
- * both NULL.  d, f: multiples of 64 up to MOE_MAX_HIDDEN / MOE_MAX_FFN. */
+ * [T][f] fp32: where g and u are kept for the backward pass, or both NULL.  d, f: multiples of 64 up to MOE_MAX_HIDDEN / MOE_MAX_FFN. */
 moe_status moe_gated_ffn(const void *x, int64_t ldx, const void *w_gate, const void *w_up,
-                         int32_t type, int32_t T, int32_t d, int32_t f, void *h, void *gate,
-                         void *up, void *stream);
+                         int32_t type, int32_t T, int32_t d, int32_t f, void *h, float *gate,
+                         float *up, void *stream);
 
 /* Its backward pass, from the gradient dh [T][f] (row stride lddh) of h and
  * the g, u kept by the forward pass: with s = sigmoid(g),
@@ -381,8 +381,8 @@ moe_status moe_gated_ffn(const void *x, int64_t ldx, const void *w_gate, const v
  * text in moe_last_error(), for sizes that the call refuses). */
 size_t moe_gated_ffn_backward_workspace_bytes(int32_t T, int32_t d, int32_t f);
 moe_status moe_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, int64_t ldx,
-                                  const void *w_gate, const void *w_up, const void *gate,
-                                  const void *up, int32_t type, int32_t T, int32_t d, int32_t f,
+                                  const void *w_gate, const void *w_up, const float *gate,
+                                  const float *up, int32_t type, int32_t T, int32_t d, int32_t f,
                                   void *dx, void *dw_gate, void *dw_up, void *workspace,
                                   size_t workspace_bytes, void *stream);
 

@@ -54,10 +54,10 @@ def matmul(xq=P[0], ldx=64, sx=P[1], wq=P[2], sw=P[3], bias=None, T=4, K=64, N=7
 
 @pytest.mark.parametrize("kw,code", [
     *[({n: None}, ERR_NULL) for n in ("xq", "sx", "wq", "sw", "y")],
-    (dict(T=-1), ERR_SHAPE), (dict(T=(1 << 22) + 1), ERR_SHAPE), (dict(K=0, ldx=64), ERR_SHAPE),
+    (dict(T=-1), ERR_SHAPE), (dict(T=(1 << 21) + 1), ERR_SHAPE), (dict(K=0, ldx=64), ERR_SHAPE),
     (dict(K=24), ERR_SHAPE), (dict(K=65552, ldx=65552), ERR_SHAPE), (dict(N=0), ERR_SHAPE),
-    (dict(N=(1 << 22) + 1), ERR_SHAPE), (dict(ldx=48), ERR_SHAPE), (dict(ldx=72), ERR_SHAPE),
-    (dict(ldx=(1 << 23) + 16), ERR_SHAPE), (dict(kind=3), ERR_UNSUPPORTED),
+    (dict(N=(1 << 21) + 1), ERR_SHAPE), (dict(ldx=48), ERR_SHAPE), (dict(ldx=72), ERR_SHAPE),
+    (dict(ldx=(1 << 22) + 16), ERR_SHAPE), (dict(kind=3), ERR_UNSUPPORTED),
     (dict(xq=P[0] + 4), ERR_ALIGN), (dict(wq=P[2] + 8), ERR_ALIGN), (dict(y=P[4] + 4), ERR_ALIGN),
     (dict(sw=P[3] + 1), ERR_ALIGN), (dict(bias=P[5] + 2), ERR_ALIGN),
     (dict(y=P[0] + 240), ERR_SHAPE), (dict(y=P[2] + 432), ERR_SHAPE), (dict(bias=P[4] + 108), ERR_SHAPE),
@@ -90,7 +90,7 @@ def gated(x=P[0], ldx=128, wg=P[1], wu=P[2], kind=BF16, T=4, d=128, f=64, h=P[3]
 
 @pytest.mark.parametrize("kw,code", [
     *[({n: None}, ERR_NULL) for n in ("x", "wg", "wu", "h", "gate", "up")],
-    (dict(T=-1), ERR_SHAPE), (dict(T=(1 << 22) + 1), ERR_SHAPE), (dict(d=96), ERR_SHAPE),
+    (dict(T=-1), ERR_SHAPE), (dict(T=(1 << 21) + 1), ERR_SHAPE), (dict(d=96), ERR_SHAPE),
     (dict(f=0), ERR_SHAPE), (dict(ldx=120), ERR_SHAPE), (dict(ldx=132), ERR_SHAPE),
     (dict(kind=F32), ERR_UNSUPPORTED), (dict(x=P[0] + 8), ERR_ALIGN), (dict(up=P[5] + 8), ERR_ALIGN),
     (dict(h=P[4] + 256), ERR_SHAPE), (dict(gate=P[1]), ERR_SHAPE), (dict(gate=P[5]), ERR_SHAPE),
@@ -125,7 +125,7 @@ def test_backward_workspace_size():
     small = fp8.gated_ffn_backward_workspace_bytes(1, 256, 512)
     big = fp8.gated_ffn_backward_workspace_bytes(4096, 256, 512)
     assert 0 < small < big
-    for bad in ((-1, 256, 512), (4, 100, 512), (4, 256, 96), ((1 << 22) + 1, 256, 512)):
+    for bad in ((-1, 256, 512), (4, 100, 512), (4, 256, 96), ((1 << 21) + 1, 256, 512)):
         assert fp8.gated_ffn_backward_workspace_bytes(*bad) == 0
         assert fp8._last_error()
 
