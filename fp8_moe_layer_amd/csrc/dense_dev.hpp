@@ -21,9 +21,10 @@
 // arrive as zeros.
 //
 // The product is taken as B * A^T, so that a lane ends up with four
-// consecutive output channels n of one token; B's rows are dealt out so that
-// the lane's NJ sub-tiles together hold 4*NJ consecutive channels.
+// consecutive output channels n of one token.
 #pragma once
+
+#include <type_traits>
 
 #include "common.hpp"
 
@@ -60,11 +61,17 @@ constexpr int kStepBytes = 128;  // bytes of a row per K step
 
 // Operands of one product.  Gated: b0 and b1 are the gate and the up matrix
 // ([N][K] each) and a tile takes as many rows from each.
+//
+// The gradients' products need operands whose K runs down the rows (16-bit
+// types only): a transposed A is [K][M] and a transposed B [K][N], with lda and
+// ldb bytes from one k to the next, M and N multiples of 64.  A transposed B
+// may be two matrices, one below the other: b0 has the first split_k rows of K.
 struct DenseIn {
   const uint8_t *a, *b0, *b1;
   int64_t lda, ldb;  // bytes from row to row
   int32_t M, N;      // tokens, output channels
-  int64_t kbytes;    // bytes of K in a row, a multiple of 16
+  int64_t kbytes;    // bytes of K in a row, a multiple of 16 (both transposed: 2 * K)
+  int64_t split_k = 0;
 };
 
 // ---------------------------------------------------------------- memory
@@ -101,6 +108,19 @@ __device__ __forceinline__ void wait_dma() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// LDS pointers in their own address space (offsets fold into the instructions).
+typedef __attribute__((address_space(3))) uint8_t *LdsPtr;
+__device__ __forceinline__ uint32_t lds_address(LdsPtr p) { return (uint32_t)(uintptr_t)p; }
+__device__ __forceinline__ v4i lds_read16(LdsPtr p) {
+  return *(const __attribute__((address_space(3))) v4i *)p;
+}
+// Four 16-bit values of one column, see Columns.
+__device__ __forceinline__ v2i lds_read8_tr(LdsPtr p) {
+  typedef short v4s __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(
+      v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)p));
+}
+
 // A row that does not exist, or a piece behind the end of K: an offset behind
 // every descriptor's end (kMaxTileBytes), however many K steps are added.
 constexpr uint32_t kPastEnd = 0x80000000u;
@@ -122,230 +142,321 @@ __device__ __forceinline__ void tile_of(int bid, int tiles_m, int tiles_n, int &
   tn = (wg - g * per) / rows;
 }
 
+// ---------------------------------------------------------------- operands of a tile
+// An operand's share of a tile's K step is a unit of LDS: 64 or more rows (of
+// tokens or channels) of 128 bytes, in 1 KB pieces that the tile's W waves
+// fetch in turn.  Each struct knows how to fetch a wave's pieces and how to
+// read the 16 bytes a lane supplies to a matrix instruction.
+
+// A: ROWS tokens with K contiguous.
+template <int ROWS, int WM, int W>
+struct TokenRows {
+  static constexpr int kPieces = ROWS / 8 / W;
+  v4u rsrc;
+  uint32_t off[kPieces];  // the lane's next byte offset
+  int pos[kPieces];       // the lane's byte inside the K step
+  int at;
+  __device__ __forceinline__ TokenRows(const DenseIn &in, int t0, int64_t k0, int wave, int wm,
+                                       int lane) {
+    const int rows = in.M - t0 < ROWS ? in.M - t0 : ROWS;
+    rsrc = buffer_of(in.a + (int64_t)t0 * in.lda, (int64_t)(rows - 1) * in.lda + in.kbytes);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int r = (i * W + wave) * 8 + (lane >> 3);
+      pos[i] = ((lane & 7) ^ (r & 7)) * 16;
+      off[i] = r < rows ? (uint32_t)(r * in.lda + k0) + pos[i] : kPastEnd;
+    }
+    const int p = lane & 15, q = lane >> 4;
+    at = (wm * WM + p) * kStepBytes + ((q ^ (p & 7)) * 16);
+  }
+  // the next step to the unit at byte `lds`; left: its bytes of K, up to 128
+  __device__ __forceinline__ void fetch(const DenseIn &, int64_t, int left, uint32_t lds, int wave) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      dma16(rsrc, pos[i] < left ? off[i] : kPastEnd, lds + (i * W + wave) * 1024);
+      off[i] += kStepBytes;
+    }
+  }
+  // token m*16 + l%16 of the wave, half `half` of the step
+  __device__ __forceinline__ v4i read(LdsPtr lds, int half, int m) const {
+    return lds_read16(lds + (at ^ (half * 64)) + m * 16 * kStepBytes);
+  }
+};
+
+// B: ROWS channel rows with K contiguous (gated: each wave's block of WN rows
+// is CH channels of b0, then the same channels of b1).  Sub-tile j's lane p
+// reads row (p/4)*4*NJ + j*4 + p%4 of a block, so that a lane's sums are 4*NJ
+// consecutive channels.
+template <int ROWS, int WN, int CH, bool GATED, int W>
+struct ChannelRows {
+  static constexpr int kPieces = ROWS / 8 / W;
+  static constexpr int NJ = CH / 16;
+  v4u rsrc, rsrc1;
+  uint32_t off[kPieces];
+  int pos[kPieces];
+  int at;
+  static __device__ __forceinline__ int key(int r) { return (r & 3) | (((r / (4 * NJ)) & 1) << 2); }
+  __device__ __forceinline__ ChannelRows(const DenseIn &in, int n0, int64_t k0, int wave, int wn,
+                                         int lane) {
+    constexpr int kChannels = GATED ? ROWS / 2 : ROWS;
+    const int rows = in.N - n0 < kChannels ? in.N - n0 : kChannels;
+    const int64_t bytes = (int64_t)(rows - 1) * in.ldb + in.kbytes;
+    rsrc = buffer_of(in.b0 + (int64_t)n0 * in.ldb, bytes);
+    rsrc1 = GATED ? buffer_of(in.b1 + (int64_t)n0 * in.ldb, bytes) : rsrc;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int r = (i * W + wave) * 8 + (lane >> 3), rr = r % WN % CH;
+      const int ch = r / WN * CH + rr;
+      pos[i] = ((lane & 7) ^ key(rr)) * 16;
+      off[i] = ch < rows ? (uint32_t)(ch * in.ldb + k0) + pos[i] : kPastEnd;
+    }
+    const int p = lane & 15, q = lane >> 4, row = (p >> 2) * 4 * NJ + (p & 3);
+    at = (wn * WN + row) * kStepBytes + ((q ^ key(row)) * 16);
+  }
+  __device__ __forceinline__ void fetch(const DenseIn &, int64_t, int left, uint32_t lds, int wave) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int piece = i * W + wave;
+      const uint32_t o = pos[i] < left ? off[i] : kPastEnd;
+      if (GATED && (piece * 8) % WN >= CH)
+        dma16(rsrc1, o, lds + piece * 1024);
+      else
+        dma16(rsrc, o, lds + piece * 1024);
+      off[i] += kStepBytes;
+    }
+  }
+  __device__ __forceinline__ v4i read(LdsPtr lds, int half, int b, int j) const {
+    return lds_read16(lds + (at ^ (half * 64)) + (b * CH + j * 4) * kStepBytes);
+  }
+  // the lane's channel of sub-tile j, element 0, in the wave's block; kRun: its
+  // sub-tiles follow each other
+  static constexpr bool kRun = true;
+  static __device__ __forceinline__ int channel(int lane, int j) {
+    return (lane >> 4) * 4 * NJ + j * 4;
+  }
+};
+
+// A or B transposed: COLS columns (tokens or channels) of 64 rows of K.  The
+// unit is blocks of 64 columns, each 64 rows of 128 bytes.  An operand's eight
+// values of K come from two ds_read_b64_tr_b16: of sixteen lanes, lane p gives
+// the address of four columns ((p%4)*4 ..) in row p/4 and receives column p of
+// the four rows.  Thirty-two lanes (two such sets, rows 8 apart) read 32 bytes
+// of eight rows; with key 2*(row/2%2) + 4*(row/8%2) those are the 64 banks.
+template <int COLS, int WC, int W>
+struct Columns {
+  static constexpr int kPieces = COLS / 8 / W;
+  uint32_t off[kPieces];
+  int at, wc;
+  static __device__ __forceinline__ int key(int r) { return (r & 2) | ((r >> 1) & 4); }
+  __device__ __forceinline__ Columns(int64_t ld, int cols, int wave, int wcol, int lane) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int piece = i * W + wave, block = piece >> 3, r = (piece & 7) * 8 + (lane >> 3);
+      off[i] = block * 64 < cols
+                   ? (uint32_t)(r * ld) + block * 128 + (((lane & 7) ^ key(r)) * 16) : kPastEnd;
+    }
+    const int p = lane & 15, r = (lane >> 4) * 8 + (p >> 2);  // row of the first read, half 0
+    at = r * 128 + ((((p & 3) >> 1) ^ key(r)) * 16) + (p & 1) * 8;
+    wc = wcol * WC;
+  }
+  // rows k .. k+63 (of `rows` rows at `base`) to the unit
+  __device__ __forceinline__ void fetch(const uint8_t *base, int64_t ld, int cols, int64_t k,
+                                        int64_t rows, uint32_t lds, int wave) {
+    const int64_t left = rows - k < 64 ? rows - k : 64;
+    const v4u rsrc = buffer_of(base + k * ld, left > 0 ? (left - 1) * ld + cols * 2 : 0);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) dma16(rsrc, off[i], lds + (i * W + wave) * 1024);
+  }
+  // columns c*16 + l%16 of the wave
+  __device__ __forceinline__ v4i read(LdsPtr lds, int half, int c) const {
+    const int col = wc + c * 16;
+    const LdsPtr a = lds + (at ^ ((col & 63) * 2)) + (col >> 6) * 8192 + half * 32 * 128;
+    const v2i lo = lds_read8_tr(a), hi = lds_read8_tr(a + 4 * 128);
+    return v4i{lo.x, lo.y, hi.x, hi.y};
+  }
+};
+
+template <int ROWS, int WM, int W>
+struct TokenColumns : Columns<ROWS, WM, W> {
+  typedef Columns<ROWS, WM, W> C;
+  const uint8_t *base;
+  int cols;
+  __device__ __forceinline__ TokenColumns(const DenseIn &in, int t0, int64_t, int wave, int wm, int lane)
+      : C(in.lda, in.M - t0, wave, wm, lane), base(in.a + (int64_t)t0 * 2), cols(in.M - t0) {}
+  __device__ __forceinline__ void fetch(const DenseIn &in, int64_t k, int, uint32_t lds, int wave) {
+    C::fetch(base, in.lda, cols, k, in.kbytes / 2, lds, wave);
+  }
+};
+
+template <int ROWS, int WN, int W>
+struct ChannelColumns : Columns<ROWS, WN, W> {
+  typedef Columns<ROWS, WN, W> C;
+  int n0, cols;
+  __device__ __forceinline__ ChannelColumns(const DenseIn &in, int n0_, int64_t, int wave, int wn, int lane)
+      : C(in.ldb, in.N - n0_, wave, wn, lane), n0(n0_), cols(in.N - n0_) {}
+  // split_k is a multiple of 64: a step lies in one of the two matrices
+  __device__ __forceinline__ void fetch(const DenseIn &in, int64_t k, int, uint32_t lds, int wave) {
+    const int64_t rows = in.kbytes / 2;
+    if (k < in.split_k)
+      C::fetch(in.b0 + (int64_t)n0 * 2, in.ldb, cols, k, in.split_k, lds, wave);
+    else
+      C::fetch(in.b1 + (int64_t)n0 * 2, in.ldb, cols, k - in.split_k, rows - in.split_k, lds, wave);
+  }
+  __device__ __forceinline__ v4i read(LdsPtr lds, int half, int, int j) const {
+    return C::read(lds, half, j);
+  }
+  static constexpr bool kRun = false;
+  static __device__ __forceinline__ int channel(int lane, int j) { return j * 16 + (lane >> 4) * 4; }
+};
+
 // ---------------------------------------------------------------- the tile
-// BM tokens by BN rows of B, TM x TN waves; GATED: half of each wave's B rows
-// come from b0 and half from b1 (the same channels).  LDS is a ring of U
-// units, A's and B's rows of a step one unit each.  KG: groups of TM x TN waves
-// that share the tile, each with a ring of its own and its own part of K; the
-// first one adds the others' sums to its own, in order, at the end.
-template <int BM, int BN, int TM, int TN, int U, int KG, bool GATED>
+enum Form { kPlainForm, kGatedForm, kBColumns, kABColumns };  // which operands, see DenseIn
+
+// BM tokens by BN rows of B, TM x TN waves; gated: half of each wave's B rows
+// come from b0 and half from b1 (the same channels).  LDS holds two K steps.
+// KG: groups of TM x TN waves that share the tile, each with its own LDS and
+// its own part of K; the first one adds the others' sums to its own, in order,
+// at the end.
+template <int BM, int BN, int TM, int TN, int KG, Form F>
 struct TileShape {
   static constexpr int kWaves = TM * TN;                 // of a K group
   static constexpr int kThreads = KG * kWaves * kWave;
   static constexpr int WM = BM / TM;                     // tokens of a wave
   static constexpr int WN = BN / TN;                     // B rows of a wave
   static constexpr int MS = WM / 16;                     // token sub-tiles
-  static constexpr int NB = GATED ? 2 : 1;               // matrices
+  static constexpr int NB = F == kGatedForm ? 2 : 1;     // matrices
   static constexpr int CH = WN / NB;                     // channels of a wave
   static constexpr int NJ = CH / 16;                     // sub-tiles of each matrix
   static constexpr int kTileChannels = BN / NB;          // channels of a workgroup
-  static constexpr int kStageBytes = (BM + BN) * kStepBytes;
-  static constexpr int kRing = U * kStageBytes / 2;      // of a K group
+  static constexpr int kUnitA = BM * kStepBytes;
+  static constexpr int kStage = (BM + BN) * kStepBytes;
+  static constexpr int kRing = 2 * kStage;               // of a K group
   static constexpr int kLdsBytes = KG * kRing;
-  static constexpr int kPiecesA = BM / 8 / kWaves;       // 1 KB pieces of A a wave fetches per step
-  static constexpr int kPiecesB = BN / 8 / kWaves;
-  static_assert(NJ >= 1 && MS >= 1 && BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0 && U >= 4 &&
-                    U % 2 == 0 && kRing >= BM * BN * 4 * (KG > 1), "tile shape");
-  // pieces of a wave in n units (n even)
-  static constexpr int in_units(int n) { return n * (kPiecesA + kPiecesB) / 2; }
+  typedef typename std::conditional<F == kABColumns, TokenColumns<BM, WM, kWaves>,
+                                    TokenRows<BM, WM, kWaves>>::type A;
+  typedef typename std::conditional<F == kBColumns || F == kABColumns,
+                                    ChannelColumns<BN, WN, kWaves>,
+                                    ChannelRows<BN, WN, CH, F == kGatedForm, kWaves>>::type B;
+  static constexpr int kPieces = A::kPieces + B::kPieces;
+  static_assert(NJ >= 1 && MS >= 1 && BM % (8 * kWaves) == 0 && BN % (8 * kWaves) == 0 &&
+                    kRing >= BM * BN * 4 * (KG > 1), "tile shape");
 };
-
-// key of B's local row r inside a wave's block of one matrix (see the file's
-// head): sub-tile j's lane p reads row (p/4)*4*NJ + j*4 + p%4.
-template <int NJ>
-__device__ __forceinline__ int key_b(int r) {
-  return (r & 3) | (((r / (4 * NJ)) & 1) << 2);
-}
 
 // One output tile.  lds: kLdsBytes bytes.  acc[b][m][j]: matrix b,
 // token sub-tile m, channel sub-tile j; element i of lane l is token
-// m*16 + l%16, channel (l/16)*4*NJ + j*4 + i of the wave's block.
+// m*16 + l%16, channel B::channel(l, j) + i of the wave's block.
 //
 // The K step's two halves are software-pipelined: the matrix instructions of
 // one half run while the wave reads the other half's operands from LDS into a
 // second set of registers.  One barrier per step, in its middle: there every
-// wave has read the whole of step k (its two units are free for step k+U/2,
-// whose fetch starts at once) and step k+1 has landed.
-template <class Op, int BM, int BN, int TM, int TN, int U, int KG, bool GATED>
+// wave has read the whole of step k (its stage is free for step k+2, whose
+// fetch starts at once) and step k+1 has landed.
+template <class Op, int BM, int BN, int TM, int TN, int KG, Form F>
 __device__ __forceinline__ void
 tile_product(const DenseIn &in, int t0, int n0, uint8_t *lds,
-             typename Op::Acc (&acc)[GATED ? 2 : 1][TileShape<BM, BN, TM, TN, U, KG, GATED>::MS]
-                                    [TileShape<BM, BN, TM, TN, U, KG, GATED>::NJ]) {
-  typedef TileShape<BM, BN, TM, TN, U, KG, GATED> S;
+             typename Op::Acc (&acc)[TileShape<BM, BN, TM, TN, KG, F>::NB]
+                                    [TileShape<BM, BN, TM, TN, KG, F>::MS]
+                                    [TileShape<BM, BN, TM, TN, KG, F>::NJ]) {
+  typedef TileShape<BM, BN, TM, TN, KG, F> S;
   const int lane = threadIdx.x & 63;
-  const int kg = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / S::kWaves;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % S::kWaves;
+  const int all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kg = all / S::kWaves, wave = all % S::kWaves;
   const int wm = wave / TN, wn = wave % TN;
-  // this K group's steps: k0 .. k0+nk-1 (those behind the end of K are zeros)
+  // this K group's steps: nk from byte k0 on (those behind the end of K are zeros)
   const int nk = ((int)((in.kbytes + kStepBytes - 1) / kStepBytes) + KG - 1) / KG;
   const int64_t k0 = (int64_t)kg * nk * kStepBytes;
-  lds += kg * S::kRing;
-
-  // what this wave fetches: piece i covers local rows 8i .. 8i+7, A's first
-  const int rows_a = in.M - t0 < BM ? in.M - t0 : BM;
-  const v4u ra = buffer_of(in.a + (int64_t)t0 * in.lda, (int64_t)(rows_a - 1) * in.lda + in.kbytes);
-  const int rows_b = in.N - n0 < S::kTileChannels ? in.N - n0 : S::kTileChannels;
-  const int64_t bytes_b = (int64_t)(rows_b - 1) * in.ldb + in.kbytes;
-  const v4u rb0 = buffer_of(in.b0 + (int64_t)n0 * in.ldb, bytes_b);
-  const v4u rb1 = GATED ? buffer_of(in.b1 + (int64_t)n0 * in.ldb, bytes_b) : rb0;
-  // off: the lane's next byte offset; pos: its byte inside the K step
-  uint32_t off_a[S::kPiecesA], off_b[S::kPiecesB];
-  int pos_a[S::kPiecesA], pos_b[S::kPiecesB];
+  const LdsPtr ring = (LdsPtr)lds + kg * S::kRing;
+  typename S::A a(in, t0, k0, wave, wm, lane);
+  typename S::B b(in, n0, k0, wave, wn, lane);
 #pragma unroll
-  for (int i = 0; i < S::kPiecesA; ++i) {
-    const int r = (i * S::kWaves + wave) * 8 + (lane >> 3);
-    pos_a[i] = ((lane & 7) ^ (r & 7)) * 16;
-    off_a[i] = r < rows_a ? (uint32_t)(r * in.lda + k0) + pos_a[i] : kPastEnd;
-  }
-#pragma unroll
-  for (int i = 0; i < S::kPiecesB; ++i) {
-    const int r = (i * S::kWaves + wave) * 8 + (lane >> 3), rr = r % S::WN;
-    const int ch = r / S::WN * S::CH + rr % S::CH;
-    pos_b[i] = ((lane & 7) ^ key_b<S::NJ>(rr % S::CH)) * 16;
-    off_b[i] = ch < rows_b ? (uint32_t)(ch * in.ldb + k0) + pos_b[i] : kPastEnd;
-  }
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds;
-  // step k's rows of A or B to the unit at byte `at` of the ring
-  auto fetch_a = [&](int k, uint32_t at) {
-    const int left = (int)(in.kbytes - k0 - (int64_t)k * kStepBytes);  // bytes of K from this step on
-#pragma unroll
-    for (int i = 0; i < S::kPiecesA; ++i) {
-      const uint32_t o = left >= kStepBytes || pos_a[i] < left ? off_a[i] : kPastEnd;
-      dma16(ra, o, lds0 + at + (i * S::kWaves + wave) * 1024);
-      off_a[i] += kStepBytes;
-    }
-  };
-  auto fetch_b = [&](int k, uint32_t at) {
-    const int left = (int)(in.kbytes - k0 - (int64_t)k * kStepBytes);
-#pragma unroll
-    for (int i = 0; i < S::kPiecesB; ++i) {
-      const int piece = i * S::kWaves + wave;
-      const uint32_t o = left >= kStepBytes || pos_b[i] < left ? off_b[i] : kPastEnd;
-      if (GATED && (piece * 8) % S::WN >= S::CH)
-        dma16(rb1, o, lds0 + at + piece * 1024);
-      else
-        dma16(rb0, o, lds0 + at + piece * 1024);
-      off_b[i] += kStepBytes;
-    }
-  };
-
-  const int p = lane & 15, q = lane >> 4;
-  const int brow = (p >> 2) * 4 * S::NJ + (p & 3);
-  const int a_at = (wm * S::WM + p) * kStepBytes + ((q ^ (p & 7)) * 16);
-  const int b_at = (wn * S::WN + brow) * kStepBytes + ((q ^ key_b<S::NJ>(brow)) * 16);
-  v4i fa[2][S::MS], fb[2][S::NB][S::NJ];
-  auto read_a = [&](uint32_t at, int half, int m) {
-    fa[half][m] = *reinterpret_cast<const v4i *>(lds + at + (a_at ^ (half * 64)) +
-                                                 m * 16 * kStepBytes);
-  };
-  auto read_b = [&](uint32_t at, int half, int b, int j) {
-    fb[half][b][j] = *reinterpret_cast<const v4i *>(lds + at + (b_at ^ (half * 64)) +
-                                                    (b * S::CH + j * 4) * kStepBytes);
-  };
-#pragma unroll
-  for (int b = 0; b < S::NB; ++b)
+  for (int i = 0; i < S::NB; ++i)
 #pragma unroll
     for (int m = 0; m < S::MS; ++m)
 #pragma unroll
-      for (int j = 0; j < S::NJ; ++j) acc[b][m][j] = typename Op::Acc{0, 0, 0, 0};
+      for (int j = 0; j < S::NJ; ++j) acc[i][m][j] = typename Op::Acc{0, 0, 0, 0};
   if (nk == 0) return;  // K = 0: the sums are zeros (the same for every K group)
 
-  // the products of one half, and among them the reads of the other half from
-  // the units at ua and ub
+  auto fetch = [&](int k, uint32_t stage) {
+    const int64_t at = k0 + (int64_t)k * kStepBytes;  // byte of K; 64 16-bit rows a step
+    const int left = in.kbytes - at < kStepBytes ? (int)(in.kbytes - at) : kStepBytes;
+    a.fetch(in, at / 2, left, lds_address(ring) + stage, wave);
+    b.fetch(in, at / 2, left, lds_address(ring) + stage + S::kUnitA, wave);
+  };
+  v4i fa[2][S::MS], fb[2][S::NB][S::NJ];
   constexpr int kReadB = S::NB * S::NJ;
   constexpr int kReads = kReadB + S::MS;
   constexpr int kPer = (kReads + S::MS - 1) / S::MS;  // reads per token sub-tile
-  auto half_step = [&](int half, uint32_t ua, uint32_t ub, bool read) {
+  auto read = [&](int r, int half, uint32_t stage) {
+    if (r < kReadB)
+      fb[half][r / S::NJ][r % S::NJ] = b.read(ring + stage + S::kUnitA, half, r / S::NJ, r % S::NJ);
+    else if (r < kReads)
+      fa[half][r - kReadB] = a.read(ring + stage, half, r - kReadB);
+  };
+  // the products of one half, and among them the reads of the other half
+  auto half_step = [&](int half, uint32_t stage, bool reads) {
 #pragma unroll
     for (int m = 0; m < S::MS; ++m) {
-      if (read) {
+      if (reads) {
 #pragma unroll
-        for (int r = m * kPer; r < (m + 1) * kPer; ++r) {
-          if (r < kReadB)
-            read_b(ub, half ^ 1, r / S::NJ, r % S::NJ);
-          else if (r < kReads)
-            read_a(ua, half ^ 1, r - kReadB);
-        }
+        for (int r = m * kPer; r < (m + 1) * kPer; ++r) read(r, half ^ 1, stage);
       }
 #pragma unroll
-      for (int b = 0; b < S::NB; ++b)
+      for (int i = 0; i < S::NB; ++i)
 #pragma unroll
         for (int j = 0; j < S::NJ; ++j)
-          acc[b][m][j] = Op::mfma(fb[half][b][j], fa[half][m], acc[b][m][j]);
+          acc[i][m][j] = Op::mfma(fb[half][i][j], fa[half][m], acc[i][m][j]);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
 
-  // unit n: A of step n/2 (n even), B of step n/2 (n odd); its slot is n % U
-  constexpr uint32_t kUnitA = BM * kStepBytes;
-  auto slot = [&](int n) -> uint32_t { return n / 2 * S::kStageBytes + (n & 1) * kUnitA; };
-#pragma unroll
-  for (int n = 0; n < U; ++n) {
-    if (n / 2 < nk) {
-      if (n & 1)
-        fetch_b(n / 2, slot(n));
-      else
-        fetch_a(n / 2, slot(n));
-    }
-  }
-  if ((U - 1) / 2 < nk)
-    wait_dma<S::in_units(U - 2)>();
-  else
+  fetch(0, 0);
+  if (nk > 1) {
+    fetch(1, S::kStage);
+    wait_dma<S::kPieces>();
+  } else {
     wait_dma<0>();
-  barrier_reads();
-  uint32_t ua = 0, ub = kUnitA;
-#pragma unroll
-  for (int r = 0; r < kReadB; ++r) read_b(ub, 0, r / S::NJ, r % S::NJ);
-#pragma unroll
-  for (int m = 0; m < S::MS; ++m) read_a(ua, 0, m);
-  auto next = [&](uint32_t u) -> uint32_t {
-    u += S::kStageBytes;
-    return u >= S::kRing ? u - S::kRing : u;
-  };
-  for (int k = 0; k + 1 < nk; ++k) {
-    half_step(0, ua, ub, true);
-    if (k + (U - 1) / 2 < nk)
-      wait_dma<S::in_units(U - 4)>();  // the units behind step k+1's may be in flight
-    else
-      wait_dma<0>();
-    barrier_reads();
-    if (k + U / 2 < nk) {
-      fetch_a(k + U / 2, ua);
-      fetch_b(k + U / 2, ub);
-    }
-    ua = next(ua);
-    ub = next(ub);
-    half_step(1, ua, ub, true);
   }
-  half_step(0, ua, ub, true);
-  half_step(1, 0, 0, false);
+  barrier_reads();
+#pragma unroll
+  for (int r = 0; r < kReads; ++r) read(r, 0, 0);
+  uint32_t stage = 0;
+  for (int k = 0; k + 1 < nk; ++k) {
+    half_step(0, stage, true);
+    wait_dma<0>();
+    barrier_reads();
+    if (k + 2 < nk) fetch(k + 2, stage);
+    stage = S::kStage - stage;
+    half_step(1, stage, true);
+  }
+  half_step(0, stage, true);
+  half_step(1, 0, false);
 
   if constexpr (KG > 1) {
     // every wave's last operands are in registers and no load is in flight, so
-    // the rings can take the partial sums: 16 bytes a lane, block by block
+    // the stages can take the partial sums: 16 bytes a lane, block by block
     barrier_reads();
-    uint8_t *mine = lds + wave * (S::WM * S::WN * 4) + lane * 16;
+    uint8_t *mine = lds + kg * S::kRing + wave * (S::WM * S::WN * 4) + lane * 16;
 #pragma unroll
-    for (int b = 0; b < S::NB; ++b)
+    for (int i = 0; i < S::NB; ++i)
 #pragma unroll
       for (int m = 0; m < S::MS; ++m)
 #pragma unroll
         for (int j = 0; j < S::NJ; ++j)
           if (kg > 0)
-            *reinterpret_cast<typename Op::Acc *>(mine + ((b * S::MS + m) * S::NJ + j) * 1024) =
-                acc[b][m][j];
+            *reinterpret_cast<typename Op::Acc *>(mine + ((i * S::MS + m) * S::NJ + j) * 1024) =
+                acc[i][m][j];
     barrier_reads();
     if (kg == 0) {
 #pragma unroll
       for (int g = 1; g < KG; ++g)
 #pragma unroll
-        for (int b = 0; b < S::NB; ++b)
+        for (int i = 0; i < S::NB; ++i)
 #pragma unroll
           for (int m = 0; m < S::MS; ++m)
 #pragma unroll
             for (int j = 0; j < S::NJ; ++j)
-              acc[b][m][j] += *reinterpret_cast<const typename Op::Acc *>(
-                  mine + g * S::kRing + ((b * S::MS + m) * S::NJ + j) * 1024);
+              acc[i][m][j] += *reinterpret_cast<const typename Op::Acc *>(
+                  mine + g * S::kRing + ((i * S::MS + m) * S::NJ + j) * 1024);
     }
   }
 }
@@ -400,8 +511,7 @@ __device__ __forceinline__ void stream_product(const DenseIn &in, int groups, ui
     wch[i] = (i * 8 + lr) % kChannels;
     woff[i] = (uint32_t)wch[i] * (uint32_t)in.ldb + pos;
   }
-  const uint32_t ring =
-      (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)lds + wave * R * S::kStage;
+  const uint32_t ring = lds_address((LdsPtr)lds) + wave * R * S::kStage;
 
   // the fetch cursor: group, step and slot; the group's descriptors
   int fg = blockIdx.x, fk = wave, fslot = 0, left = total;

@@ -176,45 +176,58 @@ struct EpiPlain {
 };
 
 // ---------------------------------------------------------------- product kernel
-template <class Op, int BM, int BN, int TM, int TN, int U, int KG, class Epi>
+// The tile's sums through the epilogue.  A lane's sub-tiles are one run of
+// 4*NJ consecutive channels, or (B transposed) NJ runs of four.
+template <class S, class Op, class Epi>
+__device__ __forceinline__ void store_tile(const DenseIn &in, const Epi &epi,
+                                           typename Op::Acc (&acc)[S::NB][S::MS][S::NJ], int t0,
+                                           int n0, int wm, int wn) {
+  const int lane = threadIdx.x & 63;
+  constexpr bool kRun = S::B::kRun;
+  constexpr int kCount = kRun ? 4 * S::NJ : 4;
+#pragma unroll
+  for (int j0 = 0; j0 < (kRun ? 1 : S::NJ); ++j0) {
+    const int ch = n0 + wn * S::CH + S::B::channel(lane, j0);
+    if (ch >= in.N) continue;
+    typename Epi::template Chan<kCount> chan;
+    epi.load(chan, ch);
+#pragma unroll
+    for (int m = 0; m < S::MS; ++m) {
+      const int t = t0 + wm * S::WM + m * 16 + (lane & 15);
+      if (t >= in.M) continue;
+      typename Op::Sum a[S::NB][kCount];
+#pragma unroll
+      for (int b = 0; b < S::NB; ++b)
+#pragma unroll
+        for (int i = 0; i < kCount; ++i) a[b][i] = acc[b][m][j0 + i / 4][i % 4];
+      epi.store(chan, t, ch, a);
+    }
+  }
+}
+
+template <class Op, int BM, int BN, int TM, int TN, int KG, Form F, class Epi>
 __global__ __launch_bounds__(TM *TN *KG *kWave) void tile_kernel(DenseIn in, Epi epi, int tiles_m,
-                                                             int tiles_n) {
-  typedef TileShape<BM, BN, TM, TN, U, KG, Epi::kGated> S;
+                                                                 int tiles_n) {
+  typedef TileShape<BM, BN, TM, TN, KG, F> S;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLdsBytes];
   int tm, tn;
   tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
   const int t0 = tm * BM, n0 = tn * S::kTileChannels;
   typename Op::Acc acc[S::NB][S::MS][S::NJ];
-  tile_product<Op, BM, BN, TM, TN, U, KG, Epi::kGated>(in, t0, n0, lds, acc);
-
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int ch = n0 + (wave % TN) * S::CH + (lane >> 4) * 4 * S::NJ;
-  if (wave >= S::kWaves || ch >= in.N) return;  // the first K group has the sums
-  typename Epi::template Chan<4 * S::NJ> chan;
-  epi.load(chan, ch);
-#pragma unroll
-  for (int m = 0; m < S::MS; ++m) {
-    const int t = t0 + (wave / TN) * S::WM + m * 16 + (lane & 15);
-    if (t >= in.M) continue;
-    typename Op::Sum a[S::NB][4 * S::NJ];
-#pragma unroll
-    for (int b = 0; b < S::NB; ++b)
-#pragma unroll
-      for (int j = 0; j < S::NJ; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[b][j * 4 + i] = acc[b][m][j][i];
-    epi.store(chan, t, ch, a);
-  }
+  tile_product<Op, BM, BN, TM, TN, KG, F>(in, t0, n0, lds, acc);
+  const int wave = threadIdx.x >> 6;
+  if (wave >= S::kWaves) return;  // the first K group has the sums
+  store_tile<S, Op>(in, epi, acc, t0, n0, wave / TN, wave % TN);
 }
 
-template <class Op, int BM, int BN, int TM, int TN, int U, int KG, class Epi>
+template <class Op, int BM, int BN, int TM, int TN, int KG, Form F, class Epi>
 hipError_t run_tile(const DenseIn &in, const Epi &epi, hipStream_t stream) {
-  typedef TileShape<BM, BN, TM, TN, U, KG, Epi::kGated> S;
+  typedef TileShape<BM, BN, TM, TN, KG, F> S;
   const int64_t tm = ((int64_t)in.M + BM - 1) / BM;
   const int64_t tn = ((int64_t)in.N + S::kTileChannels - 1) / S::kTileChannels;
   if (tm * tn == 0) return hipSuccess;
   if (tm * tn > 0x7fffffff) return hipErrorInvalidValue;
-  tile_kernel<Op, BM, BN, TM, TN, U, KG, Epi>
+  tile_kernel<Op, BM, BN, TM, TN, KG, F, Epi>
       <<<(unsigned)(tm * tn), S::kThreads, 0, stream>>>(in, epi, (int)tm, (int)tn);
   return hipGetLastError();
 }
@@ -300,13 +313,34 @@ double tile_time(const TileCost &t, const DenseIn &in) {
   return us;
 }
 
+// The tile with the least estimated time.
+template <class Op, Form F, class Epi>
+hipError_t run_tiles(const DenseIn &in, const Epi &epi, hipStream_t stream) {
+  constexpr int nb = F == kGatedForm ? 2 : 1;
+  const TileCost cost[] = {{64, 64 / nb, 1, 0.27f, 0.0f, 0.0f, 2.5f},
+                           {64, 64 / nb, 5, 0.45f, 0.06f, 0.20f, 2.5f},
+                           {64, 128 / nb, 3, 0.55f, 0.12f, 0.32f, 2.5f},
+                           {128, 128 / nb, 2, 0.74f, 0.32f, 0.53f, 2.5f},
+                           {256, 256 / nb, 1, 1.50f, 0.0f, 0.0f, 2.5f}};
+  int best = 0;
+  for (int i = 1; i < 5; ++i)
+    if (tile_time(cost[i], in) < tile_time(cost[best], in)) best = i;
+  switch (best) {
+    case 0: return run_tile<Op, 64, 64, 2, 2, 4, F, Epi>(in, epi, stream);
+    case 1: return run_tile<Op, 64, 64, 2, 2, 1, F, Epi>(in, epi, stream);
+    case 2: return run_tile<Op, 64, 128, 2, 2, 1, F, Epi>(in, epi, stream);
+    case 3: return run_tile<Op, 128, 128, 2, 2, 1, F, Epi>(in, epi, stream);
+    default: return run_tile<Op, 256, 256, 2, 4, 1, F, Epi>(in, epi, stream);
+  }
+}
+
 // Up to 32 tokens stream the weights (stream_product), unless at 17 to 32
 // there are many channels: then small tiles, which read the tokens less often,
 // are faster (bf16, T = 32, 4096 -> 2 x 14336: 35 us in tiles, 48 us streamed;
 // 14336 -> 4096 int8: 18 us streamed, 52 us in tiles).  Eight waves a
 // workgroup where the groups leave one to a compute unit, else four and two
 // workgroups (int8, one token, 14336 -> 4096: 11.0 and 14.3 us; 4096 -> 14336:
-// 13.4 and 11.9 us).  Above, the tile with the least estimated time.
+// 13.4 and 11.9 us).  Above, tiles.
 template <class Op, class Epi>
 hipError_t run_product(const DenseIn &in, const Epi &epi, hipStream_t stream) {
   if (in.M == 0) return hipSuccess;
@@ -320,21 +354,7 @@ hipError_t run_product(const DenseIn &in, const Epi &epi, hipStream_t stream) {
                           : run_stream<Op, 2, 1, 4, 4, Epi>(in, epi, 2 * kCUs, stream);
   if (in.M <= 32 && groups <= 4 * kCUs)
     return run_stream<Op, 4, 2, 4, 4, Epi>(in, epi, kCUs, stream);
-  const TileCost cost[] = {{64, 64 / nb, 1, 0.27f, 0.0f, 0.0f, 2.5f},
-                           {64, 64 / nb, 5, 0.45f, 0.06f, 0.20f, 2.5f},
-                           {64, 128 / nb, 3, 0.55f, 0.12f, 0.32f, 2.5f},
-                           {128, 128 / nb, 2, 0.74f, 0.32f, 0.53f, 2.5f},
-                           {256, 256 / nb, 1, 1.50f, 0.0f, 0.0f, 2.5f}};
-  int best = 0;
-  for (int i = 1; i < 5; ++i)
-    if (tile_time(cost[i], in) < tile_time(cost[best], in)) best = i;
-  switch (best) {
-    case 0: return run_tile<Op, 64, 64, 2, 2, 4, 4, Epi>(in, epi, stream);
-    case 1: return run_tile<Op, 64, 64, 2, 2, 4, 1, Epi>(in, epi, stream);
-    case 2: return run_tile<Op, 64, 128, 2, 2, 4, 1, Epi>(in, epi, stream);
-    case 3: return run_tile<Op, 128, 128, 2, 2, 4, 1, Epi>(in, epi, stream);
-    default: return run_tile<Op, 256, 256, 2, 4, 4, 1, Epi>(in, epi, stream);
-  }
+  return run_tiles<Op, Epi::kGated ? kGatedForm : kPlainForm>(in, epi, stream);
 }
 
 bool vec_ok(const void *p, int64_t row_bytes) {
@@ -423,85 +443,39 @@ __global__ __launch_bounds__(256) void quantize_i8_kernel(const T *__restrict__ 
 // ---------------------------------------------------------------- backward helpers
 // dg = dh * u * s * (1 + g * (1 - s)), du = dh * g * s with s = sigmoid(g), in
 // fp32 from the kept g and u, rounded once to the operands' type: the two
-// products that follow take 16-bit operands.  Written row-major as
-// dgu [T][2f] (operand of dx) and transposed as dgu_t [2f][Tp] (operand of
-// dW; the Tp - T last columns are zero).
+// products that follow take 16-bit operands.  dgu [T][2f]: a token's dg, then
+// its du.  Eight channels a thread; f is a multiple of 64.
 template <class T>
 __global__ __launch_bounds__(256) void gate_grad_kernel(const T *__restrict__ dh, int64_t lddh,
                                                         const float *__restrict__ gate,
-                                                        const float *__restrict__ up, int rows, int f,
-                                                        int64_t rows_p, T *__restrict__ dgu,
-                                                        T *__restrict__ dgu_t) {
-  __shared__ T tg[64][72], tu[64][72];
-  const int64_t t0 = (int64_t)blockIdx.x * 64;
-  const int c0 = blockIdx.y * 64;
-  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-    const int c = i & 63;
-    const int64_t t = t0 + (i >> 6);
-    T a = Elem<T>::put(0.0f), b = a;
-    if (t < rows) {
-      const float g = gate[t * f + c0 + c], u = up[t * f + c0 + c];
-      const float d = Elem<T>::get(dh[t * lddh + c0 + c]);
-      const float s = __builtin_amdgcn_rcpf(1.0f + exp_neg(g));
-      a = Elem<T>::put(d * u * s * (1.0f + g * (1.0f - s)));
-      b = Elem<T>::put(d * g * s);
-      dgu[t * 2 * f + c0 + c] = a;
-      dgu[t * 2 * f + f + c0 + c] = b;
+                                                        const float *__restrict__ up, int64_t runs,
+                                                        int f, T *__restrict__ dgu) {
+  const int per = f / 8;  // runs of a row
+  for (int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x; r < runs; r += (int64_t)gridDim.x * 256) {
+    const int64_t t = r / per;
+    const int c = (int)(r - t * per) * 8;
+    T d[8], a[8], b[8];
+    const v4i dw = load16(dh + t * lddh + c);
+    __builtin_memcpy(d, &dw, 16);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const v4f g4 = *reinterpret_cast<const v4f *>(gate + t * f + c + 4 * h);
+      const v4f u4 = *reinterpret_cast<const v4f *>(up + t * f + c + 4 * h);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float g = g4[i], u = u4[i], dv = Elem<T>::get(d[4 * h + i]);
+        const float s = __builtin_amdgcn_rcpf(1.0f + exp_neg(g));
+        a[4 * h + i] = Elem<T>::put(dv * u * s * (1.0f + g * (1.0f - s)));
+        b[4 * h + i] = Elem<T>::put(dv * g * s);
+      }
     }
-    tg[c][i >> 6] = a;
-    tu[c][i >> 6] = b;
+    v4i aw, bw;
+    __builtin_memcpy(&aw, a, 16);
+    __builtin_memcpy(&bw, b, 16);
+    T *out = dgu + t * 2 * f + c;
+    *reinterpret_cast<v4i *>(out) = aw;
+    *reinterpret_cast<v4i *>(out + f) = bw;
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-    const int64_t t = t0 + (i & 63);
-    const int c = i >> 6;
-    if (t < rows_p) {
-      dgu_t[(int64_t)(c0 + c) * rows_p + t] = tg[c][i & 63];
-      dgu_t[(int64_t)(f + c0 + c) * rows_p + t] = tu[c][i & 63];
-    }
-  }
-}
-
-// out[c][r] = in[r][c], zero for rows <= r < rows_p.
-template <class T>
-__global__ __launch_bounds__(256) void transpose_kernel(const T *__restrict__ in, int64_t ld,
-                                                        int rows, int64_t rows_p,
-                                                        T *__restrict__ out, int64_t ldo) {
-  __shared__ T tile[64][72];
-  const int64_t r0 = (int64_t)blockIdx.x * 64;
-  const int c0 = blockIdx.y * 64;
-  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-    const int64_t r = r0 + (i >> 6);
-    tile[i & 63][i >> 6] = r < rows ? in[r * ld + c0 + (i & 63)] : Elem<T>::put(0.0f);
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-    const int64_t r = r0 + (i & 63);
-    if (r < rows_p) out[(int64_t)(c0 + (i >> 6)) * ldo + r] = tile[i >> 6][i & 63];
-  }
-}
-
-int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
-size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
-
-struct BackwardLayout {
-  size_t dgu, dgu_t, x_t, w_t, total;
-};
-BackwardLayout backward_layout(int32_t T, int32_t d, int32_t f) {
-  BackwardLayout L{};
-  size_t o = 0;
-  auto take = [&](size_t elems) {
-    const size_t at = o;
-    o = up256(o + elems * 2);
-    return at;
-  };
-  const size_t tp = (size_t)up8(T);
-  L.dgu = take((size_t)T * 2 * f);
-  L.dgu_t = take(2 * (size_t)f * tp);
-  L.x_t = take((size_t)d * tp);
-  L.w_t = take((size_t)d * 2 * f);
-  L.total = o;
-  return L;
 }
 
 template <class OUT>
@@ -531,32 +505,26 @@ hipError_t gated_as(const Gated16 &p, hipStream_t stream) {
 
 template <class Op, class E>
 hipError_t backward_as(const Gated16Backward &p, hipStream_t stream) {
-  const BackwardLayout L = backward_layout(p.T, p.d, p.f);
-  E *dgu = (E *)(p.workspace + L.dgu), *dgu_t = (E *)(p.workspace + L.dgu_t);
-  E *x_t = (E *)(p.workspace + L.x_t), *w_t = (E *)(p.workspace + L.w_t);
-  const int64_t tp = up8(p.T);
-  hipError_t e = hipSuccess;
+  E *dgu = (E *)p.workspace;
+  const int64_t two_f = 2 * (int64_t)p.f;
   if (p.T > 0) {
-    const unsigned tb = (unsigned)((tp + 63) / 64);
-    gate_grad_kernel<E><<<dim3(tb, p.f / 64), 256, 0, stream>>>(
-        (const E *)p.dh, p.lddh, p.gate, p.up, p.T, p.f, tp, dgu, dgu_t);
-    transpose_kernel<E>
-        <<<dim3(tb, p.d / 64), 256, 0, stream>>>((const E *)p.x, p.ldx, p.T, tp, x_t, tp);
-    transpose_kernel<E><<<dim3(p.f / 64, p.d / 64), 256, 0, stream>>>(
-        (const E *)p.w_gate, p.d, p.f, p.f, w_t, 2 * (int64_t)p.f);
-    transpose_kernel<E><<<dim3(p.f / 64, p.d / 64), 256, 0, stream>>>(
-        (const E *)p.w_up, p.d, p.f, p.f, w_t + p.f, 2 * (int64_t)p.f);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    const int64_t k2 = (int64_t)p.f * 4;  // bytes of 2f elements
-    const DenseIn in{(const uint8_t *)dgu, (const uint8_t *)w_t, nullptr, k2, k2, p.T, p.d, k2};
+    const int64_t runs = (int64_t)p.T * p.f / 8, blocks = (runs + 255) / 256;
+    gate_grad_kernel<E><<<(unsigned)(blocks < 8 * kCUs ? blocks : 8 * kCUs), 256, 0, stream>>>(
+        (const E *)p.dh, p.lddh, p.gate, p.up, runs, p.f, dgu);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    // dx [T][d]: K runs over the 2f channels, down the rows of the two weight matrices
+    const DenseIn in{(const uint8_t *)dgu, (const uint8_t *)p.w_gate, (const uint8_t *)p.w_up,
+                     two_f * 2, (int64_t)p.d * 2, p.T, p.d, two_f * 2, p.f};
     const EpiPlain<E> epi{(E *)p.dx, nullptr, p.T, p.d, 1};
-    if ((e = run_product<Op>(in, epi, stream)) != hipSuccess) return e;
+    if ((e = run_tiles<Op, kBColumns>(in, epi, stream)) != hipSuccess) return e;
   }
-  // no tokens: K = 0, and the weights' gradients come out as zeros
-  const DenseIn in{(const uint8_t *)dgu_t, (const uint8_t *)x_t, nullptr, tp * 2, tp * 2,
-                   2 * p.f, p.d, tp * 2};
+  // dW [2f][d]: K runs over the tokens, down the rows of dgu and x.  No
+  // tokens: K = 0, and the gradients come out as zeros
+  const DenseIn in{(const uint8_t *)dgu, (const uint8_t *)p.x, nullptr, two_f * 2, p.ldx * 2,
+                   2 * p.f, p.d, (int64_t)p.T * 2, p.T};
   const EpiPlain<E> epi{(E *)p.dw_gate, (E *)p.dw_up, p.f, p.d, 1};
-  return run_product<Op>(in, epi, stream);
+  return run_tiles<Op, kABColumns>(in, epi, stream);
 }
 
 }  // namespace
@@ -591,7 +559,8 @@ hipError_t launch_gated(const Gated16 &p, hipStream_t stream) {
 }
 
 size_t gated_backward_workspace(int32_t T, int32_t d, int32_t f) {
-  return backward_layout(T, d, f).total;
+  (void)d;
+  return ((size_t)(T > 0 ? T : 1) * 2 * f * 2 + 255) / 256 * 256;  // dgu
 }
 
 hipError_t launch_gated_backward(const Gated16Backward &p, hipStream_t stream) {
