@@ -169,13 +169,13 @@ struct TokenRows {
     const int p = lane & 15, q = lane >> 4;
     at = (wm * WM + p) * kStepBytes + ((q ^ (p & 7)) * 16);
   }
-  // the next step to the unit at byte `lds`; left: its bytes of K, up to 128
-  __device__ __forceinline__ void fetch(const DenseIn &, int64_t, int left, uint32_t lds, int wave) {
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      dma16(rsrc, pos[i] < left ? off[i] : kPastEnd, lds + (i * W + wave) * 1024);
-      off[i] += kStepBytes;
-    }
+  // the next step to be fetched; left: its bytes of K, up to 128
+  int left;
+  __device__ __forceinline__ void begin(const DenseIn &, int64_t, int left_) { left = left_; }
+  // its i-th piece to the unit at byte `lds`
+  __device__ __forceinline__ void piece(int i, uint32_t lds, int wave) {
+    dma16(rsrc, pos[i] < left ? off[i] : kPastEnd, lds + (i * W + wave) * 1024);
+    off[i] += kStepBytes;
   }
   // token m*16 + l%16 of the wave, half `half` of the step
   __device__ __forceinline__ v4i read(LdsPtr lds, int half, int m) const {
@@ -213,17 +213,16 @@ struct ChannelRows {
     const int p = lane & 15, q = lane >> 4, row = (p >> 2) * 4 * NJ + (p & 3);
     at = (wn * WN + row) * kStepBytes + ((q ^ key(row)) * 16);
   }
-  __device__ __forceinline__ void fetch(const DenseIn &, int64_t, int left, uint32_t lds, int wave) {
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int piece = i * W + wave;
-      const uint32_t o = pos[i] < left ? off[i] : kPastEnd;
-      if (GATED && (piece * 8) % WN >= CH)
-        dma16(rsrc1, o, lds + piece * 1024);
-      else
-        dma16(rsrc, o, lds + piece * 1024);
-      off[i] += kStepBytes;
-    }
+  int left;
+  __device__ __forceinline__ void begin(const DenseIn &, int64_t, int left_) { left = left_; }
+  __device__ __forceinline__ void piece(int i, uint32_t lds, int wave) {
+    const int n = i * W + wave;
+    const uint32_t o = pos[i] < left ? off[i] : kPastEnd;
+    if (GATED && (n * 8) % WN >= CH)
+      dma16(rsrc1, o, lds + n * 1024);
+    else
+      dma16(rsrc, o, lds + n * 1024);
+    off[i] += kStepBytes;
   }
   __device__ __forceinline__ v4i read(LdsPtr lds, int half, int b, int j) const {
     return lds_read16(lds + (at ^ (half * 64)) + (b * CH + j * 4) * kStepBytes);
@@ -259,13 +258,15 @@ struct Columns {
     at = r * 128 + ((((p & 3) >> 1) ^ key(r)) * 16) + (p & 1) * 8;
     wc = wcol * WC;
   }
-  // rows k .. k+63 (of `rows` rows at `base`) to the unit
-  __device__ __forceinline__ void fetch(const uint8_t *base, int64_t ld, int cols, int64_t k,
-                                        int64_t rows, uint32_t lds, int wave) {
+  // the step of rows k .. k+63 (of `rows` rows at `base`)
+  v4u rsrc;
+  __device__ __forceinline__ void begin(const uint8_t *base, int64_t ld, int cols, int64_t k,
+                                        int64_t rows) {
     const int64_t left = rows - k < 64 ? rows - k : 64;
-    const v4u rsrc = buffer_of(base + k * ld, left > 0 ? (left - 1) * ld + cols * 2 : 0);
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) dma16(rsrc, off[i], lds + (i * W + wave) * 1024);
+    rsrc = buffer_of(base + k * ld, left > 0 ? (left - 1) * ld + cols * 2 : 0);
+  }
+  __device__ __forceinline__ void piece(int i, uint32_t lds, int wave) {
+    dma16(rsrc, off[i], lds + (i * W + wave) * 1024);
   }
   // columns c*16 + l%16 of the wave
   __device__ __forceinline__ v4i read(LdsPtr lds, int half, int c) const {
@@ -283,8 +284,8 @@ struct TokenColumns : Columns<ROWS, WM, W> {
   int cols;
   __device__ __forceinline__ TokenColumns(const DenseIn &in, int t0, int64_t, int wave, int wm, int lane)
       : C(in.lda, in.M - t0, wave, wm, lane), base(in.a + (int64_t)t0 * 2), cols(in.M - t0) {}
-  __device__ __forceinline__ void fetch(const DenseIn &in, int64_t k, int, uint32_t lds, int wave) {
-    C::fetch(base, in.lda, cols, k, in.kbytes / 2, lds, wave);
+  __device__ __forceinline__ void begin(const DenseIn &in, int64_t k, int) {
+    C::begin(base, in.lda, cols, k, in.kbytes / 2);
   }
 };
 
@@ -295,12 +296,10 @@ struct ChannelColumns : Columns<ROWS, WN, W> {
   __device__ __forceinline__ ChannelColumns(const DenseIn &in, int n0_, int64_t, int wave, int wn, int lane)
       : C(in.ldb, in.N - n0_, wave, wn, lane), n0(n0_), cols(in.N - n0_) {}
   // split_k is a multiple of 64: a step lies in one of the two matrices
-  __device__ __forceinline__ void fetch(const DenseIn &in, int64_t k, int, uint32_t lds, int wave) {
-    const int64_t rows = in.kbytes / 2;
-    if (k < in.split_k)
-      C::fetch(in.b0 + (int64_t)n0 * 2, in.ldb, cols, k, in.split_k, lds, wave);
-    else
-      C::fetch(in.b1 + (int64_t)n0 * 2, in.ldb, cols, k - in.split_k, rows - in.split_k, lds, wave);
+  __device__ __forceinline__ void begin(const DenseIn &in, int64_t k, int) {
+    const bool first = k < in.split_k;
+    C::begin((first ? in.b0 : in.b1) + (int64_t)n0 * 2, in.ldb, cols, first ? k : k - in.split_k,
+             first ? in.split_k : in.kbytes / 2 - in.split_k);
   }
   __device__ __forceinline__ v4i read(LdsPtr lds, int half, int, int j) const {
     return C::read(lds, half, j);
@@ -376,11 +375,17 @@ tile_product(const DenseIn &in, int t0, int n0, uint8_t *lds,
       for (int j = 0; j < S::NJ; ++j) acc[i][m][j] = typename Op::Acc{0, 0, 0, 0};
   if (nk == 0) return;  // K = 0: the sums are zeros (the same for every K group)
 
-  auto fetch = [&](int k, uint32_t stage) {
+  auto begin = [&](int k) {
     const int64_t at = k0 + (int64_t)k * kStepBytes;  // byte of K; 64 16-bit rows a step
     const int left = in.kbytes - at < kStepBytes ? (int)(in.kbytes - at) : kStepBytes;
-    a.fetch(in, at / 2, left, lds_address(ring) + stage, wave);
-    b.fetch(in, at / 2, left, lds_address(ring) + stage + S::kUnitA, wave);
+    a.begin(in, at / 2, left);
+    b.begin(in, at / 2, left);
+  };
+  auto piece = [&](int i, uint32_t stage) {
+    if (i < S::A::kPieces)
+      a.piece(i, lds_address(ring) + stage, wave);
+    else if (i < S::kPieces)
+      b.piece(i - S::A::kPieces, lds_address(ring) + stage + S::kUnitA, wave);
   };
   v4i fa[2][S::MS], fb[2][S::NB][S::NJ];
   constexpr int kReadB = S::NB * S::NJ;
@@ -392,13 +397,19 @@ tile_product(const DenseIn &in, int t0, int n0, uint8_t *lds,
     else if (r < kReads)
       fa[half][r - kReadB] = a.read(ring + stage, half, r - kReadB);
   };
-  // the products of one half, and among them the reads of the other half
-  auto half_step = [&](int half, uint32_t stage, bool reads) {
+  // the products of one half, and among them the reads of the other half and
+  // the fetch of a later step
+  constexpr int kDma = (S::kPieces + S::MS - 1) / S::MS;  // pieces per token sub-tile
+  auto half_step = [&](int half, uint32_t stage, bool reads, bool fetches) {
 #pragma unroll
     for (int m = 0; m < S::MS; ++m) {
       if (reads) {
 #pragma unroll
         for (int r = m * kPer; r < (m + 1) * kPer; ++r) read(r, half ^ 1, stage);
+      }
+      if (fetches) {
+#pragma unroll
+        for (int i = m * kDma; i < (m + 1) * kDma; ++i) piece(i, S::kStage - stage);
       }
 #pragma unroll
       for (int i = 0; i < S::NB; ++i)
@@ -407,6 +418,11 @@ tile_product(const DenseIn &in, int t0, int n0, uint8_t *lds,
           acc[i][m][j] = Op::mfma(fb[half][i][j], fa[half][m], acc[i][m][j]);
       __builtin_amdgcn_sched_barrier(0);
     }
+  };
+  auto fetch = [&](int k, uint32_t stage) {
+    begin(k);
+#pragma unroll
+    for (int i = 0; i < S::kPieces; ++i) piece(i, stage);
   };
 
   fetch(0, 0);
@@ -420,16 +436,25 @@ tile_product(const DenseIn &in, int t0, int n0, uint8_t *lds,
 #pragma unroll
   for (int r = 0; r < kReads; ++r) read(r, 0, 0);
   uint32_t stage = 0;
-  for (int k = 0; k + 1 < nk; ++k) {
-    half_step(0, stage, true);
+  auto turn = [&]() {  // the middle of a step
     wait_dma<0>();
     barrier_reads();
-    if (k + 2 < nk) fetch(k + 2, stage);
     stage = S::kStage - stage;
-    half_step(1, stage, true);
+  };
+  int k = 0;
+  for (; k + 2 < nk; ++k) {
+    half_step(0, stage, true, false);
+    turn();
+    begin(k + 2);
+    half_step(1, stage, true, true);
   }
-  half_step(0, stage, true);
-  half_step(1, 0, false);
+  if (k + 1 < nk) {
+    half_step(0, stage, true, false);
+    turn();
+    half_step(1, stage, true, false);
+  }
+  half_step(0, stage, true, false);
+  half_step(1, 0, false, false);
 
   if constexpr (KG > 1) {
     // every wave's last operands are in registers and no load is in flight, so
