@@ -312,11 +312,11 @@ struct ChannelColumns : Columns<ROWS, WN, W> {
 enum Form { kPlainForm, kGatedForm, kBColumns, kABColumns };  // which operands, see DenseIn
 
 // BM tokens by BN rows of B, TM x TN waves; gated: half of each wave's B rows
-// come from b0 and half from b1 (the same channels).  LDS holds two K steps.
-// KG: groups of TM x TN waves that share the tile, each with its own LDS and
+// come from b0 and half from b1 (the same channels).  LDS is a ring of ST K
+// steps.  KG: groups of TM x TN waves that share the tile, each with its own LDS and
 // its own part of K; the first one adds the others' sums to its own, in order,
 // at the end.
-template <int BM, int BN, int TM, int TN, int KG, Form F>
+template <int BM, int BN, int TM, int TN, int ST, int KG, Form F>
 struct TileShape {
   static constexpr int kWaves = TM * TN;                 // of a K group
   static constexpr int kThreads = KG * kWaves * kWave;
@@ -329,7 +329,7 @@ struct TileShape {
   static constexpr int kTileChannels = BN / NB;          // channels of a workgroup
   static constexpr int kUnitA = BM * kStepBytes;
   static constexpr int kStage = (BM + BN) * kStepBytes;
-  static constexpr int kRing = 2 * kStage;               // of a K group
+  static constexpr int kRing = ST * kStage;               // of a K group
   static constexpr int kLdsBytes = KG * kRing;
   typedef typename std::conditional<F == kABColumns, TokenColumns<BM, WM, kWaves>,
                                     TokenRows<BM, WM, kWaves>>::type A;
@@ -348,15 +348,17 @@ struct TileShape {
 // The K step's two halves are software-pipelined: the matrix instructions of
 // one half run while the wave reads the other half's operands from LDS into a
 // second set of registers.  One barrier per step, in its middle: there every
-// wave has read the whole of step k (its stage is free for step k+2, whose
-// fetch starts at once) and step k+1 has landed.
-template <class Op, int BM, int BN, int TM, int TN, int KG, Form F>
+// wave has read the whole of step k (its stage is free for step k+ST, which is
+// fetched among the second half's products) and step k+1 has landed.  Two or
+// more waves to a SIMD fill each other's waits; the waves that issue matrix
+// instructions go first (setprio: 1-2 %).
+template <class Op, int BM, int BN, int TM, int TN, int ST, int KG, Form F>
 __device__ __forceinline__ void
 tile_product(const DenseIn &in, int t0, int n0, uint8_t *lds,
-             typename Op::Acc (&acc)[TileShape<BM, BN, TM, TN, KG, F>::NB]
-                                    [TileShape<BM, BN, TM, TN, KG, F>::MS]
-                                    [TileShape<BM, BN, TM, TN, KG, F>::NJ]) {
-  typedef TileShape<BM, BN, TM, TN, KG, F> S;
+             typename Op::Acc (&acc)[TileShape<BM, BN, TM, TN, ST, KG, F>::NB]
+                                    [TileShape<BM, BN, TM, TN, ST, KG, F>::MS]
+                                    [TileShape<BM, BN, TM, TN, ST, KG, F>::NJ]) {
+  typedef TileShape<BM, BN, TM, TN, ST, KG, F> S;
   const int lane = threadIdx.x & 63;
   const int all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kg = all / S::kWaves, wave = all % S::kWaves;
@@ -400,7 +402,7 @@ tile_product(const DenseIn &in, int t0, int n0, uint8_t *lds,
   // the products of one half, and among them the reads of the other half and
   // the fetch of a later step
   constexpr int kDma = (S::kPieces + S::MS - 1) / S::MS;  // pieces per token sub-tile
-  auto half_step = [&](int half, uint32_t stage, bool reads, bool fetches) {
+  auto half_step = [&](int half, uint32_t stage, uint32_t into, bool reads, bool fetches) {
 #pragma unroll
     for (int m = 0; m < S::MS; ++m) {
       if (reads) {
@@ -409,13 +411,15 @@ tile_product(const DenseIn &in, int t0, int n0, uint8_t *lds,
       }
       if (fetches) {
 #pragma unroll
-        for (int i = m * kDma; i < (m + 1) * kDma; ++i) piece(i, S::kStage - stage);
+        for (int i = m * kDma; i < (m + 1) * kDma; ++i) piece(i, into);
       }
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int i = 0; i < S::NB; ++i)
 #pragma unroll
         for (int j = 0; j < S::NJ; ++j)
           acc[i][m][j] = Op::mfma(fb[half][i][j], fa[half][m], acc[i][m][j]);
+      __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -425,36 +429,37 @@ tile_product(const DenseIn &in, int t0, int n0, uint8_t *lds,
     for (int i = 0; i < S::kPieces; ++i) piece(i, stage);
   };
 
-  fetch(0, 0);
-  if (nk > 1) {
-    fetch(1, S::kStage);
-    wait_dma<S::kPieces>();
-  } else {
+#pragma unroll
+  for (int k = 0; k < ST; ++k)
+    if (k < nk) fetch(k, k * S::kStage);
+  if (nk >= ST)
+    wait_dma<(ST - 1) * S::kPieces>();
+  else
     wait_dma<0>();
-  }
   barrier_reads();
 #pragma unroll
   for (int r = 0; r < kReads; ++r) read(r, 0, 0);
   uint32_t stage = 0;
-  auto turn = [&]() {  // the middle of a step
+  auto next = [&](uint32_t s) -> uint32_t { return s + S::kStage == S::kRing ? 0 : s + S::kStage; };
+  int k = 0;
+  for (; k + ST < nk; ++k) {
+    half_step(0, stage, 0, true, false);
+    wait_dma<(ST - 2) * S::kPieces>();
+    barrier_reads();
+    begin(k + ST);
+    const uint32_t into = stage;
+    stage = next(stage);
+    half_step(1, stage, into, true, true);
+  }
+  for (; k + 1 < nk; ++k) {
+    half_step(0, stage, 0, true, false);
     wait_dma<0>();
     barrier_reads();
-    stage = S::kStage - stage;
-  };
-  int k = 0;
-  for (; k + 2 < nk; ++k) {
-    half_step(0, stage, true, false);
-    turn();
-    begin(k + 2);
-    half_step(1, stage, true, true);
+    stage = next(stage);
+    half_step(1, stage, 0, true, false);
   }
-  if (k + 1 < nk) {
-    half_step(0, stage, true, false);
-    turn();
-    half_step(1, stage, true, false);
-  }
-  half_step(0, stage, true, false);
-  half_step(1, 0, false, false);
+  half_step(0, stage, 0, true, false);
+  half_step(1, 0, 0, false, false);
 
   if constexpr (KG > 1) {
     // every wave's last operands are in registers and no load is in flight, so

@@ -2,8 +2,6 @@
 // quantisation, the int8 product with token and channel scales, the gated
 // block (both projections, SiLU and product in one kernel) in int8 and in
 // 16-bit types, and the 16-bit block's backward pass.
-#include <math.h>
-
 #include "dense.hpp"
 #include "dense_dev.hpp"
 #include "expert_dev.hpp"  // exp_neg
@@ -205,29 +203,29 @@ __device__ __forceinline__ void store_tile(const DenseIn &in, const Epi &epi,
   }
 }
 
-template <class Op, int BM, int BN, int TM, int TN, int KG, Form F, class Epi>
+template <class Op, int BM, int BN, int TM, int TN, int ST, int KG, Form F, class Epi>
 __global__ __launch_bounds__(TM *TN *KG *kWave) void tile_kernel(DenseIn in, Epi epi, int tiles_m,
                                                                  int tiles_n) {
-  typedef TileShape<BM, BN, TM, TN, KG, F> S;
+  typedef TileShape<BM, BN, TM, TN, ST, KG, F> S;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLdsBytes];
   int tm, tn;
   tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
   const int t0 = tm * BM, n0 = tn * S::kTileChannels;
   typename Op::Acc acc[S::NB][S::MS][S::NJ];
-  tile_product<Op, BM, BN, TM, TN, KG, F>(in, t0, n0, lds, acc);
+  tile_product<Op, BM, BN, TM, TN, ST, KG, F>(in, t0, n0, lds, acc);
   const int wave = threadIdx.x >> 6;
   if (wave >= S::kWaves) return;  // the first K group has the sums
   store_tile<S, Op>(in, epi, acc, t0, n0, wave / TN, wave % TN);
 }
 
-template <class Op, int BM, int BN, int TM, int TN, int KG, Form F, class Epi>
+template <class Op, int BM, int BN, int TM, int TN, int ST, int KG, Form F, class Epi>
 hipError_t run_tile(const DenseIn &in, const Epi &epi, hipStream_t stream) {
-  typedef TileShape<BM, BN, TM, TN, KG, F> S;
+  typedef TileShape<BM, BN, TM, TN, ST, KG, F> S;
   const int64_t tm = ((int64_t)in.M + BM - 1) / BM;
   const int64_t tn = ((int64_t)in.N + S::kTileChannels - 1) / S::kTileChannels;
   if (tm * tn == 0) return hipSuccess;
   if (tm * tn > 0x7fffffff) return hipErrorInvalidValue;
-  tile_kernel<Op, BM, BN, TM, TN, KG, F, Epi>
+  tile_kernel<Op, BM, BN, TM, TN, ST, KG, F, Epi>
       <<<(unsigned)(tm * tn), S::kThreads, 0, stream>>>(in, epi, (int)tm, (int)tn);
   return hipGetLastError();
 }
@@ -290,47 +288,47 @@ hipError_t run_stream(const DenseIn &in, const Epi &epi, int most, hipStream_t s
 // ---------------------------------------------------------------- choice
 constexpr int kCUs = 256;  // compute units of an MI355X
 
-// Estimated time of a product in tiles, in us.  A compute unit that holds r
-// workgroups takes max(a + b*(r-1), w*r) for a K step of all of them: alone, a
-// workgroup waits for its loads and barriers (a), a few hide each other's
-// waits (b), and then the loads or the matrix instructions are the limit (w).
-// At most `cap` workgroups fit; a round of cap per compute unit also costs c
-// to start and to store.  The constants are fits to measured products of 64 to
-// 8192 tokens, K of 768 to 28672 bytes, in int8 and bf16 (the byte counts
-// decide, not the type); the estimate is within about 15 % of them.
-struct TileCost {
-  int bm, channels, cap;
-  float a, b, w, c;
-};
-double tile_time(const TileCost &t, const DenseIn &in) {
-  const int64_t tiles = (((int64_t)in.M + t.bm - 1) / t.bm) *
-                        (((int64_t)in.N + t.channels - 1) / t.channels);
-  const double steps = (double)((in.kbytes + kStepBytes - 1) / kStepBytes);
-  auto step = [&](double r) { return fmax(t.a + t.b * (r - 1), t.w * r); };
-  const int64_t full = tiles / (kCUs * t.cap), rest = tiles % (kCUs * t.cap);
-  double us = (double)full * (t.c + steps * step(t.cap));
-  if (rest > 0) us += t.c + steps * step((double)((rest + kCUs - 1) / kCUs));
-  return us;
-}
-
-// The tile with the least estimated time.
+// The tiles, each with as much of a compute unit's LDS as it can use: one
+// workgroup to a compute unit, so the time of a product is about
+//   rounds of 256 tiles * (c + K steps * s)  us.
+// c and s are fits to 72 measured products (33 to 8192 tokens, K of 256 to
+// 32768 bytes, 256 to 16384 channels; int8, and bf16 gated; the bytes count,
+// not the type), with which the choice is on average 1 % and at most 14 %
+// slower than the best of the five, and of three more (64x64, 64x128 and
+// 128x128 with two or three workgroups to a compute unit) that gained nothing
+// beside them.  Without the 64x64 tile it is 9 % slower, without any other one
+// 2 to 4 %.
 template <class Op, Form F, class Epi>
 hipError_t run_tiles(const DenseIn &in, const Epi &epi, hipStream_t stream) {
-  constexpr int nb = F == kGatedForm ? 2 : 1;
-  const TileCost cost[] = {{64, 64 / nb, 1, 0.27f, 0.0f, 0.0f, 2.5f},
-                           {64, 64 / nb, 5, 0.45f, 0.06f, 0.20f, 2.5f},
-                           {64, 128 / nb, 3, 0.55f, 0.12f, 0.32f, 2.5f},
-                           {128, 128 / nb, 2, 0.74f, 0.32f, 0.53f, 2.5f},
-                           {256, 256 / nb, 1, 1.50f, 0.0f, 0.0f, 2.5f}};
+  constexpr int nb = F == kGatedForm ? 2 : 1;  // matrices that share a tile's columns
+  struct Tile {
+    int bm, bn;
+    double c, s;
+  };
+  constexpr Tile tiles[] = {{64, 64, 3.4, 0.19},
+                            {64, 128, 4.3, 0.29},
+                            {128, 128, 4.4, 0.46},
+                            {128, 256, 5.6, 0.74},
+                            {256, 256, 7.3, 1.16}};
+  const double steps = (double)((in.kbytes + kStepBytes - 1) / kStepBytes);
   int best = 0;
-  for (int i = 1; i < 5; ++i)
-    if (tile_time(cost[i], in) < tile_time(cost[best], in)) best = i;
+  double least = 0.0;
+  for (int i = 0; i < 5; ++i) {
+    const Tile &t = tiles[i];
+    const int64_t n = (((int64_t)in.M + t.bm - 1) / t.bm) *
+                      (((int64_t)in.N * nb + t.bn - 1) / t.bn);
+    const double us = (double)((n + kCUs - 1) / kCUs) * (t.c + steps * t.s);
+    if (i == 0 || us < least) {
+      least = us;
+      best = i;
+    }
+  }
   switch (best) {
-    case 0: return run_tile<Op, 64, 64, 2, 2, 4, F, Epi>(in, epi, stream);
-    case 1: return run_tile<Op, 64, 64, 2, 2, 1, F, Epi>(in, epi, stream);
-    case 2: return run_tile<Op, 64, 128, 2, 2, 1, F, Epi>(in, epi, stream);
-    case 3: return run_tile<Op, 128, 128, 2, 2, 1, F, Epi>(in, epi, stream);
-    default: return run_tile<Op, 256, 256, 2, 4, 1, F, Epi>(in, epi, stream);
+    case 0: return run_tile<Op, 64, 64, 2, 2, 3, 2, F, Epi>(in, epi, stream);
+    case 1: return run_tile<Op, 64, 128, 2, 4, 3, 2, F, Epi>(in, epi, stream);
+    case 2: return run_tile<Op, 128, 128, 2, 4, 4, 1, F, Epi>(in, epi, stream);
+    case 3: return run_tile<Op, 128, 256, 2, 4, 3, 1, F, Epi>(in, epi, stream);
+    default: return run_tile<Op, 256, 256, 2, 4, 2, 1, F, Epi>(in, epi, stream);
   }
 }
 
