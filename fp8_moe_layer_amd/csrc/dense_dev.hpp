@@ -498,11 +498,11 @@ tile_product(const DenseIn &in, int t0, int n0, uint8_t *lds,
 // the group's K steps in turn, each with a ring of R steps in LDS of its own,
 // so that nothing but the wave's own load counter orders the stream, which
 // runs on over the groups' borders.  At a group's end the waves' partial sums
-// meet in LDS; one wave, another each time, adds them in wave order (the same
-// bits every run) and stores, while the others stream on.
+// meet in LDS, where one more wave, which fetches nothing, adds them in wave
+// order (the same bits every run) and stores while the others stream on.
 template <int XP, int NS, int W, int R>
 struct StreamShape {
-  static constexpr int kThreads = W * kWave;
+  static constexpr int kThreads = (W + 1) * kWave;
   static constexpr int MS = (XP + 1) / 2;                 // token sub-tiles (XP: pieces of 8 tokens)
   static constexpr int kRows = 16 * NS;                   // B rows of a group
   static constexpr int kPieces = 2 * NS + XP;             // 1 KB pieces per step
@@ -512,11 +512,13 @@ struct StreamShape {
   static constexpr int kLdsBytes = kRing + 2 * W * kPart; // parts double-buffered by group
 };
 
-// fn(group, part): called by one wave per group; part: its W partial sums,
-// kPart bytes apart, each [NS][MS] blocks of 64 lanes x 4 sums (lane l: token
-// m*16 + l%16, rows s*16 + (l/16)*4 .. +3 of the group).
-template <class Op, int XP, int NS, int W, int R, bool GATED, class Fn>
-__device__ __forceinline__ void stream_product(const DenseIn &in, int groups, uint8_t *lds, Fn fn) {
+// For each group the adding wave calls load(group) ahead of time, and then
+// store(what load returned, group, part); part: the W partial sums, kPart bytes
+// apart, each [NS][MS] blocks of 64 lanes x 4 sums (lane l: token m*16 + l%16,
+// rows s*16 + (l/16)*4 .. +3 of the group).
+template <class Op, int XP, int NS, int W, int R, bool GATED, class Load, class Store>
+__device__ __forceinline__ void stream_product(const DenseIn &in, int groups, uint8_t *lds,
+                                               Load load, Store store) {
   typedef StreamShape<XP, NS, W, R> S;
   constexpr int kChannels = GATED ? S::kRows / 2 : S::kRows;  // of a group
   const int lane = threadIdx.x & 63;
@@ -526,6 +528,17 @@ __device__ __forceinline__ void stream_product(const DenseIn &in, int groups, ui
   const int mine = groups > (int)blockIdx.x
                        ? (groups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x : 0;
   const int total = mine * steps;
+  if (wave == W) {
+    int g = blockIdx.x;
+    for (int i = 0; i < mine; ++i, g += gridDim.x) {
+      const auto c = load(g);
+      barrier_reads();
+      // the next barrier comes after these reads, and the part is written again
+      // only after that
+      store(c, g, lds + S::kRing + (i & 1) * W * S::kPart);
+    }
+    return;
+  }
 
   // a piece: eight rows of 128 bytes; lane l fetches piece (l%8) ^ (l/8) of row l/8
   const int lr = lane >> 3, pos = ((lane & 7) ^ lr) * 16;
@@ -586,8 +599,7 @@ __device__ __forceinline__ void stream_product(const DenseIn &in, int groups, ui
   const int p = lane & 15, q = lane >> 4;
   const uint8_t *base = lds + wave * R * S::kStage;
   int slot = 0, todo = total;
-  int g = blockIdx.x;
-  for (int i = 0; i < mine; ++i, g += gridDim.x) {
+  for (int i = 0; i < mine; ++i) {
     typename Op::Acc acc[NS][S::MS];
 #pragma unroll
     for (int s = 0; s < NS; ++s)
@@ -632,9 +644,6 @@ __device__ __forceinline__ void stream_product(const DenseIn &in, int groups, ui
         *reinterpret_cast<typename Op::Acc *>(part + wave * S::kPart + (s * S::MS + m) * 1024 +
                                               lane * 16) = acc[s][m];
     barrier_reads();
-    // the next barrier comes after this wave's reads of `part`, and the part is
-    // written again only after that
-    if (wave == i % W) fn(g, part);
   }
 }
 

@@ -230,16 +230,28 @@ hipError_t run_tile(const DenseIn &in, const Epi &epi, hipStream_t stream) {
   return hipGetLastError();
 }
 
+constexpr int kCUs = 256;  // compute units of an MI355X
+
 // ---------------------------------------------------------------- few tokens
 template <class Op, int XP, int NS, int W, int R, class Epi>
-__global__ __launch_bounds__(W *kWave) void stream_kernel(DenseIn in, Epi epi, int groups) {
+__global__ __launch_bounds__((W + 1) * kWave) void stream_kernel(DenseIn in, Epi epi, int groups) {
   typedef StreamShape<XP, NS, W, R> S;
   typedef typename Op::Acc Acc;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLdsBytes];
   constexpr bool kGated = Epi::kGated;
   constexpr int kChannels = kGated ? S::kRows / 2 : S::kRows;
-  stream_product<Op, XP, NS, W, R, kGated>(in, groups, lds, [&](int g, const uint8_t *part) {
-    const int lane = threadIdx.x & 63;
+  constexpr int kSub = kGated && NS > 1 ? NS / 2 : NS;  // channel sub-tiles of a group
+  struct Scales {
+    typename Epi::template Chan<4> c[kSub];
+  };
+  const int lane = threadIdx.x & 63, row = (lane >> 4) * 4;
+  auto load = [&](int g) {
+    Scales c;
+#pragma unroll
+    for (int s = 0; s < kSub; ++s) epi.load(c.c[s], g * kChannels + s * 16 + row);
+    return c;
+  };
+  auto store = [&](const Scales &c, int g, const uint8_t *part) {
     auto sum = [&](int block, int l) {  // of the waves' parts, in wave order
       Acc a = *reinterpret_cast<const Acc *>(part + block * 1024 + l * 16);
 #pragma unroll
@@ -247,15 +259,12 @@ __global__ __launch_bounds__(W *kWave) void stream_kernel(DenseIn in, Epi epi, i
         a += *reinterpret_cast<const Acc *>(part + w * S::kPart + block * 1024 + l * 16);
       return a;
     };
-    const int row = (lane >> 4) * 4;
 #pragma unroll
-    for (int s = 0; s < (kGated && NS > 1 ? NS / 2 : NS); ++s) {
+    for (int s = 0; s < kSub; ++s) {
       // one gated sub-tile: rows 0-7 gate, 8-15 up, so the upper lanes have no channel
       const bool none = kGated && NS == 1 && row >= 8;
       const int ch = g * kChannels + s * 16 + row;
       if (none || ch >= in.N) continue;
-      typename Epi::template Chan<4> chan;
-      epi.load(chan, ch);
 #pragma unroll
       for (int m = 0; m < S::MS; ++m) {
         const int t = m * 16 + (lane & 15);
@@ -269,25 +278,24 @@ __global__ __launch_bounds__(W *kWave) void stream_kernel(DenseIn in, Epi epi, i
 #pragma unroll
           for (int i = 0; i < 4; ++i) a[1][i] = a1[i];
         }
-        epi.store(chan, t, ch, a);
+        epi.store(c.c[s], t, ch, a);
       }
     }
-  });
+  };
+  stream_product<Op, XP, NS, W, R, kGated>(in, groups, lds, load, store);
 }
 
 template <class Op, int XP, int NS, int W, int R, class Epi>
-hipError_t run_stream(const DenseIn &in, const Epi &epi, int most, hipStream_t stream) {
+hipError_t run_stream(const DenseIn &in, const Epi &epi, hipStream_t stream) {
   typedef StreamShape<XP, NS, W, R> S;
   constexpr int kChannels = Epi::kGated ? S::kRows / 2 : S::kRows;
   const int groups = (int)(((int64_t)in.N + kChannels - 1) / kChannels);
   stream_kernel<Op, XP, NS, W, R, Epi>
-      <<<groups < most ? groups : most, S::kThreads, 0, stream>>>(in, epi, groups);
+      <<<groups < kCUs ? groups : kCUs, S::kThreads, 0, stream>>>(in, epi, groups);
   return hipGetLastError();
 }
 
 // ---------------------------------------------------------------- choice
-constexpr int kCUs = 256;  // compute units of an MI355X
-
 // The tiles, each with as much of a compute unit's LDS as it can use: one
 // workgroup to a compute unit, so the time of a product is about
 //   rounds of 256 tiles * (c + K steps * s)  us.
@@ -332,26 +340,17 @@ hipError_t run_tiles(const DenseIn &in, const Epi &epi, hipStream_t stream) {
   }
 }
 
-// Up to 32 tokens stream the weights (stream_product), unless at 17 to 32
-// there are many channels: then small tiles, which read the tokens less often,
-// are faster (bf16, T = 32, 4096 -> 2 x 14336: 35 us in tiles, 48 us streamed;
-// 14336 -> 4096 int8: 18 us streamed, 52 us in tiles).  Eight waves a
-// workgroup where the groups leave one to a compute unit, else four and two
-// workgroups (int8, one token, 14336 -> 4096: 11.0 and 14.3 us; 4096 -> 14336:
-// 13.4 and 11.9 us).  Above, tiles.
+// Up to 32 tokens stream the weights (stream_product), one workgroup to a
+// compute unit; at 17 to 32 only few channels do, for which tiles leave compute
+// units idle (int8, T = 32, weights from HBM: 14336 -> 4096 23 us streamed and
+// 32 us in tiles; 4096 -> 14336 22 and 16 us).  Above, tiles.
 template <class Op, class Epi>
 hipError_t run_product(const DenseIn &in, const Epi &epi, hipStream_t stream) {
   if (in.M == 0) return hipSuccess;
-  constexpr int nb = Epi::kGated ? 2 : 1;
-  const int64_t groups = ((int64_t)in.N * nb + 15) / 16;  // of 16 weight rows
-  if (in.M <= 8)
-    return groups <= kCUs ? run_stream<Op, 1, 1, 8, 4, Epi>(in, epi, kCUs, stream)
-                          : run_stream<Op, 1, 1, 4, 4, Epi>(in, epi, 2 * kCUs, stream);
-  if (in.M <= 16)
-    return groups <= kCUs ? run_stream<Op, 2, 1, 8, 4, Epi>(in, epi, kCUs, stream)
-                          : run_stream<Op, 2, 1, 4, 4, Epi>(in, epi, 2 * kCUs, stream);
-  if (in.M <= 32 && groups <= 4 * kCUs)
-    return run_stream<Op, 4, 2, 4, 4, Epi>(in, epi, kCUs, stream);
+  const int64_t groups = ((int64_t)in.N * (Epi::kGated ? 2 : 1) + 15) / 16;  // of 16 weight rows
+  if (in.M <= 8) return run_stream<Op, 1, 1, 8, 6, Epi>(in, epi, stream);
+  if (in.M <= 16) return run_stream<Op, 2, 1, 8, 4, Epi>(in, epi, stream);
+  if (in.M <= 32 && groups <= 2 * kCUs) return run_stream<Op, 4, 2, 4, 4, Epi>(in, epi, stream);
   return run_tiles<Op, Epi::kGated ? kGatedForm : kPlainForm>(in, epi, stream);
 }
 
