@@ -369,6 +369,13 @@ def _type(dtype, allowed=tuple(_TYPES)):
     return _TYPES[dtype]
 
 
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+else:
+    def _raw_stream(index: int) -> int:
+        return torch.cuda.current_stream(index).cuda_stream
+
+
 class _Call:
     """One call of a dense operator: its device (that of the first tensor;
     the others must be on it too) and its stream (default: the device's
@@ -384,7 +391,7 @@ class _Call:
             raise ValueError("fp8_moe_layer_amd works on device tensors only")
         self.alloc = stream
         if stream is None:
-            self.stream = torch._C._cuda_getCurrentRawStream(dev.index)
+            self.stream = _raw_stream(dev.index)
         else:
             if stream.device != dev:
                 raise ValueError(f"stream is on {stream.device}, tensors on {dev}")
@@ -397,21 +404,19 @@ class _Call:
             raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
         if t.shape != shape:
             raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        raise ValueError(f"{name} must be contiguous")
 
-    def ptr(self, t: Optional[torch.Tensor], shape, dtype, name: str):
+    def ptr(self, t: torch.Tensor, shape, dtype, name: str):
         """Address of a contiguous tensor of that shape and type on the call's device."""
-        if t is None:
-            return None
-        if t.dtype != dtype or t.shape != shape or t.device != self.dev:
+        if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+                or t.device != self.dev):
             self._refuse(t, shape, dtype, name)
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
         return t.data_ptr()
 
     def rows(self, t: torch.Tensor, shape, dtype, name: str):
         """(address, row stride in elements) of a 2-D tensor whose rows are
         contiguous; the library checks the stride."""
-        if t.dtype != dtype or t.shape != shape or t.device != self.dev:
+        if t.dtype is not dtype or t.shape != shape or t.device != self.dev:
             self._refuse(t, shape, dtype, name)
         ld, unit = t.stride()
         if unit != 1 and t.shape[1] > 1:
@@ -430,7 +435,7 @@ class _Call:
         else:
             with torch.cuda.device(self.dev):
                 status = fn(*args, self.stream)
-        if status != 0:
+        if status:
             raise MoEError(status)
 
 
@@ -471,7 +476,7 @@ def matmul_i8(xq: torch.Tensor, sx: torch.Tensor, wq: torch.Tensor, sw: torch.Te
     xp, ldx = c.rows(xq, (T, K), torch.int8, "xq")
     c.run(_matmul_i8, xp, ldx, c.ptr(sx, (T,), torch.float32, "sx"),
           c.ptr(wq, (N, K), torch.int8, "wq"), c.ptr(sw, (N,), torch.float32, "sw"),
-          c.ptr(bias, (N,), torch.float32, "bias"), T, K, N, kind,
+          None if bias is None else c.ptr(bias, (N,), torch.float32, "bias"), T, K, N, kind,
           c.ptr(y, (T, N), y.dtype, "out"))
     return y
 

@@ -191,7 +191,8 @@ template <int ROWS, int WN, int CH, bool GATED, int W>
 struct ChannelRows {
   static constexpr int kPieces = ROWS / 8 / W;
   static constexpr int NJ = CH / 16;
-  v4u rsrc, rsrc1;
+  static_assert(8 * W % WN == 0 || !GATED, "a wave's pieces are all of one matrix");
+  v4u rsrc;
   uint32_t off[kPieces];
   int pos[kPieces];
   int at;
@@ -201,8 +202,8 @@ struct ChannelRows {
     constexpr int kChannels = GATED ? ROWS / 2 : ROWS;
     const int rows = in.N - n0 < kChannels ? in.N - n0 : kChannels;
     const int64_t bytes = (int64_t)(rows - 1) * in.ldb + in.kbytes;
-    rsrc = buffer_of(in.b0 + (int64_t)n0 * in.ldb, bytes);
-    rsrc1 = GATED ? buffer_of(in.b1 + (int64_t)n0 * in.ldb, bytes) : rsrc;
+    const uint8_t *w = GATED && wave * 8 % WN >= CH ? in.b1 : in.b0;
+    rsrc = buffer_of(w + (int64_t)n0 * in.ldb, bytes);
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int r = (i * W + wave) * 8 + (lane >> 3), rr = r % WN % CH;
@@ -216,12 +217,7 @@ struct ChannelRows {
   int left;
   __device__ __forceinline__ void begin(const DenseIn &, int64_t, int left_) { left = left_; }
   __device__ __forceinline__ void piece(int i, uint32_t lds, int wave) {
-    const int n = i * W + wave;
-    const uint32_t o = pos[i] < left ? off[i] : kPastEnd;
-    if (GATED && (n * 8) % WN >= CH)
-      dma16(rsrc1, o, lds + n * 1024);
-    else
-      dma16(rsrc, o, lds + n * 1024);
+    dma16(rsrc, pos[i] < left ? off[i] : kPastEnd, lds + (i * W + wave) * 1024);
     off[i] += kStepBytes;
   }
   __device__ __forceinline__ v4i read(LdsPtr lds, int half, int b, int j) const {
