@@ -295,6 +295,34 @@ hipError_t run_stream(const DenseIn &in, const Epi &epi, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Two products with transposed operands in one launch, the gradients dx (B
+// transposed) and dW (both transposed): neither waits for the other's last
+// tiles.  The product whose tiles take longer comes first.
+template <class Op, int BM, int BN, int TM, int TN, int ST, int KG, class Epi>
+__global__ __launch_bounds__(TM *TN *KG *kWave) void pair_kernel(DenseIn in1, Epi epi1, int2 tiles1,
+                                                                 DenseIn in2, Epi epi2, int2 tiles2,
+                                                                 int second_first) {
+  typedef TileShape<BM, BN, TM, TN, ST, KG, kBColumns> S1;
+  typedef TileShape<BM, BN, TM, TN, ST, KG, kABColumns> S2;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S1::kLdsBytes];
+  const int n1 = tiles1.x * tiles1.y, n2 = tiles2.x * tiles2.y, b = blockIdx.x;
+  const bool first = second_first ? b >= n2 : b < n1;
+  const int wave = threadIdx.x >> 6;
+  int tm, tn;
+  typename Op::Acc acc[1][S1::MS][S1::NJ];
+  if (first) {
+    tile_of(second_first ? b - n2 : b, tiles1.x, tiles1.y, tm, tn);
+    tile_product<Op, BM, BN, TM, TN, ST, KG, kBColumns>(in1, tm * BM, tn * BN, lds, acc);
+    if (wave < S1::kWaves)
+      store_tile<S1, Op>(in1, epi1, acc, tm * BM, tn * BN, wave / TN, wave % TN);
+  } else {
+    tile_of(second_first ? b : b - n1, tiles2.x, tiles2.y, tm, tn);
+    tile_product<Op, BM, BN, TM, TN, ST, KG, kABColumns>(in2, tm * BM, tn * BN, lds, acc);
+    if (wave < S2::kWaves)
+      store_tile<S2, Op>(in2, epi2, acc, tm * BM, tn * BN, wave / TN, wave % TN);
+  }
+}
+
 // ---------------------------------------------------------------- choice
 // The tiles, each with as much of a compute unit's LDS as it can use: one
 // workgroup to a compute unit, so the time of a product is about
@@ -306,38 +334,103 @@ hipError_t run_stream(const DenseIn &in, const Epi &epi, hipStream_t stream) {
 // 128x128 with two or three workgroups to a compute unit) that gained nothing
 // beside them.  Without the 64x64 tile it is 9 % slower, without any other one
 // 2 to 4 %.
+struct Tile {
+  int bm, bn;
+  double c, s;
+};
+constexpr int kTiles = 5;
+constexpr Tile kTile[kTiles] = {{64, 64, 3.4, 0.19},
+                                {64, 128, 4.3, 0.29},
+                                {128, 128, 4.4, 0.46},
+                                {128, 256, 5.6, 0.74},
+                                {256, 256, 7.3, 1.16}};
+
+// Number of tiles of a product, and the time of one; nb: matrices that share a
+// tile's columns.
+int64_t tiles_of(const Tile &t, const DenseIn &in, int nb) {
+  return (((int64_t)in.M + t.bm - 1) / t.bm) * (((int64_t)in.N * nb + t.bn - 1) / t.bn);
+}
+double time_of(const Tile &t, const DenseIn &in) {
+  return t.c + (double)((in.kbytes + kStepBytes - 1) / kStepBytes) * t.s;
+}
+
+struct Choice {
+  int tile;
+  double us;
+};
+Choice choose(const DenseIn &in, int nb) {
+  Choice best{0, 0.0};
+  for (int i = 0; i < kTiles; ++i) {
+    const int64_t n = tiles_of(kTile[i], in, nb);
+    const double us = (double)((n + kCUs - 1) / kCUs) * time_of(kTile[i], in);
+    if (i == 0 || us < best.us) best = Choice{i, us};
+  }
+  return best;
+}
+
 template <class Op, Form F, class Epi>
 hipError_t run_tiles(const DenseIn &in, const Epi &epi, hipStream_t stream) {
-  constexpr int nb = F == kGatedForm ? 2 : 1;  // matrices that share a tile's columns
-  struct Tile {
-    int bm, bn;
-    double c, s;
-  };
-  constexpr Tile tiles[] = {{64, 64, 3.4, 0.19},
-                            {64, 128, 4.3, 0.29},
-                            {128, 128, 4.4, 0.46},
-                            {128, 256, 5.6, 0.74},
-                            {256, 256, 7.3, 1.16}};
-  const double steps = (double)((in.kbytes + kStepBytes - 1) / kStepBytes);
-  int best = 0;
-  double least = 0.0;
-  for (int i = 0; i < 5; ++i) {
-    const Tile &t = tiles[i];
-    const int64_t n = (((int64_t)in.M + t.bm - 1) / t.bm) *
-                      (((int64_t)in.N * nb + t.bn - 1) / t.bn);
-    const double us = (double)((n + kCUs - 1) / kCUs) * (t.c + steps * t.s);
-    if (i == 0 || us < least) {
-      least = us;
-      best = i;
-    }
-  }
-  switch (best) {
+  switch (choose(in, F == kGatedForm ? 2 : 1).tile) {
     case 0: return run_tile<Op, 64, 64, 2, 2, 3, 2, F, Epi>(in, epi, stream);
     case 1: return run_tile<Op, 64, 128, 2, 4, 3, 2, F, Epi>(in, epi, stream);
     case 2: return run_tile<Op, 128, 128, 2, 4, 4, 1, F, Epi>(in, epi, stream);
     case 3: return run_tile<Op, 128, 256, 2, 4, 3, 1, F, Epi>(in, epi, stream);
     default: return run_tile<Op, 256, 256, 2, 4, 2, 1, F, Epi>(in, epi, stream);
   }
+}
+
+// When the last of n1 tiles of a1 us and then n2 tiles of a2 us is done, each
+// given to the compute unit that is free first.
+double pair_time(int64_t n1, double a1, int64_t n2, double a2) {
+  const int64_t busy = n1 % kCUs, idle = kCUs - busy;
+  const double t0 = (double)(n1 / kCUs) * a1, t1 = t0 + a1;  // the idle and the busy ones' start
+  if (n2 == 0) return busy > 0 ? t1 : t0;
+  const int64_t head = (int64_t)(a1 / a2);  // tiles that an idle one does in the meantime
+  if (n2 <= idle * head) return busy > 0 ? t1 : t0 + a2 * (double)((n2 + idle - 1) / idle);
+  const int64_t left = n2 - idle * head, rounds = left / kCUs, rest = left % kCUs;
+  const double turn = (double)(head + rounds);
+  return rest == 0      ? t0 + turn * a2 + (busy > 0 ? a1 - (double)head * a2 : 0.0)
+         : rest <= idle ? t0 + (turn + 1.0) * a2
+                        : t1 + (double)(rounds + 1) * a2;
+}
+
+template <class Op, int BM, int BN, int TM, int TN, int ST, int KG, class Epi>
+hipError_t run_pair_tile(const DenseIn &in1, const Epi &epi1, const DenseIn &in2, const Epi &epi2,
+                         bool second_first, hipStream_t stream) {
+  typedef TileShape<BM, BN, TM, TN, ST, KG, kBColumns> S;
+  const int2 t1 = make_int2((in1.M + BM - 1) / BM, (in1.N + BN - 1) / BN);
+  const int2 t2 = make_int2((in2.M + BM - 1) / BM, (in2.N + BN - 1) / BN);
+  const int64_t n = (int64_t)t1.x * t1.y + (int64_t)t2.x * t2.y;
+  if (n > 0x7fffffff) return hipErrorInvalidValue;
+  pair_kernel<Op, BM, BN, TM, TN, ST, KG, Epi><<<(unsigned)n, S::kThreads, 0, stream>>>(
+      in1, epi1, t1, in2, epi2, t2, second_first);
+  return hipGetLastError();
+}
+
+// One launch for both where that is faster by the estimate: they then have to
+// share a tile.  (The estimate's ratio follows the measured one: T, d, f = 2047,
+// 2048, 768: 0.85, 44 and 51 us; 4096, 2048, 1408: 0.89, 122 and 134 us; 8192,
+// 2048, 192: 1.51, 88 and 63 us; 512, 4096, 4096: 1.30, 126 and 117 us.)
+template <class Op, class Epi>
+hipError_t run_pair(const DenseIn &in1, const Epi &epi1, const DenseIn &in2, const Epi &epi2,
+                    hipStream_t stream) {
+  const bool swap = in2.kbytes > in1.kbytes;
+  const DenseIn &l = swap ? in2 : in1, &r = swap ? in1 : in2;  // the longer tiles first
+  Choice best{-1, (in1.M > 0 ? choose(in1, 1).us : 0.0) + choose(in2, 1).us};
+  for (int i = 0; i < kTiles; ++i) {
+    const double us = pair_time(tiles_of(kTile[i], l, 1), time_of(kTile[i], l),
+                                tiles_of(kTile[i], r, 1), time_of(kTile[i], r));
+    if (us < best.us) best = Choice{i, us};
+  }
+  switch (best.tile) {
+    case 0: return run_pair_tile<Op, 64, 64, 2, 2, 3, 2>(in1, epi1, in2, epi2, swap, stream);
+    case 1: return run_pair_tile<Op, 64, 128, 2, 4, 3, 2>(in1, epi1, in2, epi2, swap, stream);
+    case 2: return run_pair_tile<Op, 128, 128, 2, 4, 4, 1>(in1, epi1, in2, epi2, swap, stream);
+    case 3: return run_pair_tile<Op, 128, 256, 2, 4, 3, 1>(in1, epi1, in2, epi2, swap, stream);
+    case 4: return run_pair_tile<Op, 256, 256, 2, 4, 2, 1>(in1, epi1, in2, epi2, swap, stream);
+  }
+  const hipError_t e = run_tiles<Op, kBColumns>(in1, epi1, stream);
+  return e != hipSuccess ? e : run_tiles<Op, kABColumns>(in2, epi2, stream);
 }
 
 // Up to 32 tokens stream the weights (stream_product), one workgroup to a
@@ -565,20 +658,19 @@ hipError_t backward_as(const Gated16Backward &p, hipStream_t stream) {
     const int64_t runs = (int64_t)p.T * p.f / 8, blocks = (runs + 255) / 256;
     gate_grad_kernel<E><<<(unsigned)(blocks < 8 * kCUs ? blocks : 8 * kCUs), 256, 0, stream>>>(
         (const E *)p.dh, p.lddh, p.gate, p.up, runs, p.f, dgu);
-    hipError_t e = hipGetLastError();
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    // dx [T][d]: K runs over the 2f channels, down the rows of the two weight matrices
-    const DenseIn in{(const uint8_t *)dgu, (const uint8_t *)p.w_gate, (const uint8_t *)p.w_up,
-                     two_f * 2, (int64_t)p.d * 2, p.T, p.d, two_f * 2, p.f};
-    const EpiPlain<E> epi{(E *)p.dx, nullptr, p.T, p.d, 1};
-    if ((e = run_tiles<Op, kBColumns>(in, epi, stream)) != hipSuccess) return e;
   }
-  // dW [2f][d]: K runs over the tokens, down the rows of dgu and x.  No
-  // tokens: K = 0, and the gradients come out as zeros
-  const DenseIn in{(const uint8_t *)dgu, (const uint8_t *)p.x, nullptr, two_f * 2, p.ldx * 2,
+  // dx [T][d]: K runs over the 2f channels, down the rows of the two weight matrices
+  const DenseIn dx{(const uint8_t *)dgu, (const uint8_t *)p.w_gate, (const uint8_t *)p.w_up,
+                   two_f * 2, (int64_t)p.d * 2, p.T, p.d, two_f * 2, p.f};
+  const EpiPlain<E> to_dx{(E *)p.dx, nullptr, p.T, p.d, 1};
+  // dW [2f][d]: K runs over the tokens, down the rows of dgu and x.  No tokens:
+  // K = 0, no tile of dx, and the weights' gradients come out as zeros
+  const DenseIn dw{(const uint8_t *)dgu, (const uint8_t *)p.x, nullptr, two_f * 2, p.ldx * 2,
                    2 * p.f, p.d, (int64_t)p.T * 2, p.T};
-  const EpiPlain<E> epi{(E *)p.dw_gate, (E *)p.dw_up, p.f, p.d, 1};
-  return run_tiles<Op, kABColumns>(in, epi, stream);
+  const EpiPlain<E> to_dw{(E *)p.dw_gate, (E *)p.dw_up, p.f, p.d, 1};
+  return run_pair<Op>(dx, to_dx, dw, to_dw, stream);
 }
 
 }  // namespace
