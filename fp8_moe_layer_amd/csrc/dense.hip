@@ -99,14 +99,12 @@ moe_status moe_quantize_rows_i8(const void *x, int32_t x_type, int64_t ldx, int3
   const char *fn = "moe_quantize_rows_i8";
   if (x_type < MOE_T_F32 || x_type > MOE_T_F16)
     return fail_status(MOE_ERR_UNSUPPORTED, "%s: x_type=%d", fn, x_type);
-  if (rows < 0 || cols < 16 || cols % 16 || cols > MOE_MAX_I8_K)
-    return fail_status(MOE_ERR_SHAPE, "%s: rows=%d, cols=%d (cols: a multiple of 16 in [16, %d])",
-                       fn, rows, cols, MOE_MAX_I8_K);
+  if (cols < 16 || cols % 16 || cols > MOE_MAX_I8_K)
+    return fail_status(MOE_ERR_SHAPE, "%s: cols=%d must be a multiple of 16 in [16, %d]", fn, cols,
+                       MOE_MAX_I8_K);
   const int32_t size = type_bytes(x_type);
-  if (ldx < cols || ldx * size % 16 || ldx > ((int64_t)1 << 40))
-    return fail_status(MOE_ERR_SHAPE,
-                       "%s: row stride %lld must be at least cols=%d and a multiple of 16 bytes",
-                       fn, (long long)ldx, cols);
+  moe_status s = check_rows(fn, rows, ldx, cols, size);
+  if (s) return s;
   if (rows == 0) return ok_status();
   if (!x || !q || !scale) return fail_status(MOE_ERR_NULL, "%s: x, q and scale are required", fn);
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4))

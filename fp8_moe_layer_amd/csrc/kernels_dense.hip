@@ -224,7 +224,7 @@ hipError_t run_tile(const DenseIn &in, const Epi &epi, hipStream_t stream) {
   const int64_t tm = ((int64_t)in.M + BM - 1) / BM;
   const int64_t tn = ((int64_t)in.N + S::kTileChannels - 1) / S::kTileChannels;
   if (tm * tn == 0) return hipSuccess;
-  if (tm * tn > 0x7fffffff) return hipErrorInvalidValue;
+  if (tm * tn * S::kThreads >= (int64_t)1 << 32) return hipErrorInvalidValue;  // HIP's grid limit
   tile_kernel<Op, BM, BN, TM, TN, ST, KG, F, Epi>
       <<<(unsigned)(tm * tn), S::kThreads, 0, stream>>>(in, epi, (int)tm, (int)tn);
   return hipGetLastError();
@@ -401,7 +401,7 @@ hipError_t run_pair_tile(const DenseIn &in1, const Epi &epi1, const DenseIn &in2
   const int2 t1 = make_int2((in1.M + BM - 1) / BM, (in1.N + BN - 1) / BN);
   const int2 t2 = make_int2((in2.M + BM - 1) / BM, (in2.N + BN - 1) / BN);
   const int64_t n = (int64_t)t1.x * t1.y + (int64_t)t2.x * t2.y;
-  if (n > 0x7fffffff) return hipErrorInvalidValue;
+  if (n * S::kThreads >= (int64_t)1 << 32) return hipErrorInvalidValue;  // HIP's grid limit
   pair_kernel<Op, BM, BN, TM, TN, ST, KG, Epi><<<(unsigned)n, S::kThreads, 0, stream>>>(
       in1, epi1, t1, in2, epi2, t2, second_first);
   return hipGetLastError();

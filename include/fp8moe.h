@@ -336,7 +336,7 @@ enum { MOE_T_F32 = 0, MOE_T_BF16 = 1, MOE_T_F16 = 2 }; /* element types */
  *   q = x * r rounded once, to nearest, ties to even (|q| <= 127),
  * so x ~= q * scale within scale * (1/2 + 2^-15).
  * q [rows][cols] contiguous, scale [rows].  cols: a multiple of 16 up to
- * MOE_MAX_I8_K; rows: any. */
+ * MOE_MAX_I8_K; rows: any up to MOE_MAX_TOKENS. */
 moe_status moe_quantize_rows_i8(const void *x, int32_t x_type, int64_t ldx, int32_t rows,
                                 int32_t cols, int8_t *q, float *scale, void *stream);
 

@@ -38,7 +38,8 @@ def quantize(x=P[0], kind=F32, ldx=64, rows=4, cols=64, q=P[1], scale=P[2]):
     (dict(x=None), ERR_NULL), (dict(q=None), ERR_NULL), (dict(scale=None), ERR_NULL),
     (dict(rows=-1), ERR_SHAPE), (dict(cols=0), ERR_SHAPE), (dict(cols=40), ERR_SHAPE),
     (dict(cols=65552, ldx=65552), ERR_SHAPE), (dict(ldx=63), ERR_SHAPE), (dict(ldx=66), ERR_SHAPE),
-    (dict(kind=BF16, ldx=68), ERR_SHAPE), (dict(ldx=1 << 41), ERR_SHAPE),
+    (dict(kind=BF16, ldx=68), ERR_SHAPE), (dict(ldx=(1 << 20) + 4), ERR_SHAPE),
+    (dict(rows=(1 << 21) + 1), ERR_SHAPE),
     (dict(kind=3), ERR_UNSUPPORTED), (dict(kind=-1), ERR_UNSUPPORTED),
     (dict(x=P[0] + 8), ERR_ALIGN), (dict(q=P[1] + 4), ERR_ALIGN), (dict(scale=P[2] + 2), ERR_ALIGN),
     (dict(q=P[0] + 1008), ERR_SHAPE), (dict(scale=P[1] + 252), ERR_SHAPE),

@@ -136,7 +136,9 @@ MATMUL = [(1, 16, 1), (1, 64, 16), (2, 48, 3), (15, 112, 31), (16, 128, 64), (17
           (33, 256, 100), (48, 1408, 257), (64, 192, 200), (65, 2048, 128), (100, 14336, 130),
           (127, 320, 511), (129, 640, 1025), (255, 1408, 96), (256, 4096, 512), (257, 208, 769),
           (333, 1408, 2051), (1000, 96, 1000), (1, 14336, 4096), (7, 4096, 2048), (2100, 1024, 1536),
-          (4100, 512, 2304)]
+          (4100, 512, 2304), (9, 65536, 33), (4, 80, 70000), (16, 272, 9000), (24, 528, 8200),
+          (8, 4096, 4111), (32, 1040, 16400), (8200, 128, 4100), (2000, 768, 300), (1000, 800, 4000), (2000, 800, 4000), (3256, 16, 1163),
+          (130, 1424, 4111)]
 
 
 @pytest.mark.parametrize("T,K,N", MATMUL)
@@ -194,7 +196,8 @@ def silu_ref(g, u, eg, eu):
                                    (32, 320, 128), (63, 2048, 768), (65, 64, 1408), (130, 448, 320),
                                    (256, 256, 512), (300, 1408, 192), (700, 512, 1088),
                                    (1, 4096, 14336), (2050, 256, 2048), (5, 16384, 64),
-                                   (130, 64, 16384)])
+                                   (130, 64, 16384), (8, 2048, 4160), (16, 4096, 4160),
+                                   (31, 448, 8256), (1030, 192, 4096), (260, 832, 3456)])
 def test_gated_i8(T, d, f):
     g = gen(T + d + f)
     kind = FLOATS[(T + f // 64) % 3]
@@ -226,7 +229,14 @@ def gated_ref(x, wg, wu):
 
 GATED = [(1, 64, 64), (2, 256, 192), (15, 128, 512), (16, 2048, 768), (17, 192, 64), (33, 64, 128),
          (64, 320, 256), (65, 1408, 192), (128, 256, 512), (129, 448, 320), (257, 192, 1408),
-         (300, 2048, 64), (777, 512, 832), (2050, 256, 2048)]
+         (300, 2048, 64), (777, 512, 832), (2050, 256, 2048), (8, 512, 4160), (12, 192, 8256),
+         (2500, 128, 192), (40, 1024, 2304), (1500, 1024, 320), (1100, 640, 2304), (5000, 64, 64), (260, 832, 3456)]
+
+# and, for the gradients, sizes at which each tile is taken, by dx and dW alone and together
+GRADIENTS = GATED + [(1044, 3136, 64), (1247, 640, 1088), (45, 2240, 896), (37, 1600, 1920),
+                     (34, 3136, 1408), (1987, 832, 576), (4096, 1216, 64), (3215, 2368, 64),
+                     (268, 2880, 64), (35, 3264, 320), (586, 2752, 64), (412, 3712, 320),
+                     (626, 3712, 256), (1008, 3968, 576), (1081, 4096, 512)]
 
 
 @pytest.mark.parametrize("dtype", F16S)
@@ -283,7 +293,7 @@ def backward_ref(dh, x, wg, wu, gate, up, dtype):
 
 
 @pytest.mark.parametrize("dtype", F16S)
-@pytest.mark.parametrize("T,d,f", GATED)
+@pytest.mark.parametrize("T,d,f", GRADIENTS)
 def test_gated_backward(T, d, f, dtype):
     g = gen(T + d + f + 1)
     x = strided(normal(g, (T, d), 1.0, dtype), 8 * (T % 3))
@@ -315,6 +325,66 @@ def test_no_tokens():
     q, s = lib().quantize_rows_i8(z(0, 64))
     assert lib().matmul_i8(q, s, torch.zeros((5, 64), dtype=torch.int8, device=dev()),
                            torch.ones(5, device=dev())).shape == (0, 5)
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^32 bytes (and 2^31 values) in every array of T rows: the
+    last tokens' rows, and a few channels of the weights' gradients."""
+    T, d, f, last = 150_016, 64, 14_400, 300
+    dtype = torch.bfloat16
+    assert T * f > 2 ** 31
+    g = gen(9)
+    x = normal(g, (T, d), 1.0, dtype)
+    wg, wu = normal(g, (f, d), 0.125, dtype), normal(g, (f, d), 0.125, dtype)
+    h, gate, up = lib().gated_ffn(x, wg, wu, save=True)
+    gr, ur, eg, eu = gated_ref(x[-last:], wg, wu)
+    within(gate[-last:], gr, eg, "gate")
+    ref, tol = silu_ref(gr, ur, eg, eu)
+    within(h[-last:], ref, tol, "h")
+    # h stands in for its own gradient
+    dx, dwg, dwu = lib().gated_ffn_backward(h, x, wg, wu, gate, up)
+    (rx, _, _), (tx, _, _) = backward_ref(h[-last:], x[-last:], wg, wu, gate[-last:], up[-last:], dtype)
+    within(dx[-last:], rx, tx, "dx")
+    c = slice(f - 8, f)
+    (_, rg, ru), (_, tg, tu) = backward_ref(h[:, c].contiguous(), x, wg[c], wu[c], gate[:, c].contiguous(),
+                                            up[:, c].contiguous(), dtype)
+    within(dwg[c], rg, tg, "dw_gate")
+    within(dwu[c], ru, tu, "dw_up")
+    del gate, up, dx, dwg, dwu
+    q, s = lib().quantize_rows_i8(h)
+    rq, rs = quantize_ref(h[-last:])
+    np.testing.assert_array_equal(q[-last:].cpu().numpy(), rq)
+    w8, s8 = lib().quantize_rows_i8(wg)
+    xq, sx = lib().quantize_rows_i8(x)
+    y = lib().matmul_i8(xq, sx, w8, s8, out_dtype=dtype)
+    ref, tol = matmul_ref(xq[-last:], sx[-last:], w8, s8, None)
+    within(y[-last:], ref, tol, "y")
+    down = codes(g, (3, f))
+    sd = scales(g, 3)
+    z = lib().matmul_i8(q, s, down, sd)
+    ref, tol = matmul_ref(q[-last:], s[-last:], down, sd, None)
+    within(z[-last:], ref, tol, "z")
+
+
+@pytest.mark.parametrize("T", [3, 20, 70, 600])
+def test_rows_do_not_touch_each_other(T):
+    """A token of infinities and NaN changes no other token's outputs."""
+    g = gen(T)
+    d, f = 256, 320
+    x = normal(g, (T, d), 1.0, torch.float16)
+    wg, wu = normal(g, (f, d), 1 / 16, torch.float16), normal(g, (f, d), 1 / 16, torch.float16)
+    want = lib().gated_ffn(x, wg, wu)
+    bad = x.clone()
+    bad[T // 2, ::3], bad[T // 2, 1::3] = torch.inf, torch.nan
+    got = lib().gated_ffn(bad, wg, wu)
+    keep = torch.arange(T, device=dev()) != T // 2
+    assert torch.equal(got[keep], want[keep])
+    xq, sx = lib().quantize_rows_i8(x)
+    w8, s8 = lib().quantize_rows_i8(wg)
+    y = lib().matmul_i8(xq, sx, w8, s8)
+    sx2 = sx.clone()
+    sx2[T // 2] = torch.nan
+    assert torch.equal(lib().matmul_i8(xq, sx2, w8, s8)[keep], y[keep])
 
 
 # ------------------------------------------------------------------ together
