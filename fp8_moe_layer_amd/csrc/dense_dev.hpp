@@ -32,6 +32,7 @@ namespace fp8moe {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
 
 struct OpI8 {
   typedef v4i Acc;
@@ -300,8 +301,7 @@ struct ChannelColumns : Columns<ROWS, WN, W> {
   __device__ __forceinline__ v4i read(LdsPtr lds, int half, int, int j) const {
     return C::read(lds, half, j);
   }
-  static constexpr bool kRun = false;
-  static __device__ __forceinline__ int channel(int lane, int j) { return j * 16 + (lane >> 4) * 4; }
+  static constexpr bool kRun = false;  // sub-tile j: channels j*16 + (l/16)*4 ..
 };
 
 // ---------------------------------------------------------------- the tile
@@ -339,7 +339,8 @@ struct TileShape {
 
 // One output tile.  lds: kLdsBytes bytes.  acc[b][m][j]: matrix b,
 // token sub-tile m, channel sub-tile j; element i of lane l is token
-// m*16 + l%16, channel B::channel(l, j) + i of the wave's block.
+// m*16 + l%16, channel (l/16)*4*NJ + j*4 + i of the wave's block (B transposed:
+// j*16 + (l/16)*4 + i).
 //
 // The K step's two halves are software-pipelined: the matrix instructions of
 // one half run while the wave reads the other half's operands from LDS into a

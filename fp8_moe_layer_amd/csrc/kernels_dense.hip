@@ -187,18 +187,23 @@ struct EpiPlain {
 
 // ---------------------------------------------------------------- product kernel
 // The tile's sums through the epilogue.  A lane's sub-tiles are one run of
-// 4*NJ consecutive channels, or (B transposed) NJ runs of four.
+// 4*NJ consecutive channels; with B transposed they are runs of four, 16
+// apart, and two lanes (16 apart) trade halves of two sub-tiles, so that each
+// has eight consecutive channels of one of them.  A token's channels are
+// stored one after the other: with runs of four, and all tokens of a sub-tile
+// before the next one, lines left L2 in parts and memory was written 2.0 times
+// (dW, 235 MB) and 2.5 times (dx), now once (backward of 512x4096x4096 125 ->
+// 102 us, 256x14336x4096 278 -> 211, 4096x4096x14336 1734 -> 1666).
 template <class S, class Op, class Epi>
 __device__ __forceinline__ void store_tile(const DenseIn &in, const Epi &epi,
                                            typename Op::Acc (&acc)[S::NB][S::MS][S::NJ], int t0,
                                            int n0, int wm, int wn) {
   const int lane = threadIdx.x & 63;
-  constexpr bool kRun = S::B::kRun;
-  constexpr int kCount = kRun ? 4 * S::NJ : 4;
-#pragma unroll
-  for (int j0 = 0; j0 < (kRun ? 1 : S::NJ); ++j0) {
-    const int ch = n0 + wn * S::CH + S::B::channel(lane, j0);
-    if (ch >= in.N) continue;
+  const int c0 = n0 + wn * S::CH;
+  if constexpr (S::B::kRun) {
+    constexpr int kCount = 4 * S::NJ;
+    const int ch = c0 + S::B::channel(lane, 0);
+    if (ch >= in.N) return;
     typename Epi::template Chan<kCount> chan;
     epi.load(chan, ch);
 #pragma unroll
@@ -209,8 +214,32 @@ __device__ __forceinline__ void store_tile(const DenseIn &in, const Epi &epi,
 #pragma unroll
       for (int b = 0; b < S::NB; ++b)
 #pragma unroll
-        for (int i = 0; i < kCount; ++i) a[b][i] = acc[b][m][j0 + i / 4][i % 4];
+        for (int i = 0; i < kCount; ++i) a[b][i] = acc[b][m][i / 4][i % 4];
       epi.store(chan, t, ch, a);
+    }
+  } else {
+    const typename Epi::template Chan<8> chan{};
+    const int row = lane >> 4;  // of sixteen lanes
+    static_assert(S::NJ % 2 == 0, "sub-tiles in pairs");
+#pragma unroll
+    for (int m = 0; m < S::MS; ++m) {
+      const int t = t0 + wm * S::WM + m * 16 + (lane & 15);
+#pragma unroll
+      for (int j = 0; j < S::NJ; j += 2) {
+        // rows 0, 2 take sub-tile j, rows 1, 3 sub-tile j+1: their own four
+        // channels and the neighbour row's
+        typename Op::Sum a[1][8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const v2u x = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[0][m][j][i]),
+                                                         __float_as_uint(acc[0][m][j + 1][i]), false,
+                                                         false);
+          a[0][i] = __uint_as_float(x[0]);
+          a[0][4 + i] = __uint_as_float(x[1]);
+        }
+        const int ch = c0 + (j + (row & 1)) * 16 + (row >> 1) * 8;
+        if (t < in.M && ch < in.N) epi.store(chan, t, ch, a);
+      }
     }
   }
 }
