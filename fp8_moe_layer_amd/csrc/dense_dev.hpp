@@ -66,7 +66,8 @@ constexpr int kStepBytes = 128;  // bytes of a row per K step
 // The gradients' products need operands whose K runs down the rows (16-bit
 // types only): a transposed A is [K][M] and a transposed B [K][N], with lda and
 // ldb bytes from one k to the next, M and N multiples of 64.  A transposed B
-// may be two matrices, one below the other: b0 has the first split_k rows of K.
+// may be two matrices, one below the other: b0 has the first split_k rows of K
+// (a multiple of 64, or all of them).
 struct DenseIn {
   const uint8_t *a, *b0, *b1;
   int64_t lda, ldb;  // bytes from row to row
@@ -123,9 +124,9 @@ __device__ __forceinline__ v2i lds_read8_tr(LdsPtr p) {
 }
 
 // A row that does not exist, or a piece behind the end of K: an offset behind
-// every descriptor's end (kMaxTileBytes), however many K steps are added.
+// every descriptor's end (2^30, 256 rows of the longest row stride, 2^22),
+// however many K steps are added.
 constexpr uint32_t kPastEnd = 0x80000000u;
-constexpr int64_t kMaxTileBytes = (int64_t)1 << 30;  // 256 rows of the longest row stride
 
 // ---------------------------------------------------------------- tile order
 // Workgroups go to the eight XCDs in turn; each XCD gets a contiguous run of
@@ -292,7 +293,7 @@ struct ChannelColumns : Columns<ROWS, WN, W> {
   int n0, cols;
   __device__ __forceinline__ ChannelColumns(const DenseIn &in, int n0_, int64_t, int wave, int wn, int lane)
       : C(in.ldb, in.N - n0_, wave, wn, lane), n0(n0_), cols(in.N - n0_) {}
-  // split_k is a multiple of 64: a step lies in one of the two matrices
+  // split_k is a multiple of 64, or all of K: a step lies in one of the two matrices
   __device__ __forceinline__ void begin(const DenseIn &in, int64_t k, int) {
     const bool first = k < in.split_k;
     C::begin((first ? in.b0 : in.b1) + (int64_t)n0 * 2, in.ldb, cols, first ? k : k - in.split_k,
@@ -309,9 +310,9 @@ enum Form { kPlainForm, kGatedForm, kBColumns, kABColumns };  // which operands,
 
 // BM tokens by BN rows of B, TM x TN waves; gated: half of each wave's B rows
 // come from b0 and half from b1 (the same channels).  LDS is a ring of ST K
-// steps.  KG: groups of TM x TN waves that share the tile, each with its own LDS and
-// its own part of K; the first one adds the others' sums to its own, in order,
-// at the end.
+// steps.  KG: groups of TM x TN waves that share the tile, each with its own
+// LDS and its own part of K; the first one adds the others' sums to its own, in
+// order, at the end.
 template <int BM, int BN, int TM, int TN, int ST, int KG, Form F>
 struct TileShape {
   static constexpr int kWaves = TM * TN;                 // of a K group
@@ -325,7 +326,7 @@ struct TileShape {
   static constexpr int kTileChannels = BN / NB;          // channels of a workgroup
   static constexpr int kUnitA = BM * kStepBytes;
   static constexpr int kStage = (BM + BN) * kStepBytes;
-  static constexpr int kRing = ST * kStage;               // of a K group
+  static constexpr int kRing = ST * kStage;              // of a K group
   static constexpr int kLdsBytes = KG * kRing;
   typedef typename std::conditional<F == kABColumns, TokenColumns<BM, WM, kWaves>,
                                     TokenRows<BM, WM, kWaves>>::type A;
@@ -349,6 +350,15 @@ struct TileShape {
 // fetched among the second half's products) and step k+1 has landed.  Two or
 // more waves to a SIMD fill each other's waits; the waves that issue matrix
 // instructions go first (setprio: 1-2 %).
+//
+// What bounds it: for large products (256x256: 8192 x 4096 x 2*14336 bf16 1.39
+// PFLOP/s, 8192 x 14336 x 4096 int8 2.65 POP/s) the matrix instructions run
+// 66-73 % of the time at 1.5-1.9 GHz; alone, on the same kind of values, they
+// reach 2.0 PFLOP/s at the card's power limit, and a wave tile of 128x64 reads
+// from LDS, together with the fills, as many cycles as it multiplies.  For
+// small ones, with one tile or less to a compute unit, LDS and the loads'
+// latency (0.55 us and more): hence the rings of three or four steps and the
+// two K groups of the small tiles.
 template <class Op, int BM, int BN, int TM, int TN, int ST, int KG, Form F>
 __device__ __forceinline__ void
 tile_product(const DenseIn &in, int t0, int n0, uint8_t *lds,
@@ -496,7 +506,10 @@ tile_product(const DenseIn &in, int t0, int n0, uint8_t *lds,
 // so that nothing but the wave's own load counter orders the stream, which
 // runs on over the groups' borders.  At a group's end the waves' partial sums
 // meet in LDS, where one more wave, which fetches nothing, adds them in wave
-// order (the same bits every run) and stores while the others stream on.
+// order (the same bits every run) and stores while the others stream on.  (When
+// the fetching waves took turns at that, each group's scales, loaded behind the
+// loads in flight, stalled them all: int8 gated 4096 -> 2 x 14336, weights from
+// HBM, one token 29 us, now 22 us or 5.3 TB/s; 16 tokens 31 and 25 us.)
 template <int XP, int NS, int W, int R>
 struct StreamShape {
   static constexpr int kThreads = (W + 1) * kWave;

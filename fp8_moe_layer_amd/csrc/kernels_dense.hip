@@ -628,7 +628,8 @@ hipError_t quantize_i8_as(const T *x, int64_t ldx, int rows, int cols, int8_t *q
 // dg = dh * u * s * (1 + g * (1 - s)), du = dh * g * s with s = sigmoid(g), in
 // fp32 from the kept g and u, rounded once to the operands' type: the two
 // products that follow take 16-bit operands.  dgu [T][2f]: a token's dg, then
-// its du.  Eight channels a thread; f is a multiple of 64.
+// its du.  Eight channels a thread; f is a multiple of 64.  Bound by memory: 4096
+// x 14336 (822 MB) 172-187 us, 4.4-4.8 TB/s; a copy reaches 4.9.
 template <class T>
 __global__ __launch_bounds__(256) void gate_grad_kernel(const T *__restrict__ dh, int64_t lddh,
                                                         const float *__restrict__ gate,
