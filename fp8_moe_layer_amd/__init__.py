@@ -83,11 +83,14 @@ _k_tiers = _sig("moe_k_tiers", _i32, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp)
 _i64 = C.c_int64
 _quantize_rows_i8 = _sig("moe_quantize_rows_i8", _i32, _vp, _i32, _i64, _i32, _i32, _vp, _vp, _vp)
 _matmul_i8 = _sig("moe_matmul_i8", _i32, _vp, _i64, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp,
-                  _vp)
+                  _vp, C.c_size_t, _vp)
+_matmul_i8_ws = _sig("moe_matmul_i8_workspace_bytes", C.c_size_t, _i32, _i32, _i32)
 _gated_ffn_i8 = _sig("moe_gated_ffn_i8", _i32, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32,
-                     _i32, _vp, _vp)
+                     _i32, _vp, _vp, C.c_size_t, _vp)
+_gated_ffn_i8_ws = _sig("moe_gated_ffn_i8_workspace_bytes", C.c_size_t, _i32, _i32, _i32)
 _gated_ffn = _sig("moe_gated_ffn", _i32, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp,
-                  _vp)
+                  _vp, C.c_size_t, _vp)
+_gated_ffn_ws = _sig("moe_gated_ffn_workspace_bytes", C.c_size_t, _i32, _i32, _i32)
 _gated_bwd_ws = _sig("moe_gated_ffn_backward_workspace_bytes", C.c_size_t, _i32, _i32, _i32)
 _gated_bwd = _sig("moe_gated_ffn_backward", _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i32,
                   _i32, _i32, _i32, _vp, _vp, _vp, _vp, C.c_size_t, _vp)
@@ -429,6 +432,17 @@ class _Call:
         with _on(self.alloc):
             return torch.empty(shape, dtype=dtype, device=self.dev)
 
+    def workspace(self, size, T: int, inner: int, outputs: int):
+        """(tensor, address, bytes) of the workspace that the call can use:
+        size(T, inner, outputs) bytes, asked for only where a product is small
+        enough to be cut along its sum."""
+        if T > 16 and ((T + 63) >> 6) * ((outputs + 63) >> 6) <= 128:
+            n = size(T, inner, outputs)
+            if n:
+                ws = self.empty((n,), torch.uint8)
+                return ws, ws.data_ptr(), n
+        return None, None, 0
+
     def run(self, fn, *args):
         if torch.cuda.current_device() == self.dev.index:
             status = fn(*args, self.stream)
@@ -474,10 +488,11 @@ def matmul_i8(xq: torch.Tensor, sx: torch.Tensor, wq: torch.Tensor, sw: torch.Te
     y = c.empty((T, N), out_dtype) if out is None else out
     kind = _type(y.dtype)
     xp, ldx = c.rows(xq, (T, K), torch.int8, "xq")
+    ws, at, size = c.workspace(_matmul_i8_ws, T, K, N)
     c.run(_matmul_i8, xp, ldx, c.ptr(sx, (T,), torch.float32, "sx"),
           c.ptr(wq, (N, K), torch.int8, "wq"), c.ptr(sw, (N,), torch.float32, "sw"),
           None if bias is None else c.ptr(bias, (N,), torch.float32, "bias"), T, K, N, kind,
-          c.ptr(y, (T, N), y.dtype, "out"))
+          c.ptr(y, (T, N), y.dtype, "out"), at, size)
     return y
 
 
@@ -492,11 +507,12 @@ def gated_ffn_i8(xq: torch.Tensor, sx: torch.Tensor, w_gate: torch.Tensor, s_gat
     h = c.empty((T, f), out_dtype) if out is None else out
     kind = _type(h.dtype)
     xp, ldx = c.rows(xq, (T, d), torch.int8, "xq")
+    ws, at, size = c.workspace(_gated_ffn_i8_ws, T, d, f)
     c.run(_gated_ffn_i8, xp, ldx, c.ptr(sx, (T,), torch.float32, "sx"),
           c.ptr(w_gate, (f, d), torch.int8, "w_gate"),
           c.ptr(s_gate, (f,), torch.float32, "s_gate"), c.ptr(w_up, (f, d), torch.int8, "w_up"),
           c.ptr(s_up, (f,), torch.float32, "s_up"), T, d, f, kind,
-          c.ptr(h, (T, f), h.dtype, "out"))
+          c.ptr(h, (T, f), h.dtype, "out"), at, size)
     return h
 
 
@@ -525,9 +541,10 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
     h = c.empty((T, f), x.dtype) if out is None else out
     gate, up = (c.empty((T, f), torch.float32), c.empty((T, f), torch.float32)) if save else (None, None)
     xp, ldx = c.rows(x, (T, d), x.dtype, "x")
+    ws, at, size = c.workspace(_gated_ffn_ws, T, d, f)
     c.run(_gated_ffn, xp, ldx, c.ptr(w_gate, (f, d), x.dtype, "w_gate"),
           c.ptr(w_up, (f, d), x.dtype, "w_up"), kind, T, d, f, c.ptr(h, (T, f), x.dtype, "out"),
-          None if gate is None else gate.data_ptr(), None if up is None else up.data_ptr())
+          None if gate is None else gate.data_ptr(), None if up is None else up.data_ptr(), at, size)
     return (h, gate, up) if save else h
 
 

@@ -78,6 +78,13 @@ moe_status check_rows(const char *fn, int32_t T, int64_t ld, int32_t cols, int32
   return MOE_OK;
 }
 
+moe_status check_product_dims(const char *fn, int32_t K, int32_t N) {
+  if (K < 16 || K % 16 || K > MOE_MAX_I8_K || N < 1 || N > MOE_MAX_TOKENS)
+    return fail_status(MOE_ERR_SHAPE, "%s: K=%d (a multiple of 16 in [16, %d]), N=%d (in [1, %d])",
+                       fn, K, MOE_MAX_I8_K, N, MOE_MAX_TOKENS);
+  return MOE_OK;
+}
+
 moe_status check_gated_dims(const char *fn, int32_t d, int32_t f) {
   if (d < 64 || d % 64 || d > MOE_MAX_HIDDEN)
     return fail_status(MOE_ERR_SHAPE, "%s: d=%d must be a multiple of 64 in [64, %d]", fn, d,
@@ -85,6 +92,16 @@ moe_status check_gated_dims(const char *fn, int32_t d, int32_t f) {
   if (f < 64 || f % 64 || f > MOE_MAX_FFN)
     return fail_status(MOE_ERR_SHAPE, "%s: f=%d must be a multiple of 64 in [64, %d]", fn, f,
                        MOE_MAX_FFN);
+  return MOE_OK;
+}
+
+// An optional workspace: NULL, or at least `need` bytes.
+moe_status check_workspace(const char *fn, const void *workspace, size_t bytes, size_t need) {
+  if (!workspace) return MOE_OK;
+  if (bytes < need)
+    return fail_status(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn, bytes, need);
+  if (!aligned(workspace, 256))
+    return fail_status(MOE_ERR_ALIGN, "%s: workspace must be 256-byte aligned", fn);
   return MOE_OK;
 }
 
@@ -117,32 +134,33 @@ moe_status moe_quantize_rows_i8(const void *x, int32_t x_type, int64_t ldx, int3
 
 moe_status moe_matmul_i8(const int8_t *xq, int64_t ldx, const float *sx, const int8_t *wq,
                          const float *sw, const float *bias, int32_t T, int32_t K, int32_t N,
-                         int32_t y_type, void *y, void *stream) {
+                         int32_t y_type, void *y, void *workspace, size_t workspace_bytes,
+                         void *stream) {
   const char *fn = "moe_matmul_i8";
   if (y_type < MOE_T_F32 || y_type > MOE_T_F16)
     return fail_status(MOE_ERR_UNSUPPORTED, "%s: y_type=%d", fn, y_type);
-  if (K < 16 || K % 16 || K > MOE_MAX_I8_K || N < 1 || N > MOE_MAX_TOKENS)
-    return fail_status(MOE_ERR_SHAPE, "%s: K=%d (a multiple of 16 in [16, %d]), N=%d (in [1, %d])",
-                       fn, K, MOE_MAX_I8_K, N, MOE_MAX_TOKENS);
-  moe_status s = check_rows(fn, T, ldx, K, 1);
-  if (s) return s;
+  moe_status s = check_product_dims(fn, K, N);
+  if (s || (s = check_rows(fn, T, ldx, K, 1))) return s;
   if (T == 0) return ok_status();
   if (!xq || !sx || !wq || !sw || !y)
     return fail_status(MOE_ERR_NULL, "%s: xq, sx, wq, sw and y are required", fn);
   if (!all_aligned({xq, wq, y}, 16) || !all_aligned({sx, sw, bias}, 4))
     return fail_status(MOE_ERR_ALIGN, "%s: xq, wq and y must be 16-byte, scales and bias 4-byte "
                        "aligned", fn);
-  const Span out[] = {{y, (int64_t)T * N * type_bytes(y_type)}};
+  const size_t need = matmul_i8_workspace(T, K, N);
+  if ((s = check_workspace(fn, workspace, workspace_bytes, need))) return s;
+  const Span out[] = {{y, (int64_t)T * N * type_bytes(y_type)}, {workspace, (int64_t)need}};
   const Span in[] = {{xq, span_rows(T, ldx, K, 1)}, {sx, (int64_t)T * 4}, {wq, (int64_t)N * K},
                      {sw, (int64_t)N * 4},          {bias, (int64_t)N * 4}};
-  if (clash(out, in)) return fail_status(MOE_ERR_SHAPE, "%s: y overlaps an input", fn);
-  const I8Product p{xq, ldx, sx, wq, sw, bias, T, K, N, y_type, y};
+  if (clash(out, in)) return fail_status(MOE_ERR_SHAPE, "%s: y or the workspace overlaps an input or the other", fn);
+  const I8Product p{xq, ldx, sx, wq, sw, bias, T, K, N, y_type, y, workspace};
   return finish(launch_matmul_i8(p, as_stream(stream)), fn);
 }
 
 moe_status moe_gated_ffn_i8(const int8_t *xq, int64_t ldx, const float *sx, const int8_t *w_gate,
                             const float *s_gate, const int8_t *w_up, const float *s_up, int32_t T,
-                            int32_t d, int32_t f, int32_t h_type, void *h, void *stream) {
+                            int32_t d, int32_t f, int32_t h_type, void *h, void *workspace,
+                            size_t workspace_bytes, void *stream) {
   const char *fn = "moe_gated_ffn_i8";
   if (h_type < MOE_T_F32 || h_type > MOE_T_F16)
     return fail_status(MOE_ERR_UNSUPPORTED, "%s: h_type=%d", fn, h_type);
@@ -155,18 +173,20 @@ moe_status moe_gated_ffn_i8(const int8_t *xq, int64_t ldx, const float *sx, cons
   if (!all_aligned({xq, w_gate, w_up, h}, 16) || !all_aligned({sx, s_gate, s_up}, 4))
     return fail_status(MOE_ERR_ALIGN, "%s: xq, w_gate, w_up and h must be 16-byte, scales 4-byte "
                        "aligned", fn);
+  const size_t need = gated_i8_workspace(T, d, f);
+  if ((s = check_workspace(fn, workspace, workspace_bytes, need))) return s;
   const int64_t wb = (int64_t)f * d;
-  const Span out[] = {{h, (int64_t)T * f * type_bytes(h_type)}};
+  const Span out[] = {{h, (int64_t)T * f * type_bytes(h_type)}, {workspace, (int64_t)need}};
   const Span in[] = {{xq, span_rows(T, ldx, d, 1)}, {sx, (int64_t)T * 4}, {w_gate, wb}, {w_up, wb},
                      {s_gate, (int64_t)f * 4},      {s_up, (int64_t)f * 4}};
-  if (clash(out, in)) return fail_status(MOE_ERR_SHAPE, "%s: h overlaps an input", fn);
-  const I8Gated p{xq, ldx, sx, w_gate, w_up, s_gate, s_up, T, d, f, h_type, h};
+  if (clash(out, in)) return fail_status(MOE_ERR_SHAPE, "%s: h or the workspace overlaps an input or the other", fn);
+  const I8Gated p{xq, ldx, sx, w_gate, w_up, s_gate, s_up, T, d, f, h_type, h, workspace};
   return finish(launch_gated_i8(p, as_stream(stream)), fn);
 }
 
 moe_status moe_gated_ffn(const void *x, int64_t ldx, const void *w_gate, const void *w_up,
                          int32_t type, int32_t T, int32_t d, int32_t f, void *h, float *gate,
-                         float *up, void *stream) {
+                         float *up, void *workspace, size_t workspace_bytes, void *stream) {
   const char *fn = "moe_gated_ffn";
   if (type != MOE_T_BF16 && type != MOE_T_F16)
     return fail_status(MOE_ERR_UNSUPPORTED, "%s: type=%d (MOE_T_BF16 or MOE_T_F16)", fn, type);
@@ -180,12 +200,35 @@ moe_status moe_gated_ffn(const void *x, int64_t ldx, const void *w_gate, const v
   if (!all_aligned({x, w_gate, w_up, h, gate, up}, 16))
     return fail_status(MOE_ERR_ALIGN, "%s: every array must be 16-byte aligned", fn);
   const int64_t wb = (int64_t)f * d * 2, hb = (int64_t)T * f * 2;
-  const Span out[] = {{h, hb}, {gate, 2 * hb}, {up, 2 * hb}};
+  const size_t need = gated_workspace(T, d, f);
+  if ((s = check_workspace(fn, workspace, workspace_bytes, need))) return s;
+  const Span out[] = {{h, hb}, {gate, 2 * hb}, {up, 2 * hb}, {workspace, (int64_t)need}};
   const Span in[] = {{x, span_rows(T, ldx, d, 2)}, {w_gate, wb}, {w_up, wb}};
   if (clash(out, in))
     return fail_status(MOE_ERR_SHAPE, "%s: an output overlaps an input or another output", fn);
-  const Gated16 p{x, ldx, w_gate, w_up, T, d, f, type, h, gate, up};
+  const Gated16 p{x, ldx, w_gate, w_up, T, d, f, type, h, gate, up, workspace};
   return finish(launch_gated(p, as_stream(stream)), fn);
+}
+
+size_t moe_matmul_i8_workspace_bytes(int32_t T, int32_t K, int32_t N) {
+  const char *fn = "moe_matmul_i8_workspace_bytes";
+  if (check_product_dims(fn, K, N) || check_rows(fn, T, K, K, 1)) return 0;
+  (void)ok_status();
+  return matmul_i8_workspace(T, K, N);
+}
+
+size_t moe_gated_ffn_i8_workspace_bytes(int32_t T, int32_t d, int32_t f) {
+  const char *fn = "moe_gated_ffn_i8_workspace_bytes";
+  if (check_gated_dims(fn, d, f) || check_rows(fn, T, d, d, 1)) return 0;
+  (void)ok_status();
+  return gated_i8_workspace(T, d, f);
+}
+
+size_t moe_gated_ffn_workspace_bytes(int32_t T, int32_t d, int32_t f) {
+  const char *fn = "moe_gated_ffn_workspace_bytes";
+  if (check_gated_dims(fn, d, f) || check_rows(fn, T, d, d, 2)) return 0;
+  (void)ok_status();
+  return gated_workspace(T, d, f);
 }
 
 size_t moe_gated_ffn_backward_workspace_bytes(int32_t T, int32_t d, int32_t f) {

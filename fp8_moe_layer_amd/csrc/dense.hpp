@@ -26,7 +26,9 @@ struct I8Product {
   const float *sw, *bias;
   int32_t T, K, N, out_type;
   void *y;
+  void *workspace;  // matmul_i8_workspace bytes or NULL
 };
+size_t matmul_i8_workspace(int32_t T, int32_t K, int32_t N);
 hipError_t launch_matmul_i8(const I8Product &p, hipStream_t stream);
 
 // h = SiLU(g) * u from int8 operands.
@@ -38,7 +40,9 @@ struct I8Gated {
   const float *s_gate, *s_up;
   int32_t T, d, f, out_type;
   void *h;
+  void *workspace;  // gated_i8_workspace bytes or NULL
 };
+size_t gated_i8_workspace(int32_t T, int32_t d, int32_t f);
 hipError_t launch_gated_i8(const I8Gated &p, hipStream_t stream);
 
 // h = SiLU(x Wg^T) * (x Wu^T) in 16-bit types; gate, up: the two products
@@ -50,7 +54,9 @@ struct Gated16 {
   int32_t T, d, f, type;
   void *h;
   float *gate, *up;
+  void *workspace;  // gated_workspace bytes or NULL
 };
+size_t gated_workspace(int32_t T, int32_t d, int32_t f);
 hipError_t launch_gated(const Gated16 &p, hipStream_t stream);
 
 struct Gated16Backward {

@@ -341,7 +341,8 @@ struct TileShape {
 // One output tile.  lds: kLdsBytes bytes.  acc[b][m][j]: matrix b,
 // token sub-tile m, channel sub-tile j; element i of lane l is token
 // m*16 + l%16, channel (l/16)*4*NJ + j*4 + i of the wave's block (B transposed:
-// j*16 + (l/16)*4 + i).
+// j*16 + (l/16)*4 + i).  The sums are those of part `split` of `splits` equal
+// parts of K.
 //
 // The K step's two halves are software-pipelined: the matrix instructions of
 // one half run while the wave reads the other half's operands from LDS into a
@@ -361,7 +362,7 @@ struct TileShape {
 // two K groups of the small tiles.
 template <class Op, int BM, int BN, int TM, int TN, int ST, int KG, Form F>
 __device__ __forceinline__ void
-tile_product(const DenseIn &in, int t0, int n0, uint8_t *lds,
+tile_product(const DenseIn &in, int t0, int n0, int split, int splits, uint8_t *lds,
              typename Op::Acc (&acc)[TileShape<BM, BN, TM, TN, ST, KG, F>::NB]
                                     [TileShape<BM, BN, TM, TN, ST, KG, F>::MS]
                                     [TileShape<BM, BN, TM, TN, ST, KG, F>::NJ]) {
@@ -371,8 +372,9 @@ tile_product(const DenseIn &in, int t0, int n0, uint8_t *lds,
   const int kg = all / S::kWaves, wave = all % S::kWaves;
   const int wm = wave / TN, wn = wave % TN;
   // this K group's steps: nk from byte k0 on (those behind the end of K are zeros)
-  const int nk = ((int)((in.kbytes + kStepBytes - 1) / kStepBytes) + KG - 1) / KG;
-  const int64_t k0 = (int64_t)kg * nk * kStepBytes;
+  const int steps = (int)((in.kbytes + kStepBytes - 1) / kStepBytes);
+  const int nk = (steps + KG * splits - 1) / (KG * splits);
+  const int64_t k0 = (int64_t)(split * KG + kg) * nk * kStepBytes;
   const LdsPtr ring = (LdsPtr)lds + kg * S::kRing;
   typename S::A a(in, t0, k0, wave, wm, lane);
   typename S::B b(in, n0, k0, wave, wn, lane);

@@ -185,6 +185,61 @@ struct EpiPlain {
   }
 };
 
+// The sums of one part of K as they are, for finish_kernel: [split][matrix][M]
+// rows of `ld` (a multiple of 8 channels, so that every run is whole).
+template <class Sum, int NB>
+struct EpiPartial {
+  static constexpr bool kGated = NB == 2;
+  Sum *part;
+  int32_t M, N, ld, split;
+  template <int CNT>
+  struct Chan {};
+  template <int CNT>
+  __device__ __forceinline__ void load(Chan<CNT> &, int) const {}
+  template <int CNT>
+  __device__ __forceinline__ void store(const Chan<CNT> &, int t, int ch, const Sum (&a)[NB][CNT]) const {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      Sum *row = part + ((int64_t)(split * NB + b) * M + t) * ld + ch;
+#pragma unroll
+      for (int i = 0; i < CNT; i += 4) {
+        v4i w;
+        __builtin_memcpy(&w, a[b] + i, 16);
+        *reinterpret_cast<v4i *>(row + i) = w;
+      }
+    }
+  }
+};
+template <class Epi>
+struct IsPartial : std::false_type {};
+template <class Sum, int NB>
+struct IsPartial<EpiPartial<Sum, NB>> : std::true_type {};
+
+// The parts added in order, then the product's own epilogue: four channels of
+// a token to a thread.
+template <class Sum, class Epi>
+__global__ __launch_bounds__(256) void finish_kernel(const Sum *__restrict__ part, int splits, int M,
+                                                     int ld, Epi epi) {
+  constexpr int NB = Epi::kGated ? 2 : 1;
+  typedef Sum V __attribute__((ext_vector_type(4)));
+  const int per = (epi.N + 3) / 4;
+  const int r = blockIdx.x * 256 + threadIdx.x;
+  if (r >= M * per) return;
+  const int t = r / per, ch = (r - t * per) * 4;
+  typename Epi::template Chan<4> chan;
+  epi.load(chan, ch);
+  Sum a[NB][4];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    V v = {0, 0, 0, 0};
+    for (int s = 0; s < splits; ++s)
+      v += *reinterpret_cast<const V *>(part + ((int64_t)(s * NB + b) * M + t) * ld + ch);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[b][i] = v[i];
+  }
+  epi.store(chan, t, ch, a);
+}
+
 // ---------------------------------------------------------------- product kernel
 // The tile's sums through the epilogue.  A lane's sub-tiles are one run of
 // 4*NJ consecutive channels; with B transposed they are runs of four, 16
@@ -246,28 +301,33 @@ __device__ __forceinline__ void store_tile(const DenseIn &in, const Epi &epi,
 
 template <class Op, int BM, int BN, int TM, int TN, int ST, int KG, Form F, class Epi>
 __global__ __launch_bounds__(TM *TN *KG *kWave) void tile_kernel(DenseIn in, Epi epi, int tiles_m,
-                                                                 int tiles_n) {
+                                                                 int tiles_n, int splits) {
   typedef TileShape<BM, BN, TM, TN, ST, KG, F> S;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLdsBytes];
-  int tm, tn;
-  tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  int tm, tn, bid = blockIdx.x, split = 0;
+  if constexpr (IsPartial<Epi>::value) {
+    split = bid / (tiles_m * tiles_n);
+    bid -= split * (tiles_m * tiles_n);
+    epi.split = split;
+  }
+  tile_of(bid, tiles_m, tiles_n, tm, tn);
   const int t0 = tm * BM, n0 = tn * S::kTileChannels;
   typename Op::Acc acc[S::NB][S::MS][S::NJ];
-  tile_product<Op, BM, BN, TM, TN, ST, KG, F>(in, t0, n0, lds, acc);
+  tile_product<Op, BM, BN, TM, TN, ST, KG, F>(in, t0, n0, split, splits, lds, acc);
   const int wave = threadIdx.x >> 6;
   if (wave >= S::kWaves) return;  // the first K group has the sums
   store_tile<S, Op>(in, epi, acc, t0, n0, wave / TN, wave % TN);
 }
 
 template <class Op, int BM, int BN, int TM, int TN, int ST, int KG, Form F, class Epi>
-hipError_t run_tile(const DenseIn &in, const Epi &epi, hipStream_t stream) {
+hipError_t run_tile(const DenseIn &in, const Epi &epi, hipStream_t stream, int splits = 1) {
   typedef TileShape<BM, BN, TM, TN, ST, KG, F> S;
   const int64_t tm = ((int64_t)in.M + BM - 1) / BM;
   const int64_t tn = ((int64_t)in.N + S::kTileChannels - 1) / S::kTileChannels;
   if (tm * tn == 0) return hipSuccess;
-  if (tm * tn * S::kThreads >= (int64_t)1 << 32) return hipErrorInvalidValue;  // HIP's grid limit
+  if (tm * tn * splits * S::kThreads >= (int64_t)1 << 32) return hipErrorInvalidValue;  // HIP's grid limit
   tile_kernel<Op, BM, BN, TM, TN, ST, KG, F, Epi>
-      <<<(unsigned)(tm * tn), S::kThreads, 0, stream>>>(in, epi, (int)tm, (int)tn);
+      <<<(unsigned)(tm * tn * splits), S::kThreads, 0, stream>>>(in, epi, (int)tm, (int)tn, splits);
   return hipGetLastError();
 }
 
@@ -353,12 +413,12 @@ __global__ __launch_bounds__(TM *TN *KG *kWave) void pair_kernel(DenseIn in1, Ep
   typename Op::Acc acc[1][S1::MS][S1::NJ];
   if (first) {
     tile_of(second_first ? b - n2 : b, tiles1.x, tiles1.y, tm, tn);
-    tile_product<Op, BM, BN, TM, TN, ST, KG, kBColumns>(in1, tm * BM, tn * BN, lds, acc);
+    tile_product<Op, BM, BN, TM, TN, ST, KG, kBColumns>(in1, tm * BM, tn * BN, 0, 1, lds, acc);
     if (wave < S1::kWaves)
       store_tile<S1, Op>(in1, epi1, acc, tm * BM, tn * BN, wave / TN, wave % TN);
   } else {
     tile_of(second_first ? b : b - n1, tiles2.x, tiles2.y, tm, tn);
-    tile_product<Op, BM, BN, TM, TN, ST, KG, kABColumns>(in2, tm * BM, tn * BN, lds, acc);
+    tile_product<Op, BM, BN, TM, TN, ST, KG, kABColumns>(in2, tm * BM, tn * BN, 0, 1, lds, acc);
     if (wave < S2::kWaves)
       store_tile<S2, Op>(in2, epi2, acc, tm * BM, tn * BN, wave / TN, wave % TN);
   }
@@ -395,23 +455,58 @@ double time_of(const Tile &t, const DenseIn &in) {
   return t.c + (double)((in.kbytes + kStepBytes - 1) / kStepBytes) * t.s;
 }
 
+// With no more than 128 of the 64x64 tiles half of the compute units are idle:
+// then K may be cut in parts for as many workgroups as there are compute units,
+// whose sums a second launch adds (about 5 us with its launch, and the parts'
+// bytes, written and read, at 3 TB/s).  int8 64 x 14336 x 4096 24 -> 17 us, bf16
+// gated 40 x 16384 x 320 42 -> 20 us, backward 8192 x 256 x 192 40 -> 27 us, 7 x
+// 640 x 11264 78 -> 34 us.
 struct Choice {
-  int tile;
+  int tile, splits;
   double us;
 };
-Choice choose(const DenseIn &in, int nb) {
-  Choice best{0, 0.0};
+int64_t part_ld(int32_t N) { return ((int64_t)N + 7) / 8 * 8; }
+int64_t part_bytes(const DenseIn &in, int nb, int splits) {
+  return splits > 1 ? (int64_t)splits * nb * in.M * part_ld(in.N) * 4 : 0;
+}
+Choice choose(const DenseIn &in, int nb, bool can_split) {
+  Choice best{0, 1, 0.0};
   for (int i = 0; i < kTiles; ++i) {
     const int64_t n = tiles_of(kTile[i], in, nb);
     const double us = (double)((n + kCUs - 1) / kCUs) * time_of(kTile[i], in);
-    if (i == 0 || us < best.us) best = Choice{i, us};
+    if (i == 0 || us < best.us) best = Choice{i, 1, us};
+  }
+  const int64_t n = tiles_of(kTile[0], in, nb);
+  if (can_split && n > 0 && n <= kCUs / 2) {
+    const int64_t steps = (in.kbytes + kStepBytes - 1) / kStepBytes;
+    for (int splits = 2; splits <= kCUs / n && splits * 4 <= steps; ++splits) {
+      const double us = kTile[0].c + (double)((steps + splits - 1) / splits) * kTile[0].s + 5.0 +
+                        (double)part_bytes(in, nb, splits) * 2.0 / 3e6;
+      if (us < best.us) best = Choice{0, splits, us};
+    }
   }
   return best;
 }
 
 template <class Op, Form F, class Epi>
-hipError_t run_tiles(const DenseIn &in, const Epi &epi, hipStream_t stream) {
-  switch (choose(in, F == kGatedForm ? 2 : 1).tile) {
+hipError_t run_split(const DenseIn &in, const Epi &epi, int splits, void *part, hipStream_t stream) {
+  typedef typename Op::Sum Sum;
+  const int ld = (int)part_ld(in.N);
+  const EpiPartial<Sum, F == kGatedForm ? 2 : 1> sums{(Sum *)part, in.M, in.N, ld, 0};
+  const hipError_t e = run_tile<Op, 64, 64, 2, 2, 3, 2, F>(in, sums, stream, splits);
+  if (e != hipSuccess) return e;
+  const int64_t runs = (int64_t)in.M * ((in.N + 3) / 4);
+  finish_kernel<Sum, Epi><<<(unsigned)((runs + 255) / 256), 256, 0, stream>>>((const Sum *)part,
+                                                                            splits, in.M, ld, epi);
+  return hipGetLastError();
+}
+
+// part: room for the parts of a K that is cut (part_bytes), or NULL: then it is not.
+template <class Op, Form F, class Epi>
+hipError_t run_tiles(const DenseIn &in, const Epi &epi, void *part, hipStream_t stream) {
+  const Choice c = choose(in, F == kGatedForm ? 2 : 1, part != nullptr);
+  if (c.splits > 1) return run_split<Op, F>(in, epi, c.splits, part, stream);
+  switch (c.tile) {
     case 0: return run_tile<Op, 64, 64, 2, 2, 3, 2, F, Epi>(in, epi, stream);
     case 1: return run_tile<Op, 64, 128, 2, 4, 3, 2, F, Epi>(in, epi, stream);
     case 2: return run_tile<Op, 128, 128, 2, 4, 4, 1, F, Epi>(in, epi, stream);
@@ -454,14 +549,14 @@ hipError_t run_pair_tile(const DenseIn &in1, const Epi &epi1, const DenseIn &in2
 // 2048, 192: 1.51, 88 and 63 us; 512, 4096, 4096: 1.30, 126 and 117 us.)
 template <class Op, class Epi>
 hipError_t run_pair(const DenseIn &in1, const Epi &epi1, const DenseIn &in2, const Epi &epi2,
-                    hipStream_t stream) {
+                    void *part, hipStream_t stream) {
   const bool swap = in2.kbytes > in1.kbytes;
   const DenseIn &l = swap ? in2 : in1, &r = swap ? in1 : in2;  // the longer tiles first
-  Choice best{-1, (in1.M > 0 ? choose(in1, 1).us : 0.0) + choose(in2, 1).us};
+  Choice best{-1, 1, (in1.M > 0 ? choose(in1, 1, true).us : 0.0) + choose(in2, 1, true).us};
   for (int i = 0; i < kTiles; ++i) {
     const double us = pair_time(tiles_of(kTile[i], l, 1), time_of(kTile[i], l),
                                 tiles_of(kTile[i], r, 1), time_of(kTile[i], r));
-    if (us < best.us) best = Choice{i, us};
+    if (us < best.us) best = Choice{i, 1, us};
   }
   switch (best.tile) {
     case 0: return run_pair_tile<Op, 64, 64, 2, 2, 3, 2>(in1, epi1, in2, epi2, swap, stream);
@@ -470,22 +565,26 @@ hipError_t run_pair(const DenseIn &in1, const Epi &epi1, const DenseIn &in2, con
     case 3: return run_pair_tile<Op, 128, 256, 2, 4, 3, 1>(in1, epi1, in2, epi2, swap, stream);
     case 4: return run_pair_tile<Op, 256, 256, 2, 4, 2, 1>(in1, epi1, in2, epi2, swap, stream);
   }
-  const hipError_t e = run_tiles<Op, kBColumns>(in1, epi1, stream);
-  return e != hipSuccess ? e : run_tiles<Op, kABColumns>(in2, epi2, stream);
+  const hipError_t e = in1.M > 0 ? run_tiles<Op, kBColumns>(in1, epi1, part, stream) : hipSuccess;
+  return e != hipSuccess ? e : run_tiles<Op, kABColumns>(in2, epi2, part, stream);
 }
 
 // Up to 32 tokens stream the weights (stream_product), one workgroup to a
 // compute unit; at 17 to 32 only few channels do, for which tiles leave compute
 // units idle (int8, T = 32, weights from HBM: 14336 -> 4096 23 us streamed and
 // 32 us in tiles; 4096 -> 14336 22 and 16 us).  Above, tiles.
+bool streams(const DenseIn &in, int nb) {
+  return in.M <= 16 || (in.M <= 32 && ((int64_t)in.N * nb + 15) / 16 <= 2 * kCUs);
+}
+
 template <class Op, class Epi>
-hipError_t run_product(const DenseIn &in, const Epi &epi, hipStream_t stream) {
+hipError_t run_product(const DenseIn &in, const Epi &epi, void *part, hipStream_t stream) {
   if (in.M == 0) return hipSuccess;
-  const int64_t groups = ((int64_t)in.N * (Epi::kGated ? 2 : 1) + 15) / 16;  // of 16 weight rows
+  if (!streams(in, Epi::kGated ? 2 : 1))
+    return run_tiles<Op, Epi::kGated ? kGatedForm : kPlainForm>(in, epi, part, stream);
   if (in.M <= 8) return run_stream<Op, 1, 1, 8, 6, Epi>(in, epi, stream);
   if (in.M <= 16) return run_stream<Op, 2, 1, 8, 4, Epi>(in, epi, stream);
-  if (in.M <= 32 && groups <= 2 * kCUs) return run_stream<Op, 4, 2, 4, 4, Epi>(in, epi, stream);
-  return run_tiles<Op, Epi::kGated ? kGatedForm : kPlainForm>(in, epi, stream);
+  return run_stream<Op, 4, 2, 4, 4, Epi>(in, epi, stream);
 }
 
 // ---------------------------------------------------------------- int8 quantisation
@@ -663,11 +762,26 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const T *__restrict__ dh
   }
 }
 
+// A product's operands as far as the choice of its form goes.
+DenseIn sizes(int64_t M, int64_t N, int64_t kbytes) {
+  DenseIn in{};
+  in.M = (int32_t)M;
+  in.N = (int32_t)N;
+  in.kbytes = kbytes;
+  return in;
+}
+size_t product_workspace(const DenseIn &in, int nb) {
+  if (in.M == 0 || streams(in, nb)) return 0;
+  return (size_t)part_bytes(in, nb, choose(in, nb, true).splits);
+}
+size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
+size_t dgu_bytes(int32_t T, int32_t f) { return up256((size_t)(T > 0 ? T : 1) * 2 * f * 2); }
+
 template <class OUT>
 hipError_t matmul_i8_as(const I8Product &p, hipStream_t stream) {
   const DenseIn in{(const uint8_t *)p.xq, (const uint8_t *)p.wq, nullptr, p.ldx, p.K, p.T, p.N, p.K};
   const EpiI8<OUT> epi{p.sx, p.sw, p.bias, (OUT *)p.y, p.N};
-  return run_product<OpI8>(in, epi, stream);
+  return run_product<OpI8>(in, epi, p.workspace, stream);
 }
 
 template <class OUT>
@@ -675,7 +789,7 @@ hipError_t gated_i8_as(const I8Gated &p, hipStream_t stream) {
   const DenseIn in{(const uint8_t *)p.xq, (const uint8_t *)p.w_gate, (const uint8_t *)p.w_up,
                    p.ldx, p.d, p.T, p.f, p.d};
   const EpiI8Gated<OUT> epi{p.sx, p.s_gate, p.s_up, (OUT *)p.h, p.f};
-  return run_product<OpI8>(in, epi, stream);
+  return run_product<OpI8>(in, epi, p.workspace, stream);
 }
 
 template <class Op, class E>
@@ -683,7 +797,7 @@ hipError_t gated_as(const Gated16 &p, hipStream_t stream) {
   const DenseIn in{(const uint8_t *)p.x, (const uint8_t *)p.w_gate, (const uint8_t *)p.w_up,
                    p.ldx * 2, (int64_t)p.d * 2, p.T, p.f, (int64_t)p.d * 2};
   const EpiGated<E> epi{(E *)p.h, p.gate, p.up, p.f};
-  return run_product<Op>(in, epi, stream);
+  return run_product<Op>(in, epi, p.workspace, stream);
 }
 
 template <class Op, class E>
@@ -706,7 +820,7 @@ hipError_t backward_as(const Gated16Backward &p, hipStream_t stream) {
   const DenseIn dw{(const uint8_t *)dgu, (const uint8_t *)p.x, nullptr, two_f * 2, p.ldx * 2,
                    2 * p.f, p.d, (int64_t)p.T * 2, p.T};
   const EpiPlain<E> to_dw{(E *)p.dw_gate, (E *)p.dw_up, p.f, p.d};
-  return run_pair<Op>(dx, to_dx, dw, to_dw, stream);
+  return run_pair<Op>(dx, to_dx, dw, to_dw, p.workspace + dgu_bytes(p.T, p.f), stream);
 }
 
 }  // namespace
@@ -736,9 +850,21 @@ hipError_t launch_gated(const Gated16 &p, hipStream_t stream) {
                              : gated_as<OpF16, _Float16>(p, stream);
 }
 
+size_t matmul_i8_workspace(int32_t T, int32_t K, int32_t N) {
+  return product_workspace(sizes(T, N, K), 1);
+}
+size_t gated_i8_workspace(int32_t T, int32_t d, int32_t f) {
+  return product_workspace(sizes(T, f, d), 2);
+}
+size_t gated_workspace(int32_t T, int32_t d, int32_t f) {
+  return product_workspace(sizes(T, f, 2 * (int64_t)d), 2);
+}
+// dgu, and the parts of dx's and then of dW's products
 size_t gated_backward_workspace(int32_t T, int32_t d, int32_t f) {
-  (void)d;
-  return ((size_t)(T > 0 ? T : 1) * 2 * f * 2 + 255) / 256 * 256;  // dgu
+  const DenseIn dx = sizes(T, d, 4 * (int64_t)f), dw = sizes(2 * (int64_t)f, d, 2 * (int64_t)T);
+  const int64_t a = T > 0 ? part_bytes(dx, 1, choose(dx, 1, true).splits) : 0;
+  const int64_t b = part_bytes(dw, 1, choose(dw, 1, true).splits);
+  return dgu_bytes(T, f) + (size_t)(a > b ? a : b);
 }
 
 hipError_t launch_gated_backward(const Gated16Backward &p, hipStream_t stream) {

@@ -325,7 +325,17 @@ moe_status moe_fused_forward_noalloc(const moe_dims *dims /*host*/, const float 
  * array is 16-byte aligned (scales and bias 4-byte).  An output that shares
  * memory with an input or with another output is MOE_ERR_SHAPE.  T = 0 is
  * valid: the arrays with T rows may then be NULL, and nothing is written but
- * the weights' gradients, which are zeros.  Inputs are finite, as everywhere. */
+ * the weights' gradients, which are zeros.  Inputs are finite, as everywhere.
+ *
+ * Workspaces: a product with few outputs and a long sum is cut along the sum
+ * for more workgroups, whose partial sums need room; the *_workspace_bytes
+ * functions give it (0 where the product is not cut, and, with a text in
+ * moe_last_error(), for sizes that the call refuses).  The workspace is a
+ * device buffer of at least that size, 256-byte aligned, not touched by
+ * anything else while the work is in flight; it need not be cleared.  Where it
+ * is said to be optional, NULL runs the product uncut.  Sums are taken in an
+ * order that depends on the sizes and on whether there is a workspace alone, so
+ * equal calls give equal bits. */
 enum { MOE_T_F32 = 0, MOE_T_BF16 = 1, MOE_T_F16 = 2 }; /* element types */
 #define MOE_MAX_TOKENS (1 << 21) /* rows of one call, and outputs N of moe_matmul_i8 */
 #define MOE_MAX_I8_K 65536       /* longest int8 row: its products' sum fits 31 bits */
@@ -346,26 +356,32 @@ moe_status moe_quantize_rows_i8(const void *x, int32_t x_type, int64_t ldx, int3
  * once to y_type (fp16: past 65504 to infinity).  xq [T][K] with row stride
  * ldx, sx [T], wq [N][K], sw [N], bias [N] fp32 or NULL, y [T][N].
  * K: a multiple of 16 up to MOE_MAX_I8_K; T and N: any up to MOE_MAX_TOKENS. */
+size_t moe_matmul_i8_workspace_bytes(int32_t T, int32_t K, int32_t N);
 moe_status moe_matmul_i8(const int8_t *xq, int64_t ldx, const float *sx, const int8_t *wq,
                          const float *sw, const float *bias, int32_t T, int32_t K, int32_t N,
-                         int32_t y_type, void *y, void *stream);
+                         int32_t y_type, void *y, void *workspace /*optional*/,
+                         size_t workspace_bytes, void *stream);
 
 /* The gated block on int8 codes, in one kernel:
  *   g = xq w_gate^T * sx * s_gate, u = xq w_up^T * sx * s_up, h = SiLU(g) * u
  * xq [T][d] with row stride ldx, w_gate, w_up [f][d], s_gate, s_up [f],
  * h [T][f] in h_type.  d, f: multiples of 64 up to MOE_MAX_HIDDEN / MOE_MAX_FFN. */
+size_t moe_gated_ffn_i8_workspace_bytes(int32_t T, int32_t d, int32_t f);
 moe_status moe_gated_ffn_i8(const int8_t *xq, int64_t ldx, const float *sx, const int8_t *w_gate,
                             const float *s_gate, const int8_t *w_up, const float *s_up, int32_t T,
-                            int32_t d, int32_t f, int32_t h_type, void *h, void *stream);
+                            int32_t d, int32_t f, int32_t h_type, void *h,
+                            void *workspace /*optional*/, size_t workspace_bytes, void *stream);
 
 /* The gated block in bf16 or fp16 (`type`, of x, the weights and h), in one
  * kernel:
  *   g = x w_gate^T, u = x w_up^T (fp32 sums), h = SiLU(g) * u, rounded once
  * x [T][d] with row stride ldx, w_gate, w_up [f][d], h [T][f].  gate, up
  * [T][f] fp32: where g and u are kept for the backward pass, or both NULL.  d, f: multiples of 64 up to MOE_MAX_HIDDEN / MOE_MAX_FFN. */
+size_t moe_gated_ffn_workspace_bytes(int32_t T, int32_t d, int32_t f);
 moe_status moe_gated_ffn(const void *x, int64_t ldx, const void *w_gate, const void *w_up,
                          int32_t type, int32_t T, int32_t d, int32_t f, void *h, float *gate,
-                         float *up, void *stream);
+                         float *up, void *workspace /*optional*/, size_t workspace_bytes,
+                         void *stream);
 
 /* Its backward pass, from the gradient dh [T][f] (row stride lddh) of h and
  * the g, u kept by the forward pass: with s = sigmoid(g),
@@ -374,11 +390,7 @@ moe_status moe_gated_ffn(const void *x, int64_t ldx, const void *w_gate, const v
  *   dx = dg w_gate + du w_up   [T][d],
  *   dw_gate = dg^T x, dw_up = du^T x   [f][d],
  * fp32 sums, each output rounded once to `type` and overwritten (not added
- * to).  Sums are taken in an order that depends on the sizes alone, so equal
- * inputs give equal bits.  workspace: a device buffer of at least
- * moe_gated_ffn_backward_workspace_bytes(T, d, f), 256-byte aligned, not
- * touched by anything else while the work is in flight (the size is 0, with a
- * text in moe_last_error(), for sizes that the call refuses). */
+ * to).  The workspace (moe_gated_ffn_backward_workspace_bytes) is required. */
 size_t moe_gated_ffn_backward_workspace_bytes(int32_t T, int32_t d, int32_t f);
 moe_status moe_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, int64_t ldx,
                                   const void *w_gate, const void *w_up, const float *gate,

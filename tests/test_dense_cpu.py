@@ -23,7 +23,7 @@ def test_every_dense_symbol_is_exported_by_both_libraries():
     src = open(os.path.join(ROOT, "include", "fp8moe.h")).read()
     src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
     names = {n for n in re.findall(r"\b(moe_\w+)\s*\(", src) if "_i8" in n or "gated" in n}
-    assert len(names) == 6
+    assert len(names) == 9
     for path in (fp8.LIB_PATH, fp8.DEBUG_LIB_PATH):
         if path.exists():
             lib = C.CDLL(str(path))
@@ -49,8 +49,9 @@ def test_quantize_refuses(kw, code):
     assert fp8._last_error().startswith(b"moe_quantize_rows_i8")
 
 
-def matmul(xq=P[0], ldx=64, sx=P[1], wq=P[2], sw=P[3], bias=None, T=4, K=64, N=7, kind=F32, y=P[4]):
-    return fp8._matmul_i8(xq, ldx, sx, wq, sw, bias, T, K, N, kind, y, None)
+def matmul(xq=P[0], ldx=64, sx=P[1], wq=P[2], sw=P[3], bias=None, T=4, K=64, N=7, kind=F32, y=P[4],
+           ws=None, wsb=0):
+    return fp8._matmul_i8(xq, ldx, sx, wq, sw, bias, T, K, N, kind, y, ws, wsb, None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -69,8 +70,8 @@ def test_matmul_refuses(kw, code):
 
 
 def gated_i8(xq=P[0], ldx=128, sx=P[1], wg=P[2], sg=P[3], wu=P[4], su=P[5], T=4, d=128, f=64,
-             kind=BF16, h=P[6]):
-    return fp8._gated_ffn_i8(xq, ldx, sx, wg, sg, wu, su, T, d, f, kind, h, None)
+             kind=BF16, h=P[6], ws=None, wsb=0):
+    return fp8._gated_ffn_i8(xq, ldx, sx, wg, sg, wu, su, T, d, f, kind, h, ws, wsb, None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -85,8 +86,9 @@ def test_gated_i8_refuses(kw, code):
     assert fp8._last_error().startswith(b"moe_gated_ffn_i8")
 
 
-def gated(x=P[0], ldx=128, wg=P[1], wu=P[2], kind=BF16, T=4, d=128, f=64, h=P[3], gate=P[4], up=P[5]):
-    return fp8._gated_ffn(x, ldx, wg, wu, kind, T, d, f, h, gate, up, None)
+def gated(x=P[0], ldx=128, wg=P[1], wu=P[2], kind=BF16, T=4, d=128, f=64, h=P[3], gate=P[4], up=P[5],
+          ws=None, wsb=0):
+    return fp8._gated_ffn(x, ldx, wg, wu, kind, T, d, f, h, gate, up, ws, wsb, None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -120,6 +122,31 @@ def backward(dh=P[0], lddh=64, x=P[1], ldx=128, wg=P[2], wu=P[3], gate=P[4], up=
 def test_backward_refuses(kw, code):
     assert backward(**kw) == code, fp8._last_error()
     assert fp8._last_error().startswith(b"moe_gated_ffn_backward")
+
+
+def test_optional_workspaces():
+    """Products with few outputs and a long sum can be cut; what they then ask
+    for is checked, and so is where it lies."""
+    assert fp8._matmul_i8_ws(64, 16384, 64) > 0 and fp8._gated_ffn_ws(64, 4096, 64) > 0
+    assert fp8._gated_ffn_i8_ws(64, 8192, 64) > 0
+    for few in (fp8._matmul_i8_ws(16, 16384, 64), fp8._matmul_i8_ws(8192, 4096, 4096),
+                fp8._matmul_i8_ws(64, 64, 64), fp8._matmul_i8_ws(0, 4096, 64)):
+        assert few == 0
+    for bad in (fp8._matmul_i8_ws(64, 100, 64), fp8._matmul_i8_ws(-1, 4096, 64),
+                fp8._gated_ffn_ws(64, 100, 64), fp8._gated_ffn_i8_ws(64, 128, 100)):
+        assert bad == 0 and fp8._last_error()
+    big = dict(T=64, K=16384, ldx=16384, N=64)
+    n = fp8._matmul_i8_ws(64, 16384, 64)
+    assert matmul(**big, ws=P[9], wsb=n - 1) == ERR_WORKSPACE
+    assert matmul(**big, ws=P[9] + 16, wsb=n) == ERR_ALIGN
+    assert matmul(**big, ws=P[4], wsb=n) == ERR_SHAPE       # over y
+    assert matmul(**big, ws=P[2], wsb=n) == ERR_SHAPE       # over the weights
+    n = fp8._gated_ffn_i8_ws(64, 8192, 64)
+    assert gated_i8(T=64, d=8192, ldx=8192, ws=P[9], wsb=n - 1) == ERR_WORKSPACE
+    assert gated_i8(T=64, d=8192, ldx=8192, ws=P[6], wsb=n) == ERR_SHAPE
+    n = fp8._gated_ffn_ws(64, 4096, 64)
+    assert gated(T=64, d=4096, ldx=4096, ws=P[9], wsb=n - 1) == ERR_WORKSPACE
+    assert gated(T=64, d=4096, ldx=4096, ws=P[5], wsb=n) == ERR_SHAPE
 
 
 def test_backward_workspace_size():

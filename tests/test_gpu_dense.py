@@ -138,7 +138,8 @@ MATMUL = [(1, 16, 1), (1, 64, 16), (2, 48, 3), (15, 112, 31), (16, 128, 64), (17
           (333, 1408, 2051), (1000, 96, 1000), (1, 14336, 4096), (7, 4096, 2048), (2100, 1024, 1536),
           (4100, 512, 2304), (9, 65536, 33), (4, 80, 70000), (16, 272, 9000), (24, 528, 8200),
           (8, 4096, 4111), (32, 1040, 16400), (8200, 128, 4100), (2000, 768, 300), (1000, 800, 4000), (2000, 800, 4000), (3256, 16, 1163),
-          (130, 1424, 4111)]
+          (130, 1424, 4111), (40, 16384, 33), (33, 8192, 321), (64, 14336, 4096), (130, 4112, 7),
+          (300, 6160, 515)]
 
 
 @pytest.mark.parametrize("T,K,N", MATMUL)
@@ -181,6 +182,24 @@ def test_matmul_i8_longest_row(T):
     assert bool((y == float(2 ** 30)).all())
 
 
+@pytest.mark.parametrize("T,K,N", [(64, 16384, 64), (33, 8192, 321), (128, 14336, 515)])
+def test_a_cut_product_equals_the_uncut_one(T, K, N):
+    """int8 sums are exact, so cutting K (with a workspace, here one full of
+    rubbish) changes no bit; and the workspace is written nowhere else."""
+    m, g = lib(), gen(T)
+    xq, wq, sx, sw = codes(g, (T, K)), codes(g, (N, K)), scales(g, T), scales(g, N)
+    n = m._matmul_i8_ws(T, K, N)
+    assert n > 0
+    ws = torch.full((n + 512,), 0xFF, dtype=torch.uint8, device=dev())
+    y, z = torch.empty((T, N), device=dev()), torch.empty((T, N), device=dev())
+    args = (xq.data_ptr(), K, sx.data_ptr(), wq.data_ptr(), sw.data_ptr(), None, T, K, N, 0)
+    st = torch.cuda.current_stream().cuda_stream
+    assert m._matmul_i8(*args, y.data_ptr(), ws.data_ptr(), n, st) == 0
+    assert m._matmul_i8(*args, z.data_ptr(), None, 0, st) == 0
+    assert torch.equal(y, z) and torch.equal(y, m.matmul_i8(xq, sx, wq, sw))
+    assert bool((ws[n:] == 0xFF).all())
+
+
 # ------------------------------------------------------------------ gated block, int8
 
 def silu_ref(g, u, eg, eu):
@@ -197,7 +216,8 @@ def silu_ref(g, u, eg, eu):
                                    (256, 256, 512), (300, 1408, 192), (700, 512, 1088),
                                    (1, 4096, 14336), (2050, 256, 2048), (5, 16384, 64),
                                    (130, 64, 16384), (8, 2048, 4160), (16, 4096, 4160),
-                                   (31, 448, 8256), (1030, 192, 4096), (260, 832, 3456)])
+                                   (31, 448, 8256), (1030, 192, 4096), (260, 832, 3456), (40, 16384, 64),
+                                   (33, 8192, 320), (200, 6208, 192)])
 def test_gated_i8(T, d, f):
     g = gen(T + d + f)
     kind = FLOATS[(T + f // 64) % 3]
@@ -230,13 +250,15 @@ def gated_ref(x, wg, wu):
 GATED = [(1, 64, 64), (2, 256, 192), (15, 128, 512), (16, 2048, 768), (17, 192, 64), (33, 64, 128),
          (64, 320, 256), (65, 1408, 192), (128, 256, 512), (129, 448, 320), (257, 192, 1408),
          (300, 2048, 64), (777, 512, 832), (2050, 256, 2048), (8, 512, 4160), (12, 192, 8256),
-         (2500, 128, 192), (40, 1024, 2304), (1500, 1024, 320), (1100, 640, 2304), (5000, 64, 64), (260, 832, 3456)]
+         (2500, 128, 192), (40, 1024, 2304), (1500, 1024, 320), (1100, 640, 2304), (5000, 64, 64), (260, 832, 3456), (40, 4096, 128), (90, 16384, 64),
+         (200, 3136, 192)]
 
 # and, for the gradients, sizes at which each tile is taken, by dx and dW alone and together
 GRADIENTS = GATED + [(1044, 3136, 64), (1247, 640, 1088), (45, 2240, 896), (37, 1600, 1920),
                      (34, 3136, 1408), (1987, 832, 576), (4096, 1216, 64), (3215, 2368, 64),
                      (268, 2880, 64), (35, 3264, 320), (586, 2752, 64), (412, 3712, 320),
-                     (626, 3712, 256), (1008, 3968, 576), (1081, 4096, 512)]
+                     (626, 3712, 256), (1008, 3968, 576), (1081, 4096, 512), (7, 640, 11264),
+                     (8192, 256, 192), (1, 1024, 4096), (3001, 128, 64), (70, 192, 8192)]
 
 
 @pytest.mark.parametrize("dtype", F16S)
