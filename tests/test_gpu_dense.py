@@ -13,6 +13,8 @@ ulp of fp32, relative):
   compensated form a few ulp, the reciprocal 1);
 - the output's rounding: half a step of its type.
 """
+import ctypes as C
+
 import numpy as np
 import pytest
 import torch
@@ -503,12 +505,12 @@ def test_trained_weights_served_in_int8(T):
         gr * torch.sigmoid(gr) * ur).abs())
 
 
-def test_captured_and_replayed_with_work_in_between():
+@pytest.mark.parametrize("T,d,f", [(70, 256, 320), (5, 256, 320), (40, 2048, 64)])
+def test_captured_and_replayed_with_work_in_between(T, d, f):
     """The whole chain, training and serving, in one graph; every replay
     against the eager result on its own inputs, with eager calls of the same
     operators between the replays."""
     g = gen(1)
-    T, d, f = 70, 256, 320
     dtype = torch.float16
     x, dh = normal(g, (T, d), 1, dtype), normal(g, (T, f), 1, dtype)
     wg, wu = normal(g, (f, d), d ** -0.5, dtype), normal(g, (f, d), d ** -0.5, dtype)
@@ -555,6 +557,64 @@ def test_a_stream_of_its_own():
         assert all(torch.equal(a, b) for a, b in zip(grads, wantb))
         ref, tol = matmul_ref(q, sc, q, sc, None)
         within(y, ref, tol)
+
+
+def test_two_streams_at_once():
+    """The same operators on two streams, each with its own inputs, at the same
+    time: nothing is shared but the weights."""
+    g = gen(8)
+    wg, wu = normal(g, (320, 2048), 1 / 45, torch.bfloat16), normal(g, (320, 2048), 1 / 45, torch.bfloat16)
+    xs = [normal(g, (n, 2048), 1, torch.bfloat16) for n in (300, 40)]
+
+    def step(x, stream=None):
+        h, ga, up = lib().gated_ffn(x, wg, wu, save=True, stream=stream)
+        return [h, *lib().gated_ffn_backward(h, x, wg, wu, ga, up, stream=stream)]
+
+    want = [step(x) for x in xs]
+    torch.cuda.synchronize()
+    ss = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[step(x, s) for _ in range(8)] for x, s in zip(xs, ss)]
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        for r in runs:
+            assert all(torch.equal(a, b) for a, b in zip(w, r))
+
+
+def test_the_debug_build():
+    """The device-checked build gives the same bits, and names a row that is
+    not finite."""
+    if not lib().DEBUG_LIB_PATH.exists():
+        pytest.skip("libfp8moe_debug.so not built")
+    dbg = C.CDLL(str(lib().DEBUG_LIB_PATH))
+    for name in ("_quantize_rows_i8", "_gated_ffn", "_gated_bwd"):
+        fn = getattr(lib(), name)
+        getattr(dbg, fn.__name__).argtypes = fn.argtypes
+    dbg.moe_last_error.restype = C.c_char_p
+    g = gen(4)
+    T, d, f = 50, 128, 192
+    x = normal(g, (T, d), 1, torch.float16)
+    wg, wu = normal(g, (f, d), 0.1, torch.float16), normal(g, (f, d), 0.1, torch.float16)
+    h, ga, up = lib().gated_ffn(x, wg, wu, save=True)
+    h2, ga2, up2 = torch.empty_like(h), torch.empty_like(ga), torch.empty_like(up)
+    p = lambda t: t.data_ptr()
+    torch.cuda.synchronize()
+    assert dbg.moe_gated_ffn(p(x), d, p(wg), p(wu), 2, T, d, f, p(h2), p(ga2), p(up2), None, 0, None) == 0
+    assert torch.equal(h, h2) and torch.equal(ga, ga2) and torch.equal(up, up2)
+    want = lib().gated_ffn_backward(h, x, wg, wu, ga, up)
+    got = [torch.empty_like(t) for t in want]
+    n = lib().gated_ffn_backward_workspace_bytes(T, d, f)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev())
+    torch.cuda.synchronize()
+    assert dbg.moe_gated_ffn_backward(p(h), f, p(x), d, p(wg), p(wu), p(ga), p(up), 2, T, d, f,
+                                      *map(p, got), p(ws), n, None) == 0
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    q, s = torch.empty((T, d), dtype=torch.int8, device=dev()), torch.empty(T, device=dev())
+    bad = x.clone()
+    bad[3, 5] = torch.nan
+    torch.cuda.synchronize()
+    assert dbg.moe_quantize_rows_i8(p(x), 2, d, T, d, p(q), p(s), None) == 0
+    assert dbg.moe_quantize_rows_i8(p(bad), 2, d, T, d, p(q), p(s), None) == 7
+    assert b"non-finite" in dbg.moe_last_error()
 
 
 def test_the_binding_refuses():
