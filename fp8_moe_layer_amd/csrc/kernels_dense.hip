@@ -639,8 +639,16 @@ struct Run {
   }
 };
 
-// LANES threads to a row (a wave, or the workgroup of 256), P runs of 16 bytes
-// each, held in registers between the maximum and the codes, so that the row
+// The maximum of each sixteen lanes, in all of them.
+__device__ __forceinline__ float max16(float v) {
+  v = fmaxf(v, dpp_mov<kDppQuadXor1>(v));
+  v = fmaxf(v, dpp_mov<kDppQuadXor2>(v));
+  v = fmaxf(v, dpp_mov<kDppHalfMirror>(v));
+  return fmaxf(v, dpp_mov<kDppMirror>(v));
+}
+
+// LANES threads to a row (sixteen, a wave, or the workgroup of 256), P runs of
+// 16 bytes each, held in registers between the maximum and the codes, so that the row
 // is read once.  P = 0: a row too long for that is read twice, the second time
 // from cache.  Bound by memory: 8191 x 14336 bf16 (352 MB) 91 us with the row
 // read twice, 68 us so (5.2 TB/s).
@@ -651,7 +659,7 @@ __global__ __launch_bounds__(256) void quantize_i8_kernel(const T *__restrict__ 
                                                           float *__restrict__ scale) {
   constexpr int kCount = Run<T>::kCount;
   const int64_t row = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
-  if (row >= rows) return;  // a whole wave (LANES 64), or never
+  if (row >= rows) return;  // whole rows of lanes, or never (LANES 256)
   const int lane = threadIdx.x % LANES;
   const T *xr = x + row * ldx;
   int8_t *qr = q + row * cols;
@@ -673,7 +681,7 @@ __global__ __launch_bounds__(256) void quantize_i8_kernel(const T *__restrict__ 
       amax = v[0].amax(amax);
     }
   }
-  amax = wave_max(amax);
+  amax = LANES == 16 ? max16(amax) : wave_max(amax);
   if constexpr (LANES > kWave) {
     __shared__ float red[LANES / kWave];
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = amax;
@@ -699,8 +707,9 @@ __global__ __launch_bounds__(256) void quantize_i8_kernel(const T *__restrict__ 
   if (lane == 0) scale[row] = k.s;
 }
 
-// A wave takes a row of up to four runs a lane (1024 fp32 or 2048 16-bit
-// values), a workgroup longer ones.
+// Sixteen lanes take a row of up to 48 runs (192 fp32 or 384 16-bit values), a
+// wave one of up to 256 runs, a workgroup longer ones (65536 x 192 bf16: 17 us
+// with a wave to a row, 9.5 us with sixteen lanes; 8192 x 512 fp16: 4.5 and 4.9).
 template <class T>
 hipError_t quantize_i8_as(const T *x, int64_t ldx, int rows, int cols, int8_t *q, float *scale,
                           hipStream_t stream) {
@@ -709,7 +718,9 @@ hipError_t quantize_i8_as(const T *x, int64_t ldx, int rows, int cols, int8_t *q
   quantize_i8_kernel<T, LANES, P>                                                       \
       <<<(unsigned)(((int64_t)rows + 256 / LANES - 1) / (256 / LANES)), 256, 0, stream>>>( \
           x, ldx, rows, cols, q, scale)
-  if (runs <= 64 * 4)
+  if (runs <= 16 * 3)
+    FP8MOE_QUANTIZE(16, 3);
+  else if (runs <= 64 * 4)
     FP8MOE_QUANTIZE(64, 4);
   else if (runs <= 256 * 4)
     FP8MOE_QUANTIZE(256, 4);

@@ -95,7 +95,8 @@ def quantize_ref(x):
 @pytest.mark.parametrize("dtype", FLOATS)
 @pytest.mark.parametrize("rows,cols,pad", [
     (1, 16, 0), (3, 48, 16), (5, 1008, 0), (17, 1024, 32), (2, 1040, 0), (9, 4096, 0), (4, 14336, 8),
-    (3, 16384, 0), (2, 16400, 0), (1, 65536, 0), (1000, 64, 0), (257, 2048, 0)])
+    (3, 16384, 0), (2, 16400, 0), (1, 65536, 0), (1000, 64, 0), (257, 2048, 0), (67, 256, 0), (35, 272, 16),
+    (18, 512, 0), (21, 528, 0), (1031, 192, 0)])
 def test_quantize_rows_i8(rows, cols, pad, dtype):
     g = gen(rows * 7 + cols)
     x = normal(g, (rows, cols)) * torch.exp(3 * normal(g, (rows, 1)))
