@@ -436,7 +436,7 @@ class _Call:
         """(tensor, address, bytes) of the workspace that the call can use:
         size(T, inner, outputs) bytes, asked for only where a product is small
         enough to be cut along its sum."""
-        if T > 16 and ((T + 63) >> 6) * ((outputs + 63) >> 6) <= 128:
+        if T > 32 and ((T + 63) >> 6) * ((outputs + 63) >> 6) <= 128:
             n = size(T, inner, outputs)
             if n:
                 ws = self.empty((n,), torch.uint8)

@@ -570,21 +570,32 @@ hipError_t run_pair(const DenseIn &in1, const Epi &epi1, const DenseIn &in2, con
 }
 
 // Up to 32 tokens stream the weights (stream_product), one workgroup to a
-// compute unit; at 17 to 32 only few channels do, for which tiles leave compute
-// units idle (int8, T = 32, weights from HBM: 14336 -> 4096 23 us streamed and
-// 32 us in tiles; 4096 -> 14336 22 and 16 us).  Above, tiles.
-bool streams(const DenseIn &in, int nb) {
-  return in.M <= 16 || (in.M <= 32 && ((int64_t)in.N * nb + 15) / 16 <= 2 * kCUs);
+// compute unit.  At 17 to 32 the tokens are as large a part of what is fetched
+// as the weights: a group is then 16 weight rows where the groups leave one to a
+// compute unit (weights from HBM, T = 32, int8 14336 -> 4096: 17 us, 21 with 32
+// rows, 32 in tiles), else 32, and for many channels of a short K tiles are as
+// fast or faster (bf16 gated 4096 -> 2 x 14336: 50 us streamed, 58 in tiles;
+// int8, half the bytes of K: 28 and 26.5).  Above, tiles.
+enum class Stream { kNo, k8, k16, k32, k32Wide };
+Stream streams(const DenseIn &in, int nb) {
+  const int64_t groups = ((int64_t)in.N * nb + 15) / 16;  // of 16 weight rows
+  if (in.M <= 8) return Stream::k8;
+  if (in.M <= 16) return Stream::k16;
+  if (in.M > 32) return Stream::kNo;
+  if (groups <= kCUs) return Stream::k32;
+  return groups <= 2 * kCUs || in.kbytes > 6144 ? Stream::k32Wide : Stream::kNo;
 }
 
 template <class Op, class Epi>
 hipError_t run_product(const DenseIn &in, const Epi &epi, void *part, hipStream_t stream) {
   if (in.M == 0) return hipSuccess;
-  if (!streams(in, Epi::kGated ? 2 : 1))
-    return run_tiles<Op, Epi::kGated ? kGatedForm : kPlainForm>(in, epi, part, stream);
-  if (in.M <= 8) return run_stream<Op, 1, 1, 8, 6, Epi>(in, epi, stream);
-  if (in.M <= 16) return run_stream<Op, 2, 1, 8, 4, Epi>(in, epi, stream);
-  return run_stream<Op, 4, 2, 4, 4, Epi>(in, epi, stream);
+  switch (streams(in, Epi::kGated ? 2 : 1)) {
+    case Stream::k8: return run_stream<Op, 1, 1, 8, 6, Epi>(in, epi, stream);
+    case Stream::k16: return run_stream<Op, 2, 1, 8, 4, Epi>(in, epi, stream);
+    case Stream::k32: return run_stream<Op, 4, 1, 6, 3, Epi>(in, epi, stream);
+    case Stream::k32Wide: return run_stream<Op, 4, 2, 4, 4, Epi>(in, epi, stream);
+    default: return run_tiles<Op, Epi::kGated ? kGatedForm : kPlainForm>(in, epi, part, stream);
+  }
 }
 
 // ---------------------------------------------------------------- int8 quantisation
@@ -782,7 +793,7 @@ DenseIn sizes(int64_t M, int64_t N, int64_t kbytes) {
   return in;
 }
 size_t product_workspace(const DenseIn &in, int nb) {
-  if (in.M == 0 || streams(in, nb)) return 0;
+  if (in.M == 0 || streams(in, nb) != Stream::kNo) return 0;
   return (size_t)part_bytes(in, nb, choose(in, nb, true).splits);
 }
 size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
