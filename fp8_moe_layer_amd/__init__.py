@@ -364,12 +364,14 @@ def combine(dm: Dims, perm: dict, y, topk_ids, topk_w, stream=None):
 # --------------------------------------------------------------------------- dense feed-forward
 
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # MOE_T_*
+_TYPES16 = {torch.bfloat16: 1, torch.float16: 2}
 
 
-def _type(dtype, allowed=tuple(_TYPES)):
-    if dtype not in allowed:
+def _type(dtype, allowed=_TYPES):
+    kind = allowed.get(dtype)
+    if kind is None:
         raise TypeError(f"expected one of {[str(t) for t in allowed]}, got {dtype}")
-    return _TYPES[dtype]
+    return kind
 
 
 if hasattr(torch._C, "_cuda_getCurrentRawStream"):
@@ -386,15 +388,16 @@ class _Call:
     runs with that device current.  A small product takes the GPU 3 us, so the
     checks are kept cheap: torch.cuda.current_stream alone builds an object in
     1.9 us, the raw handle comes in 0.1."""
-    __slots__ = ("dev", "stream", "alloc")
+    __slots__ = ("dev", "index", "stream", "alloc")
 
     def __init__(self, first: torch.Tensor, stream):
-        dev = self.dev = first.device
-        if dev.type != "cuda":
+        if not first.is_cuda:
             raise ValueError("fp8_moe_layer_amd works on device tensors only")
+        dev = self.dev = first.device
+        self.index = first.get_device()
         self.alloc = stream
         if stream is None:
-            self.stream = _raw_stream(dev.index)
+            self.stream = _raw_stream(self.index)
         else:
             if stream.device != dev:
                 raise ValueError(f"stream is on {stream.device}, tensors on {dev}")
@@ -412,14 +415,14 @@ class _Call:
     def ptr(self, t: torch.Tensor, shape, dtype, name: str):
         """Address of a contiguous tensor of that shape and type on the call's device."""
         if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
-                or t.device != self.dev):
+                or t.get_device() != self.index):
             self._refuse(t, shape, dtype, name)
         return t.data_ptr()
 
     def rows(self, t: torch.Tensor, shape, dtype, name: str):
         """(address, row stride in elements) of a 2-D tensor whose rows are
         contiguous; the library checks the stride."""
-        if t.dtype is not dtype or t.shape != shape or t.device != self.dev:
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != self.index:
             self._refuse(t, shape, dtype, name)
         ld, unit = t.stride()
         if unit != 1 and t.shape[1] > 1:
@@ -444,7 +447,7 @@ class _Call:
         return None, None, 0
 
     def run(self, fn, *args):
-        if torch.cuda.current_device() == self.dev.index:
+        if torch.cuda.current_device() == self.index:
             status = fn(*args, self.stream)
         else:
             with torch.cuda.device(self.dev):
@@ -454,9 +457,10 @@ class _Call:
 
 
 def _shape2(t: torch.Tensor, name: str):
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected 2 dimensions, got {t.dim()}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: expected 2 dimensions, got {len(shape)}")
+    return shape
 
 
 def quantize_rows_i8(x: torch.Tensor, q: Optional[torch.Tensor] = None,
@@ -514,9 +518,6 @@ def gated_ffn_i8(xq: torch.Tensor, sx: torch.Tensor, w_gate: torch.Tensor, s_gat
           c.ptr(s_up, (f,), torch.float32, "s_up"), T, d, f, kind,
           c.ptr(h, (T, f), h.dtype, "out"), at, size)
     return h
-
-
-_TYPES16 = (torch.bfloat16, torch.float16)
 
 
 def _no_autograd(fn: str, *tensors):
