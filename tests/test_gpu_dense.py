@@ -299,6 +299,17 @@ def test_gated_far_values():
         within(h, ref, 400 * U * ref.abs())
 
 
+@pytest.mark.parametrize("T", [1, 20, 70, 300])
+@pytest.mark.parametrize("dtype,small,w", [(torch.float16, 2.0 ** -20, 1.0),
+                                           (torch.bfloat16, 2.0 ** -130, 2.0 ** 60)])
+def test_subnormal_operands_count(dtype, small, w, T):
+    """Powers of two, so the sums are exact: flushed operands would give 0."""
+    x = torch.full((T, 64), small, device=dev()).to(dtype)
+    wt = torch.full((64, 64), w, device=dev()).to(dtype)
+    _, gate, up = lib().gated_ffn(x, wt, wt, save=True)
+    assert bool((gate == 64 * small * w).all()) and torch.equal(gate, up)
+
+
 def backward_ref(dh, x, wg, wu, gate, up, dtype):
     """Gradients from the kept products in 64 bits, each with its bound."""
     dh, x, wg, wu, g, u = (t.double() for t in (dh, x, wg, wu, gate, up))
