@@ -561,7 +561,10 @@ def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor,
     """Gradients of gated_ffn (moe_gated_ffn_backward) from dh [T, f] (rows
     may be strided) and the gate, up that gated_ffn(save=True) returned:
     (dx, dw_gate, dw_up) in x's type, written over whatever dx, dw_gate, dw_up
-    held.  workspace: uint8, gated_ffn_backward_workspace_bytes(T, d, f) or
+    held.  In fp16 the gradients of the two products are held times one power
+    of two, so that neither an unscaled loss nor values past 65504 on the way
+    to ordinary gradients lose them (up to 2^24, see the C call).
+    workspace: uint8, gated_ffn_backward_workspace_bytes(T, d, f) or
     more, 256-byte aligned; allocated here when not given."""
     (T, d), (f, _) = _shape2(x, "x"), _shape2(w_gate, "w_gate")
     _no_autograd("gated_ffn_backward", dh, x, w_gate, w_up, gate, up)

@@ -168,20 +168,30 @@ struct EpiGated {
   }
 };
 
-// A plain product: rows below `split` go to y0, the others to y1.
+// A plain product: rows below `split` go to y0, the others to y1.  unit: what
+// one of the fp16 operand's units is worth (see grad_factor), or NULL.
 template <class T>
 struct EpiPlain {
   static constexpr bool kGated = false;
+  static constexpr bool kUnits = std::is_same<T, _Float16>::value;
   T *y0, *y1;
   int32_t split, N;
+  const float *unit;
   template <int CNT>
-  struct Chan {};
+  struct Chan {
+    float unit;
+  };
   template <int CNT>
-  __device__ __forceinline__ void load(Chan<CNT> &, int) const {}
+  __device__ __forceinline__ void load(Chan<CNT> &c, int) const {
+    c.unit = kUnits && unit ? *unit : 1.0f;
+  }
   template <int CNT>
-  __device__ __forceinline__ void store(const Chan<CNT> &, int t, int ch, const float (&a)[1][CNT]) const {
+  __device__ __forceinline__ void store(const Chan<CNT> &c, int t, int ch, const float (&a)[1][CNT]) const {
     T *row = t < split ? y0 + (int64_t)t * N : y1 + (int64_t)(t - split) * N;
-    store_run<T, CNT>(row + ch, a[0], N - ch);
+    float v[CNT];
+#pragma unroll
+    for (int i = 0; i < CNT; ++i) v[i] = kUnits ? a[0][i] * c.unit : a[0][i];
+    store_run<T, CNT>(row + ch, v, N - ch);
   }
 };
 
@@ -273,7 +283,8 @@ __device__ __forceinline__ void store_tile(const DenseIn &in, const Epi &epi,
       epi.store(chan, t, ch, a);
     }
   } else {
-    const typename Epi::template Chan<8> chan{};
+    typename Epi::template Chan<8> chan;
+    epi.load(chan, 0);  // nothing of a channel's own
     const int row = lane >> 4;  // of sixteen lanes
     static_assert(S::NJ % 2 == 0, "sub-tiles in pairs");
 #pragma unroll
@@ -751,12 +762,61 @@ hipError_t quantize_i8_as(const T *x, int64_t ldx, int rows, int cols, int8_t *q
 // products that follow take 16-bit operands.  dgu [T][2f]: a token's dg, then
 // its du.  Eight channels a thread; f is a multiple of 64.  Bound by memory: 4096
 // x 14336 (822 MB) 172-187 us, 4.4-4.8 TB/s; a copy reaches 4.9.
+//
+// bf16 has fp32's range.  fp16 has not: gradients of an unscaled loss lie among
+// its subnormal numbers, those of a scaled one pass 65504 before the sums,
+// whose weights are far below 1.  So in fp16 dg and du are multiplied by a power
+// of two, one for the whole call, because it has to leave both dx's sums over
+// channels and dW's over tokens: grad_factor of the largest.  It is known only
+// when all of them are; they are stored as they are, with each workgroup's
+// largest, and a second launch, which ends at once where the factor is 1,
+// writes them again where it is not (its workgroups all find the same factor).
+// The sums are multiplied by the factor's inverse before they are rounded.
+// The second launch costs 3.3 us (backward 2047 x 2048 x 768 fp16 40.4 -> 43.7
+// us, 4096 x 4096 x 14336 1759 -> 1767), and a second pass where it writes: 45.3
+// and 1909.
+constexpr float kGradLow = 0.25f;           // see grad_factor
+constexpr float kGradHigh = 65504.0f;       // fp16's largest
+constexpr float kGradCounted = 0x1p24f;
+constexpr int kGradGroups = 8 * kCUs;       // workgroups, and their largest values
+constexpr size_t kGradScratch = ((size_t)kGradGroups + 64) * 4;  // and the unit
+
+// The power of two that brings `largest` to 2^14 .. 65504.  1 from 2^-2 up to 65504:
+// then what is below fp16's normal numbers is below 2^-12 of the largest, and
+// held to within 2^-23 of it.
+__device__ __forceinline__ float grad_factor(float largest) {
+  if (largest == 0.0f || (largest >= kGradLow && largest <= kGradHigh)) return 1.0f;
+  const int e = (int)(__float_as_uint(largest) >> 23) - 127;  // floor(log2), -127 where subnormal
+  const int up = 15 - e < 100 ? 15 - e : 100;
+  const float k = __uint_as_float((uint32_t)(127 + up) << 23);
+  return largest * k > kGradHigh ? 0.5f * k : k;
+}
+// A value's part in the largest: what is not finite has none, nor what is over
+// 2^24, so that a token which has gone astray does not take the others' bits.
+// (dx of a finite value over 2^24 would pass 65504 with weights of d^-1/2 even
+// for the longest d.)  Such a value ends as an infinity.
+__device__ __forceinline__ float grad_counted(float v) {
+  const float a = fabsf(v);
+  return a <= kGradCounted ? a : 0.0f;
+}
+
+// The largest of the workgroup's values (256 threads), in all of them.
+__device__ __forceinline__ float group_max(float v) {
+  __shared__ float red[256 / kWave];
+  v = wave_max(v);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+}
+
+// One workgroup's share of dgu, multiplied by k; the largest counted value of a thread.
 template <class T>
-__global__ __launch_bounds__(256) void gate_grad_kernel(const T *__restrict__ dh, int64_t lddh,
-                                                        const float *__restrict__ gate,
-                                                        const float *__restrict__ up, int64_t runs,
-                                                        int f, T *__restrict__ dgu) {
+__device__ __forceinline__ float gate_grad_share(const T *dh, int64_t lddh, const float *gate,
+                                                 const float *up, int64_t runs, int f, T *dgu,
+                                                 float k) {
+  constexpr bool kUnits = EpiPlain<T>::kUnits;
   const int per = f / 8;  // runs of a row
+  float largest = 0.0f;
   for (int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x; r < runs; r += (int64_t)gridDim.x * 256) {
     const int64_t t = r / per;
     const int c = (int)(r - t * per) * 8;
@@ -771,8 +831,14 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const T *__restrict__ dh
       for (int i = 0; i < 4; ++i) {
         const float g = g4[i], u = u4[i], dv = Elem<T>::get(d[4 * h + i]);
         const float s = __builtin_amdgcn_rcpf(1.0f + exp_neg(g));
-        a[4 * h + i] = Elem<T>::put(dv * u * s * (1.0f + g * (1.0f - s)));
-        b[4 * h + i] = Elem<T>::put(dv * g * s);
+        float dg = dv * u * s * (1.0f + g * (1.0f - s)), du = dv * g * s;
+        if constexpr (kUnits) {
+          largest = fmaxf(largest, fmaxf(grad_counted(dg), grad_counted(du)));
+          dg *= k;
+          du *= k;
+        }
+        a[4 * h + i] = Elem<T>::put(dg);
+        b[4 * h + i] = Elem<T>::put(du);
       }
     }
     v4i aw, bw;
@@ -782,6 +848,35 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const T *__restrict__ dh
     *reinterpret_cast<v4i *>(out) = aw;
     *reinterpret_cast<v4i *>(out + f) = bw;
   }
+  return largest;
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void gate_grad_kernel(const T *__restrict__ dh, int64_t lddh,
+                                                        const float *__restrict__ gate,
+                                                        const float *__restrict__ up, int64_t runs,
+                                                        int f, T *__restrict__ dgu,
+                                                        float *__restrict__ largest) {
+  float v = gate_grad_share<T>(dh, lddh, gate, up, runs, f, dgu, 1.0f);
+  if constexpr (EpiPlain<T>::kUnits) {
+    v = group_max(v);
+    if (threadIdx.x == 0) largest[blockIdx.x] = v;
+  }
+}
+
+// dgu again, times the factor of the n largest values, unless that is 1; *unit:
+// the factor's inverse.
+__global__ __launch_bounds__(256) void gate_scale_kernel(const _Float16 *__restrict__ dh, int64_t lddh,
+                                                         const float *__restrict__ gate,
+                                                         const float *__restrict__ up, int64_t runs,
+                                                         int f, _Float16 *__restrict__ dgu,
+                                                         const float *__restrict__ largest, int n,
+                                                         float *__restrict__ unit) {
+  float v = 0.0f;
+  for (int i = threadIdx.x; i < n; i += 256) v = fmaxf(v, largest[i]);
+  const float k = grad_factor(group_max(v));
+  if (blockIdx.x == 0 && threadIdx.x == 0) *unit = 1.0f / k;
+  if (k != 1.0f) gate_grad_share<_Float16>(dh, lddh, gate, up, runs, f, dgu, k);
 }
 
 // A product's operands as far as the choice of its form goes.
@@ -825,24 +920,29 @@ hipError_t gated_as(const Gated16 &p, hipStream_t stream) {
 template <class Op, class E>
 hipError_t backward_as(const Gated16Backward &p, hipStream_t stream) {
   E *dgu = (E *)p.workspace;
+  float *largest = (float *)(p.workspace + dgu_bytes(p.T, p.f)), *unit = largest + kGradGroups;
   const int64_t two_f = 2 * (int64_t)p.f;
   if (p.T > 0) {
     const int64_t runs = (int64_t)p.T * p.f / 8, blocks = (runs + 255) / 256;
-    gate_grad_kernel<E><<<(unsigned)(blocks < 8 * kCUs ? blocks : 8 * kCUs), 256, 0, stream>>>(
-        (const E *)p.dh, p.lddh, p.gate, p.up, runs, p.f, dgu);
+    const int groups = (int)(blocks < kGradGroups ? blocks : kGradGroups);
+    gate_grad_kernel<E><<<groups, 256, 0, stream>>>((const E *)p.dh, p.lddh, p.gate, p.up, runs, p.f,
+                                                    dgu, largest);
+    if constexpr (EpiPlain<E>::kUnits)
+      gate_scale_kernel<<<groups, 256, 0, stream>>>((const E *)p.dh, p.lddh, p.gate, p.up, runs, p.f,
+                                                    dgu, largest, groups, unit);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   // dx [T][d]: K runs over the 2f channels, down the rows of the two weight matrices
   const DenseIn dx{(const uint8_t *)dgu, (const uint8_t *)p.w_gate, (const uint8_t *)p.w_up,
                    two_f * 2, (int64_t)p.d * 2, p.T, p.d, two_f * 2, p.f};
-  const EpiPlain<E> to_dx{(E *)p.dx, nullptr, p.T, p.d};
+  const EpiPlain<E> to_dx{(E *)p.dx, nullptr, p.T, p.d, unit};
   // dW [2f][d]: K runs over the tokens, down the rows of dgu and x.  No tokens:
   // K = 0, no tile of dx, and the weights' gradients come out as zeros
   const DenseIn dw{(const uint8_t *)dgu, (const uint8_t *)p.x, nullptr, two_f * 2, p.ldx * 2,
                    2 * p.f, p.d, (int64_t)p.T * 2, p.T};
-  const EpiPlain<E> to_dw{(E *)p.dw_gate, (E *)p.dw_up, p.f, p.d};
-  return run_pair<Op>(dx, to_dx, dw, to_dw, p.workspace + dgu_bytes(p.T, p.f), stream);
+  const EpiPlain<E> to_dw{(E *)p.dw_gate, (E *)p.dw_up, p.f, p.d, p.T > 0 ? unit : nullptr};
+  return run_pair<Op>(dx, to_dx, dw, to_dw, p.workspace + dgu_bytes(p.T, p.f) + kGradScratch, stream);
 }
 
 }  // namespace
@@ -881,12 +981,12 @@ size_t gated_i8_workspace(int32_t T, int32_t d, int32_t f) {
 size_t gated_workspace(int32_t T, int32_t d, int32_t f) {
   return product_workspace(sizes(T, f, 2 * (int64_t)d), 2);
 }
-// dgu, and the parts of dx's and then of dW's products
+// dgu, its largest values, and the parts of dx's and then of dW's products
 size_t gated_backward_workspace(int32_t T, int32_t d, int32_t f) {
   const DenseIn dx = sizes(T, d, 4 * (int64_t)f), dw = sizes(2 * (int64_t)f, d, 2 * (int64_t)T);
   const int64_t a = T > 0 ? part_bytes(dx, 1, choose(dx, 1, true).splits) : 0;
   const int64_t b = part_bytes(dw, 1, choose(dw, 1, true).splits);
-  return dgu_bytes(T, f) + (size_t)(a > b ? a : b);
+  return dgu_bytes(T, f) + kGradScratch + (size_t)(a > b ? a : b);
 }
 
 hipError_t launch_gated_backward(const Gated16Backward &p, hipStream_t stream) {

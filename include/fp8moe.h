@@ -390,7 +390,12 @@ moe_status moe_gated_ffn(const void *x, int64_t ldx, const void *w_gate, const v
  *   dx = dg w_gate + du w_up   [T][d],
  *   dw_gate = dg^T x, dw_up = du^T x   [f][d],
  * fp32 sums, each output rounded once to `type` and overwritten (not added
- * to).  The workspace (moe_gated_ffn_backward_workspace_bytes) is required. */
+ * to).  With MOE_T_F16, dg and du are held times a power of two, one for the
+ * call: 1 where the largest of them, M, is from 2^-2 to 65504, else the one that
+ * brings M to 2^14 .. 65504 (M >= 2^-85).  So each is off by at most half an
+ * fp16 step of its own or M * 2^-39, whichever is more (2^-25 where the factor
+ * is 1).  Values over 2^24 have no part in M and may become infinite.
+ * The workspace (moe_gated_ffn_backward_workspace_bytes) is required. */
 size_t moe_gated_ffn_backward_workspace_bytes(int32_t T, int32_t d, int32_t f);
 moe_status moe_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, int64_t ldx,
                                   const void *w_gate, const void *w_up, const float *gate,

@@ -1,0 +1,114 @@
+"""Dense feed-forward operators at the ends of their types' ranges, on the GPU,
+against 64 bits: gradients of small and of large dh.  The bounds are those of
+test_gpu_dense.py, where not said otherwise."""
+import pytest
+import torch
+
+from gpu_common import dev, lib
+from test_gpu_dense import F16S, HALF, TINY, U, gen, normal, within
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ gradients, small and large
+
+def factor_floor(dg, du):
+    """Half the smallest step of dg and du as they are held in fp16: they are
+    multiplied by a power of two that brings the largest M of them (of those up
+    to 2^24) to 2^15 .. 65504, where M is not in 2^-2 .. 65504 already.  So the
+    step is 2^-24, or at most 2^-24 * M / 2^14 (M * factor >= 2^14 in any case)."""
+    a = torch.cat([dg.abs().flatten(), du.abs().flatten()])
+    m = float(a[a <= 2.0 ** 24].max())
+    return max(2.0 ** -39 * m, TINY[torch.float16] if 0.24 < m < 65600 else 0.0)
+
+
+def gradients_of(dh, x, wg, wu, gate, up):
+    """Of the definition in 64 bits, each with its bound."""
+    dtype = dh.dtype
+    d64 = [t.double() for t in (dh, x, wg, wu, gate, up)]
+    dh, x, wg, wu, g, u = d64
+    s = torch.sigmoid(g)
+    dg, du = dh * u * s * (1 + g * (1 - s)), dh * g * s
+    floor = factor_floor(dg, du) if dtype == torch.float16 else TINY[dtype]
+    eg = (dh * u).abs() * s * (1 + g.abs()) * 24 * U + HALF[dtype] * dg.abs() * (1 + 2 ** -8) + floor
+    eu = du.abs() * 12 * U + HALF[dtype] * du.abs() * (1 + 2 ** -8) + floor
+    sums = lambda k: (k / 32 + 32) * 2 * U
+    ag, au, ax = (dg.abs() + eg).t().contiguous(), (du.abs() + eu).t().contiguous(), x.abs()
+    f, T = wg.shape[0], x.shape[0]
+    tx = eg @ wg.abs() + eu @ wu.abs() + sums(2 * f) * (ag.t() @ wg.abs() + au.t() @ wu.abs())
+    tg = eg.t().contiguous() @ ax + sums(T) * (ag @ ax)
+    tu = eu.t().contiguous() @ ax + sums(T) * (au @ ax)
+    return ((dg @ wg + du @ wu, dg.t().contiguous() @ x, du.t().contiguous() @ x), (tx, tg, tu))
+
+
+# one launch for both, both cut, both in tiles, one token, one of them cut
+RANGE_SIZES = [(70, 256, 320), (40, 2048, 64), (7, 640, 1088), (1, 128, 64), (600, 64, 192), (8192, 128, 64)]
+
+
+@pytest.mark.parametrize("dtype", F16S)
+@pytest.mark.parametrize("std", [2.0 ** -22, 2.0 ** -20, 2.0 ** -14, 2.0 ** -7, 2.0 ** 10, 2.0 ** 14])
+@pytest.mark.parametrize("T,d,f", RANGE_SIZES)
+def test_gradients_of_any_magnitude(T, d, f, std, dtype):
+    """dh from fp16's smallest values to its largest, u of 30 where dh is
+    large, so that dg and du pass 65504 though no gradient does."""
+    g = gen(T + f)
+    big = std > 1
+    dh = normal(g, (T, f), std, dtype)
+    dh = torch.where(dh.isfinite(), dh, torch.zeros_like(dh))  # 2^14: four standard deviations
+    # so that dx and dW are ordinary numbers of the type
+    scale = 2.0 ** -13 if big else 16.0
+    x = normal(g, (T, d), scale, dtype)
+    wg, wu = normal(g, (f, d), scale, dtype), normal(g, (f, d), scale, dtype)
+    gate, up = normal(g, (T, f), 2.0), normal(g, (T, f), 30.0 if big else 1.0)
+    got = lib().gated_ffn_backward(dh, x, wg, wu, gate, up)
+    refs, tols = gradients_of(dh, x, wg, wu, gate, up)
+    for o, ref, tol, name in zip(got, refs, tols, ("dx", "dw_gate", "dw_up")):
+        within(o, ref, tol, f"T={T} d={d} f={f} {dtype} std {std} {name}")
+    again = lib().gated_ffn_backward(dh, x, wg, wu, gate, up)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+def test_gradients_that_are_not_finite_stay_where_they_are():
+    """A token whose gradient is infinite or absurdly large does not choose
+    the factor of the others, which are small."""
+    g = gen(3)
+    T, d, f = 70, 256, 320
+    dtype = torch.float16
+    dh = normal(g, (T, f), 2.0 ** -18, dtype)
+    x, wg, wu = normal(g, (T, d), 1.0, dtype), normal(g, (f, d), 1.0, dtype), normal(g, (f, d), 1.0, dtype)
+    gate, up = normal(g, (T, f), 2.0), normal(g, (T, f))
+    want = lib().gated_ffn_backward(dh, x, wg, wu, gate, up)[0]
+    keep = torch.arange(T, device=dev()) != 33
+    for value in (torch.inf, torch.nan):
+        bad = dh.clone()
+        bad[33, 5] = value
+        assert torch.equal(lib().gated_ffn_backward(bad, x, wg, wu, gate, up)[0][keep], want[keep])
+    far = up.clone()
+    far[33, 7], bad = 1e35, dh.clone()
+    bad[33, 7] = 1.0
+    got = lib().gated_ffn_backward(bad, x, wg, wu, gate, far)[0]
+    # du of that channel is 1 * SiLU(gate), which is an ordinary value: factor 1
+    refs, tols = gradients_of(bad, x, wg, wu, gate, far)
+    within(got[keep], refs[0][keep], tols[0][keep] + 2 * f * TINY[dtype] * float(wg.abs().max()))
+
+
+@pytest.mark.parametrize("T,d,f", [(70, 256, 320), (40, 2048, 64)])
+def test_captured_with_gradients_of_changing_magnitude(T, d, f):
+    g = gen(4)
+    dtype = torch.float16
+    x, dh = normal(g, (T, d), 1, dtype), normal(g, (T, f), 1, dtype)
+    wg, wu = normal(g, (f, d), d ** -0.5, dtype), normal(g, (f, d), d ** -0.5, dtype)
+    gate, up = normal(g, (T, f), 2.0), normal(g, (T, f))
+    step = lambda: lib().gated_ffn_backward(dh, x, wg, wu, gate, up)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for std in (1.0, 2.0 ** -18, 2.0 ** 9, 0.5, 2.0 ** -20, 0.0):
+        dh.copy_(normal(g, (T, f), std, dtype))
+        up.copy_(normal(g, (T, f), 100.0 if std > 1 else 1.0))
+        eager = [t.clone() for t in step()]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(captured, eager)), std
