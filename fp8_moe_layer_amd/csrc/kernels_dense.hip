@@ -71,10 +71,16 @@ __device__ __forceinline__ void store_run(T *dst, const float (&v)[CNT], int val
   }
 }
 
-// SiLU(g) * u with the reciprocal instruction (1 ulp) for the divide.
-__device__ __forceinline__ float silu_mul(float g, float u) {
-  return g * __builtin_amdgcn_rcpf(1.0f + exp_neg(g)) * u;
+// 1 / (1 + e^-g) with the reciprocal instruction (1 ulp) for the divide.  g is
+// held within +-130, where e^-g is 0 or infinite already: past 2.36e38 the
+// exponent g * log2(e) would overflow, and the exponential's compensation make a
+// NaN of it.
+__device__ __forceinline__ float sigmoid(float g) {
+  return __builtin_amdgcn_rcpf(1.0f + exp_neg(__builtin_amdgcn_fmed3f(g, -130.0f, 130.0f)));
 }
+
+// SiLU(g) * u.
+__device__ __forceinline__ float silu_mul(float g, float u) { return g * sigmoid(g) * u; }
 
 // ---------------------------------------------------------------- epilogues
 // An epilogue takes a lane's 4*NJ consecutive channels of one token.
@@ -830,8 +836,9 @@ __device__ __forceinline__ float gate_grad_share(const T *dh, int64_t lddh, cons
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float g = g4[i], u = u4[i], dv = Elem<T>::get(d[4 * h + i]);
-        const float s = __builtin_amdgcn_rcpf(1.0f + exp_neg(g));
-        float dg = dv * u * s * (1.0f + g * (1.0f - s)), du = dv * g * s;
+        // the factors of s first: where s is 0, dv * u or dv * g may be infinite
+        const float s = sigmoid(g);
+        float dg = dv * (u * (s * (1.0f + g * (1.0f - s)))), du = dv * (g * s);
         if constexpr (kUnits) {
           largest = fmaxf(largest, fmaxf(grad_counted(dg), grad_counted(du)));
           dg *= k;

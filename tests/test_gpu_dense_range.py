@@ -1,11 +1,12 @@
 """Dense feed-forward operators at the ends of their types' ranges, on the GPU,
-against 64 bits: gradients of small and of large dh.  The bounds are those of
+against 64 bits: gradients of small and of large dh, values near fp32's
+largest.  The bounds are those of
 test_gpu_dense.py, where not said otherwise."""
 import pytest
 import torch
 
 from gpu_common import dev, lib
-from test_gpu_dense import F16S, HALF, TINY, U, gen, normal, within
+from test_gpu_dense import F16S, FLOATS, HALF, TINY, U, gen, normal, within
 
 pytestmark = pytest.mark.gpu
 
@@ -112,3 +113,70 @@ def test_captured_with_gradients_of_changing_magnitude(T, d, f):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(captured, eager)), std
+
+
+# ------------------------------------------------------------------ far values
+
+FAR = [2.3e38, 2.4e38, 2.9e38, 3.3e38, 1e30, 200.0, 0.0]
+
+
+@pytest.mark.parametrize("T", [14, 40, 300])
+def test_silu_up_to_the_largest_numbers(T):
+    """h is g * u for a large g and 0 for a large negative one, never NaN: bf16
+    and int8 operands reach every fp32 value."""
+    far = torch.tensor([s * v for v in FAR for s in (1, -1)], device=dev()).repeat(-(-T // 14))[:T]
+    d = f = 64
+    x = torch.zeros((T, d), device=dev())
+    x[:, 0] = far / 2.0 ** 64
+    wg, wu = torch.zeros((f, d), device=dev()), torch.zeros((f, d), device=dev())
+    wg[:, 0], wu[:, 0] = 2.0 ** 64, 2.0 ** -64 / 2.0 ** 10
+    b16 = lambda t: t.to(torch.bfloat16)
+    h, gate, up = lib().gated_ffn(b16(x), b16(wg), b16(wu), save=True)
+    g, u = gate.double(), up.double()
+    assert bool(gate.isfinite().all()) and float(gate.max()) > 3e38
+    ref = g * torch.sigmoid(g) * u
+    within(h, ref, 400 * U * ref.abs())
+
+    xq = torch.zeros((T, d), dtype=torch.int8, device=dev())
+    xq[:, 0] = 1
+    wq = xq[:1].expand(f, d).contiguous()
+    sg, su = torch.full((f,), 2.0 ** 64, device=dev()), torch.full((f,), 2.0 ** -74, device=dev())
+    for kind in FLOATS:
+        h = lib().gated_ffn_i8(xq, far / 2.0 ** 64, wq, sg, wq, su, out_dtype=kind)
+        g = far.double()[:, None].expand(T, f)
+        ref = g * torch.sigmoid(g) * (g * 2.0 ** -138)
+        if kind == torch.float16:
+            ref = torch.where(ref > 65520, torch.full_like(ref, torch.inf), ref)
+            assert torch.equal(h[ref.isinf()].double(), ref[ref.isinf()])
+            h, ref = h[~ref.isinf()], ref[~ref.isinf()]
+        within(h, ref, 400 * U * ref.abs())
+
+
+def test_gradients_up_to_the_largest_numbers():
+    """dg and du where g, u or dh is near the largest fp32 or bf16 number and
+    the gradient itself is not: each is an ordinary number or 0, never NaN."""
+    T, d, f = 4, 64, 64
+    dtype = torch.bfloat16
+    g = torch.zeros((T, f), device=dev())
+    u, dh = torch.full((T, f), 2.0 ** -100, device=dev()), torch.full((T, f), 2.0 ** -60, device=dev())
+    for i, v in enumerate(FAR):
+        g[:, 2 * i], g[:, 2 * i + 1] = v, -v
+    u[:, 20], g[:, 20] = 3e38, -200.0           # dh * u is finite, s = 0
+    u[:, 21], g[:, 21], dh[:, 21] = 3e38, -200.0, 2.0 ** 100   # dh * u would be infinite
+    dh[:, 22], g[:, 22] = 2.0 ** 120, -1e30     # dh * g would be infinite
+    dh[:, 23], g[:, 23], u[:, 23] = 2.0 ** 120, -120.0, 2.0 ** 60
+    x = torch.full((T, d), 1.0, device=dev()).to(dtype)
+    w = torch.full((f, d), 2.0 ** -60, device=dev()).to(dtype)
+    got = lib().gated_ffn_backward(dh.to(dtype), x, w, w, g, u)
+    s = torch.sigmoid(g.double())
+    dhd = dh.to(dtype).double()
+    dg, du = dhd * u.double() * s * (1 + g.double() * (1 - s)), dhd * g.double() * s
+    assert all(bool(t.isfinite().all()) for t in got)
+    refs, tols = gradients_of(dh.to(dtype), x, w, w, g, u)
+    # channels of s = e^-200 and e^-120: their sigmoid is 0 in fp32
+    small = (g <= -100)
+    lost_g, lost_u = torch.where(small, dg.abs(), 0 * dg), torch.where(small, du.abs(), 0 * du)
+    wd, xd = w.double(), x.double()
+    extra = (lost_g @ wd + lost_u @ wd, lost_g.t().contiguous() @ xd, lost_u.t().contiguous() @ xd)
+    for o, ref, tol, e, name in zip(got, refs, tols, extra, ("dx", "dw_gate", "dw_up")):
+        within(o, ref, tol + e, name)
