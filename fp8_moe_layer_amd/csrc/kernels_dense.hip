@@ -622,6 +622,10 @@ hipError_t run_product(const DenseIn &in, const Epi &epi, void *part, hipStream_
 // fma(x, r, 1.5 * 2^23) is that rounding itself, of the exact product and in
 // one step: the sum's last place is 1, and its low byte the code in two's
 // complement (|x * r| <= 127 * (1 + 2^-24)^2, which rounds to at most 127).
+// The maximum is taken of the values' bits without the sign: as integers they
+// order like the magnitudes, with NaN above infinity, so a row with a NaN gets
+// a NaN for its scale and one with an infinity an infinite scale (all its codes
+// are 0: a product with it is 0 * inf, NaN), and neither passes for numbers.
 constexpr float kI8Max = 127.0f;
 constexpr float kI8Floor = 0x1p-100f;
 constexpr float kRoundMagic = 12582912.0f;  // 1.5 * 2^23
@@ -630,7 +634,7 @@ struct I8Scale {
   float r, s;
 };
 __device__ __forceinline__ I8Scale i8_scale(float amax) {
-  const float m = fmaxf(amax, kI8Floor);
+  const float m = amax < kI8Floor ? kI8Floor : amax;  // NaN stays
   return I8Scale{kI8Max / m, amax == 0.0f ? 1.0f : m / kI8Max};
 }
 
@@ -647,11 +651,11 @@ struct Run {
     const v4i w = load16(p);
     __builtin_memcpy(v, &w, 16);
   }
-  __device__ __forceinline__ float amax(float m) const {
+  __device__ __forceinline__ int amax(int m) const {
 #pragma unroll
     for (int i = 0; i < kCount; ++i) {
       const float f = Elem<T>::get(v[i]);
-      m = fmaxf(m, fabsf(f));
+      m = max(m, __float_as_int(fabsf(f)));
       if constexpr (kDebugChecks) dcheck(__builtin_isfinite(f), kDbgNonFinite);
     }
     return m;
@@ -668,11 +672,11 @@ struct Run {
 };
 
 // The maximum of each sixteen lanes, in all of them.
-__device__ __forceinline__ float max16(float v) {
-  v = fmaxf(v, dpp_mov<kDppQuadXor1>(v));
-  v = fmaxf(v, dpp_mov<kDppQuadXor2>(v));
-  v = fmaxf(v, dpp_mov<kDppHalfMirror>(v));
-  return fmaxf(v, dpp_mov<kDppMirror>(v));
+__device__ __forceinline__ int max16(int v) {
+  v = max(v, dpp_mov<kDppQuadXor1>(v));
+  v = max(v, dpp_mov<kDppQuadXor2>(v));
+  v = max(v, dpp_mov<kDppHalfMirror>(v));
+  return max(v, dpp_mov<kDppMirror>(v));
 }
 
 // LANES threads to a row (sixteen, a wave, or the workgroup of 256), P runs of
@@ -691,7 +695,7 @@ __global__ __launch_bounds__(256) void quantize_i8_kernel(const T *__restrict__ 
   const int lane = threadIdx.x % LANES;
   const T *xr = x + row * ldx;
   int8_t *qr = q + row * cols;
-  float amax = 0.0f;
+  int amax = 0;  // the bits of a magnitude
   Run<T> v[P > 0 ? P : 1];
   if constexpr (P > 0) {
 #pragma unroll
@@ -709,16 +713,19 @@ __global__ __launch_bounds__(256) void quantize_i8_kernel(const T *__restrict__ 
       amax = v[0].amax(amax);
     }
   }
-  amax = LANES == 16 ? max16(amax) : wave_max(amax);
+  if constexpr (LANES == 16)
+    amax = max16(amax);
+  else
+    amax = wave_reduce(amax, [](int a, int b) { return max(a, b); });
   if constexpr (LANES > kWave) {
-    __shared__ float red[LANES / kWave];
+    __shared__ int red[LANES / kWave];
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = amax;
     __syncthreads();
     amax = red[0];
 #pragma unroll
-    for (int w = 1; w < LANES / kWave; ++w) amax = fmaxf(amax, red[w]);
+    for (int w = 1; w < LANES / kWave; ++w) amax = max(amax, red[w]);
   }
-  const I8Scale k = i8_scale(amax);
+  const I8Scale k = i8_scale(__int_as_float(amax));
   if constexpr (P > 0) {
 #pragma unroll
     for (int j = 0; j < P; ++j) {

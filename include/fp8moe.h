@@ -344,7 +344,9 @@ enum { MOE_T_F32 = 0, MOE_T_BF16 = 1, MOE_T_F16 = 2 }; /* element types */
  * ldx): with a = max |x| of the row and m = max(a, 2^-100),
  *   r = fl(127 / m), scale = fl(m / 127) (1 for an all-zero row),
  *   q = x * r rounded once, to nearest, ties to even (|q| <= 127),
- * so x ~= q * scale within scale * (1/2 + 2^-15).
+ * so x ~= q * scale within scale * (1/2 + 2^-15).  A row that is not finite does
+ * not pass for one that is: with a NaN its scale is NaN and its codes mean
+ * nothing, with an infinity its scale is infinite and its codes are 0.
  * q [rows][cols] contiguous, scale [rows].  cols: a multiple of 16 up to
  * MOE_MAX_I8_K; rows: any up to MOE_MAX_TOKENS. */
 moe_status moe_quantize_rows_i8(const void *x, int32_t x_type, int64_t ldx, int32_t rows,

@@ -1,12 +1,12 @@
 """Dense feed-forward operators at the ends of their types' ranges, on the GPU,
 against 64 bits: gradients of small and of large dh, values near fp32's
-largest.  The bounds are those of
+largest, and rows that are not finite.  The bounds are those of
 test_gpu_dense.py, where not said otherwise."""
 import pytest
 import torch
 
 from gpu_common import dev, lib
-from test_gpu_dense import F16S, FLOATS, HALF, TINY, U, gen, normal, within
+from test_gpu_dense import (F16S, FLOATS, HALF, TINY, U, codes, gen, normal, quantize_ref, scales, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -180,3 +180,35 @@ def test_gradients_up_to_the_largest_numbers():
     extra = (lost_g @ wd + lost_u @ wd, lost_g.t().contiguous() @ xd, lost_u.t().contiguous() @ xd)
     for o, ref, tol, e, name in zip(got, refs, tols, extra, ("dx", "dw_gate", "dw_up")):
         within(o, ref, tol + e, name)
+
+
+# ------------------------------------------------------------------ rows that are not finite
+
+@pytest.mark.parametrize("dtype", FLOATS)
+@pytest.mark.parametrize("cols", [64, 192, 512, 1024, 4096, 8192, 16384, 32784])
+def test_a_row_with_nan_has_a_nan_scale(cols, dtype):
+    """And so everything made from it is NaN; a row with an infinity has an
+    infinite scale; the other rows are what they are alone."""
+    rows = 41
+    x = normal(gen(cols), (rows, cols), 1.0, dtype)
+    rq, rs = quantize_ref(x)
+    bad = x.clone()
+    nan, inf = [0, 7, 18, 40], [3, 22]
+    for i, r in enumerate(nan):
+        bad[r, [0, cols - 1, cols // 2, 33][i]] = torch.nan if i % 2 else -torch.nan
+    bad[18] = torch.nan
+    bad[40, 1] = torch.inf
+    bad[3, cols - 1], bad[22, 5] = torch.inf, -torch.inf
+    q, s = lib().quantize_rows_i8(bad)
+    keep = [i for i in range(rows) if i not in nan + inf]
+    assert bool(s[nan].isnan().all()) and bool((s[inf] == torch.inf).all())
+    assert not bool(q[inf].any())
+    assert torch.equal(s[keep].cpu(), torch.from_numpy(rs)[keep])
+    assert torch.equal(q[keep].cpu(), torch.from_numpy(rq)[keep])
+    if cols <= 4096:
+        g = gen(1)
+        y = lib().matmul_i8(q, s, codes(g, (65, cols)), scales(g, 65))
+        w = codes(g, (64, cols))
+        outs = [y] if cols % 64 else [y, lib().gated_ffn_i8(q, s, w, scales(g, 64), w, scales(g, 64))]
+        for o in outs:
+            assert bool(o[nan + inf].isnan().all()) and bool(o[keep].isfinite().all())
