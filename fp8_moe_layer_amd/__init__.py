@@ -14,6 +14,7 @@ from dataclasses import dataclass
 from typing import Optional
 
 import torch
+import torch.autograd.forward_ad as _forward_ad
 
 _HERE = pathlib.Path(__file__).resolve().parent
 LIB_PATH = _HERE / "libfp8moe.so"
@@ -362,6 +363,8 @@ def combine(dm: Dims, perm: dict, y, topk_ids, topk_w, stream=None):
 
 
 # --------------------------------------------------------------------------- dense feed-forward
+# Plain calls: autograd does not see them, and they refuse what it would have
+# to record (_no_autograd).
 
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # MOE_T_*
 _TYPES16 = {torch.bfloat16: 1, torch.float16: 2}
@@ -463,6 +466,24 @@ def _shape2(t: torch.Tensor, name: str):
     return shape
 
 
+def _no_autograd(fn: str, *tensors):
+    """Refuses what autograd would have to record (or, in forward mode, to
+    push forward): the calls' results do not depend on their inputs as far as
+    it can see, and the gradients would be lost without a word."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise RuntimeError(
+                    f"{fn} is not recorded by autograd: call it under torch.no_grad() or on detached "
+                    "tensors (gated_ffn, inside a torch.autograd.Function, has its gradients from "
+                    "gated_ffn_backward)")
+    # the level that dual tensors live on, -1 outside of all (0 if there is no telling)
+    if getattr(_forward_ad, "_current_level", 0) >= 0:
+        for t in tensors:
+            if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
+                raise RuntimeError(f"{fn} has no forward-mode derivative")
+
+
 def quantize_rows_i8(x: torch.Tensor, q: Optional[torch.Tensor] = None,
                      scale: Optional[torch.Tensor] = None, stream=None):
     """Per-row symmetric int8 quantisation of x [rows, cols] (fp32, bf16 or
@@ -470,6 +491,7 @@ def quantize_rows_i8(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     x ~= codes * scale (moe_quantize_rows_i8).  For activations per token, for
     weight matrices per output channel."""
     rows, cols = _shape2(x, "x")
+    _no_autograd("quantize_rows_i8", x)
     c = _Call(x, stream)
     kind = _type(x.dtype)
     xp, ldx = c.rows(x, x.shape, x.dtype, "x")
@@ -488,6 +510,7 @@ def matmul_i8(xq: torch.Tensor, sx: torch.Tensor, wq: torch.Tensor, sw: torch.Te
     wq [N, K] with a scale per output channel, bias fp32 [N]; y [T, N] in
     out_dtype (or out's type): fp32, bf16 or fp16."""
     (T, K), (N, _) = _shape2(xq, "xq"), _shape2(wq, "wq")
+    _no_autograd("matmul_i8", sx, sw, bias)
     c = _Call(xq, stream)
     y = c.empty((T, N), out_dtype) if out is None else out
     kind = _type(y.dtype)
@@ -507,6 +530,7 @@ def gated_ffn_i8(xq: torch.Tensor, sx: torch.Tensor, w_gate: torch.Tensor, s_gat
     (moe_gated_ffn_i8): w_gate, w_up int8 [f, d] with a scale per channel;
     h [T, f] in out_dtype (or out's type)."""
     (T, d), (f, _) = _shape2(xq, "xq"), _shape2(w_gate, "w_gate")
+    _no_autograd("gated_ffn_i8", sx, s_gate, s_up)
     c = _Call(xq, stream)
     h = c.empty((T, f), out_dtype) if out is None else out
     kind = _type(h.dtype)
@@ -520,21 +544,12 @@ def gated_ffn_i8(xq: torch.Tensor, sx: torch.Tensor, w_gate: torch.Tensor, s_gat
     return h
 
 
-def _no_autograd(fn: str, *tensors):
-    if torch.is_grad_enabled():
-        for t in tensors:
-            if t.requires_grad:
-                raise RuntimeError(
-                    f"{fn} is not recorded by autograd: call it under torch.no_grad() (inside a "
-                    "torch.autograd.Function, say) and take the gradients from gated_ffn_backward")
-
-
 def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
               out: Optional[torch.Tensor] = None, save: bool = False, stream=None):
     """h = SiLU(x w_gate^T) * (x w_up^T) in one kernel (moe_gated_ffn): x
     [T, d] (rows may be strided), w_gate, w_up [f, d], all bf16 or all fp16.
     Returns h [T, f]; with save=True (h, gate, up), the two products in fp32 as
-    gated_ffn_backward takes them.  Autograd does not see the call."""
+    gated_ffn_backward takes them."""
     (T, d), (f, _) = _shape2(x, "x"), _shape2(w_gate, "w_gate")
     _no_autograd("gated_ffn", x, w_gate, w_up)
     c = _Call(x, stream)

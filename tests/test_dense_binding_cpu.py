@@ -1,0 +1,52 @@
+"""The dense operators' Python binding, what it refuses before it looks for a
+GPU: tensors that autograd would have to record."""
+import pytest
+import torch
+import torch.autograd.forward_ad as fwad
+
+fp8 = pytest.importorskip("fp8_moe_layer_amd", reason="libfp8moe.so not built")
+
+
+def _args(dtype=torch.bfloat16):
+    x, w = torch.ones(4, 64, dtype=dtype), torch.ones(64, 64, dtype=dtype)
+    g = torch.ones(4, 64)
+    q, wq, s, sw = torch.ones(4, 64, dtype=torch.int8), torch.ones(64, 64, dtype=torch.int8), torch.ones(4), torch.ones(64)
+    return {
+        "quantize_rows_i8": (dict(x=x), ("x",)),
+        "matmul_i8": (dict(xq=q, sx=s, wq=wq, sw=sw, bias=sw.clone()), ("sx", "sw", "bias")),
+        "gated_ffn_i8": (dict(xq=q, sx=s, w_gate=wq, s_gate=sw, w_up=wq, s_up=sw.clone()),
+                         ("sx", "s_gate", "s_up")),
+        "gated_ffn": (dict(x=x, w_gate=w, w_up=w.clone()), ("x", "w_gate", "w_up")),
+        "gated_ffn_backward": (dict(dh=x, x=x.clone(), w_gate=w, w_up=w.clone(), gate=g, up=g.clone()),
+                               ("dh", "x", "w_gate", "w_up", "gate", "up")),
+    }
+
+
+CASES = [(fn, name) for fn, (_, names) in _args().items() for name in names]
+
+
+@pytest.mark.parametrize("fn,name", CASES)
+def test_what_autograd_would_record_is_refused(fn, name):
+    kw = dict(_args()[fn][0])
+    kw[name] = kw[name].clone().requires_grad_()
+    with pytest.raises(RuntimeError, match=f"{fn} is not recorded by autograd"):
+        getattr(fp8, fn)(**kw)
+    for allowed in (lambda: torch.no_grad(), lambda: torch.inference_mode()):
+        with allowed(), pytest.raises(ValueError, match="device tensors"):  # the next check
+            getattr(fp8, fn)(**kw)
+    kw[name] = kw[name].detach()
+    with pytest.raises(ValueError, match="device tensors"):
+        getattr(fp8, fn)(**kw)
+
+
+@pytest.mark.parametrize("fn,name", CASES)
+def test_forward_mode_tangents_are_refused(fn, name):
+    kw = dict(_args()[fn][0])
+    with fwad.dual_level():
+        plain = dict(kw)
+        kw[name] = fwad.make_dual(kw[name], torch.ones_like(kw[name]))
+        for mode in (torch.enable_grad, torch.no_grad):
+            with mode(), pytest.raises(RuntimeError, match=f"{fn} has no forward-mode derivative"):
+                getattr(fp8, fn)(**kw)
+        with pytest.raises(ValueError, match="device tensors"):
+            getattr(fp8, fn)(**plain)
