@@ -459,10 +459,17 @@ class _Call:
             raise MoEError(status)
 
 
+_INT32_MAX = 0x7fffffff
+
+
 def _shape2(t: torch.Tensor, name: str):
+    """A matrix's shape.  Both sizes reach the library as 32-bit integers, which
+    ctypes cuts off without a word; its own limits are far below."""
     shape = t.shape
     if len(shape) != 2:
         raise ValueError(f"{name}: expected 2 dimensions, got {len(shape)}")
+    if shape[0] > _INT32_MAX or shape[1] > _INT32_MAX:
+        raise ValueError(f"{name}: shape {tuple(shape)} is past the operators' limits")
     return shape
 
 
@@ -565,7 +572,8 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
 
 
 def gated_ffn_backward_workspace_bytes(T: int, d: int, f: int) -> int:
-    return int(_gated_bwd_ws(T, d, f))
+    fit = lambda v: max(-1, min(v, _INT32_MAX))  # both refused, like all past the limits
+    return int(_gated_bwd_ws(fit(T), fit(d), fit(f)))
 
 
 def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor,

@@ -1,5 +1,6 @@
 """The dense operators' Python binding, what it refuses before it looks for a
-GPU: tensors that autograd would have to record."""
+GPU: tensors that autograd would have to record, sizes that its 32-bit integers
+cannot hold."""
 import pytest
 import torch
 import torch.autograd.forward_ad as fwad
@@ -50,3 +51,25 @@ def test_forward_mode_tangents_are_refused(fn, name):
                 getattr(fp8, fn)(**kw)
         with pytest.raises(ValueError, match="device tensors"):
             getattr(fp8, fn)(**plain)
+
+
+HUGE = 2 ** 32 + 4  # 4 in 32 bits
+
+
+@pytest.mark.parametrize("fn,name", [
+    ("quantize_rows_i8", "x"), ("matmul_i8", "xq"), ("matmul_i8", "wq"), ("gated_ffn_i8", "xq"),
+    ("gated_ffn_i8", "w_gate"), ("gated_ffn", "x"), ("gated_ffn", "w_gate"), ("gated_ffn_backward", "x"),
+    ("gated_ffn_backward", "w_gate")])
+def test_sizes_past_32_bits_are_refused(fn, name):
+    for shape in ((HUGE, 64), (4, HUGE)):
+        kw = dict(_args()[fn][0])
+        kw[name] = kw[name][:1, :1].expand(shape)
+        with pytest.raises(ValueError, match=f"{name}: shape .* is past the operators' limits"):
+            getattr(fp8, fn)(**kw)
+
+
+def test_workspace_of_sizes_past_32_bits():
+    assert fp8.gated_ffn_backward_workspace_bytes(4, 64, 64) > 0
+    for bad in ((HUGE, 64, 64), (4, 2 ** 32 + 64, 64), (4, 64, 2 ** 32 + 64), (4 - 2 ** 32, 64, 64)):
+        assert fp8.gated_ffn_backward_workspace_bytes(*bad) == 0
+        assert fp8._last_error()
