@@ -9,6 +9,7 @@ fails loudly when the library has not been built.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import pathlib
 from dataclasses import dataclass
 from typing import Optional
@@ -384,6 +385,19 @@ else:
         return torch.cuda.current_stream(index).cuda_stream
 
 
+def _by_sizes(fn):
+    """A size function of the library, which goes by the three sizes alone, its
+    answers kept: a call through ctypes takes 0.6 us."""
+    @functools.lru_cache(maxsize=4096)
+    def size(T: int, inner: int, outputs: int) -> int:
+        return fn(T, inner, outputs)
+    return size
+
+
+_matmul_i8_size, _gated_ffn_i8_size, _gated_ffn_size = map(
+    _by_sizes, (_matmul_i8_ws, _gated_ffn_i8_ws, _gated_ffn_ws))
+
+
 class _Call:
     """One call of a dense operator: its device (that of the first tensor;
     the others must be on it too) and its stream (default: the device's
@@ -440,13 +454,11 @@ class _Call:
 
     def workspace(self, size, T: int, inner: int, outputs: int):
         """(tensor, address, bytes) of the workspace that the call can use:
-        size(T, inner, outputs) bytes, asked for only where a product is small
-        enough to be cut along its sum."""
-        if T > 32 and ((T + 63) >> 6) * ((outputs + 63) >> 6) <= 128:
-            n = size(T, inner, outputs)
-            if n:
-                ws = self.empty((n,), torch.uint8)
-                return ws, ws.data_ptr(), n
+        size(T, inner, outputs) bytes, most often none."""
+        n = size(T, inner, outputs)
+        if n:
+            ws = self.empty((n,), torch.uint8)
+            return ws, ws.data_ptr(), n
         return None, None, 0
 
     def run(self, fn, *args):
@@ -522,7 +534,7 @@ def matmul_i8(xq: torch.Tensor, sx: torch.Tensor, wq: torch.Tensor, sw: torch.Te
     y = c.empty((T, N), out_dtype) if out is None else out
     kind = _type(y.dtype)
     xp, ldx = c.rows(xq, (T, K), torch.int8, "xq")
-    ws, at, size = c.workspace(_matmul_i8_ws, T, K, N)
+    ws, at, size = c.workspace(_matmul_i8_size, T, K, N)
     c.run(_matmul_i8, xp, ldx, c.ptr(sx, (T,), torch.float32, "sx"),
           c.ptr(wq, (N, K), torch.int8, "wq"), c.ptr(sw, (N,), torch.float32, "sw"),
           None if bias is None else c.ptr(bias, (N,), torch.float32, "bias"), T, K, N, kind,
@@ -542,7 +554,7 @@ def gated_ffn_i8(xq: torch.Tensor, sx: torch.Tensor, w_gate: torch.Tensor, s_gat
     h = c.empty((T, f), out_dtype) if out is None else out
     kind = _type(h.dtype)
     xp, ldx = c.rows(xq, (T, d), torch.int8, "xq")
-    ws, at, size = c.workspace(_gated_ffn_i8_ws, T, d, f)
+    ws, at, size = c.workspace(_gated_ffn_i8_size, T, d, f)
     c.run(_gated_ffn_i8, xp, ldx, c.ptr(sx, (T,), torch.float32, "sx"),
           c.ptr(w_gate, (f, d), torch.int8, "w_gate"),
           c.ptr(s_gate, (f,), torch.float32, "s_gate"), c.ptr(w_up, (f, d), torch.int8, "w_up"),
@@ -564,7 +576,7 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
     h = c.empty((T, f), x.dtype) if out is None else out
     gate, up = (c.empty((T, f), torch.float32), c.empty((T, f), torch.float32)) if save else (None, None)
     xp, ldx = c.rows(x, (T, d), x.dtype, "x")
-    ws, at, size = c.workspace(_gated_ffn_ws, T, d, f)
+    ws, at, size = c.workspace(_gated_ffn_size, T, d, f)
     c.run(_gated_ffn, xp, ldx, c.ptr(w_gate, (f, d), x.dtype, "w_gate"),
           c.ptr(w_up, (f, d), x.dtype, "w_up"), kind, T, d, f, c.ptr(h, (T, f), x.dtype, "out"),
           None if gate is None else gate.data_ptr(), None if up is None else up.data_ptr(), at, size)

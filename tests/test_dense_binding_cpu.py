@@ -73,3 +73,12 @@ def test_workspace_of_sizes_past_32_bits():
     for bad in ((HUGE, 64, 64), (4, 2 ** 32 + 64, 64), (4, 64, 2 ** 32 + 64), (4 - 2 ** 32, 64, 64)):
         assert fp8.gated_ffn_backward_workspace_bytes(*bad) == 0
         assert fp8._last_error()
+
+
+@pytest.mark.parametrize("T,outputs", [(1, 64), (33, 64), (5000, 50000)])
+def test_the_library_alone_says_whether_a_call_gets_a_workspace(T, outputs):
+    call = object.__new__(fp8._Call)
+    call.alloc, call.dev = None, torch.device("cpu")
+    ws, at, n = call.workspace(lambda *sizes: 512 if sizes == (T, 128, outputs) else 0, T, 128, outputs)
+    assert n == 512 and ws.numel() == 512 and at == ws.data_ptr()
+    assert call.workspace(lambda *sizes: 0, T, 128, outputs) == (None, None, 0)
