@@ -94,6 +94,7 @@ _gated_ffn = _sig("moe_gated_ffn", _i32, _vp, _i64, _vp, _vp, _i32, _i32, _i32, 
                   _vp, C.c_size_t, _vp)
 _gated_ffn_ws = _sig("moe_gated_ffn_workspace_bytes", C.c_size_t, _i32, _i32, _i32)
 _gated_bwd_ws = _sig("moe_gated_ffn_backward_workspace_bytes", C.c_size_t, _i32, _i32, _i32)
+_dense_form = _sig("moe_dense_form", _i32, _i32, _i32, _i32, _i32, _i32, C.POINTER(_i32))
 _gated_bwd = _sig("moe_gated_ffn_backward", _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i32,
                   _i32, _i32, _i32, _vp, _vp, _vp, _vp, C.c_size_t, _vp)
 
@@ -619,6 +620,26 @@ def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor,
           c.ptr(dw_gate, (f, d), t16, "dw_gate"), c.ptr(dw_up, (f, d), t16, "dw_up"),
           c.ptr(workspace, workspace.shape, torch.uint8, "workspace"), workspace.numel())
     return dx, dw_gate, dw_up
+
+
+DENSE_OPS = ("matmul_i8", "gated_ffn_i8", "gated_ffn", "gated_ffn_backward")  # MOE_DENSE_*
+_STREAMS = ("stream 8", "stream 16", "stream 32", "stream 32 wide")
+_TILES = ("64x64", "64x128", "128x128", "128x256", "256x256")
+# MOE_FORM_*
+_FORMS = {0: "none", 8: "cut", **{1 + i: n for i, n in enumerate(_STREAMS)},
+          **{16 + i: f"tile {n}" for i, n in enumerate(_TILES)},
+          **{24 + i: f"pair {n}" for i, n in enumerate(_TILES)},
+          **{32 + i: f"pair {n}, dW first" for i, n in enumerate(_TILES)}}
+
+
+def dense_form(op: str, T: int, inner: int, outputs: int):
+    """Names of the kernels that an operator (one of DENSE_OPS) takes for its
+    sizes, as the functions above call it (moe_dense_form): one name, of
+    gated_ffn_backward one for dx and one for dw_gate and dw_up.  A host call."""
+    forms = (_i32 * 2)()
+    _check(_dense_form(DENSE_OPS.index(op), T, inner, outputs, 1, forms))
+    names = tuple(_FORMS[v] for v in forms)
+    return names if op == "gated_ffn_backward" else names[0]
 
 
 # --------------------------------------------------------------------------- whole layer

@@ -9,6 +9,11 @@ using namespace fp8moe;
 
 static_assert(MOE_T_F32 == kTypeF32 && MOE_T_BF16 == kTypeBf16 && MOE_T_F16 == kTypeF16, "types");
 static_assert(MOE_MAX_I8_K == kMaxI8K, "K limit");
+static_assert(MOE_DENSE_MATMUL_I8 == kOpMatmulI8 && MOE_DENSE_GATED_I8 == kOpGatedI8 &&
+                  MOE_DENSE_GATED == kOpGated && MOE_DENSE_GATED_BACKWARD == kOpGatedBackward, "ops");
+static_assert(MOE_FORM_NONE == kFormNone && MOE_FORM_STREAM == kFormStream && MOE_FORM_CUT == kFormCut &&
+                  MOE_FORM_TILE == kFormTile && MOE_FORM_PAIR == kFormPair &&
+                  MOE_FORM_PAIR_SECOND == kFormPairSecond, "forms");
 
 namespace {
 
@@ -271,6 +276,22 @@ moe_status moe_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, i
   const Gated16Backward p{dh, lddh, x, ldx, w_gate, w_up, gate, up, T, d, f, type,
                           dx, dw_gate, dw_up, (char *)workspace};
   return finish(launch_gated_backward(p, as_stream(stream)), fn);
+}
+
+moe_status moe_dense_form(int32_t op, int32_t T, int32_t inner, int32_t outputs, int32_t workspace,
+                          int32_t *forms) {
+  const char *fn = "moe_dense_form";
+  if (op < MOE_DENSE_MATMUL_I8 || op > MOE_DENSE_GATED_BACKWARD)
+    return fail_status(MOE_ERR_UNSUPPORTED, "%s: op=%d", fn, op);
+  moe_status s = op == MOE_DENSE_MATMUL_I8 ? check_product_dims(fn, inner, outputs)
+                                           : check_gated_dims(fn, inner, outputs);
+  if (s || (s = check_rows(fn, T, inner, inner, op < MOE_DENSE_GATED ? 1 : 2))) return s;
+  if (!forms) return fail_status(MOE_ERR_NULL, "%s: forms is required", fn);
+  int32_t form[2];
+  dense_form(op, T, inner, outputs, workspace != 0, form);
+  forms[0] = form[0];
+  forms[1] = form[1];
+  return ok_status();
 }
 
 }  // extern "C"

@@ -73,6 +73,20 @@ struct Gated16Backward {
 size_t gated_backward_workspace(int32_t T, int32_t d, int32_t f);
 hipError_t launch_gated_backward(const Gated16Backward &p, hipStream_t stream);
 
+// Which kernels the sizes take (MOE_DENSE_* and MOE_FORM_* of the C ABI); the
+// launchers above go by the same choice.
+enum : int32_t { kOpMatmulI8 = 0, kOpGatedI8 = 1, kOpGated = 2, kOpGatedBackward = 3 };
+enum : int32_t {
+  kFormNone = 0,
+  kFormStream = 1,       // + 0..3
+  kFormCut = 8,
+  kFormTile = 16,        // + 0..4
+  kFormPair = 24,        // + 0..4
+  kFormPairSecond = 32,  // + 0..4
+};
+void dense_form(int32_t op, int32_t T, int32_t inner, int32_t outputs, bool workspace,
+                int32_t (&form)[2]);
+
 uint32_t debug_take_dense();
 
 }  // namespace fp8moe

@@ -564,18 +564,31 @@ hipError_t run_pair_tile(const DenseIn &in1, const Epi &epi1, const DenseIn &in2
 // share a tile.  (The estimate's ratio follows the measured one: T, d, f = 2047,
 // 2048, 768: 0.85, 44 and 51 us; 4096, 2048, 1408: 0.89, 122 and 134 us; 8192,
 // 2048, 192: 1.51, 88 and 63 us; 512, 4096, 4096: 1.30, 126 and 117 us.)
-template <class Op, class Epi>
-hipError_t run_pair(const DenseIn &in1, const Epi &epi1, const DenseIn &in2, const Epi &epi2,
-                    void *part, hipStream_t stream) {
+struct PairChoice {
+  int tile;           // of both, -1: two launches
+  bool second_first;  // the longer tiles first
+};
+PairChoice choose_pair(const DenseIn &in1, const DenseIn &in2) {
   const bool swap = in2.kbytes > in1.kbytes;
-  const DenseIn &l = swap ? in2 : in1, &r = swap ? in1 : in2;  // the longer tiles first
-  Choice best{-1, 1, (in1.M > 0 ? choose(in1, 1, true).us : 0.0) + choose(in2, 1, true).us};
+  const DenseIn &l = swap ? in2 : in1, &r = swap ? in1 : in2;
+  double best = (in1.M > 0 ? choose(in1, 1, true).us : 0.0) + choose(in2, 1, true).us;
+  PairChoice c{-1, swap};
   for (int i = 0; i < kTiles; ++i) {
     const double us = pair_time(tiles_of(kTile[i], l, 1), time_of(kTile[i], l),
                                 tiles_of(kTile[i], r, 1), time_of(kTile[i], r));
-    if (us < best.us) best = Choice{i, 1, us};
+    if (us < best) {
+      best = us;
+      c.tile = i;
+    }
   }
-  switch (best.tile) {
+  return c;
+}
+template <class Op, class Epi>
+hipError_t run_pair(const DenseIn &in1, const Epi &epi1, const DenseIn &in2, const Epi &epi2,
+                    void *part, hipStream_t stream) {
+  const PairChoice c = choose_pair(in1, in2);
+  const bool swap = c.second_first;
+  switch (c.tile) {
     case 0: return run_pair_tile<Op, 64, 64, 2, 2, 3, 2>(in1, epi1, in2, epi2, swap, stream);
     case 1: return run_pair_tile<Op, 64, 128, 2, 4, 3, 2>(in1, epi1, in2, epi2, swap, stream);
     case 2: return run_pair_tile<Op, 128, 128, 2, 4, 4, 1>(in1, epi1, in2, epi2, swap, stream);
@@ -901,6 +914,10 @@ DenseIn sizes(int64_t M, int64_t N, int64_t kbytes) {
   in.kbytes = kbytes;
   return in;
 }
+DenseIn dx_sizes(int32_t T, int32_t d, int32_t f) { return sizes(T, d, 4 * (int64_t)f); }
+DenseIn dw_sizes(int32_t T, int32_t d, int32_t f) {
+  return sizes(2 * (int64_t)f, d, 2 * (int64_t)T);
+}
 size_t product_workspace(const DenseIn &in, int nb) {
   if (in.M == 0 || streams(in, nb) != Stream::kNo) return 0;
   return (size_t)part_bytes(in, nb, choose(in, nb, true).splits);
@@ -995,9 +1012,34 @@ size_t gated_i8_workspace(int32_t T, int32_t d, int32_t f) {
 size_t gated_workspace(int32_t T, int32_t d, int32_t f) {
   return product_workspace(sizes(T, f, 2 * (int64_t)d), 2);
 }
+
+void dense_form(int32_t op, int32_t T, int32_t inner, int32_t outputs, bool workspace,
+                int32_t (&form)[2]) {
+  form[0] = form[1] = kFormNone;
+  auto tiles = [](const Choice &c) { return c.splits > 1 ? kFormCut : kFormTile + c.tile; };
+  if (op != kOpGatedBackward) {
+    const DenseIn in = sizes(T, outputs, op == kOpGated ? 2 * (int64_t)inner : inner);
+    const int nb = op == kOpMatmulI8 ? 1 : 2;
+    if (T == 0) return;
+    const Stream st = streams(in, nb);
+    form[0] = st != Stream::kNo ? kFormStream + (int)st - (int)Stream::k8
+                                : tiles(choose(in, nb, workspace));
+    return;
+  }
+  const DenseIn dx = dx_sizes(T, inner, outputs), dw = dw_sizes(T, inner, outputs);
+  const PairChoice c = choose_pair(dx, dw);
+  if (c.tile >= 0) {
+    form[0] = form[1] = (c.second_first ? kFormPairSecond : kFormPair) + c.tile;
+    if (T == 0) form[0] = kFormNone;
+    return;
+  }
+  if (T > 0) form[0] = tiles(choose(dx, 1, true));
+  form[1] = tiles(choose(dw, 1, true));
+}
+
 // dgu, its largest values, and the parts of dx's and then of dW's products
 size_t gated_backward_workspace(int32_t T, int32_t d, int32_t f) {
-  const DenseIn dx = sizes(T, d, 4 * (int64_t)f), dw = sizes(2 * (int64_t)f, d, 2 * (int64_t)T);
+  const DenseIn dx = dx_sizes(T, d, f), dw = dw_sizes(T, d, f);
   const int64_t a = T > 0 ? part_bytes(dx, 1, choose(dx, 1, true).splits) : 0;
   const int64_t b = part_bytes(dw, 1, choose(dw, 1, true).splits);
   return dgu_bytes(T, f) + kGradScratch + (size_t)(a > b ? a : b);

@@ -468,6 +468,36 @@ moe_status moe_fused_forward_timed(const moe_dims *dims /*host*/, const float *x
                                    size_t workspace_bytes, void *const *stage_events /*host*/,
                                    int32_t n_events, void *stream);
 
+/* Which kernels a dense operator takes for its sizes (T, d or K, f or N), which
+ * alone decide, so that a test or a profile can name them.  forms [2], HOST
+ * memory: the product's form and 0; of the backward pass, that of dx and that
+ * of dW (workspace is not looked at: it has one).
+ *   MOE_FORM_STREAM + i   up to 32 tokens: groups of 16 weight rows and up to 8,
+ *                         16, 32 tokens; of 32 rows and 32 tokens
+ *   MOE_FORM_CUT          64x64 tiles, K cut in parts (workspace != 0)
+ *   MOE_FORM_TILE + i     tiles of 64x64, 64x128, 128x128, 128x256, 256x256
+ *   MOE_FORM_PAIR + i     dx and dW in one launch of such tiles, dx's first
+ *   MOE_FORM_PAIR_SECOND + i   the same, dW's first
+ * The choice may change from version to version; results stay within the
+ * operators' rounding.  Errors: MOE_ERR_UNSUPPORTED (op), MOE_ERR_SHAPE (sizes
+ * the operator refuses), MOE_ERR_NULL. */
+enum {
+  MOE_DENSE_MATMUL_I8 = 0,
+  MOE_DENSE_GATED_I8 = 1,
+  MOE_DENSE_GATED = 2,
+  MOE_DENSE_GATED_BACKWARD = 3
+};
+enum {
+  MOE_FORM_NONE = 0,
+  MOE_FORM_STREAM = 1,
+  MOE_FORM_CUT = 8,
+  MOE_FORM_TILE = 16,
+  MOE_FORM_PAIR = 24,
+  MOE_FORM_PAIR_SECOND = 32
+};
+moe_status moe_dense_form(int32_t op, int32_t T, int32_t inner, int32_t outputs, int32_t workspace,
+                          int32_t *forms /*host*/);
+
 const char *moe_status_str(moe_status s);
 const char *moe_last_error(void); /* thread-local detail of this thread's last failing call */
 int32_t moe_abi_version(void);
