@@ -212,3 +212,29 @@ def test_a_row_with_nan_has_a_nan_scale(cols, dtype):
         outs = [y] if cols % 64 else [y, lib().gated_ffn_i8(q, s, w, scales(g, 64), w, scales(g, 64))]
         for o in outs:
             assert bool(o[nan + inf].isnan().all()) and bool(o[keep].isfinite().all())
+
+
+@pytest.mark.parametrize("T", [3, 12, 20, 70, 600])
+def test_a_poisoned_token_changes_no_other(T):
+    """Of the int8 gated block (its scale is NaN) and of the backward pass (its
+    dh, and its g and u, are infinite or NaN): no other token's h or dx."""
+    g = gen(T)
+    d, f, at = 256, 320, T // 2
+    keep = torch.arange(T, device=dev()) != at
+    xq, sx, wg, wu = codes(g, (T, d)), scales(g, T), codes(g, (f, d)), codes(g, (f, d))
+    sg, su = scales(g, f) * 0.1, scales(g, f) * 0.1
+    want = lib().gated_ffn_i8(xq, sx, wg, sg, wu, su)
+    bad = sx.clone()
+    bad[at] = torch.nan
+    got = lib().gated_ffn_i8(xq, bad, wg, sg, wu, su)
+    assert torch.equal(got[keep], want[keep]) and bool(got[at].isnan().all())
+    for dtype in F16S:
+        x, dh = normal(g, (T, d), 1, dtype), normal(g, (T, f), 1, dtype)
+        wg, wu = normal(g, (f, d), 1 / 16, dtype), normal(g, (f, d), 1 / 16, dtype)
+        gate, up = normal(g, (T, f), 2.0), normal(g, (T, f))
+        want = lib().gated_ffn_backward(dh, x, wg, wu, gate, up)[0]
+        bdh, bg, bu = dh.clone(), gate.clone(), up.clone()
+        bdh[at, ::3], bdh[at, 1::3], bg[at, ::7], bu[at, ::5] = torch.inf, torch.nan, -torch.inf, torch.nan
+        got = lib().gated_ffn_backward(bdh, x, wg, wu, bg, bu)[0]
+        assert torch.equal(got[keep], want[keep]), dtype
+        assert bool(got[at].isnan().all())
