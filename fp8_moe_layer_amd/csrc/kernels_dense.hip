@@ -599,21 +599,28 @@ hipError_t run_pair(const DenseIn &in1, const Epi &epi1, const DenseIn &in2, con
   return e != hipSuccess ? e : run_tiles<Op, kABColumns>(in2, epi2, part, stream);
 }
 
-// Up to 32 tokens stream the weights (stream_product), one workgroup to a
-// compute unit.  At 17 to 32 the tokens are as large a part of what is fetched
-// as the weights: a group is then 16 weight rows where the groups leave one to a
-// compute unit (weights from HBM, T = 32, int8 14336 -> 4096: 17 us, 21 with 32
-// rows, 32 in tiles), else 32, and for many channels of a short K tiles are as
-// fast or faster (bf16 gated 4096 -> 2 x 14336: 50 us streamed, 58 in tiles;
-// int8, half the bytes of K: 28 and 26.5).  Above, tiles.
+// Up to 16 tokens stream the weights (stream_product), one workgroup to a
+// compute unit.  At 17 to 32 the tokens are as large a part of what is fetched as
+// the weights: a group is then 16 weight rows where the groups leave one to a
+// compute unit, else 32, and tiles are faster for many groups or long rows.
+// Streamed and in tiles at 288 sizes of 17, 24 and 32 tokens (rows of 1 to 32 KB, 32 to
+// 1792 groups; int8, gated int8, gated bf16; weights from HBM), the tiles' time
+// over the stream's, on average:
+//   up to 256 groups, rows up to 16 KB 1.10, longer 0.86;
+//   257 to 512 groups 1.13 and 0.91;
+//   more groups 0.95, but 1.07 for gated rows of 8 KB, where a tile's rows, which
+//   lie 8 KB apart, slow its fetches down (gated bf16 4096 -> 2 x 14336: 54 us
+//   in tiles, 47 to 51 streamed; 3584 -> 2 x 14336 38 and 40 to 45).
+// So chosen, a size takes 0.9 % longer than in the better of the two on average, 23 %
+// at most.
 enum class Stream { kNo, k8, k16, k32, k32Wide };
 Stream streams(const DenseIn &in, int nb) {
   const int64_t groups = ((int64_t)in.N * nb + 15) / 16;  // of 16 weight rows
   if (in.M <= 8) return Stream::k8;
   if (in.M <= 16) return Stream::k16;
-  if (in.M > 32) return Stream::kNo;
+  if (in.M > 32 || in.kbytes > 16384) return Stream::kNo;
   if (groups <= kCUs) return Stream::k32;
-  return groups <= 2 * kCUs || in.kbytes > 6144 ? Stream::k32Wide : Stream::kNo;
+  return groups <= 2 * kCUs || (nb == 2 && in.kbytes == 8192) ? Stream::k32Wide : Stream::kNo;
 }
 
 template <class Op, class Epi>

@@ -18,12 +18,12 @@ MATMUL_FORMS = {
 }
 GATED_I8_FORMS = {
     "stream 8": (7, 192, 320), "stream 16": (11, 1088, 192), "stream 32": (23, 448, 2048),
-    "stream 32 wide": (19, 6208, 4160), "cut": (33, 4032, 192), "tile 64x64": (61, 320, 192),
+    "stream 32 wide": (19, 6208, 2112), "cut": (33, 4032, 192), "tile 64x64": (61, 320, 192),
     "tile 64x128": (65, 192, 4160), "tile 128x128": (69, 192, 8384), "tile 128x256": (131, 192, 8512),
     "tile 256x256": (397, 192, 8256),
 }
 # the widest stream at more of the channels that take it
-MORE_WIDE = [(24, 448, 2112), (17, 64, 2176), (32, 4096, 4096)]
+MORE_WIDE = [(24, 448, 2112), (17, 64, 2176), (32, 4096, 4096), (17, 8192, 4160)]
 
 
 @pytest.mark.parametrize("kind", FLOATS, ids=str)
