@@ -352,11 +352,14 @@ struct TileShape {
 // more waves to a SIMD fill each other's waits; the waves that issue matrix
 // instructions go first (setprio: 1-2 %).
 //
-// What bounds it: for large products (256x256: 8192 x 4096 x 2*14336 bf16 1.39
-// PFLOP/s, 8192 x 14336 x 4096 int8 2.65 POP/s) the matrix instructions run
-// 66-73 % of the time at 1.5-1.9 GHz; alone, on the same kind of values, they
-// reach 2.0 PFLOP/s at the card's power limit, and a wave tile of 128x64 reads
-// from LDS, together with the fills, as many cycles as it multiplies.  For
+// What bounds it: for large products (256x256: 8192 x 4096 x 2*14336 bf16 1.38
+// PFLOP/s, 8192 x 14336 x 4096 int8 2.64 POP/s) power and LDS.  Power: on zeros the
+// same instructions take 1075 us instead of 1397, int8 267 instead of 364, the
+// backward pass of 4096 x 4096 x 14336 1480 instead of 1650; matrix instructions
+// alone reach 1.9-2.1 PFLOP/s and 3.7-4.1 POP/s on such values, 2.4 and 4.9 on
+// zeros.
+// LDS: on zeros the products still reach 74 % of that only; a wave tile of 128x64
+// reads from LDS, together with the fills, as many cycles as it multiplies.  For
 // small ones, with one tile or less to a compute unit, LDS and the loads'
 // latency (0.55 us and more): hence the rings of three or four steps and the
 // two K groups of the small tiles.

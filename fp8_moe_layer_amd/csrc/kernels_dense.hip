@@ -443,15 +443,18 @@ __global__ __launch_bounds__(TM *TN *KG *kWave) void pair_kernel(DenseIn in1, Ep
 
 // ---------------------------------------------------------------- choice
 // The tiles, each with as much of a compute unit's LDS as it can use: one
-// workgroup to a compute unit, so the time of a product is about
-//   rounds of 256 tiles * (c + K steps * s)  us.
-// c and s are fits to 72 measured products (33 to 8192 tokens, K of 256 to
+// workgroup to a compute unit, so the time of a product goes with
+//   rounds of 256 tiles * (c + K steps * s).
+// c and s (us) are fits to 71 measured products (33 to 8192 tokens, K of 256 to
 // 32768 bytes, 256 to 16384 channels; int8, and bf16 gated; the bytes count,
-// not the type), with which the choice is on average 1 % and at most 14 %
-// slower than the best of the five, and of three more (64x64, 64x128 and
-// 128x128 with two or three workgroups to a compute unit) that gained nothing
-// beside them.  Without the 64x64 tile it is 9 % slower, without any other one
-// 2 to 4 %.
+// not the type).  What it gives ranks the tiles, it does not foretell their times:
+// those are 0.8 to 1.5 times as long (the longer, the more, as the clock drops).
+// The choice by it is the best of the five at all 71, and on average 1 % and at
+// most 14 % slower than the best of them and of three more (64x64, 64x128 and
+// 128x128 with two or three workgroups to a compute unit).  Without the 64x64 tile
+// it is 9 % slower, without any other one 2 to 4 %.  For the transposed forms, and
+// for one launch or two (choose_pair), it was held against all tiles at 40 backward
+// passes: on average 0.7 % and at most 4 % slower than the best.
 struct Tile {
   int bm, bn;
   double c, s;
@@ -463,7 +466,7 @@ constexpr Tile kTile[kTiles] = {{64, 64, 3.4, 0.19},
                                 {128, 256, 5.6, 0.74},
                                 {256, 256, 7.3, 1.16}};
 
-// Number of tiles of a product, and the time of one; nb: matrices that share a
+// Number of tiles of a product, and the estimated time of one; nb: matrices that share a
 // tile's columns.
 int64_t tiles_of(const Tile &t, const DenseIn &in, int nb) {
   return (((int64_t)in.M + t.bm - 1) / t.bm) * (((int64_t)in.N * nb + t.bn - 1) / t.bn);
