@@ -43,6 +43,11 @@ class Dims(C.Structure):
                 ("n_shared", _i32), ("block_m", _i32), ("flags", C.c_uint32)]
 
 
+class _NormDims(C.Structure):
+    _fields_ = [("T", _i32), ("d", _i32), ("type", _i32), ("w_type", _i32), ("gate_rows", _i32),
+                ("scale", C.c_float), ("offset", C.c_float), ("eps", C.c_float)]
+
+
 class _Weights(C.Structure):
     _fields_ = [(n, _vp) for n in ("w_gate", "w_up", "s_gate", "s_up", "w_down", "s_down",
                                    "ws_gate", "ws_up", "ws_down", "ss_gate", "ss_up", "ss_down")]
@@ -97,6 +102,12 @@ _gated_bwd_ws = _sig("moe_gated_ffn_backward_workspace_bytes", C.c_size_t, _i32,
 _dense_form = _sig("moe_dense_form", _i32, _i32, _i32, _i32, _i32, _i32, C.POINTER(_i32))
 _gated_bwd = _sig("moe_gated_ffn_backward", _i32, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i32,
                   _i32, _i32, _i32, _vp, _vp, _vp, _vp, C.c_size_t, _vp)
+_NP = C.POINTER(_NormDims)
+_norm_residual = _sig("moe_norm_residual", _i32, _NP, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp,
+                      _vp, _vp, _vp, _vp)
+_norm_bwd_ws = _sig("moe_norm_residual_backward_workspace_bytes", C.c_size_t, _NP)
+_norm_bwd = _sig("moe_norm_residual_backward", _i32, _NP, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
+                 _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, C.c_size_t, _vp)
 
 N_STAGE_EVENTS = 8
 STAGES = ("route", "topk", "permute", "gate_up", "requant", "down", "combine")
@@ -640,6 +651,168 @@ def dense_form(op: str, T: int, inner: int, outputs: int):
     _check(_dense_form(DENSE_OPS.index(op), T, inner, outputs, 1, forms))
     names = tuple(_FORMS[v] for v in forms)
     return names if op == "gated_ffn_backward" else names[0]
+
+
+# --------------------------------------------------------------------------- norms around a block
+# Plain calls like the dense operators above.
+
+class _Norm:
+    """The arguments that a norm's forward and backward calls share, checked: the
+    dims, and pointers to the vectors.  Vectors are of one type, fp32 or x's."""
+    __slots__ = ("call", "dims", "shape", "w_type", "w_post", "gate", "ldg", "w_next")
+
+    def __init__(self, first, T, d, w_post, gate, w_next, scale, offset, eps, stream):
+        c = self.call = _Call(first, stream)
+        vectors = [v for v in (w_post, gate, w_next) if v is not None]
+        self.w_type = vectors[0].dtype if vectors else first.dtype
+        if self.w_type is not torch.float32 and self.w_type is not first.dtype:
+            raise TypeError(f"weights and gate are {first.dtype} or torch.float32, got {self.w_type}")
+        self.shape = (T, d)
+        self.w_post = None if w_post is None else c.ptr(w_post, (d,), self.w_type, "w_post")
+        self.w_next = None if w_next is None else c.ptr(w_next, (d,), self.w_type, "w_next")
+        self.gate, self.ldg, rows = None, 0, 0
+        if gate is not None:
+            rows = _shape2(gate, "gate")[0]
+            if rows < 1 and T > 0 or rows > 1 and T % rows:
+                raise ValueError(f"gate: {rows} rows for {T} tokens")
+            if rows:
+                self.gate, self.ldg = c.rows(gate, (rows, d), self.w_type, "gate")
+        self.dims = _NormDims(T, d, _type(first.dtype), _TYPES[self.w_type], rows, scale, offset, eps)
+
+    def rows(self, t, dtype, name):
+        return (None, 0) if t is None else self.call.rows(t, self.shape, dtype, name)
+
+
+def _out(c, t, shape, dtype, name):
+    """(tensor, address) of an output: the caller's, or a new one."""
+    if t is None:
+        t = c.empty(shape, dtype)
+        return t, t.data_ptr()
+    return t, c.ptr(t, shape, dtype, name)
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, offset: float = 0.0,
+             out: Optional[torch.Tensor] = None, save: bool = False, stream=None):
+    """x * rstd * (offset + weight) with rstd = 1 / sqrt(mean(x^2) + eps), row by
+    row (moe_norm_residual without a sum): x [T, d] fp32, bf16 or fp16 (rows may
+    be strided), weight [d] fp32 or x's type.  With save=True (n, rstd), rstd
+    [T] fp32 as rms_norm_backward takes it."""
+    T, d = _shape2(x, "x")
+    _no_autograd("rms_norm", x, weight)
+    m = _Norm(x, T, d, None, None, weight, 1.0, offset, eps, stream)
+    xp, ldx = m.rows(x, x.dtype, "x")
+    n, at = _out(m.call, out, (T, d), x.dtype, "out")
+    rstd = m.call.empty((T,), torch.float32) if save else None
+    m.call.run(_norm_residual, C.byref(m.dims), xp, ldx, None, 0, None, None, 0, m.w_next, None, at,
+               None, rstd.data_ptr() if save else None)
+    return (n, rstd) if save else n
+
+
+def norm_residual(x: torch.Tensor, y: torch.Tensor, w_post: Optional[torch.Tensor] = None,
+                  gate: Optional[torch.Tensor] = None, w_next: Optional[torch.Tensor] = None,
+                  scale: float = 1.0, eps: float = 1e-6, offset: float = 0.0,
+                  r: Optional[torch.Tensor] = None, n: Optional[torch.Tensor] = None,
+                  save: bool = False, stream=None):
+    """r = x + scale * gate * z, where z = y, or with w_post the norm of y; and
+    with w_next n, the norm of r, for the next block (moe_norm_residual).  x, y
+    [T, d] fp32, bf16 or fp16 (rows may be strided); w_post, w_next [d]; gate
+    [G, d], a row for each T / G tokens (rows may be strided); vectors fp32 or
+    x's type.  Returns r, with w_next (r, n); with save=True always
+    (r, n, rstd_y, rstd_r), None for what there is not, the rstd fp32 [T] as
+    norm_residual_backward takes them."""
+    T, d = _shape2(x, "x")
+    _no_autograd("norm_residual", x, y, w_post, gate, w_next)
+    m = _Norm(x, T, d, w_post, gate, w_next, scale, offset, eps, stream)
+    c = m.call
+    xp, ldx = m.rows(x, x.dtype, "x")
+    yp, ldy = m.rows(y, x.dtype, "y")
+    r, rp = _out(c, r, (T, d), x.dtype, "r")
+    np_ = None
+    if w_next is not None:
+        n, np_ = _out(c, n, (T, d), x.dtype, "n")
+    elif n is not None:
+        raise ValueError("n needs w_next")
+    rstd_y = c.empty((T,), torch.float32) if save and w_post is not None else None
+    rstd_r = c.empty((T,), torch.float32) if save and w_next is not None else None
+    c.run(_norm_residual, C.byref(m.dims), xp, ldx, yp, ldy, m.w_post, m.gate, m.ldg, m.w_next, rp, np_,
+          None if rstd_y is None else rstd_y.data_ptr(), None if rstd_r is None else rstd_r.data_ptr())
+    if save:
+        return r, n, rstd_y, rstd_r
+    return r if w_next is None else (r, n)
+
+
+def _norm_backward(m, dr, dn, x, y, rstd_y, rstd_r, has, dx, dy, workspace):
+    """The library's backward call; has: which of w_post, gate, w_next there are
+    (the gate's shape for the gate).  (dx, dy, dw_post, dgate, dw_next)."""
+    c, (T, d), t = m.call, m.shape, x.dtype
+    post, gate, nxt = has
+    drp, lddr = m.rows(dr, t, "dr")
+    dnp, lddn = m.rows(dn, t, "dn")
+    xp, ldx = m.rows(x, t, "x")
+    yp, ldy = m.rows(y, t, "y")
+    dx, dxp = _out(c, dx, (T, d), t, "dx")
+    dyp = None
+    if y is not None:
+        dy, dyp = _out(c, dy, (T, d), t, "dy")
+    dw_post = c.empty((d,), m.w_type) if post else None
+    dgate = c.empty(gate, m.w_type) if gate else None
+    dw_next = c.empty((d,), m.w_type) if nxt else None
+    at = lambda v: None if v is None or v.numel() == 0 else v.data_ptr()
+    need = int(_norm_bwd_ws(C.byref(m.dims)))
+    if workspace is None and need:
+        workspace = c.empty((need,), torch.uint8)
+    elif workspace is not None:
+        c.ptr(workspace, workspace.shape, torch.uint8, "workspace")
+    c.run(_norm_bwd, C.byref(m.dims), drp, lddr, dnp, lddn, xp, ldx, yp, ldy,
+          c.ptr(rstd_y, (T,), torch.float32, "rstd_y") if post else None,
+          c.ptr(rstd_r, (T,), torch.float32, "rstd_r") if nxt else None, m.w_post, m.gate, m.ldg,
+          m.w_next, dxp, dyp, at(dw_post), at(dgate), at(dw_next), at(workspace),
+          0 if workspace is None else workspace.numel())
+    return dx, dy, dw_post, dgate, dw_next
+
+
+def rms_norm_backward(dn: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                      offset: float = 0.0, dr: Optional[torch.Tensor] = None,
+                      dx: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                      stream=None):
+    """Gradients of rms_norm from dn and its saved rstd: (dx, dweight).  dr [T,
+    d]: x's gradient from elsewhere (the residual stream), added to dx."""
+    T, d = _shape2(x, "x")
+    _no_autograd("rms_norm_backward", dn, x, weight, rstd, dr)
+    m = _Norm(x, T, d, None, None, weight, 1.0, offset, 1.0, stream)
+    dx, _, _, _, dw = _norm_backward(m, dr, dn, x, None, None, rstd, (False, None, True), dx, None,
+                                     workspace)
+    return dx, dw
+
+
+def norm_residual_backward(dr: Optional[torch.Tensor], dn: Optional[torch.Tensor], x: torch.Tensor,
+                           y: torch.Tensor, rstd_y: Optional[torch.Tensor],
+                           rstd_r: Optional[torch.Tensor], w_post: Optional[torch.Tensor] = None,
+                           gate: Optional[torch.Tensor] = None,
+                           w_next: Optional[torch.Tensor] = None, scale: float = 1.0,
+                           offset: float = 0.0, dx: Optional[torch.Tensor] = None,
+                           dy: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of norm_residual (moe_norm_residual_backward) from dr and dn
+    [T, d] (dr None: zeros; dn goes with w_next), the forward call's inputs and
+    its saved rstd_y, rstd_r: (dx, dy, dw_post, dgate, dw_next), None for what
+    there is not, written over whatever dx and dy held.  workspace: uint8,
+    256-byte aligned, norm_backward_workspace_bytes(T, d, gate rows) or more;
+    allocated here when not given."""
+    T, d = _shape2(x, "x")
+    _no_autograd("norm_residual_backward", dr, dn, x, y, rstd_y, rstd_r, w_post, gate, w_next)
+    if (dn is None) != (w_next is None):
+        raise ValueError("dn and w_next go together")
+    if dr is None and dn is None:
+        raise ValueError("dr or dn is required")
+    m = _Norm(x, T, d, w_post, gate, w_next, scale, offset, 1.0, stream)
+    return _norm_backward(m, dr, dn, x, y, rstd_y, rstd_r,
+                          (w_post is not None, None if gate is None else tuple(gate.shape),
+                           w_next is not None), dx, dy, workspace)
+
+
+def norm_backward_workspace_bytes(T: int, d: int, gate_rows: int = 0) -> int:
+    return int(_norm_bwd_ws(C.byref(_NormDims(T, d, 0, 0, gate_rows, 1.0, 0.0, 1.0))))
 
 
 # --------------------------------------------------------------------------- whole layer

@@ -406,6 +406,65 @@ moe_status moe_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, i
                                   size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------ */
+/* Norms around a block                                                      */
+/* ------------------------------------------------------------------------ */
+
+/* What stands before and after a feed-forward block, in one pass over the
+ * rows: the norm of the block's output, its gate, the residual sum, and the
+ * norm that the next block starts with.  With rstd(v) = 1 / sqrt(mean(v^2) + eps):
+ *
+ *   z = y * rstd(y) * (offset + w_post)     (z = y where w_post is NULL)
+ *   r = x + scale * gate * z                (gate = 1 where it is NULL)
+ *   n = r * rstd(r) * (offset + w_next)     (no n where w_next is NULL)
+ *
+ * in fp32, r and n each rounded once to `type`; n goes by r as it was before
+ * that.  Where y is NULL there is no sum: n = norm(x), and r, w_post, gate and
+ * rstd_y are NULL.
+ * x, y [T][d] with row strides ldx, ldy; r, n [T][d]; w_post, w_next [d]; gate
+ * [gate_rows][d] with row stride ldg: row t / (T / gate_rows) is token t's, so
+ * one row is a gate per channel and T rows are a gate per token.  rstd_y,
+ * rstd_r [T] fp32: kept for the backward pass, or NULL.
+ * Row strides are in ELEMENTS, as for the dense operators; every array is
+ * 16-byte aligned (rstd 4-byte), outputs overlap nothing.  Inputs are finite,
+ * and so are the fp32 sums of squares. */
+typedef struct {
+  int32_t T;         /* tokens, 0 .. MOE_MAX_TOKENS */
+  int32_t d;         /* a multiple of 16 up to MOE_MAX_HIDDEN */
+  int32_t type;      /* MOE_T_* of rows and their gradients */
+  int32_t w_type;    /* of w_post, gate, w_next and their gradients: fp32 or `type` */
+  int32_t gate_rows; /* 0 without a gate; divides T (T = 0: 0 or 1) */
+  float scale, offset;
+  float eps; /* a positive normal number; the backward pass does not use it */
+} moe_norm_dims;
+moe_status moe_norm_residual(const moe_norm_dims *dims /*host*/, const void *x, int64_t ldx,
+                             const void *y, int64_t ldy, const void *w_post, const void *gate,
+                             int64_t ldg, const void *w_next, void *r, void *n, float *rstd_y,
+                             float *rstd_r, void *stream);
+
+/* Its backward pass, from the gradients dr (NULL: zeros) and dn of r and n, the
+ * forward pass's inputs and its rstd_y, rstd_r.  With v^ = v * rstd(v):
+ *   D = dr + rstd_r * (a - r^ * mean(a * r^)),  a = dn * (offset + w_next)
+ *   dx = D,  dw_next = sum_t dn * r^
+ *   dgate = sum over the gate row's tokens of scale * D * z
+ *   c = scale * D * gate,  dw_post = sum_t c * y^
+ *   dy = rstd_y * (b - y^ * mean(b * y^)),  b = c * (offset + w_post)
+ *                                           (dy = c where w_post is NULL)
+ * r is formed again from x and y, as the forward pass had it before rounding.
+ * Sums in fp32 in an order that depends on T, d and gate_rows alone; each output
+ * is rounded once and overwritten (not added to).  A vector and its gradient are
+ * given together or not at all; x, dn and rstd_r are read where there is w_next.
+ * T = 0 writes the vectors' gradients, zeros.  The workspace
+ * (moe_norm_residual_backward_workspace_bytes), 256-byte aligned, is required. */
+size_t moe_norm_residual_backward_workspace_bytes(const moe_norm_dims *dims /*host*/);
+moe_status moe_norm_residual_backward(const moe_norm_dims *dims /*host*/, const void *dr,
+                                      int64_t lddr, const void *dn, int64_t lddn, const void *x,
+                                      int64_t ldx, const void *y, int64_t ldy, const float *rstd_y,
+                                      const float *rstd_r, const void *w_post, const void *gate,
+                                      int64_t ldg, const void *w_next, void *dx, void *dy,
+                                      void *dw_post, void *dgate, void *dw_next, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ */
 /* Diagnostics                                                               */
 /* ------------------------------------------------------------------------ */
 
