@@ -108,6 +108,12 @@ _norm_residual = _sig("moe_norm_residual", _i32, _NP, _vp, _i64, _vp, _i64, _vp,
 _norm_bwd_ws = _sig("moe_norm_residual_backward_workspace_bytes", C.c_size_t, _NP)
 _norm_bwd = _sig("moe_norm_residual_backward", _i32, _NP, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
                  _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, C.c_size_t, _vp)
+_quantize_rows_mx4 = _sig("moe_quantize_rows_mx4", _i32, _vp, _i32, _i64, _i32, _i32, _vp, _vp, _vp)
+_dequantize_rows_mx4 = _sig("moe_dequantize_rows_mx4", _i32, _vp, _vp, _i32, _i32, _i32, _vp, _vp)
+_packed_mx4_bytes = _sig("moe_packed_mx4_bytes", _i64, _i32, _i32)
+_pack_mx4 = _sig("moe_pack_mx4", _i32, _vp, _vp, _i32, _i32, _vp, _vp)
+_matmul_mx4 = _sig("moe_matmul_mx4", _i32, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp)
+_ffn_mx4 = _sig("moe_ffn_mx4", _i32, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp)
 
 N_STAGE_EVENTS = 8
 STAGES = ("route", "topk", "permute", "gate_up", "requant", "down", "combine")
@@ -813,6 +819,121 @@ def norm_residual_backward(dr: Optional[torch.Tensor], dn: Optional[torch.Tensor
 
 def norm_backward_workspace_bytes(T: int, d: int, gate_rows: int = 0) -> int:
     return int(_norm_bwd_ws(C.byref(_NormDims(T, d, 0, 0, gate_rows, 1.0, 0.0, 1.0))))
+
+
+# --------------------------------------------------------------------------- 4-bit weights
+# Plain calls like the dense operators above.
+
+def quantize_rows_mx4(x: torch.Tensor, codes: Optional[torch.Tensor] = None,
+                      scales: Optional[torch.Tensor] = None, stream=None):
+    """Quantisation of x [rows, cols] (fp32, bf16 or fp16; rows may be strided)
+    to e2m1 codes with a power-of-two scale per group of 32
+    (moe_quantize_rows_mx4): (codes uint8 [rows, cols/2], two to a byte, scales
+    uint8 [rows, cols/32], byte b for 2^(b-127))."""
+    rows, cols = _shape2(x, "x")
+    _no_autograd("quantize_rows_mx4", x)
+    c = _Call(x, stream)
+    kind = _type(x.dtype)
+    xp, ldx = c.rows(x, x.shape, x.dtype, "x")
+    codes, cp = _out(c, codes, (rows, cols // 2), torch.uint8, "codes")
+    scales, sp = _out(c, scales, (rows, cols // 32), torch.uint8, "scales")
+    c.run(_quantize_rows_mx4, xp, kind, ldx, rows, cols, cp, sp)
+    return codes, scales
+
+
+def _mx4_parts(codes, scales, stream):
+    """(call, rows, cols, addresses) of codes with their scales."""
+    rows, half = _shape2(codes, "codes")
+    c = _Call(codes, stream)
+    cols = 2 * half
+    if cols > _INT32_MAX or cols % 32:
+        raise ValueError(f"codes: {cols} values a row, a multiple of 32 is expected")
+    return (c, rows, cols, c.ptr(codes, (rows, half), torch.uint8, "codes"),
+            c.ptr(scales, (rows, cols // 32), torch.uint8, "scales"))
+
+
+def dequantize_rows_mx4(codes: torch.Tensor, scales: torch.Tensor,
+                        out_dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None,
+                        stream=None) -> torch.Tensor:
+    """The values [rows, cols] of quantize_rows_mx4's codes and scales in
+    out_dtype (or out's type) (moe_dequantize_rows_mx4)."""
+    c, rows, cols, cp, sp = _mx4_parts(codes, scales, stream)
+    out, at = _out(c, out, (rows, cols), out_dtype if out is None else out.dtype, "out")
+    c.run(_dequantize_rows_mx4, cp, sp, rows, cols, _type(out.dtype), at)
+    return out
+
+
+@dataclass(frozen=True)
+class Mx4Matrix:
+    """A weight matrix of `rows` output channels by `cols` inputs in the order
+    that the 4-bit products read (pack_mx4)."""
+    data: torch.Tensor  # uint8, packed_mx4_bytes(rows, cols)
+    rows: int
+    cols: int
+
+
+def packed_mx4_bytes(rows: int, cols: int) -> int:
+    """Bytes of a packed matrix (0 for sizes that are refused)."""
+    fit = lambda v: max(-1, min(v, _INT32_MAX))  # both refused, like all past the limits
+    return int(_packed_mx4_bytes(fit(rows), fit(cols)))
+
+
+def pack_mx4(codes: torch.Tensor, scales: torch.Tensor, out: Optional[torch.Tensor] = None,
+             stream=None) -> Mx4Matrix:
+    """Lays out codes [rows, cols/2] and scales [rows, cols/32] of a weight matrix
+    for matmul_mx4 and gated_ffn_mx4, once, when it is loaded (moe_pack_mx4).
+    out: uint8, packed_mx4_bytes(rows, cols), or allocated here."""
+    c, rows, cols, cp, sp = _mx4_parts(codes, scales, stream)
+    out, at = _out(c, out, (packed_mx4_bytes(rows, cols),), torch.uint8, "out")
+    c.run(_pack_mx4, cp, sp, rows, cols, at)
+    return Mx4Matrix(out, rows, cols)
+
+
+@functools.lru_cache(maxsize=4096)
+def _mx4_shape(rows: int, cols: int):
+    return torch.Size((packed_mx4_bytes(rows, cols),))
+
+
+def _mx4_ptr(c: _Call, w: Mx4Matrix, rows: int, cols: int, name: str):
+    if w.rows != rows or w.cols != cols:
+        raise ValueError(f"{name}: expected {rows} channels by {cols} inputs, got {w.rows} by {w.cols}")
+    return c.ptr(w.data, _mx4_shape(rows, cols), torch.uint8, name)
+
+
+def matmul_mx4(x: torch.Tensor, w: Mx4Matrix, bias: Optional[torch.Tensor] = None,
+               out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+               stream=None) -> torch.Tensor:
+    """y = x w^T (+ bias) with packed 4-bit weights (moe_matmul_mx4): x [T, K]
+    bf16 or fp16 (rows may be strided), bias fp32 [N]; y [T, N] in x's type, or
+    in out_dtype (or out's type): x's or fp32."""
+    T, K = _shape2(x, "x")
+    N = w.rows
+    _no_autograd("matmul_mx4", x, bias)
+    c = _Call(x, stream)
+    kind = _type(x.dtype, _TYPES16)
+    y, at = _out(c, out, (T, N), (out_dtype or x.dtype) if out is None else out.dtype, "out")
+    xp, ldx = c.rows(x, (T, K), x.dtype, "x")
+    c.run(_matmul_mx4, xp, ldx, _mx4_ptr(c, w, N, K, "w"),
+          None if bias is None else c.ptr(bias, (N,), torch.float32, "bias"), kind, T, K, N,
+          _type(y.dtype), at)
+    return y
+
+
+def gated_ffn_mx4(x: torch.Tensor, w_gate: Mx4Matrix, w_up: Mx4Matrix,
+                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """h = SiLU(x w_gate^T) * (x w_up^T) with packed 4-bit weights in one kernel
+    (moe_ffn_mx4): x [T, d] bf16 or fp16 (rows may be strided); h [T, f] in x's
+    type.  matmul_mx4 on h is the down projection."""
+    T, d = _shape2(x, "x")
+    f = w_gate.rows
+    _no_autograd("gated_ffn_mx4", x)
+    c = _Call(x, stream)
+    kind = _type(x.dtype, _TYPES16)
+    h, at = _out(c, out, (T, f), x.dtype, "out")
+    xp, ldx = c.rows(x, (T, d), x.dtype, "x")
+    c.run(_ffn_mx4, xp, ldx, _mx4_ptr(c, w_gate, f, d, "w_gate"), _mx4_ptr(c, w_up, f, d, "w_up"), kind,
+          T, d, f, at)
+    return h
 
 
 # --------------------------------------------------------------------------- whole layer

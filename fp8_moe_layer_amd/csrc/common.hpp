@@ -158,6 +158,14 @@ __device__ __forceinline__ float wave_sum(float v) {
   return wave_reduce(v, [](float a, float b) { return a + b; });
 }
 
+// Largest of each row of 16 lanes, in all of them.
+__device__ __forceinline__ int wave_row_max(int v) {
+  auto most = [](int a, int b) { return a > b ? a : b; };
+  v = most(v, dpp_mov<kDppQuadXor1>(v));
+  v = most(v, dpp_mov<kDppQuadXor2>(v));
+  v = most(v, dpp_mov<kDppHalfMirror>(v));
+  return most(v, dpp_mov<kDppMirror>(v));
+}
 
 // Inclusive prefix sum over the 64 lanes.
 __device__ __forceinline__ int wave_incl_scan(int v, int lane) {

@@ -1,0 +1,142 @@
+// mx4.hip -- C entry points of the 4-bit operators (include/fp8moe.h): host-side
+// validation and kernel enqueueing.
+#include "mx4.hpp"
+
+#include "dense.hpp"
+#include "entry.hpp"
+
+using namespace fp8moe;
+
+static_assert(MOE_MX4_GROUP == kMxGroup, "group");
+
+namespace {
+
+moe_status finish(hipError_t e, const char *fn) {
+  if (e != hipSuccess)
+    return fail_status(MOE_ERR_HIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
+  return ok_status();
+}
+
+moe_status check_matrix(const char *fn, int32_t rows, int32_t cols) {
+  if (rows < 0 || rows > MOE_MAX_TOKENS || cols < MOE_MX4_GROUP || cols % MOE_MX4_GROUP ||
+      cols > MOE_MAX_MX4_K)
+    return fail_status(MOE_ERR_SHAPE, "%s: rows=%d (in [0, %d]), cols=%d (a multiple of %d up to %d)",
+                       fn, rows, MOE_MAX_TOKENS, cols, MOE_MX4_GROUP, MOE_MAX_MX4_K);
+  return MOE_OK;
+}
+
+moe_status check_types(const char *fn, int32_t x_type, int32_t y_type) {
+  if ((x_type != MOE_T_BF16 && x_type != MOE_T_F16) || (y_type != x_type && y_type != MOE_T_F32))
+    return fail_status(MOE_ERR_UNSUPPORTED,
+                       "%s: x_type=%d (MOE_T_BF16 or MOE_T_F16), y_type=%d (the same or MOE_T_F32)",
+                       fn, x_type, y_type);
+  return MOE_OK;
+}
+
+int64_t code_bytes(int32_t rows, int32_t cols) { return (int64_t)rows * (cols / 2); }
+int64_t scale_bytes(int32_t rows, int32_t cols) { return (int64_t)rows * (cols / MOE_MX4_GROUP); }
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_quantize_rows_mx4(const void *x, int32_t x_type, int64_t ldx, int32_t rows,
+                                 int32_t cols, uint8_t *codes, uint8_t *scales, void *stream) {
+  const char *fn = "moe_quantize_rows_mx4";
+  if (x_type < MOE_T_F32 || x_type > MOE_T_F16)
+    return fail_status(MOE_ERR_UNSUPPORTED, "%s: x_type=%d", fn, x_type);
+  const int32_t size = type_bytes(x_type);
+  moe_status s = check_matrix(fn, rows, cols);
+  if (s || (s = check_rows(fn, rows, ldx, cols, size))) return s;
+  if (rows == 0) return ok_status();
+  if (!x || !codes || !scales)
+    return fail_status(MOE_ERR_NULL, "%s: x, codes and scales are required", fn);
+  if (!all_aligned({x, codes}, 16))
+    return fail_status(MOE_ERR_ALIGN, "%s: x and codes must be 16-byte aligned", fn);
+  const Span out[] = {{codes, code_bytes(rows, cols)}, {scales, scale_bytes(rows, cols)}};
+  const Span in[] = {{x, span_rows(rows, ldx, cols, size)}};
+  if (clash(out, in)) return fail_status(MOE_ERR_SHAPE, "%s: codes, scales and x overlap", fn);
+  return finish(launch_quantize_mx4(x, x_type, ldx, rows, cols, codes, scales, as_stream(stream)), fn);
+}
+
+moe_status moe_dequantize_rows_mx4(const uint8_t *codes, const uint8_t *scales, int32_t rows,
+                                   int32_t cols, int32_t y_type, void *y, void *stream) {
+  const char *fn = "moe_dequantize_rows_mx4";
+  if (y_type < MOE_T_F32 || y_type > MOE_T_F16)
+    return fail_status(MOE_ERR_UNSUPPORTED, "%s: y_type=%d", fn, y_type);
+  moe_status s = check_matrix(fn, rows, cols);
+  if (s) return s;
+  if (rows == 0) return ok_status();
+  if (!codes || !scales || !y)
+    return fail_status(MOE_ERR_NULL, "%s: codes, scales and y are required", fn);
+  if (!all_aligned({codes, y}, 16))
+    return fail_status(MOE_ERR_ALIGN, "%s: codes and y must be 16-byte aligned", fn);
+  const Span out[] = {{y, (int64_t)rows * cols * type_bytes(y_type)}};
+  const Span in[] = {{codes, code_bytes(rows, cols)}, {scales, scale_bytes(rows, cols)}};
+  if (clash(out, in)) return fail_status(MOE_ERR_SHAPE, "%s: y overlaps an input", fn);
+  return finish(launch_dequantize_mx4(codes, scales, rows, cols, y_type, y, as_stream(stream)), fn);
+}
+
+int64_t moe_packed_mx4_bytes(int32_t rows, int32_t cols) {
+  if (rows < 1) rows = -1;
+  if (check_matrix("moe_packed_mx4_bytes", rows, cols)) return 0;
+  (void)ok_status();
+  return Mx4Layout(rows, cols).bytes();
+}
+
+moe_status moe_pack_mx4(const uint8_t *codes, const uint8_t *scales, int32_t rows, int32_t cols,
+                        void *packed, void *stream) {
+  const char *fn = "moe_pack_mx4";
+  if (rows < 1) rows = -1;
+  moe_status s = check_matrix(fn, rows, cols);
+  if (s) return s;
+  if (!codes || !scales || !packed)
+    return fail_status(MOE_ERR_NULL, "%s: codes, scales and packed are required", fn);
+  if (!all_aligned({codes, packed}, 16))
+    return fail_status(MOE_ERR_ALIGN, "%s: codes and packed must be 16-byte aligned", fn);
+  const Span out[] = {{packed, Mx4Layout(rows, cols).bytes()}};
+  const Span in[] = {{codes, code_bytes(rows, cols)}, {scales, scale_bytes(rows, cols)}};
+  if (clash(out, in)) return fail_status(MOE_ERR_SHAPE, "%s: packed overlaps an input", fn);
+  return finish(launch_pack_mx4(codes, scales, rows, cols, (uint8_t *)packed, as_stream(stream)), fn);
+}
+
+moe_status moe_matmul_mx4(const void *x, int64_t ldx, const void *w, const float *bias, int32_t x_type,
+                          int32_t T, int32_t K, int32_t N, int32_t y_type, void *y, void *stream) {
+  const char *fn = "moe_matmul_mx4";
+  moe_status s = check_types(fn, x_type, y_type);
+  if (s || (s = check_matrix(fn, N < 1 ? -1 : N, K)) || (s = check_rows(fn, T, ldx, K, 2))) return s;
+  if (T == 0) return ok_status();
+  if (!x || !w || !y) return fail_status(MOE_ERR_NULL, "%s: x, w and y are required", fn);
+  if (!all_aligned({x, w, y}, 16) || !aligned(bias, 4))
+    return fail_status(MOE_ERR_ALIGN, "%s: x, w and y must be 16-byte, bias 4-byte aligned", fn);
+  const Span out[] = {{y, (int64_t)T * N * type_bytes(y_type)}};
+  const Span in[] = {{x, span_rows(T, ldx, K, 2)}, {w, Mx4Layout(N, K).bytes()}, {bias, (int64_t)N * 4}};
+  if (clash(out, in)) return fail_status(MOE_ERR_SHAPE, "%s: y overlaps an input", fn);
+  const Mx4Product p{x, ldx, (const uint8_t *)w, nullptr, bias, T, K, N, x_type, y_type, y};
+  return finish(launch_mx4_product(p, as_stream(stream)), fn);
+}
+
+moe_status moe_ffn_mx4(const void *x, int64_t ldx, const void *w_gate, const void *w_up, int32_t type,
+                       int32_t T, int32_t d, int32_t f, void *h, void *stream) {
+  const char *fn = "moe_ffn_mx4";
+  moe_status s = check_types(fn, type, type);
+  if (s) return s;
+  if (d < 32 || d % 32 || d > MOE_MAX_HIDDEN || f < 32 || f % 32 || f > MOE_MAX_FFN)
+    return fail_status(MOE_ERR_SHAPE, "%s: d=%d, f=%d must be multiples of 32 in [32, %d] and [32, %d]",
+                       fn, d, f, MOE_MAX_HIDDEN, MOE_MAX_FFN);
+  if ((s = check_rows(fn, T, ldx, d, 2))) return s;
+  if (T == 0) return ok_status();
+  if (!x || !w_gate || !w_up || !h)
+    return fail_status(MOE_ERR_NULL, "%s: x, w_gate, w_up and h are required", fn);
+  if (!all_aligned({x, w_gate, w_up, h}, 16))
+    return fail_status(MOE_ERR_ALIGN, "%s: every array must be 16-byte aligned", fn);
+  const int64_t wb = Mx4Layout(f, d).bytes();
+  const Span out[] = {{h, (int64_t)T * f * 2}};
+  const Span in[] = {{x, span_rows(T, ldx, d, 2)}, {w_gate, wb}, {w_up, wb}};
+  if (clash(out, in)) return fail_status(MOE_ERR_SHAPE, "%s: h overlaps an input", fn);
+  const Mx4Product p{x, ldx, (const uint8_t *)w_gate, (const uint8_t *)w_up, nullptr, T, d, f, type,
+                     type, h};
+  return finish(launch_mx4_product(p, as_stream(stream)), fn);
+}
+
+}  // extern "C"

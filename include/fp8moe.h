@@ -406,6 +406,66 @@ moe_status moe_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, i
                                   size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------ */
+/* 4-bit weights                                                             */
+/* ------------------------------------------------------------------------ */
+
+/* Weights served in 4 bits: e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives; the sign is the high bit) and a power-of-two scale to each group of
+ * 32 values of a row, 4.25 bits a value.  As a checkpoint has them:
+ *   codes  [rows][cols/2], value 2i in the low half of byte i,
+ *   scales [rows][cols/32], byte b for 2^(b-127); 255: the group is no number,
+ * made by moe_quantize_rows_mx4 or from elsewhere, and laid out once for the
+ * products by moe_pack_mx4 (an opaque order in which a wave's loads are whole
+ * pieces of 1 KB).  Activations are bf16 or fp16 rows, not quantised; row
+ * strides are as for the dense operators.  Inputs are finite; the sums
+ * sum_k |x[k]| too, in fp32. */
+#define MOE_MX4_GROUP 32
+#define MOE_MAX_MX4_K 65536 /* longest row */
+
+/* Quantisation of x [rows][cols] (x_type, row stride ldx) group by group: with a
+ * the group's largest magnitude, e = the smallest integer with a <= 7 * 2^e, but
+ * at least -126 (0 for a group of zeros), each value's code is that of x * 2^-e
+ * rounded to nearest, ties to the even code, 6 at most in magnitude: off by at
+ * most 2^e.  A group with an infinity or a NaN gets the scale byte 255 and
+ * codes of 0.  cols: a multiple of 32 up to MOE_MAX_MX4_K; rows: any up to
+ * MOE_MAX_TOKENS. */
+moe_status moe_quantize_rows_mx4(const void *x, int32_t x_type, int64_t ldx, int32_t rows,
+                                 int32_t cols, uint8_t *codes, uint8_t *scales, void *stream);
+
+/* The values that codes and scales stand for, y [rows][cols] contiguous, rounded
+ * once to y_type (in fp32 and, from 2^-126 on, in bf16 they are exact); NaN where
+ * the scale is 255. */
+moe_status moe_dequantize_rows_mx4(const uint8_t *codes, const uint8_t *scales, int32_t rows,
+                                   int32_t cols, int32_t y_type, void *y, void *stream);
+
+/* Packed weights of a matrix of `rows` output channels by `cols` inputs: their
+ * size (0, with a text in moe_last_error(), for sizes that are refused), and
+ * their layout from codes and scales; packed 16-byte aligned.  The weights keep
+ * their values but for groups whose scale is below 2^-121 of their row's largest,
+ * which may become zeros.  Every output of a row with a scale byte above 251
+ * (2^124) is a NaN. */
+int64_t moe_packed_mx4_bytes(int32_t rows, int32_t cols);
+moe_status moe_pack_mx4(const uint8_t *codes, const uint8_t *scales, int32_t rows, int32_t cols,
+                        void *packed, void *stream);
+
+/* Product with packed weights w of N channels by K inputs:
+ *   y[t][n] = sum_k x[t][k] * w[n][k] (+ bias[n])
+ * x [T][K] in x_type (bf16 or fp16), y [T][N] in y_type (x_type or fp32), bias
+ * fp32 [N] or NULL.  The weights are exact in bf16; with fp16 rows those below
+ * 2^-35 of the largest scale of their channel are rounded to steps of 2^-36 of
+ * it.  Sums in fp32, rounded once.  K: a multiple of 32 up to MOE_MAX_MX4_K; T
+ * and N: any up to MOE_MAX_TOKENS. */
+moe_status moe_matmul_mx4(const void *x, int64_t ldx, const void *w, const float *bias, int32_t x_type,
+                          int32_t T, int32_t K, int32_t N, int32_t y_type, void *y, void *stream);
+
+/* The gated block on packed weights of f channels by d inputs, in one kernel:
+ *   g = x w_gate^T, u = x w_up^T (fp32 sums), h = SiLU(g) * u, rounded once
+ * x [T][d], h [T][f] in `type`.  d, f: multiples of 32 up to MOE_MAX_HIDDEN /
+ * MOE_MAX_FFN.  (moe_matmul_mx4 on h is the down projection.) */
+moe_status moe_ffn_mx4(const void *x, int64_t ldx, const void *w_gate, const void *w_up, int32_t type,
+                       int32_t T, int32_t d, int32_t f, void *h, void *stream);
+
+/* ------------------------------------------------------------------------ */
 /* Norms around a block                                                      */
 /* ------------------------------------------------------------------------ */
 

@@ -1,0 +1,141 @@
+"""4-bit weights: the reference quantiser against its definition, and what the
+entry points refuse (every call fails host validation, so nothing is enqueued
+and no GPU is needed, or has no tokens)."""
+import numpy as np
+import pytest
+import torch
+
+import mx4_ref
+
+fp8 = pytest.importorskip("fp8_moe_layer_amd", reason="libfp8moe.so not built")
+
+OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_UNSUPPORTED, ERR_WORKSPACE = range(6)
+MB = 1 << 20
+P = [(i + 1) * 256 * MB for i in range(8)]  # distinct regions, never dereferenced
+F32, BF16, F16 = 0, 1, 2
+
+
+def test_reference_quantiser_picks_the_nearest_code():
+    """Every value within one unit of its scale of what its codes stand for, and no
+    code nearer; the scale the smallest that holds the group."""
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn((7, 256), generator=g) * torch.exp(3 * torch.randn((7, 1), generator=g))
+    codes, scales = (torch.from_numpy(a) for a in mx4_ref.quantize(x))
+    v, s = mx4_ref.values(codes, scales), torch.exp2(scales.double() - 127).repeat_interleave(32, 1)
+    grid = torch.tensor(np.concatenate([mx4_ref.GRID, -mx4_ref.GRID]))
+    best = ((x.double() / s)[..., None] - grid).abs().amin(-1) * s
+    assert bool(((x.double() - v).abs() <= best * (1 + 1e-12)).all()) and bool(((x.double() - v).abs() <= s).all())
+    top = x.double().abs().view(7, 8, 32).amax(2)
+    unit = torch.exp2(scales.double() - 127)
+    assert bool((top <= 7 * unit).all()) and bool((top > 3.5 * unit).all())
+
+
+def quantize(x=P[0], kind=F32, ldx=64, rows=4, cols=64, codes=P[1], scales=P[2]):
+    return fp8._quantize_rows_mx4(x, kind, ldx, rows, cols, codes, scales, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    *[({n: None}, ERR_NULL) for n in ("x", "codes", "scales")],
+    (dict(rows=-1), ERR_SHAPE), (dict(rows=(1 << 21) + 1), ERR_SHAPE), (dict(cols=0), ERR_SHAPE),
+    (dict(cols=48), ERR_SHAPE), (dict(cols=65568, ldx=65568), ERR_SHAPE), (dict(ldx=60), ERR_SHAPE),
+    (dict(ldx=66), ERR_SHAPE), (dict(kind=3), ERR_UNSUPPORTED), (dict(kind=-1), ERR_UNSUPPORTED),
+    (dict(x=P[0] + 8), ERR_ALIGN), (dict(codes=P[1] + 4), ERR_ALIGN),
+    (dict(codes=P[0] + 1008), ERR_SHAPE), (dict(scales=P[1] + 127), ERR_SHAPE),
+])
+def test_quantize_refuses(kw, code):
+    assert quantize(**kw) == code, fp8._last_error()
+    assert fp8._last_error().startswith(b"moe_quantize_rows_mx4")
+
+
+def dequantize(codes=P[0], scales=P[1], rows=4, cols=64, kind=F32, y=P[2]):
+    return fp8._dequantize_rows_mx4(codes, scales, rows, cols, kind, y, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    *[({n: None}, ERR_NULL) for n in ("codes", "scales", "y")],
+    (dict(rows=-1), ERR_SHAPE), (dict(cols=16), ERR_SHAPE), (dict(kind=4), ERR_UNSUPPORTED),
+    (dict(codes=P[0] + 4), ERR_ALIGN), (dict(y=P[2] + 8), ERR_ALIGN), (dict(y=P[0] + 112), ERR_SHAPE),
+    (dict(scales=P[2] + 1023), ERR_SHAPE),
+])
+def test_dequantize_refuses(kw, code):
+    assert dequantize(**kw) == code, fp8._last_error()
+    assert fp8._last_error().startswith(b"moe_dequantize_rows_mx4")
+
+
+def pack(codes=P[0], scales=P[1], rows=40, cols=64, packed=P[2]):
+    return fp8._pack_mx4(codes, scales, rows, cols, packed, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    *[({n: None}, ERR_NULL) for n in ("codes", "scales", "packed")],
+    (dict(rows=0), ERR_SHAPE), (dict(rows=-5), ERR_SHAPE), (dict(cols=33), ERR_SHAPE),
+    (dict(codes=P[0] + 8), ERR_ALIGN), (dict(packed=P[2] + 4), ERR_ALIGN),
+    (dict(packed=P[0] + 1264), ERR_SHAPE), (dict(scales=P[2] + 16), ERR_SHAPE),
+])
+def test_pack_refuses(kw, code):
+    assert pack(**kw) == code, fp8._last_error()
+    assert fp8._last_error().startswith(b"moe_pack_mx4")
+
+
+def test_packed_size():
+    # 32 channels of 128 inputs: two blocks of a tile, a piece of scales, 16 factors
+    assert fp8.packed_mx4_bytes(1, 32) == fp8.packed_mx4_bytes(32, 128) == 2 * (1024 + 256 + 64)
+    assert fp8.packed_mx4_bytes(33, 544) == 4 * (5 * 1024 + 2 * 256 + 64)
+    assert fp8.packed_mx4_bytes(0, 32) == fp8.packed_mx4_bytes(4, 40) == 0 and fp8._last_error()
+    assert fp8.packed_mx4_bytes(1 << 40, 32) == fp8.packed_mx4_bytes(4, 1 << 40) == 0
+
+
+def matmul(x=P[0], ldx=64, w=P[1], bias=None, x_type=BF16, T=4, K=64, N=40, y_type=F32, y=P[2]):
+    return fp8._matmul_mx4(x, ldx, w, bias, x_type, T, K, N, y_type, y, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    *[({n: None}, ERR_NULL) for n in ("x", "w", "y")],
+    (dict(T=-1), ERR_SHAPE), (dict(T=(1 << 21) + 1), ERR_SHAPE), (dict(K=80, ldx=80), ERR_SHAPE),
+    (dict(K=0), ERR_SHAPE), (dict(N=0), ERR_SHAPE), (dict(N=(1 << 21) + 1), ERR_SHAPE),
+    (dict(ldx=56), ERR_SHAPE), (dict(ldx=68), ERR_SHAPE), (dict(ldx=(1 << 21) + 8), ERR_SHAPE),
+    (dict(x_type=F32), ERR_UNSUPPORTED), (dict(y_type=F16), ERR_UNSUPPORTED), (dict(x_type=7), ERR_UNSUPPORTED),
+    (dict(x=P[0] + 8), ERR_ALIGN), (dict(w=P[1] + 8), ERR_ALIGN), (dict(y=P[2] + 4), ERR_ALIGN),
+    (dict(bias=P[3] + 2), ERR_ALIGN), (dict(y=P[0] + 496), ERR_SHAPE), (dict(y=P[1] + 5360), ERR_SHAPE),
+    (dict(bias=P[2] + 636), ERR_SHAPE),
+])
+def test_matmul_refuses(kw, code):
+    assert matmul(**kw) == code, fp8._last_error()
+    assert fp8._last_error().startswith(b"moe_matmul_mx4")
+
+
+def gated(x=P[0], ldx=64, wg=P[1], wu=P[2], kind=F16, T=4, d=64, f=96, h=P[3]):
+    return fp8._ffn_mx4(x, ldx, wg, wu, kind, T, d, f, h, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    *[({n: None}, ERR_NULL) for n in ("x", "wg", "wu", "h")],
+    (dict(T=-2), ERR_SHAPE), (dict(d=48), ERR_SHAPE), (dict(d=16416, ldx=16416), ERR_SHAPE),
+    (dict(f=40), ERR_SHAPE), (dict(f=16416), ERR_SHAPE), (dict(f=0), ERR_SHAPE), (dict(ldx=32), ERR_SHAPE),
+    (dict(kind=F32), ERR_UNSUPPORTED), (dict(wu=P[2] + 8), ERR_ALIGN), (dict(h=P[0]), ERR_SHAPE),
+    (dict(h=P[2] + 64), ERR_SHAPE),
+])
+def test_gated_refuses(kw, code):
+    assert gated(**kw) == code, fp8._last_error()
+    assert fp8._last_error().startswith(b"moe_ffn_mx4")
+
+
+def test_no_tokens_is_valid():
+    assert quantize(rows=0, x=None, codes=None, scales=None) == OK
+    assert dequantize(rows=0, codes=None, scales=None, y=None) == OK
+    assert matmul(T=0, x=None, y=None) == OK and gated(T=0, x=None, h=None) == OK
+
+
+def test_binding_refuses_host_tensors_and_autograd():
+    x, u8 = torch.randn(4, 64), torch.zeros((4, 32), dtype=torch.uint8)
+    w = fp8.Mx4Matrix(torch.zeros(fp8.packed_mx4_bytes(32, 64), dtype=torch.uint8), 32, 64)
+    for call in (lambda: fp8.quantize_rows_mx4(x), lambda: fp8.dequantize_rows_mx4(u8, u8[:, :2]),
+                 lambda: fp8.pack_mx4(u8, u8[:, :2]), lambda: fp8.matmul_mx4(x.bfloat16(), w),
+                 lambda: fp8.gated_ffn_mx4(x.bfloat16(), w, w)):
+        with pytest.raises(ValueError, match="device tensors"):
+            call()
+    p = x.bfloat16().requires_grad_()
+    for call in (lambda: fp8.matmul_mx4(p, w), lambda: fp8.gated_ffn_mx4(p, w, w),
+                 lambda: fp8.quantize_rows_mx4(p)):
+        with pytest.raises(RuntimeError, match="autograd"):
+            call()
