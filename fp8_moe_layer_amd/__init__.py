@@ -26,6 +26,7 @@ MOE_F_PERSISTENT = 2
 MOE_F_FUSED_COMBINE = 4
 MAX_EXPERTS = 512
 MAX_K = 32
+MX4_MAX_TOKENS = 32  # MOE_MX4_MAX_TOKENS
 
 if not LIB_PATH.exists():
     raise ImportError(
@@ -41,6 +42,10 @@ _i32 = C.c_int32
 class Dims(C.Structure):
     _fields_ = [("T", _i32), ("d", _i32), ("f", _i32), ("E", _i32), ("k_max", _i32),
                 ("n_shared", _i32), ("block_m", _i32), ("flags", C.c_uint32)]
+
+
+class _Mx4Weights(C.Structure):
+    _fields_ = [(n, _vp) for n in ("w_gate", "w_up", "w_down", "ws_gate", "ws_up", "ws_down")]
 
 
 class _NormDims(C.Structure):
@@ -114,6 +119,9 @@ _packed_mx4_bytes = _sig("moe_packed_mx4_bytes", _i64, _i32, _i32)
 _pack_mx4 = _sig("moe_pack_mx4", _i32, _vp, _vp, _i32, _i32, _vp, _vp)
 _matmul_mx4 = _sig("moe_matmul_mx4", _i32, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp)
 _ffn_mx4 = _sig("moe_ffn_mx4", _i32, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp)
+_mx4_workspace_bytes = _sig("moe_mx4_workspace_bytes", C.c_size_t, _DP)
+_mx4_forward = _sig("moe_mx4_forward", _i32, _DP, _i32, _vp, _i64, _vp, _vp, _vp, C.POINTER(_Mx4Weights),
+                    _vp, _vp, _vp, _vp, _vp, C.c_size_t, _vp)
 
 N_STAGE_EVENTS = 8
 STAGES = ("route", "topk", "permute", "gate_up", "requant", "down", "combine")
@@ -934,6 +942,126 @@ def gated_ffn_mx4(x: torch.Tensor, w_gate: Mx4Matrix, w_up: Mx4Matrix,
     c.run(_ffn_mx4, xp, ldx, _mx4_ptr(c, w_gate, f, d, "w_gate"), _mx4_ptr(c, w_up, f, d, "w_up"), kind,
           T, d, f, at)
     return h
+
+
+@dataclass
+class Mx4Experts:
+    """4-bit weights of a mixture-of-experts layer's experts: packed matrices (as
+    pack_mx4 lays them out), gate and up of f channels by d inputs, down of d by f."""
+    d: int
+    f: int
+    w_gate: torch.Tensor  # uint8 [E, packed_mx4_bytes(f, d)]
+    w_up: torch.Tensor
+    w_down: torch.Tensor  # uint8 [E, packed_mx4_bytes(d, f)]
+    ws_gate: Optional[torch.Tensor] = None  # shared experts
+    ws_up: Optional[torch.Tensor] = None
+    ws_down: Optional[torch.Tensor] = None
+
+    @property
+    def E(self) -> int:
+        return int(self.w_gate.shape[0])
+
+    @property
+    def n_shared(self) -> int:
+        return 0 if self.ws_gate is None else int(self.ws_gate.shape[0])
+
+    @staticmethod
+    def empty(E: int, d: int, f: int, n_shared: int = 0, device="cuda") -> "Mx4Experts":
+        u8 = lambda n, r, c: torch.empty((n, packed_mx4_bytes(r, c)), dtype=torch.uint8, device=device)
+        w = Mx4Experts(d, f, u8(E, f, d), u8(E, f, d), u8(E, d, f))
+        if n_shared:
+            w.ws_gate, w.ws_up, w.ws_down = u8(n_shared, f, d), u8(n_shared, f, d), u8(n_shared, d, f)
+        return w
+
+    def set_expert(self, which: str, e: int, codes: torch.Tensor, scales: torch.Tensor,
+                   shared: bool = False):
+        """Lays out one expert's matrix ("gate", "up" or "down") in slot e, from
+        codes and scales as quantize_rows_mx4 gives them."""
+        rows, cols = (self.d, self.f) if which == "down" else (self.f, self.d)
+        if tuple(codes.shape) != (rows, cols // 2):
+            raise ValueError(f"codes: expected shape {(rows, cols // 2)}, got {tuple(codes.shape)}")
+        pack_mx4(codes, scales, out=getattr(self, ("ws_" if shared else "w_") + which)[e])
+
+    def struct(self, c: _Call) -> _Mx4Weights:
+        gu, dn = packed_mx4_bytes(self.f, self.d), packed_mx4_bytes(self.d, self.f)
+        E, S = self.E, self.n_shared
+        at = lambda name, n, size: c.ptr(getattr(self, name), (n, size), torch.uint8, name)
+        shared = [at("ws_gate", S, gu), at("ws_up", S, gu), at("ws_down", S, dn)] if S else [None] * 3
+        return _Mx4Weights(at("w_gate", E, gu), at("w_up", E, gu), at("w_down", E, dn), *shared)
+
+
+class Mx4MoELayer:
+    """One mixture-of-experts layer with 4-bit experts, for steps of up to
+    MX4_MAX_TOKENS tokens (moe_mx4_forward): router, top-k, the picked and the
+    shared experts and their weighted sum in three launches on the current
+    stream.  w_router [E, d] and router_bias [E] fp32.  A workspace per stream is
+    allocated for the largest step so far and kept; a captured call has one of
+    its own, which the graph keeps."""
+
+    def __init__(self, weights: Mx4Experts, w_router: Optional[torch.Tensor], k_max: int,
+                 router_bias: Optional[torch.Tensor] = None):
+        self.w = weights
+        self.w_router = w_router
+        self.router_bias = router_bias
+        self.k_max = k_max
+        self._ws = {}
+        c = _Call(weights.w_gate, None)
+        self._index = c.index
+        self._wstruct = weights.struct(c)
+        E, d = weights.E, weights.d
+        self._router = None if w_router is None else c.ptr(w_router, (E, d), torch.float32, "w_router")
+        self._bias = None if router_bias is None else c.ptr(router_bias, (E,), torch.float32, "router_bias")
+        self._need = {}
+
+    def dims(self, T: int) -> Dims:
+        return dims(T, self.w.d, self.w.f, self.w.E, self.k_max, self.w.n_shared)
+
+    def _step(self, T: int):
+        """(dims, workspace bytes) of a step of T tokens."""
+        step = self._need.get(T)
+        if step is None:
+            dm = self.dims(T)
+            n = int(_mx4_workspace_bytes(C.byref(dm)))
+            if n == 0:
+                raise MoEError(int(2))
+            step = self._need[T] = (dm, n)
+        return step
+
+    def _workspace(self, c: _Call, n: int):
+        if torch.cuda.is_current_stream_capturing():
+            return c.empty((n,), torch.uint8)
+        ws = self._ws.get(c.stream)
+        if ws is None or ws.numel() < n:
+            ws = self._ws[c.stream] = c.empty((n,), torch.uint8)
+        return ws
+
+    def forward(self, x: torch.Tensor, k_per_token: Optional[torch.Tensor] = None,
+                logits_override: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                topk_ids: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+        """x [T, d] bf16 or fp16 (rows may be strided) -> out [T, d] in its type.
+        k_per_token int32 [T]; logits_override fp32 [T, E]; topk_ids int32 and
+        topk_w fp32 [T, k_max]: where the picks are written, if given."""
+        T, d = _shape2(x, "x")
+        _no_autograd("Mx4MoELayer.forward", x, logits_override)
+        c = _Call(x, stream)
+        if c.index != self._index:
+            raise ValueError(f"x is on {c.dev}, the weights are on cuda:{self._index}")
+        kind = _type(x.dtype, _TYPES16)
+        xp, ldx = c.rows(x, (T, self.w.d), x.dtype, "x")
+        dm, need = self._step(T)
+        out, at = _out(c, out, (T, d), x.dtype, "out")
+        i32, f32, K = torch.int32, torch.float32, self.k_max
+        opt = lambda t, shape, dtype, name: None if t is None else c.ptr(t, shape, dtype, name)
+        ws = self._workspace(c, need)
+        c.run(_mx4_forward, C.byref(dm), kind, xp, ldx, self._router, self._bias,
+              opt(k_per_token, (T,), i32, "k_per_token"), C.byref(self._wstruct),
+              opt(logits_override, (T, self.w.E), f32, "logits_override"), at,
+              opt(topk_ids, (T, K), i32, "topk_ids"), opt(topk_w, (T, K), f32, "topk_w"),
+              ws.data_ptr(), ws.numel())
+        return out
+
+    __call__ = forward
 
 
 # --------------------------------------------------------------------------- whole layer

@@ -18,7 +18,8 @@ LIB = HERE / "libfp8moe.so"
 LIB_DEBUG = HERE / "libfp8moe_debug.so"
 SOURCES = ["kernels_route.hip", "kernels_permute.hip", "kernels_expert.hip", "kernels_persistent.hip",
            "abi.hip", "batching.hip", "kernels_dense.hip", "dense.hip",
-           "kernels_norm.hip", "norm.hip", "kernels_mx4.hip", "mx4.hip"]
+           "kernels_norm.hip", "norm.hip", "kernels_mx4.hip",
+           "kernels_mx4_moe.hip", "mx4.hip"]
 ARCH = os.environ.get("FP8MOE_ARCH", "gfx950")
 
 HIPCC_FLAGS = [

@@ -189,7 +189,7 @@ __device__ __forceinline__ void load_factors(const uint8_t *block, const Mx4Layo
 // Up to 16*XT tokens: a workgroup takes R blocks of 16 rows (gated: of each
 // matrix), its W waves their pieces of K in turn; their sums meet in LDS and are
 // added in wave order.
-template <class Op, class OUT, int XT, int R, bool GATED, int W>
+template <class Op, class OUT, int XT, int R, bool GATED, int W, int D>
 __global__ __launch_bounds__(W * kWave) void mx4_few_kernel(Mx4Product p) {
   constexpr int NR = GATED ? 2 * R : R;
   __shared__ v4f part[W][NR][XT][kWave];
@@ -216,12 +216,17 @@ __global__ __launch_bounds__(W * kWave) void mx4_few_kernel(Mx4Product p) {
   for (int r = 0; r < NR; ++r)
 #pragma unroll
     for (int m = 0; m < XT; ++m) acc[r][m] = v4f{0.f, 0.f, 0.f, 0.f};
-  mx4_stream<Op, XT, NR>(block, l, wave, W, lane,
-                         [&](int kt, int j, int m) {
-                           if (kt * 4 + q >= groups) return v4i{0, 0, 0, 0};
-                           return load16(row[m] + kt * 128 + j * 8);
-                         },
-                         acc);
+  Mx4Ring<Op, XT, NR, D> ring;
+  run_ring<D>(
+      l.kt > wave ? (l.kt - wave + W - 1) / W : 0,
+      [&](int c, int i) {
+        const int kt = wave + i * W;
+        const bool in = kt * 4 + q < groups;
+        ring.load(c, block, l, kt, lane, [&](int j, int m) {
+          return in ? load16(row[m] + kt * 128 + j * 8) : v4i{0, 0, 0, 0};
+        });
+      },
+      [&](int c, int) { ring.multiply(c, acc); });
 #pragma unroll
   for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -375,9 +380,9 @@ template <class Op, class OUT, bool GATED>
 hipError_t launch_product(const Mx4Product &p, hipStream_t stream) {
   const Mx4Layout l(p.N, p.K);
   if (p.T <= 16) {
-    mx4_few_kernel<Op, OUT, 1, 1, GATED, 8><<<l.blocks, 8 * kWave, 0, stream>>>(p);
+    mx4_few_kernel<Op, OUT, 1, 1, GATED, 8, GATED ? 3 : 4><<<l.blocks, 8 * kWave, 0, stream>>>(p);
   } else if (p.T <= 32) {
-    mx4_few_kernel<Op, OUT, 2, 1, GATED, 8><<<l.blocks, 8 * kWave, 0, stream>>>(p);
+    mx4_few_kernel<Op, OUT, 2, 1, GATED, 8, 2><<<l.blocks, 8 * kWave, 0, stream>>>(p);
   } else {
     constexpr int BM = 128, BN = 128;
     const int channels = GATED ? BN / 2 : BN;

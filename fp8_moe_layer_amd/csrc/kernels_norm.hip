@@ -427,6 +427,8 @@ struct Backward {
 
 }  // namespace
 
+FP8MOE_DEBUG_TAKE(norm)
+
 hipError_t launch_norm_forward(const NormForward &p, hipStream_t stream) {
   return with_types(p.type, p.w_type, p.d, Forward{p, stream});
 }

@@ -2,18 +2,31 @@
 // validation and kernel enqueueing.
 #include "mx4.hpp"
 
+#include "common.hpp"
 #include "dense.hpp"
 #include "entry.hpp"
 
 using namespace fp8moe;
 
-static_assert(MOE_MX4_GROUP == kMxGroup, "group");
+static_assert(MOE_MX4_GROUP == kMxGroup && MOE_MX4_MAX_TOKENS == kMx4MaxTokens &&
+                  MOE_MX4_MAX_SHARED == kMx4MaxShared && MOE_MAX_EXPERTS == kMaxExperts &&
+                  MOE_MAX_K == kMaxK, "limits");
 
 namespace {
 
+// The end of an entry point that enqueued work (in the debug build: wait for it
+// and report the device checks that failed).
 moe_status finish(hipError_t e, const char *fn) {
   if (e != hipSuccess)
     return fail_status(MOE_ERR_HIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
+#ifdef FP8MOE_DEBUG
+  const uint32_t b = debug_take_mx4();
+  if (b)
+    return fail_status(MOE_ERR_DEVICE_CHECK, "%s: device checks failed (0x%x):%s%s%s", fn, b,
+                       (b & 1u) ? " k_per_token outside [1, k_max];" : "",
+                       (b & 2u) ? " non-finite router logit;" : "",
+                       (b & 0x80000000u) ? " the check words could not be read;" : "");
+#endif
   return ok_status();
 }
 
@@ -30,6 +43,22 @@ moe_status check_types(const char *fn, int32_t x_type, int32_t y_type) {
     return fail_status(MOE_ERR_UNSUPPORTED,
                        "%s: x_type=%d (MOE_T_BF16 or MOE_T_F16), y_type=%d (the same or MOE_T_F32)",
                        fn, x_type, y_type);
+  return MOE_OK;
+}
+
+moe_status check_layer(const char *fn, const moe_dims *m) {
+  if (!m) return fail_status(MOE_ERR_NULL, "%s: dims is required", fn);
+  if (m->flags) return fail_status(MOE_ERR_UNSUPPORTED, "%s: flags=0x%x must be 0", fn, m->flags);
+  if (m->T < 0 || m->T > MOE_MX4_MAX_TOKENS)
+    return fail_status(MOE_ERR_SHAPE, "%s: T=%d must be in [0, %d]", fn, m->T, MOE_MX4_MAX_TOKENS);
+  if (m->d < 32 || m->d % 32 || m->d > MOE_MAX_HIDDEN || m->f < 32 || m->f % 32 || m->f > MOE_MAX_FFN)
+    return fail_status(MOE_ERR_SHAPE, "%s: d=%d, f=%d must be multiples of 32 in [32, %d] and [32, %d]",
+                       fn, m->d, m->f, MOE_MAX_HIDDEN, MOE_MAX_FFN);
+  if (m->E < 1 || m->E > MOE_MAX_EXPERTS || m->k_max < 1 || m->k_max > MOE_MAX_K || m->k_max > m->E ||
+      m->n_shared < 0 || m->n_shared > MOE_MX4_MAX_SHARED)
+    return fail_status(MOE_ERR_SHAPE, "%s: E=%d (in [1, %d]), k_max=%d (in [1, min(E, %d)]), n_shared=%d "
+                       "(in [0, %d])", fn, m->E, MOE_MAX_EXPERTS, m->k_max, MOE_MAX_K, m->n_shared,
+                       MOE_MX4_MAX_SHARED);
   return MOE_OK;
 }
 
@@ -137,6 +166,57 @@ moe_status moe_ffn_mx4(const void *x, int64_t ldx, const void *w_gate, const voi
   const Mx4Product p{x, ldx, (const uint8_t *)w_gate, (const uint8_t *)w_up, nullptr, T, d, f, type,
                      type, h};
   return finish(launch_mx4_product(p, as_stream(stream)), fn);
+}
+
+size_t moe_mx4_workspace_bytes(const moe_dims *dims) {
+  if (check_layer("moe_mx4_workspace_bytes", dims)) return 0;
+  (void)ok_status();
+  return mx4_moe_workspace(dims->T, dims->f, dims->E, dims->n_shared, dims->k_max);
+}
+
+moe_status moe_mx4_forward(const moe_dims *dims, int32_t type, const void *x, int64_t ldx,
+                           const float *w_router, const float *router_bias,
+                           const int32_t *k_per_token, const moe_mx4_weights *w,
+                           const float *logits_override, void *out, int32_t *topk_ids_out,
+                           float *topk_w_out, void *workspace, size_t workspace_bytes, void *stream) {
+  const char *fn = "moe_mx4_forward";
+  moe_status s = check_layer(fn, dims);
+  if (s || (s = check_types(fn, type, type)) || (s = check_rows(fn, dims->T, ldx, dims->d, 2))) return s;
+  const moe_dims &m = *dims;
+  if (m.T == 0) return ok_status();
+  if (!x || !out || !w || !w->w_gate || !w->w_up || !w->w_down ||
+      (m.n_shared > 0 && (!w->ws_gate || !w->ws_up || !w->ws_down)))
+    return fail_status(MOE_ERR_NULL, "%s: x, out and the experts' matrices are required", fn);
+  if (!w_router && !logits_override)
+    return fail_status(MOE_ERR_NULL, "%s: w_router or logits_override is required", fn);
+  if (!all_aligned({x, out, w_router, w->w_gate, w->w_up, w->w_down, w->ws_gate, w->ws_up, w->ws_down}, 16) ||
+      !all_aligned({router_bias, k_per_token, logits_override, topk_ids_out, topk_w_out}, 4))
+    return fail_status(MOE_ERR_ALIGN, "%s: x, out, w_router and the matrices must be 16-byte, the other "
+                       "arrays 4-byte aligned", fn);
+  const size_t need = mx4_moe_workspace(m.T, m.f, m.E, m.n_shared, m.k_max);
+  if (!workspace || workspace_bytes < need)
+    return fail_status(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn,
+                       workspace ? workspace_bytes : (size_t)0, need);
+  if (!aligned(workspace, 256))
+    return fail_status(MOE_ERR_ALIGN, "%s: workspace must be 256-byte aligned", fn);
+  const int64_t gu = Mx4Layout(m.f, m.d).bytes(), dn = Mx4Layout(m.d, m.f).bytes();
+  const int64_t slots = (int64_t)m.T * m.k_max * 4, scores = (int64_t)m.T * m.E * 4;
+  const Span outs[] = {{out, (int64_t)m.T * m.d * 2}, {topk_ids_out, slots}, {topk_w_out, slots},
+                       {workspace, (int64_t)need}};
+  const Span ins[] = {{x, span_rows(m.T, ldx, m.d, 2)},
+                      {logits_override ? nullptr : w_router, (int64_t)m.E * m.d * 4},
+                      {logits_override ? nullptr : router_bias, (int64_t)m.E * 4},
+                      {k_per_token, (int64_t)m.T * 4}, {logits_override, scores},
+                      {w->w_gate, m.E * gu}, {w->w_up, m.E * gu}, {w->w_down, m.E * dn},
+                      {w->ws_gate, m.n_shared * gu}, {w->ws_up, m.n_shared * gu},
+                      {w->ws_down, m.n_shared * dn}};
+  if (clash(outs, ins))
+    return fail_status(MOE_ERR_SHAPE, "%s: an output or the workspace overlaps an input or another output", fn);
+  auto u8 = [](const void *p) { return static_cast<const uint8_t *>(p); };
+  const Mx4Moe p{x, ldx, m.T, m.d, m.f, m.E, m.n_shared, m.k_max, type, w_router, router_bias,
+                 logits_override, k_per_token, u8(w->w_gate), u8(w->w_up), u8(w->w_down), u8(w->ws_gate),
+                 u8(w->ws_up), u8(w->ws_down), out, topk_ids_out, topk_w_out, (char *)workspace};
+  return finish(launch_mx4_moe(p, as_stream(stream)), fn);
 }
 
 }  // extern "C"

@@ -56,4 +56,24 @@ struct Mx4Product {
 };
 hipError_t launch_mx4_product(const Mx4Product &p, hipStream_t stream);
 
+// A whole MoE layer of up to kMx4MaxTokens tokens.  Expert e's matrices follow
+// each other by the packed size of one.
+constexpr int kMx4MaxTokens = 32, kMx4MaxShared = 32;
+struct Mx4Moe {
+  const void *x;
+  int64_t ldx;
+  int32_t T, d, f, E, S, k_max, type;
+  const float *w_router, *bias;    // w_router: NULL with override
+  const float *logits_override;
+  const int32_t *kpt;
+  const uint8_t *w_gate, *w_up, *w_down, *ws_gate, *ws_up, *ws_down;
+  void *out;
+  int32_t *ids_out;
+  float *w_out;
+  char *workspace;
+};
+size_t mx4_moe_workspace(int32_t T, int32_t f, int32_t E, int32_t S, int32_t k_max);
+hipError_t launch_mx4_moe(const Mx4Moe &p, hipStream_t stream);
+uint32_t debug_take_mx4();
+
 }  // namespace fp8moe

@@ -82,60 +82,74 @@ __device__ __forceinline__ float mx4_factor(const uint8_t *block, const Mx4Layou
   return reinterpret_cast<const float *>(block + l.factors)[row] * (Op::kShift ? 0x1p-15f : 1.0f);
 }
 
-// Few tokens: a wave's share of the products of NR blocks of 16 rows with XT x 16
-// tokens.  It takes pieces of four tiles, `first`, first + stride, ... of the
-// blocks; the next piece's weights are loaded before this one's products.
-// x(kt, j, m): the lane's activations of tile kt, step j, tokens m*16 ...
-// acc[r][m]: element i of lane l is row (l/16)*4 + i, token m*16 + l%16.
-template <class Op, int XT, int NR, class XLoad>
-__device__ __forceinline__ void mx4_stream(const uint8_t *const (&block)[NR], const Mx4Layout &l,
-                                           int first, int stride, int lane, XLoad x,
-                                           v4f (&acc)[NR][XT]) {
-  const int pieces = (l.kt + 3) / 4;
-  v4i w[NR][4];
-  uint32_t s[NR];
-  auto fetch = [&](int u) {
+// Few tokens: what a wave has in flight of the stream of tiles of NR blocks of 16
+// rows against XT x 16 tokens, D tiles deep.  Loads return in the order of their
+// issue, so a tile's activations are asked for with its weights, D tiles ahead:
+// asked for when they are needed, they would come behind every weight in flight.
+// ABS: the rows' factors go into the scales (bf16 operands only), so that one
+// accumulator can take blocks of several matrices.
+template <class Op, int XT, int NR, int D, bool ABS = false>
+struct Mx4Ring {
+  v4i w[D][NR];
+  uint32_t s[D][NR];
+  float f[D][NR];
+  typename Op::X x[D][4][XT];
+
+  // Tile kt of the blocks into slot c.  load_x(j, m): the lane's activations of
+  // step j, tokens m*16 ...
+  template <class LoadX>
+  __device__ __forceinline__ void load(int c, const uint8_t *const (&block)[NR], const Mx4Layout &l,
+                                       int kt, int lane, LoadX load_x) {
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
-      s[r] = *reinterpret_cast<const uint32_t *>(block[r] + l.scales + (int64_t)u * 256 + lane * 4);
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-        if (u * 4 + t < l.kt) w[r][t] = load16_nt(block[r] + (int64_t)(u * 4 + t) * 1024 + lane * 16);
+      w[c][r] = load16_nt(block[r] + (int64_t)kt * 1024 + lane * 16);
+      s[c][r] = block[r][l.scales + (kt >> 2) * 256 + lane * 4 + (kt & 3)];
+      if (ABS) f[c][r] = reinterpret_cast<const float *>(block[r] + l.factors)[lane & 15];
     }
-  };
-  if (first < pieces) fetch(first);
-  for (int u = first; u < pieces; u += stride) {
-    v4i cw[NR][4];
-    uint32_t cs[NR];
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      cs[r] = s[r];
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) cw[r][t] = w[r][t];
-    }
-    if (u + stride < pieces) fetch(u + stride);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int kt = u * 4 + t;
-      if (kt >= l.kt) break;
-      float sc[NR];
-#pragma unroll
-      for (int r = 0; r < NR; ++r) sc[r] = mx4_scale<Op>(cs[r], t);
-      typename Op::X xs[4][XT];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int m = 0; m < XT; ++m) xs[j][m] = x(kt, j, m);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const v4i a = mx4_operand<Op>(cw[r][t][j], sc[r]);
-#pragma unroll
-          for (int m = 0; m < XT; ++m) acc[r][m] = Op::mfma(a, xs[j][m], acc[r][m]);
-        }
-    }
+      for (int m = 0; m < XT; ++m) x[c][j][m] = load_x(j, m);
   }
+  // acc[r][m] += the slot's products: element i of lane l is row (l/16)*4 + i,
+  // token m*16 + l%16
+  __device__ __forceinline__ void multiply(int c, v4f (&acc)[NR][XT]) const {
+    float sc[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) sc[r] = mx4_scale<Op>(s[c][r], 0) * (ABS ? f[c][r] : 1.0f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const v4i a = mx4_operand<Op>(w[c][r][j], sc[r]);
+#pragma unroll
+        for (int m = 0; m < XT; ++m) acc[r][m] = Op::mfma(a, x[c][j][m], acc[r][m]);
+      }
+  }
+};
+
+// Runs n tiles through a ring of D: load(c, i) asks for tile i into slot c,
+// use(c, i) multiplies it.
+template <int D, class Load, class Use>
+__device__ __forceinline__ void run_ring(int n, Load load, Use use) {
+#pragma unroll
+  for (int c = 0; c < D; ++c)
+    if (c < n) load(c, c);
+  int i = 0;
+  // no branches between the loads: the compiler's waits then leave D - 1 tiles in flight
+  for (; i + 2 * D <= n; i += D)
+#pragma unroll
+    for (int c = 0; c < D; ++c) {
+      use(c, i + c);
+      load(c, i + c + D);
+    }
+  for (; i < n; i += D)
+#pragma unroll
+    for (int c = 0; c < D; ++c)
+      if (i + c < n) {
+        use(c, i + c);
+        if (i + c + D < n) load(c, i + c + D);
+      }
 }
 
 // channel of row p of block b

@@ -4,12 +4,24 @@
 
 #include <float.h>
 
+#include "common.hpp"
 #include "dense.hpp"
 #include "entry.hpp"
 
 using namespace fp8moe;
 
 namespace {
+
+// The end of an entry point that enqueued work (the debug build waits for it).
+moe_status finish(hipError_t e, const char *fn) {
+  if (e != hipSuccess)
+    return fail_status(MOE_ERR_HIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
+#ifdef FP8MOE_DEBUG
+  if (debug_take_norm())
+    return fail_status(MOE_ERR_DEVICE_CHECK, "%s: the check words could not be read", fn);
+#endif
+  return ok_status();
+}
 
 moe_status check_dims(const char *fn, const moe_norm_dims *m) {
   if (!m) return fail_status(MOE_ERR_NULL, "%s: dims is required", fn);
@@ -72,10 +84,7 @@ moe_status moe_norm_residual(const moe_norm_dims *dims, const void *x, int64_t l
     return fail_status(MOE_ERR_SHAPE, "%s: an output overlaps an input or another output", fn);
   const NormForward p{m.T, m.d, m.type, m.w_type, m.gate_rows, m.scale, m.offset, m.eps, x, ldx, y,
                       ldy, w_post, gate, ldg, w_next, r, n, rstd_y, rstd_r};
-  const hipError_t e = launch_norm_forward(p, as_stream(stream));
-  if (e != hipSuccess)
-    return fail_status(MOE_ERR_HIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
-  return ok_status();
+  return finish(launch_norm_forward(p, as_stream(stream)), fn);
 }
 
 size_t moe_norm_residual_backward_workspace_bytes(const moe_norm_dims *dims) {
@@ -140,10 +149,7 @@ moe_status moe_norm_residual_backward(const moe_norm_dims *dims, const void *dr,
   const NormBackward p{m.T, m.d, m.type, m.w_type, m.gate_rows, m.scale, m.offset, dr, lddr, dn, lddn,
                        x, ldx, y, ldy, rstd_y, rstd_r, w_post, gate, ldg, w_next, dx, dy, dw_post,
                        dgate, dw_next, static_cast<float *>(workspace)};
-  const hipError_t e = launch_norm_backward(p, as_stream(stream));
-  if (e != hipSuccess)
-    return fail_status(MOE_ERR_HIP, "%s: launch failed: %s", fn, hipGetErrorString(e));
-  return ok_status();
+  return finish(launch_norm_backward(p, as_stream(stream)), fn);
 }
 
 }  // extern "C"

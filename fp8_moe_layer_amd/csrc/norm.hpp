@@ -44,5 +44,6 @@ struct NormBackward {
 };
 size_t norm_backward_workspace(int32_t T, int32_t d, int32_t gate_rows);
 hipError_t launch_norm_backward(const NormBackward &p, hipStream_t stream);
+uint32_t debug_take_norm();
 
 }  // namespace fp8moe

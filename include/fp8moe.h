@@ -465,6 +465,40 @@ moe_status moe_matmul_mx4(const void *x, int64_t ldx, const void *w, const float
 moe_status moe_ffn_mx4(const void *x, int64_t ldx, const void *w_gate, const void *w_up, int32_t type,
                        int32_t T, int32_t d, int32_t f, void *h, void *stream);
 
+/* Forward pass of a whole mixture-of-experts layer of a few tokens with 4-bit
+ * experts, in three launches: router logits (or logits_override), top-k and
+ * softmax weights, the picked experts' gated blocks, their down projections and
+ * the weighted sum, and the shared experts.  Against moe_fused_forward: nothing
+ * is permuted, activations are not quantised (bf16 or fp16 rows in and out,
+ * `type`), and the logits are summed in 64 bits, then rounded to fp32; ids and
+ * weights are moe_route_topk's of those.  SiLU(g) * u times the routing weight is
+ * held with 16 bits, the sum over experts and channels in fp32, rounded once.
+ * dims: T up to MOE_MX4_MAX_TOKENS (0 is valid), d and f multiples of 32 up to
+ * MOE_MAX_HIDDEN / MOE_MAX_FFN, E, k_max as everywhere, n_shared up to
+ * MOE_MX4_MAX_SHARED; block_m is ignored, flags must be 0.
+ * x [T][d] with row stride ldx; w_router [E][d] (may be NULL with
+ * logits_override); router_bias [E] or NULL (added to the sums, not to
+ * logits_override); k_per_token [T] or NULL; logits_override [T][E] fp32 or NULL;
+ * out [T][d]; topk_ids_out / topk_w_out [T][k_max] or NULL.
+ * Weights: E (n_shared) packed matrices one after the other, gate and up of f
+ * channels by d inputs, down of d by f.  The down projections' weights are bf16
+ * numbers as they are: below 2^-125 they may count as zero, and a channel with a
+ * scale byte above 251 in an expert in use is a NaN for every token.
+ * workspace: moe_mx4_workspace_bytes(dims), 256-byte aligned, not touched by
+ * anything else while the work is in flight; it need not be cleared. */
+#define MOE_MX4_MAX_TOKENS 32
+#define MOE_MX4_MAX_SHARED 32
+typedef struct {
+  const void *w_gate, *w_up, *w_down;    /* [E] */
+  const void *ws_gate, *ws_up, *ws_down; /* [n_shared]; NULL when 0 */
+} moe_mx4_weights;
+size_t moe_mx4_workspace_bytes(const moe_dims *dims /*host*/);
+moe_status moe_mx4_forward(const moe_dims *dims /*host*/, int32_t type, const void *x, int64_t ldx,
+                           const float *w_router, const float *router_bias,
+                           const int32_t *k_per_token, const moe_mx4_weights *w /*host*/,
+                           const float *logits_override, void *out, int32_t *topk_ids_out,
+                           float *topk_w_out, void *workspace, size_t workspace_bytes, void *stream);
+
 /* ------------------------------------------------------------------------ */
 /* Norms around a block                                                      */
 /* ------------------------------------------------------------------------ */

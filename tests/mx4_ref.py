@@ -62,3 +62,39 @@ def gated(x, wg, wu):
     s = g * torch.sigmoid(g)
     es = 1.1 * (eg + 2 * U * g.abs()) + 8 * U * s.abs()
     return s * u, es * (u.abs() + eu) + s.abs() * (eu + 2 * U * u.abs()) + 3 * U * (s * u).abs()
+
+
+def routing(logits, k_max, k_per_token=None):
+    """ids (-1 in empty slots) and weights in fp64 from fp32 logits: descending, ties
+    to the lower index."""
+    T, E = logits.shape
+    order = torch.sort(logits, dim=1, descending=True, stable=True)[1][:, :k_max]
+    top = torch.gather(logits.double(), 1, order)
+    kt = torch.full((T,), k_max, device=logits.device) if k_per_token is None else k_per_token
+    there = torch.arange(k_max, device=logits.device)[None] < kt[:, None]
+    p = torch.softmax(torch.where(there, top, -torch.inf), 1)
+    return torch.where(there, order, -1), p
+
+
+def layer(x, ids, p, experts, shared):
+    """(out, its error) of the layer for given picks.  experts, shared: lists of
+    (gate, up, down) values in fp64.  A routing weight is off by an exponential, a
+    sum of up to 32 and a division, under 64u for logits within 30 of each other; h
+    is held with 16 bits (2^-17, half a step); the sum over experts and channels runs
+    through 2 x K/32 instructions."""
+    T, d = x.shape
+    out = torch.zeros((T, d), dtype=torch.float64, device=x.device)
+    size, err = torch.zeros_like(out), torch.zeros_like(out)
+    K = 0
+    for e, (wg, wu, wd) in list(enumerate(experts)) + [(-2, w) for w in shared]:
+        weight = torch.ones((T, 1), dtype=torch.float64, device=x.device) if e == -2 else \
+            torch.where(ids == e, p, 0.0).sum(1, keepdim=True)
+        if not bool((weight != 0).any()):
+            continue
+        h, eh = gated(x, wg, wu)
+        h, eh = h * weight, eh * weight + (64 * U + 2.0 ** -17) * (h * weight).abs()
+        out += h @ wd.t()
+        size += h.abs() @ wd.abs().t()
+        err += eh @ wd.abs().t()
+        K += wd.shape[1]
+    return out, err + 2 * (K / 32 + 52) * 2 * U * size

@@ -1,0 +1,157 @@
+"""The 4-bit mixture-of-experts layer of a few tokens on the GPU: picks exactly,
+outputs element by element against 64 bits (bounds: mx4_ref.py)."""
+import pytest
+import torch
+
+import mx4_ref
+from gpu_common import dev, lib
+from test_gpu_dense import F16S, gen, guarded, normal, strided, within
+
+pytestmark = pytest.mark.gpu
+
+
+class Layer:
+    def __init__(self, d, f, E, k, S=0, bias=False, seed=0):
+        g = self.g = gen(seed + d + f + E)
+        self.d, self.f, self.E, self.k = d, f, E, k
+        self.router = normal(g, (E, d), d ** -0.5)
+        self.bias = normal(g, (E,)) if bias else None
+        w = lib().Mx4Experts.empty(E, d, f, S)
+        self.values = []
+        for e in range(E + S):
+            three = []
+            for which, shape in (("gate", (f, d)), ("up", (f, d)), ("down", (d, f))):
+                codes, scales = lib().quantize_rows_mx4(normal(g, shape, shape[1] ** -0.5))
+                w.set_expert(which, e if e < E else e - E, codes, scales, shared=e >= E)
+                three.append(mx4_ref.values(codes, scales))
+            self.values.append(tuple(three))
+        self.op = lib().Mx4MoELayer(w, self.router, k, self.bias)
+
+    def logits(self, x):
+        s = x.double() @ self.router.double().t()
+        return (s if self.bias is None else s + self.bias.double()).float()
+
+    def check(self, x, kpt=None, override=None, what=""):
+        T = x.shape[0]
+        ids = torch.full((T, self.k), -7, dtype=torch.int32, device=dev())
+        w = torch.full((T, self.k), -7.0, device=dev())
+        out, ok = guarded((T, self.d), x.dtype)
+        self.op.forward(x, k_per_token=kpt, logits_override=override, out=out, topk_ids=ids, topk_w=w)
+        ok()
+        rid, p = mx4_ref.routing(self.logits(x) if override is None else override, self.k, kpt)
+        assert torch.equal(ids.long(), rid), what
+        assert float((w.double() - p).abs().max()) <= 64 * mx4_ref.U
+        ref, tol = mx4_ref.layer(x, rid, p, self.values[:self.E], self.values[self.E:])
+        within(out, ref, tol, what)
+        assert torch.equal(out, self.op.forward(x, k_per_token=kpt, logits_override=override))
+        return out
+
+
+@pytest.mark.parametrize("dtype", F16S)
+@pytest.mark.parametrize("d,f,E,k,S", [(32, 32, 1, 1, 0), (64, 96, 4, 2, 0), (256, 512, 8, 2, 1),
+                                       (544, 160, 70, 5, 2), (2048, 768, 128, 8, 0), (160, 1056, 130, 6, 0),
+                                       (96, 64, 512, 32, 3), (1056, 2080, 3, 3, 0)])
+def test_tokens_and_shapes(d, f, E, k, S, dtype):
+    layer = Layer(d, f, E, k, S, bias=E % 2 == 0)
+    for T in (1, 2, 3, 15, 16, 17, 31, 32):
+        layer.check(strided(normal(layer.g, (T, d), 1, dtype), 8 if T % 2 else 0), what=f"T {T}")
+
+
+def test_per_token_budgets_ties_and_given_logits():
+    layer = Layer(128, 64, 16, 6, 1)
+    for T in (5, 32):
+        x = normal(layer.g, (T, 128), 1, torch.bfloat16)
+        kpt = torch.randint(1, 7, (T,), device=dev(), generator=layer.g, dtype=torch.int32)
+        layer.check(x, kpt=kpt)
+        layer.check(x, override=torch.zeros((T, 16), device=dev()))  # all tie
+        lumps = torch.randint(-2, 3, (T, 16), device=dev(), generator=layer.g).float()
+        layer.check(x, kpt=kpt, override=lumps)
+        one = torch.zeros((T, 16), device=dev())
+        one[:, 9], one[:, 3] = 20, 10  # every token on the same experts
+        layer.check(x, override=one)
+
+
+def test_logits_are_summed_in_64_bits():
+    """Two experts whose scores differ by less than an fp32 sum's rounding."""
+    d, E = 4096, 8
+    layer = Layer(d, 32, E, 2)
+    x = (normal(layer.g, (4, d)) * 100).bfloat16()
+    layer.router[:] = layer.router[0]
+    layer.router[:, 0] += torch.arange(E, device=dev()) * 2.0 ** -22
+    layer.check(x)
+
+
+@pytest.mark.parametrize("T", [4, 20])
+def test_a_poisoned_token_stays_alone(T):
+    layer = Layer(256, 128, 8, 2, 1)
+    x = normal(layer.g, (T, 256), 1, torch.bfloat16)
+    clean = layer.op.forward(x)
+    x[2] = torch.nan
+    ids = torch.empty((T, 2), dtype=torch.int32, device=dev())
+    got = layer.op.forward(x, topk_ids=ids)
+    keep = torch.arange(T, device=dev()) != 2
+    assert torch.equal(got[keep], clean[keep]) and bool(got[2].isnan().all())
+    assert bool(((ids >= 0) & (ids < 8)).all())
+
+
+def test_no_tokens_other_sizes_and_a_workspace_that_was_filled():
+    """Steps of changing size on one layer; what a workspace held before does not matter."""
+    layer = Layer(96, 96, 8, 2, 1)
+    assert layer.op.forward(torch.empty((0, 96), dtype=torch.bfloat16, device=dev())).shape == (0, 96)
+    for T in (3, 32, 1, 9, 32):
+        x = normal(layer.g, (T, 96), 1, torch.bfloat16)
+        a = layer.check(x, what=f"T {T}")
+        for ws in layer.op._ws.values():
+            ws.fill_(0xFF)
+        assert torch.equal(a, layer.op.forward(x))
+
+
+def test_streams_and_graphs():
+    """Two streams at once, each with a workspace of its own; graphs captured and
+    replayed with eager steps of the same layer between."""
+    layer = Layer(512, 256, 16, 4, 1)
+    xs = [normal(layer.g, (T, 512), 1, torch.float16) for T in (1, 12, 32)]
+    want = [layer.op.forward(x) for x in xs]
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (a, b):
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[layer.op.forward(x, stream=s) for s in (a, b)] for _ in range(3) for x in xs]
+    torch.cuda.synchronize()
+    for i, pair in enumerate(got):
+        assert all(torch.equal(o, want[i % 3]) for o in pair)
+    graphs = []
+    for x in xs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = layer.op.forward(x)
+        graphs.append((graph, out))
+    for k in range(4):
+        for x in xs:
+            x.copy_(normal(gen(k), tuple(x.shape), 1, torch.float16))
+        for graph, _ in graphs:
+            graph.replay()
+        eager = [layer.op.forward(x) for x in xs]
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, e) for (_, o), e in zip(graphs, eager)), k
+
+
+def test_refusals_on_the_device():
+    f = lib()
+    layer = Layer(64, 32, 4, 2)
+    x = torch.ones((2, 64), dtype=torch.bfloat16, device=dev())
+    with pytest.raises(f.MoEError, match="T=33"):
+        layer.op.forward(x[:1].repeat(33, 1))
+    with pytest.raises(TypeError, match="expected one of"):
+        layer.op.forward(x.float())
+    with pytest.raises(ValueError, match="shape"):
+        layer.op.forward(x[:, :32])
+    with pytest.raises(ValueError, match="topk_ids"):
+        layer.op.forward(x, topk_ids=torch.empty((2, 3), dtype=torch.int32, device=dev()))
+    with pytest.raises(f.MoEError, match="k_max"):
+        f.Mx4MoELayer(layer.op.w, layer.router, 5).forward(x)
+    with pytest.raises(f.MoEError, match="logits_override is required"):
+        f.Mx4MoELayer(layer.op.w, None, 2).forward(x)
+    with pytest.raises(ValueError, match="w_router"):
+        f.Mx4MoELayer(layer.op.w, layer.router[:2], 2)
+    with pytest.raises(ValueError, match="codes: expected shape"):
+        layer.op.w.set_expert("gate", 0, *f.quantize_rows_mx4(torch.ones((64, 32), device=dev())))

@@ -1,6 +1,8 @@
 """4-bit weights: the reference quantiser against its definition, and what the
 entry points refuse (every call fails host validation, so nothing is enqueued
 and no GPU is needed, or has no tokens)."""
+import ctypes as C
+
 import numpy as np
 import pytest
 import torch
@@ -139,3 +141,43 @@ def test_binding_refuses_host_tensors_and_autograd():
                  lambda: fp8.quantize_rows_mx4(p)):
         with pytest.raises(RuntimeError, match="autograd"):
             call()
+
+
+# ------------------------------------------------------------------ the layer
+
+def layer(dm={}, kind=BF16, x=P[0], ldx=64, router=P[1], bias=None, kpt=None, w={}, override=None, out=P[2],
+          ids=None, tw=None, ws=P[3], wsb=MB):
+    m = None if dm is None else C.byref(fp8.dims(**{**dict(T=4, d=64, f=32, E=8, k_max=2), **dm}))
+    parts = {**dict(w_gate=P[4], w_up=P[5], w_down=P[6]), **w} if w is not None else None
+    return fp8._mx4_forward(m, kind, x, ldx, router, bias, kpt,
+                            None if parts is None else C.byref(fp8._Mx4Weights(**parts)), override, out, ids, tw,
+                            ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dm=None), ERR_NULL), (dict(w=None), ERR_NULL),
+    *[({n: None}, ERR_NULL) for n in ("x", "router", "out")],
+    *[(dict(w={n: None}), ERR_NULL) for n in ("w_gate", "w_up", "w_down")],
+    (dict(dm=dict(n_shared=1)), ERR_NULL),
+    (dict(dm=dict(T=33)), ERR_SHAPE), (dict(dm=dict(T=-1)), ERR_SHAPE), (dict(dm=dict(d=48), ldx=48), ERR_SHAPE),
+    (dict(dm=dict(f=16)), ERR_SHAPE), (dict(dm=dict(d=16416), ldx=16416), ERR_SHAPE), (dict(dm=dict(E=0)), ERR_SHAPE),
+    (dict(dm=dict(E=513)), ERR_SHAPE), (dict(dm=dict(k_max=0)), ERR_SHAPE), (dict(dm=dict(k_max=9)), ERR_SHAPE),
+    (dict(dm=dict(E=64, k_max=33)), ERR_SHAPE), (dict(dm=dict(n_shared=33)), ERR_SHAPE), (dict(ldx=56), ERR_SHAPE),
+    (dict(dm=dict(no_requant=True)), ERR_UNSUPPORTED), (dict(kind=F32), ERR_UNSUPPORTED),
+    (dict(ws=None), ERR_WORKSPACE), (dict(wsb=512), ERR_WORKSPACE), (dict(ws=P[3] + 64), ERR_ALIGN),
+    (dict(x=P[0] + 8), ERR_ALIGN), (dict(out=P[2] + 4), ERR_ALIGN), (dict(w=dict(w_up=P[5] + 8)), ERR_ALIGN),
+    (dict(ids=P[7] + 2), ERR_ALIGN), (dict(kpt=P[7] + 1), ERR_ALIGN),
+    (dict(out=P[0]), ERR_SHAPE), (dict(ws=P[5]), ERR_SHAPE), (dict(ids=P[3] + 16), ERR_SHAPE),
+    (dict(ids=P[7], tw=P[7] + 28), ERR_SHAPE), (dict(out=P[1] + 2032), ERR_SHAPE), (dict(tw=P[6]), ERR_SHAPE),
+])
+def test_layer_refuses(kw, code):
+    assert layer(**kw) == code, fp8._last_error()
+    assert fp8._last_error().startswith(b"moe_mx4_forward")
+
+
+def test_layer_workspace_and_no_tokens():
+    size = lambda **kw: fp8._mx4_workspace_bytes(C.byref(fp8.dims(**{**dict(T=4, d=64, f=32, E=8, k_max=2), **kw})))
+    # scores, a list of experts, and h's two halves by (token, pick) rows
+    assert 4 * 8 * 4 + 2 * 8 * 32 * 2 < size() < size(T=32) < size(T=32, f=16384, n_shared=2) < 64 * MB
+    assert size(T=33) == 0 and b"T=33" in fp8._last_error()
+    assert layer(dm=dict(T=0), x=None, out=None, ws=None) == OK
