@@ -141,18 +141,24 @@ __global__ __launch_bounds__(256) void pack_mx4_kernel(const uint8_t *codes, con
   }
   __syncthreads();
   const int lane = threadIdx.x & 63, row = mx4_channel(blockIdx.x, lane & 15), top = largest[lane & 15];
-  for (int t = threadIdx.x >> 6; t < (l.kt + 3) / 4 * 4; t += 4) {
-    const int g = t * 4 + (lane >> 4);
+  for (int t = threadIdx.x >> 6; t < l.kt; t += 4) {
     v4i c{0, 0, 0, 0};
-    int s = 0;
-    if (row < rows && g < groups) {
-      s = 124 + scales[(int64_t)row * groups + g] - top;
-      if (s >= 1 && s <= 124) c = load16(codes + (int64_t)row * (cols / 2) + g * 16);
+    uint32_t bytes = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int g = t * 4 + j;
+      int s = 0;
+      if (row < rows && g < groups) {
+        s = 124 + scales[(int64_t)row * groups + g] - top;
+        if (s >= 1 && s <= 124)
+          c[j] = reinterpret_cast<const int *>(codes + (int64_t)row * (cols / 2) + g * 16)[lane >> 4];
+      }
+      // a group of zeros, or of weights below 2^-121 of the row's largest scale
+      if (s < 1 || s > 124) s = 124;
+      bytes |= (uint32_t)s << (8 * j);
     }
-    // a group of zeros, or of weights below 2^-121 of the row's largest scale
-    if (s < 1 || s > 124) s = 124;
-    if (t < l.kt) *reinterpret_cast<v4i *>(block + (int64_t)t * 1024 + lane * 16) = c;
-    block[l.scales + (t >> 2) * 256 + lane * 4 + (t & 3)] = (uint8_t)s;
+    *reinterpret_cast<v4i *>(block + (int64_t)t * 1024 + lane * 16) = c;
+    if (lane < 16) *reinterpret_cast<uint32_t *>(block + l.scales + t * 64 + lane * 4) = bytes;
   }
 }
 
@@ -209,7 +215,7 @@ __global__ __launch_bounds__(W * kWave) void mx4_few_kernel(Mx4Product p) {
 #pragma unroll
   for (int m = 0; m < XT; ++m) {
     const int t = m * 16 + (lane & 15);
-    row[m] = x + (int64_t)(t < p.T ? t : p.T - 1) * p.ldx + q * kMxGroup;
+    row[m] = x + (int64_t)(t < p.T ? t : p.T - 1) * p.ldx + q * 8;
   }
   v4f acc[NR][XT];
 #pragma unroll
@@ -221,9 +227,8 @@ __global__ __launch_bounds__(W * kWave) void mx4_few_kernel(Mx4Product p) {
       l.kt > wave ? (l.kt - wave + W - 1) / W : 0,
       [&](int c, int i) {
         const int kt = wave + i * W;
-        const bool in = kt * 4 + q < groups;
         ring.load(c, block, l, kt, lane, [&](int j, int m) {
-          return in ? load16(row[m] + kt * 128 + j * 8) : v4i{0, 0, 0, 0};
+          return kt * 4 + j < groups ? load16(row[m] + kt * 128 + j * 32) : v4i{0, 0, 0, 0};
         });
       },
       [&](int c, int) { ring.multiply(c, acc); });
@@ -321,7 +326,7 @@ __global__ __launch_bounds__(TM *TN *kWave) void mx4_tile_kernel(Mx4Product p, i
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       w[r] = load16(block[r] + (int64_t)kt * 1024 + lane * 16);
-      s[r] = block[r][l.scales + (kt >> 2) * 256 + lane * 4 + (kt & 3)];
+      s[r] = *reinterpret_cast<const uint32_t *>(block[r] + l.scales + kt * 64 + c * 4);
     }
   };
   xs.fetch(0, left(0), lds_address(base), wave);
@@ -331,11 +336,11 @@ __global__ __launch_bounds__(TM *TN *kWave) void mx4_tile_kernel(Mx4Product p, i
     wait_dma<0>();
     barrier_reads();
     v4i cw[NR];
-    float sc[NR];
+    uint32_t cs[NR];
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       cw[r] = w[r];
-      sc[r] = mx4_scale<Op>(s[r], 0);
+      cs[r] = s[r];
     }
     if (kt + 1 < l.kt) {
       xs.fetch(kt + 1, left(kt + 1), lds_address(base) + (BM * 256 - stage), wave);
@@ -346,10 +351,10 @@ __global__ __launch_bounds__(TM *TN *kWave) void mx4_tile_kernel(Mx4Product p, i
       v4i fx[MS];
 #pragma unroll
       for (int m = 0; m < MS; ++m)
-        fx[m] = lds_read16(base + stage + (wm * WM + m * 16 + c) * 256 + (((q * 4 + j) ^ c) * 16));
+        fx[m] = lds_read16(base + stage + (wm * WM + m * 16 + c) * 256 + (((j * 4 + q) ^ c) * 16));
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
-        const v4i a = mx4_operand<Op>(cw[r][j], sc[r]);
+        const v4i a = mx4_operand<Op>(cw[r][j], mx4_scale<Op>(cs[r], j));
 #pragma unroll
         for (int m = 0; m < MS; ++m) acc[r][m] = Op::mfma(a, fx[m], acc[r][m]);
       }

@@ -201,7 +201,7 @@ __global__ __launch_bounds__(TEAMS *kTeamWaves *kWave) void mx4_gate_up_kernel(M
       const int c = m * 16 + c16;
       there[m] = c < count;
       const int t = there[m] ? r.row_token[row0 + c] : 0;
-      row[m] = static_cast<const typename Op::E *>(p.x) + (int64_t)t * p.ldx + q * kMxGroup;
+      row[m] = static_cast<const typename Op::E *>(p.x) + (int64_t)t * p.ldx + q * 8;
     }
   };
   enter();
@@ -220,9 +220,8 @@ __global__ __launch_bounds__(TEAMS *kTeamWaves *kWave) void mx4_gate_up_kernel(M
       [&](int c, int) {
         const int kt = tw + at * kTeamWaves;
         if (item < items && kt < l.kt) {
-          const bool in = kt * 4 + q < groups;
           ring.load(c, block, l, kt, lane, [&](int j, int m) {
-            return in && there[m] ? load16(row[m] + kt * 128 + j * 8) : v4i{0, 0, 0, 0};
+            return kt * 4 + j < groups && there[m] ? load16(row[m] + kt * 128 + j * 32) : v4i{0, 0, 0, 0};
           });
         }
         if (++at == tiles) {
@@ -315,15 +314,14 @@ __global__ __launch_bounds__(W *kWave) void mx4_down_kernel(Mx4Moe p, const char
           for (int m = 0; m < XT; ++m) {
             const int t = m * 16 + c16;
             there[m] = (tokens >> t) & 1u;
-            from[m] = (int64_t)(row0 + __popc(tokens & below(t))) * p.f + q * kMxGroup;
+            from[m] = (int64_t)(row0 + __popc(tokens & below(t))) * p.f + q * 8;
           }
         }
-        const bool in = kt * 4 + q < groups;
         ring.load(c, block, l, kt, lane, [&](int j, int m) {
           Mx4Pair::X x{{0, 0, 0, 0}, {0, 0, 0, 0}};
-          if (in && there[m]) {
-            x.hi = load16(hi + from[m] + kt * 128 + j * 8);
-            x.lo = load16(lo + from[m] + kt * 128 + j * 8);
+          if (kt * 4 + j < groups && there[m]) {
+            x.hi = load16(hi + from[m] + kt * 128 + j * 32);
+            x.lo = load16(lo + from[m] + kt * 128 + j * 32);
           }
           return x;
         });

@@ -17,12 +17,11 @@ constexpr int kMx4MaxScale = 251;
 // channel (b/2)*32 + (p/4)*8 + (b%2)*4 + p%4, so that the four rows that a lane
 // gets from a matrix instruction are, over a pair of blocks, eight consecutive
 // channels.  A block is
-//   tiles      kt x 1024 bytes: bytes l*16 .. of a tile are the 32 codes of
-//              row l%16, inputs (l/16)*32 .. of the tile, as they stand in the
-//              row (the first of two in the low half)
-//   scales     ceil(kt/4) x 256 bytes: byte l*4 + t%4 of the piece t/4 is that of
-//              tile t's lane l, 124 + e - E with e the group's exponent and E the
-//              row's largest
+//   tiles      kt x 1024 bytes: dword j of the 16 bytes at l*16 of a tile are the
+//              codes of row l%16, inputs j*32 + (l/16)*8 .. of the tile, as they
+//              stand in the row (the first of two in the low half)
+//   scales     kt x 64 bytes: byte p*4 + j of a tile is that of row p, inputs j*32
+//              .., 124 + e - E with e the group's exponent and E the row's largest
 //   factors    16 floats: 2^(E + 3), a NaN for a row with a scale that is none
 // (rows behind the last and inputs behind the end are zeros).  The code values
 // times the scales' powers of two are the row's weights over its factor: at
@@ -34,7 +33,7 @@ struct Mx4Layout {
   int64_t scales, factors, block_bytes;
   __host__ __device__ Mx4Layout(int32_t rows, int32_t cols)
       : blocks(2 * ((rows + 31) / 32)), kt((cols + 127) / 128), scales((int64_t)kt * 1024),
-        factors(scales + (int64_t)((kt + 3) / 4) * 256), block_bytes(factors + 64) {}
+        factors(scales + (int64_t)kt * 64), block_bytes(factors + 64) {}
   int64_t bytes() const { return blocks * block_bytes; }
 };
 

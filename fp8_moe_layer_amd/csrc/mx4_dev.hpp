@@ -2,10 +2,12 @@
 // instructions: the conversion of a tile's codes, and the stream of weights for
 // few tokens that the dense products and the MoE layer share.
 //
-// A matrix instruction (16x16x32) takes 8 values of K from each lane.  Lane l's
-// 16 bytes of a tile are 32 codes of one group, so four instructions use them
-// up, and one scale serves them all; of the activations the lane supplies the
-// same 32 inputs, (l/16)*32 .. of the tile.  v_cvt_scalef32_pk_{bf16,f16}_fp4
+// A matrix instruction (16x16x32) takes 8 values of K from each lane.  A tile's
+// four instructions take a group of 32 inputs each, lane l inputs (l/16)*8 .. of
+// it: its 16 bytes of codes are a dword for each, its row's four scales another
+// dword, and of the activations a wave's loads are runs of 64 bytes a token.
+// (With a group to a lane, 16 bytes of every 64, the loads took the vector cache
+// four times as long: 16 x 14336 x 4096 18.9 us.)  v_cvt_scalef32_pk_{bf16,f16}_fp4
 // turns two codes and a power of two into two 16-bit values at full rate: 16 of
 // them to four matrix instructions.
 #pragma once
@@ -66,16 +68,16 @@ struct Mx4Pair {
   }
 };
 
-// The operand of step j (codes 8j .. 8j+7 of the lane).
+// The operand of a group from the lane's dword of its codes.
 template <class Op>
 __device__ __forceinline__ v4i mx4_operand(int codes, float scale) {
   return v4i{Op::template pair<0>(codes, scale), Op::template pair<1>(codes, scale),
              Op::template pair<2>(codes, scale), Op::template pair<3>(codes, scale)};
 }
-// The scale of tile t%4 = i from its piece's dword.
+// The scale of a tile's group j from its row's dword.
 template <class Op>
-__device__ __forceinline__ float mx4_scale(uint32_t bytes, int i) {
-  return __uint_as_float((((bytes >> (8 * i)) & 0xffu) << 23) + ((uint32_t)Op::kShift << 23));
+__device__ __forceinline__ float mx4_scale(uint32_t bytes, int j) {
+  return __uint_as_float((((bytes >> (8 * j)) & 0xffu) << 23) + ((uint32_t)Op::kShift << 23));
 }
 template <class Op>
 __device__ __forceinline__ float mx4_factor(const uint8_t *block, const Mx4Layout &l, int row) {
@@ -96,14 +98,14 @@ struct Mx4Ring {
   typename Op::X x[D][4][XT];
 
   // Tile kt of the blocks into slot c.  load_x(j, m): the lane's activations of
-  // step j, tokens m*16 ...
+  // group j, tokens m*16 ...
   template <class LoadX>
   __device__ __forceinline__ void load(int c, const uint8_t *const (&block)[NR], const Mx4Layout &l,
                                        int kt, int lane, LoadX load_x) {
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       w[c][r] = load16_nt(block[r] + (int64_t)kt * 1024 + lane * 16);
-      s[c][r] = block[r][l.scales + (kt >> 2) * 256 + lane * 4 + (kt & 3)];
+      s[c][r] = *reinterpret_cast<const uint32_t *>(block[r] + l.scales + kt * 64 + (lane & 15) * 4);
       if (ABS) f[c][r] = reinterpret_cast<const float *>(block[r] + l.factors)[lane & 15];
     }
 #pragma unroll
@@ -114,14 +116,12 @@ struct Mx4Ring {
   // acc[r][m] += the slot's products: element i of lane l is row (l/16)*4 + i,
   // token m*16 + l%16
   __device__ __forceinline__ void multiply(int c, v4f (&acc)[NR][XT]) const {
-    float sc[NR];
-#pragma unroll
-    for (int r = 0; r < NR; ++r) sc[r] = mx4_scale<Op>(s[c][r], 0) * (ABS ? f[c][r] : 1.0f);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
-        const v4i a = mx4_operand<Op>(w[c][r][j], sc[r]);
+        const float sc = mx4_scale<Op>(s[c][r], j);
+        const v4i a = mx4_operand<Op>(w[c][r][j], ABS ? sc * f[c][r] : sc);
 #pragma unroll
         for (int m = 0; m < XT; ++m) acc[r][m] = Op::mfma(a, x[c][j][m], acc[r][m]);
       }

@@ -80,9 +80,9 @@ def test_pack_refuses(kw, code):
 
 
 def test_packed_size():
-    # 32 channels of 128 inputs: two blocks of a tile, a piece of scales, 16 factors
-    assert fp8.packed_mx4_bytes(1, 32) == fp8.packed_mx4_bytes(32, 128) == 2 * (1024 + 256 + 64)
-    assert fp8.packed_mx4_bytes(33, 544) == 4 * (5 * 1024 + 2 * 256 + 64)
+    # 32 channels of 128 inputs: two blocks of a tile with its scales, 16 factors
+    assert fp8.packed_mx4_bytes(1, 32) == fp8.packed_mx4_bytes(32, 128) == 2 * (1024 + 64 + 64)
+    assert fp8.packed_mx4_bytes(33, 544) == 4 * (5 * 1024 + 5 * 64 + 64)
     assert fp8.packed_mx4_bytes(0, 32) == fp8.packed_mx4_bytes(4, 40) == 0 and fp8._last_error()
     assert fp8.packed_mx4_bytes(1 << 40, 32) == fp8.packed_mx4_bytes(4, 1 << 40) == 0
 
@@ -98,7 +98,7 @@ def matmul(x=P[0], ldx=64, w=P[1], bias=None, x_type=BF16, T=4, K=64, N=40, y_ty
     (dict(ldx=56), ERR_SHAPE), (dict(ldx=68), ERR_SHAPE), (dict(ldx=(1 << 21) + 8), ERR_SHAPE),
     (dict(x_type=F32), ERR_UNSUPPORTED), (dict(y_type=F16), ERR_UNSUPPORTED), (dict(x_type=7), ERR_UNSUPPORTED),
     (dict(x=P[0] + 8), ERR_ALIGN), (dict(w=P[1] + 8), ERR_ALIGN), (dict(y=P[2] + 4), ERR_ALIGN),
-    (dict(bias=P[3] + 2), ERR_ALIGN), (dict(y=P[0] + 496), ERR_SHAPE), (dict(y=P[1] + 5360), ERR_SHAPE),
+    (dict(bias=P[3] + 2), ERR_ALIGN), (dict(y=P[0] + 496), ERR_SHAPE), (dict(y=P[1] + 4464), ERR_SHAPE),
     (dict(bias=P[2] + 636), ERR_SHAPE),
 ])
 def test_matmul_refuses(kw, code):
