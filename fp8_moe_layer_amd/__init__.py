@@ -117,8 +117,11 @@ _quantize_rows_mx4 = _sig("moe_quantize_rows_mx4", _i32, _vp, _i32, _i64, _i32, 
 _dequantize_rows_mx4 = _sig("moe_dequantize_rows_mx4", _i32, _vp, _vp, _i32, _i32, _i32, _vp, _vp)
 _packed_mx4_bytes = _sig("moe_packed_mx4_bytes", _i64, _i32, _i32)
 _pack_mx4 = _sig("moe_pack_mx4", _i32, _vp, _vp, _i32, _i32, _vp, _vp)
-_matmul_mx4 = _sig("moe_matmul_mx4", _i32, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp)
-_ffn_mx4 = _sig("moe_ffn_mx4", _i32, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp)
+_matmul_mx4 = _sig("moe_matmul_mx4", _i32, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp,
+                   C.c_size_t, _vp)
+_matmul_mx4_ws = _sig("moe_matmul_mx4_workspace_bytes", C.c_size_t, _i32, _i32, _i32)
+_ffn_mx4 = _sig("moe_ffn_mx4", _i32, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, C.c_size_t, _vp)
+_ffn_mx4_ws = _sig("moe_ffn_mx4_workspace_bytes", C.c_size_t, _i32, _i32, _i32)
 _mx4_workspace_bytes = _sig("moe_mx4_workspace_bytes", C.c_size_t, _DP)
 _mx4_forward = _sig("moe_mx4_forward", _i32, _DP, _i32, _vp, _i64, _vp, _vp, _vp, C.POINTER(_Mx4Weights),
                     _vp, _vp, _vp, _vp, _vp, C.c_size_t, _vp)
@@ -420,8 +423,8 @@ def _by_sizes(fn):
     return size
 
 
-_matmul_i8_size, _gated_ffn_i8_size, _gated_ffn_size = map(
-    _by_sizes, (_matmul_i8_ws, _gated_ffn_i8_ws, _gated_ffn_ws))
+_matmul_i8_size, _gated_ffn_i8_size, _gated_ffn_size, _matmul_mx4_size, _ffn_mx4_size = map(
+    _by_sizes, (_matmul_i8_ws, _gated_ffn_i8_ws, _gated_ffn_ws, _matmul_mx4_ws, _ffn_mx4_ws))
 
 
 class _Call:
@@ -921,9 +924,10 @@ def matmul_mx4(x: torch.Tensor, w: Mx4Matrix, bias: Optional[torch.Tensor] = Non
     kind = _type(x.dtype, _TYPES16)
     y, at = _out(c, out, (T, N), (out_dtype or x.dtype) if out is None else out.dtype, "out")
     xp, ldx = c.rows(x, (T, K), x.dtype, "x")
-    c.run(_matmul_mx4, xp, ldx, _mx4_ptr(c, w, N, K, "w"),
-          None if bias is None else c.ptr(bias, (N,), torch.float32, "bias"), kind, T, K, N,
-          _type(y.dtype), at)
+    wp = _mx4_ptr(c, w, N, K, "w")
+    ws, wsp, size = c.workspace(_matmul_mx4_size, T, K, N)
+    c.run(_matmul_mx4, xp, ldx, wp, None if bias is None else c.ptr(bias, (N,), torch.float32, "bias"),
+          kind, T, K, N, _type(y.dtype), at, wsp, size)
     return y
 
 
@@ -939,8 +943,9 @@ def gated_ffn_mx4(x: torch.Tensor, w_gate: Mx4Matrix, w_up: Mx4Matrix,
     kind = _type(x.dtype, _TYPES16)
     h, at = _out(c, out, (T, f), x.dtype, "out")
     xp, ldx = c.rows(x, (T, d), x.dtype, "x")
-    c.run(_ffn_mx4, xp, ldx, _mx4_ptr(c, w_gate, f, d, "w_gate"), _mx4_ptr(c, w_up, f, d, "w_up"), kind,
-          T, d, f, at)
+    gp, up = _mx4_ptr(c, w_gate, f, d, "w_gate"), _mx4_ptr(c, w_up, f, d, "w_up")
+    ws, wsp, size = c.workspace(_ffn_mx4_size, T, d, f)
+    c.run(_ffn_mx4, xp, ldx, gp, up, kind, T, d, f, at, wsp, size)
     return h
 
 

@@ -192,70 +192,227 @@ __device__ __forceinline__ void load_factors(const uint8_t *block, const Mx4Layo
 }
 
 // ---------------------------------------------------------------- few tokens
-// Up to 16*XT tokens: a workgroup takes R blocks of 16 rows (gated: of each
-// matrix), its W waves their pieces of K in turn; their sums meet in LDS and are
-// added in wave order.
-template <class Op, class OUT, int XT, int R, bool GATED, int W, int D>
-__global__ __launch_bounds__(W * kWave) void mx4_few_kernel(Mx4Product p) {
-  constexpr int NR = GATED ? 2 * R : R;
-  __shared__ v4f part[W][NR][XT][kWave];
+// Up to 64 tokens the product is a stream of the weights, each byte used once,
+// and what costs beside them is the activations, which every workgroup needs
+// whole: at 16 tokens a tile's are four times its weights.  So a workgroup takes a
+// part of K (`slices` of them, joined by a second launch where there is more than
+// one) whose activations it puts into LDS once, all of its WR x WK waves use them
+// (WR along the channels, WK along K in turn, their sums meeting in LDS), and no
+// barrier stands in the stream of the weights, which go from memory to the
+// registers of the one wave that uses them.
+struct FewPlan {
+  int xt;      // 16-token sub-tiles: 1, 2, 4
+  int wr, wk;  // waves
+  int nb;      // blocks of channels of a wave
+  int slices, tiles;  // parts of K, and tiles of one
+  int rows;    // tokens in LDS: a power of two
+  size_t lds;
+};
+
+constexpr int kFewWaves = 8;
+constexpr int kFewLds = 128 * 1024;  // of activations
+constexpr int kFewGroups = 224;      // workgroups that fill the 256 compute units well enough
+
+// Where the activations of all of K fit into LDS, one launch does it: as many
+// waves along the channels as leave kFewGroups workgroups (each of them reads the
+// activations, from the L2 at 10 TB/s in all).  Where they do not, a second launch
+// is needed anyway (2 us and more), and K is cut until kFewGroups workgroups of
+// four or eight waves along the channels have work: by then the activations are
+// less than the weights.  Weights from HBM, us, waves along the channels x slices:
+//   one token 14336 -> 4096      1x1 9.3, 1x2 11.3, 2x1 12.3, 4x4 12.6
+//   one token 4096 -> 2 x 14336  4x1 15.2, 2x1 15.2, 1x1 17
+//   16 tokens 14336 -> 4096      4x4 13.0, 2x4 16.8, 1x4 22
+//   16 tokens 4096 -> 2 x 14336  4x1 16.5, 2x1 23, 8x1 19
+//   32 tokens 14336 -> 4096      4x7 16.4, 8x7 18.9; 4096 -> 2 x 14336: 8x2 23.3, 4x2 25.0
+FewPlan few_plan(int32_t T, int32_t K, int32_t N, bool gated) {
+  FewPlan f{};
+  const Mx4Layout l(N, K);
+  f.xt = T <= 16 ? 1 : T <= 32 ? 2 : 4;
+  f.nb = gated || f.xt == 1 ? 1 : 2;
+  for (f.rows = 1; f.rows < T; f.rows *= 2) {
+  }
+  const int most = kFewLds / (f.rows * 256);  // tiles in LDS
+  f.slices = (l.kt + most - 1) / most;
+  auto groups = [&]() { return (l.blocks + f.wr * f.nb - 1) / (f.wr * f.nb); };
+  if (f.slices == 1) {
+    for (f.wr = 4; f.wr > 1 && groups() < kFewGroups; f.wr /= 2) {
+    }
+  } else {
+    f.wr = f.xt == 1 || !gated ? 4 : 8;
+    const int fill = (kFewGroups + groups() - 1) / groups();
+    if (f.slices < fill) f.slices = fill;
+  }
+  f.wk = kFewWaves / f.wr;
+  f.tiles = (l.kt + f.slices - 1) / f.slices;
+  f.slices = (l.kt + f.tiles - 1) / f.tiles;
+  const size_t parts = (size_t)kFewWaves * f.nb * (gated ? 2 : 1) * f.xt * 1024;
+  const size_t stage = ((size_t)f.tiles * f.rows * 256 + 1023) / 1024 * 1024;
+  f.lds = stage > parts ? stage : parts;
+  return f;
+}
+
+// y's four channels of one token from their sums; the types of few tokens' outputs
+// are told apart here, at run time.
+template <class Op>
+__device__ __forceinline__ void few_store(const Mx4Product &p, int t, int ch, v4f v, const float (&f)[4]) {
+  if (t >= p.T || ch >= p.N) return;
+  if (p.out_type == kTypeF32)
+    Mx4Out<float>{p.bias, static_cast<float *>(p.y), p.T, p.N}.store(t, ch, v, f);
+  else
+    Mx4Out<typename Op::E>{p.bias, static_cast<typename Op::E *>(p.y), p.T, p.N}.store(t, ch, v, f);
+}
+template <class Op>
+__device__ __forceinline__ void few_store(const Mx4Product &p, int t, int ch, v4f g, const float (&fg)[4],
+                                          v4f u, const float (&fu)[4]) {
+  if (t >= p.T || ch >= p.N) return;
+  Mx4Out<typename Op::E>{nullptr, static_cast<typename Op::E *>(p.y), p.T, p.N}.store(t, ch, g, fg, u, fu);
+}
+
+template <class Op, int XT, int NB, bool GATED, int WR, int WK, int D>
+__global__ __launch_bounds__(WR *WK *kWave) void mx4_few_kernel(Mx4Product p, int slices, int tiles,
+                                                            int rows, v4f *partial) {
+  constexpr int NR = GATED ? 2 * NB : NB, W = WR * WK;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t few_lds[];
   const Mx4Layout l(p.N, p.K);
-  const int lane = threadIdx.x & 63, q = lane >> 4;
+  const int lane = threadIdx.x & 63, q = lane >> 4, c16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int b0 = blockIdx.x * R;
+  const int wr = wave / WK, wk = wave % WK;
+  const int slice = blockIdx.x % slices, b0 = ((blockIdx.x / slices) * WR + wr) * NB;
+  const int k0 = slice * tiles, n = l.kt - k0 < tiles ? l.kt - k0 : tiles;
   const uint8_t *block[NR];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    block[r] = p.w0 + (b0 + r) * l.block_bytes;
-    if (GATED) block[R + r] = p.w1 + (b0 + r) * l.block_bytes;
-  }
-  const int groups = p.K / kMxGroup;
-  const typename Op::E *x = static_cast<const typename Op::E *>(p.x);
-  const typename Op::E *row[XT];  // columns behind the last token repeat it
-#pragma unroll
-  for (int m = 0; m < XT; ++m) {
-    const int t = m * 16 + (lane & 15);
-    row[m] = x + (int64_t)(t < p.T ? t : p.T - 1) * p.ldx + q * 8;
+  for (int r = 0; r < NB; ++r) {
+    const int b = b0 + r < l.blocks ? b0 + r : l.blocks - 1;  // behind the last: not stored
+    block[r] = p.w0 + b * l.block_bytes;
+    if (GATED) block[NB + r] = p.w1 + b * l.block_bytes;
   }
   v4f acc[NR][XT];
 #pragma unroll
   for (int r = 0; r < NR; ++r)
 #pragma unroll
     for (int m = 0; m < XT; ++m) acc[r][m] = v4f{0.f, 0.f, 0.f, 0.f};
-  Mx4Ring<Op, XT, NR, D> ring;
-  run_ring<D>(
-      l.kt > wave ? (l.kt - wave + W - 1) / W : 0,
-      [&](int c, int i) {
-        const int kt = wave + i * W;
-        ring.load(c, block, l, kt, lane, [&](int j, int m) {
-          return kt * 4 + j < groups ? load16(row[m] + kt * 128 + j * 32) : v4i{0, 0, 0, 0};
-        });
-      },
-      [&](int c, int) { ring.multiply(c, acc); });
+  Mx4Weights<Op, NR, D> ring;
+  const LdsPtr xs = (LdsPtr)few_lds;
+  auto stage = [&]() {
+    // 1 KB pieces, four rows of 256 bytes; row i is tile i / rows, token i % rows
+    const int64_t kbytes = (int64_t)(p.K - k0 * 128) * 2;
+    const v4u rsrc = buffer_of(static_cast<const uint8_t *>(p.x) + (int64_t)k0 * 256,
+                               (int64_t)(p.T - 1) * p.ldx * 2 + kbytes);
+    const int shift = 31 - __builtin_clz(rows), pieces = (n * rows + 3) / 4;
+    for (int i = wave; i < pieces; i += W) {
+      const int at = i * 4 + (lane >> 4), t = at & (rows - 1), kt = at >> shift;
+      const int byte = kt * 256 + (c16 ^ (t & 15)) * 16;
+      dma16(rsrc, t < p.T && kt < n && byte < kbytes ? (uint32_t)(t * p.ldx * 2 + byte) : kPastEnd,
+            lds_address(xs) + i * 1024);
+    }
+    wait_dma<0>();
+    barrier_reads();
+  };
+  const int mine = n > wk ? (n - wk + WK - 1) / WK : 0;
+  auto load = [&](int c, int i) { ring.load(c, block, l, k0 + wk + i * WK, lane); };
+  int row[XT];  // columns behind the last token repeat another
+#pragma unroll
+  for (int m = 0; m < XT; ++m) row[m] = (m * 16 + c16) & (rows - 1);
+  auto use = [&](int c, int i) {
+    const LdsPtr at = xs + (wk + i * WK) * rows * 256;
+    ring.template multiply<XT>(
+        c, [&](int j, int m) { return lds_read16(at + row[m] * 256 + (((j * 4 + q) ^ (row[m] & 15)) * 16)); },
+        acc);
+  };
+  run_ring<D>(mine, load, use, stage);
+  // the waves' sums meet where the activations were
+  barrier_reads();
+  v4f *part = reinterpret_cast<v4f *>(few_lds);
 #pragma unroll
   for (int r = 0; r < NR; ++r)
 #pragma unroll
-    for (int m = 0; m < XT; ++m) part[wave][r][m][lane] = acc[r][m];
-  __syncthreads();
-  const Mx4Out<OUT> out{p.bias, static_cast<OUT *>(p.y), p.T, p.N};
-  for (int i = wave; i < R * XT; i += W) {
-    const int r = i / XT, m = i % XT, t = m * 16 + (lane & 15), ch = mx4_channel(b0 + r, q * 4);
-    v4f a = part[0][r][m][lane];
+    for (int m = 0; m < XT; ++m) part[(((wk * WR + wr) * NR + r) * XT + m) * kWave + lane] = acc[r][m];
+  barrier_reads();
+  for (int i = wave; i < WR * NB * XT; i += W) {
+    const int m = i % XT, r = i / XT % NB, g = i / (XT * NB);
+    const int b = ((blockIdx.x / slices) * WR + g) * NB + r;
+    if (b >= l.blocks) continue;
+    auto sum = [&](int rr) {
+      v4f v = part[((g * NR + rr) * XT + m) * kWave + lane];
 #pragma unroll
-    for (int w = 1; w < W; ++w) a += part[w][r][m][lane];
-    float f[4];
-    load_factors<Op>(block[r], l, q, f);
+      for (int w = 1; w < WK; ++w) v += part[(((w * WR + g) * NR + rr) * XT + m) * kWave + lane];
+      return v;
+    };
+    const v4f a = sum(r);
+    v4f u = a;
+    if constexpr (GATED) u = sum(NB + r);
+    if (slices > 1) {
+      v4f *to = partial + (((int64_t)slice * l.blocks + b) * (GATED ? 2 : 1) * XT + m) * kWave + lane;
+      to[0] = a;
+      if constexpr (GATED) to[XT * kWave] = u;
+      continue;
+    }
+    float f[4], fu[4];
+    load_factors<Op>(p.w0 + b * l.block_bytes, l, q, f);
+    const int t = m * 16 + c16, ch = mx4_channel(b, q * 4);
     if constexpr (GATED) {
-      v4f u = part[0][R + r][m][lane];
-#pragma unroll
-      for (int w = 1; w < W; ++w) u += part[w][R + r][m][lane];
-      float fu[4];
-      load_factors<Op>(block[R + r], l, q, fu);
-      if (t < p.T && ch < p.N) out.store(t, ch, a, f, u, fu);
+      load_factors<Op>(p.w1 + b * l.block_bytes, l, q, fu);
+      few_store<Op>(p, t, ch, a, f, u, fu);
     } else {
-      if (t < p.T && ch < p.N) out.store(t, ch, a, f);
+      few_store<Op>(p, t, ch, a, f);
     }
   }
+}
+
+// The slices' sums, in order; a wave per block and 16 tokens.
+template <class Op, bool GATED>
+__global__ __launch_bounds__(256) void mx4_join_kernel(Mx4Product p, int slices, int xt, const v4f *partial) {
+  const Mx4Layout l(p.N, p.K);
+  const int lane = threadIdx.x & 63, i = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int b = i / xt, m = i % xt;
+  if (b >= l.blocks) return;
+  const int64_t step = (int64_t)l.blocks * (GATED ? 2 : 1) * xt * kWave;
+  const v4f *at = partial + ((int64_t)b * (GATED ? 2 : 1) * xt + m) * kWave + lane;
+  v4f a = at[0], u = a;
+  if constexpr (GATED) u = at[xt * kWave];
+  for (int s = 1; s < slices; ++s) {
+    a += at[s * step];
+    if constexpr (GATED) u += at[s * step + xt * kWave];
+  }
+  float f[4], fu[4];
+  const int q = lane >> 4, t = m * 16 + (lane & 15), ch = mx4_channel(b, q * 4);
+  load_factors<Op>(p.w0 + b * l.block_bytes, l, q, f);
+  if constexpr (GATED) {
+    load_factors<Op>(p.w1 + b * l.block_bytes, l, q, fu);
+    few_store<Op>(p, t, ch, a, f, u, fu);
+  } else {
+    few_store<Op>(p, t, ch, a, f);
+  }
+}
+
+template <class Op, bool GATED, int XT, int NB, int WR, int WK, int D>
+hipError_t launch_few_form(const Mx4Product &p, const FewPlan &f, hipStream_t stream) {
+  const Mx4Layout l(p.N, p.K);
+  const int groups = (l.blocks + WR * NB - 1) / (WR * NB);
+  v4f *partial = static_cast<v4f *>(p.workspace);
+  mx4_few_kernel<Op, XT, NB, GATED, WR, WK, D>
+      <<<groups * f.slices, WR * WK * kWave, f.lds, stream>>>(p, f.slices, f.tiles, f.rows, partial);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || f.slices == 1) return e;
+  mx4_join_kernel<Op, GATED><<<(l.blocks * XT + 3) / 4, 256, 0, stream>>>(p, f.slices, XT, partial);
+  return hipGetLastError();
+}
+
+template <class Op, bool GATED, int XT>
+hipError_t launch_few_rows(const Mx4Product &p, const FewPlan &f, hipStream_t stream) {
+  constexpr int NB = GATED || XT == 1 ? 1 : 2, W = kFewWaves, D = XT == 1 ? 4 : 3;
+  if (f.wr == 1) return launch_few_form<Op, GATED, XT, NB, 1, W, D>(p, f, stream);
+  if (f.wr == 2) return launch_few_form<Op, GATED, XT, NB, 2, W / 2, D>(p, f, stream);
+  if (f.wr == 4) return launch_few_form<Op, GATED, XT, NB, 4, W / 4, D>(p, f, stream);
+  return launch_few_form<Op, GATED, XT, NB, 8, W / 8, D>(p, f, stream);
+}
+
+template <class Op, bool GATED>
+hipError_t launch_few(const Mx4Product &p, hipStream_t stream) {
+  const FewPlan f = few_plan(p.T, p.K, p.N, GATED);
+  if (f.xt == 1) return launch_few_rows<Op, GATED, 1>(p, f, stream);
+  if (f.xt == 2) return launch_few_rows<Op, GATED, 2>(p, f, stream);
+  return launch_few_rows<Op, GATED, 4>(p, f, stream);
 }
 
 // ---------------------------------------------------------------- tiles
@@ -384,10 +541,8 @@ __global__ __launch_bounds__(TM *TN *kWave) void mx4_tile_kernel(Mx4Product p, i
 template <class Op, class OUT, bool GATED>
 hipError_t launch_product(const Mx4Product &p, hipStream_t stream) {
   const Mx4Layout l(p.N, p.K);
-  if (p.T <= 16) {
-    mx4_few_kernel<Op, OUT, 1, 1, GATED, 8, GATED ? 3 : 4><<<l.blocks, 8 * kWave, 0, stream>>>(p);
-  } else if (p.T <= 32) {
-    mx4_few_kernel<Op, OUT, 2, 1, GATED, 8, 2><<<l.blocks, 8 * kWave, 0, stream>>>(p);
+  if (p.T <= 64) {
+    return launch_few<Op, GATED>(p, stream);
   } else {
     constexpr int BM = 128, BN = 128;
     const int channels = GATED ? BN / 2 : BN;
@@ -434,6 +589,13 @@ hipError_t launch_pack_mx4(const uint8_t *codes, const uint8_t *scales, int32_t 
                            uint8_t *packed, hipStream_t stream) {
   pack_mx4_kernel<<<Mx4Layout(rows, cols).blocks, 256, 0, stream>>>(codes, scales, rows, cols, packed);
   return hipGetLastError();
+}
+
+size_t mx4_product_workspace(int32_t T, int32_t K, int32_t N, bool gated) {
+  if (T == 0 || T > 64) return 0;
+  const FewPlan f = few_plan(T, K, N, gated);
+  if (f.slices == 1) return 0;
+  return (size_t)f.slices * Mx4Layout(N, K).blocks * (gated ? 2 : 1) * f.xt * 1024;
 }
 
 hipError_t launch_mx4_product(const Mx4Product &p, hipStream_t stream) {

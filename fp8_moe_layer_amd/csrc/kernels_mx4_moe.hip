@@ -271,7 +271,8 @@ __global__ __launch_bounds__(TEAMS *kTeamWaves *kWave) void mx4_gate_up_kernel(M
         }
         barrier_reads();  // the sums are read: they can be written again
         done += stride;
-      });
+      },
+      [] {});
 }
 
 // ---------------------------------------------------------------- down
@@ -327,7 +328,7 @@ __global__ __launch_bounds__(W *kWave) void mx4_down_kernel(Mx4Moe p, const char
         });
         for (kt += W; kt >= l.kt; kt -= l.kt) ++a;
       },
-      [&](int c, int) { ring.multiply(c, acc); });
+      [&](int c, int) { ring.multiply(c, acc); }, [] {});
 #pragma unroll
   for (int m = 0; m < XT; ++m) part[wave][m][lane] = acc[0][m];
   __syncthreads();

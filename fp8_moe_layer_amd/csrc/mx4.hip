@@ -46,14 +46,27 @@ moe_status check_types(const char *fn, int32_t x_type, int32_t y_type) {
   return MOE_OK;
 }
 
+moe_status check_block(const char *fn, int32_t d, int32_t f) {
+  if (d < 32 || d % 32 || d > MOE_MAX_HIDDEN || f < 32 || f % 32 || f > MOE_MAX_FFN)
+    return fail_status(MOE_ERR_SHAPE, "%s: d=%d, f=%d must be multiples of 32 in [32, %d] and [32, %d]",
+                       fn, d, f, MOE_MAX_HIDDEN, MOE_MAX_FFN);
+  return MOE_OK;
+}
+
+// A required workspace (of no bytes: none).
+moe_status need_workspace(const char *fn, const void *workspace, size_t bytes, size_t need) {
+  if (need && !workspace)
+    return fail_status(MOE_ERR_WORKSPACE, "%s: a workspace of %zu bytes is needed", fn, need);
+  return check_workspace(fn, workspace, bytes, need);
+}
+
 moe_status check_layer(const char *fn, const moe_dims *m) {
   if (!m) return fail_status(MOE_ERR_NULL, "%s: dims is required", fn);
   if (m->flags) return fail_status(MOE_ERR_UNSUPPORTED, "%s: flags=0x%x must be 0", fn, m->flags);
   if (m->T < 0 || m->T > MOE_MX4_MAX_TOKENS)
     return fail_status(MOE_ERR_SHAPE, "%s: T=%d must be in [0, %d]", fn, m->T, MOE_MX4_MAX_TOKENS);
-  if (m->d < 32 || m->d % 32 || m->d > MOE_MAX_HIDDEN || m->f < 32 || m->f % 32 || m->f > MOE_MAX_FFN)
-    return fail_status(MOE_ERR_SHAPE, "%s: d=%d, f=%d must be multiples of 32 in [32, %d] and [32, %d]",
-                       fn, m->d, m->f, MOE_MAX_HIDDEN, MOE_MAX_FFN);
+  const moe_status s = check_block(fn, m->d, m->f);
+  if (s) return s;
   if (m->E < 1 || m->E > MOE_MAX_EXPERTS || m->k_max < 1 || m->k_max > MOE_MAX_K || m->k_max > m->E ||
       m->n_shared < 0 || m->n_shared > MOE_MX4_MAX_SHARED)
     return fail_status(MOE_ERR_SHAPE, "%s: E=%d (in [1, %d]), k_max=%d (in [1, min(E, %d)]), n_shared=%d "
@@ -129,8 +142,16 @@ moe_status moe_pack_mx4(const uint8_t *codes, const uint8_t *scales, int32_t row
   return finish(launch_pack_mx4(codes, scales, rows, cols, (uint8_t *)packed, as_stream(stream)), fn);
 }
 
+size_t moe_matmul_mx4_workspace_bytes(int32_t T, int32_t K, int32_t N) {
+  const char *fn = "moe_matmul_mx4_workspace_bytes";
+  if (check_matrix(fn, N < 1 ? -1 : N, K) || check_rows(fn, T, K, K, 2)) return 0;
+  (void)ok_status();
+  return mx4_product_workspace(T, K, N, false);
+}
+
 moe_status moe_matmul_mx4(const void *x, int64_t ldx, const void *w, const float *bias, int32_t x_type,
-                          int32_t T, int32_t K, int32_t N, int32_t y_type, void *y, void *stream) {
+                          int32_t T, int32_t K, int32_t N, int32_t y_type, void *y, void *workspace,
+                          size_t workspace_bytes, void *stream) {
   const char *fn = "moe_matmul_mx4";
   moe_status s = check_types(fn, x_type, y_type);
   if (s || (s = check_matrix(fn, N < 1 ? -1 : N, K)) || (s = check_rows(fn, T, ldx, K, 2))) return s;
@@ -138,33 +159,43 @@ moe_status moe_matmul_mx4(const void *x, int64_t ldx, const void *w, const float
   if (!x || !w || !y) return fail_status(MOE_ERR_NULL, "%s: x, w and y are required", fn);
   if (!all_aligned({x, w, y}, 16) || !aligned(bias, 4))
     return fail_status(MOE_ERR_ALIGN, "%s: x, w and y must be 16-byte, bias 4-byte aligned", fn);
-  const Span out[] = {{y, (int64_t)T * N * type_bytes(y_type)}};
+  const size_t need = mx4_product_workspace(T, K, N, false);
+  if ((s = need_workspace(fn, workspace, workspace_bytes, need))) return s;
+  const Span out[] = {{y, (int64_t)T * N * type_bytes(y_type)}, {workspace, (int64_t)need}};
   const Span in[] = {{x, span_rows(T, ldx, K, 2)}, {w, Mx4Layout(N, K).bytes()}, {bias, (int64_t)N * 4}};
-  if (clash(out, in)) return fail_status(MOE_ERR_SHAPE, "%s: y overlaps an input", fn);
-  const Mx4Product p{x, ldx, (const uint8_t *)w, nullptr, bias, T, K, N, x_type, y_type, y};
+  if (clash(out, in))
+    return fail_status(MOE_ERR_SHAPE, "%s: y or the workspace overlaps an input or the other", fn);
+  const Mx4Product p{x, ldx, (const uint8_t *)w, nullptr, bias, T, K, N, x_type, y_type, y, workspace};
   return finish(launch_mx4_product(p, as_stream(stream)), fn);
 }
 
+size_t moe_ffn_mx4_workspace_bytes(int32_t T, int32_t d, int32_t f) {
+  const char *fn = "moe_ffn_mx4_workspace_bytes";
+  if (check_block(fn, d, f) || check_rows(fn, T, d, d, 2)) return 0;
+  (void)ok_status();
+  return mx4_product_workspace(T, d, f, true);
+}
+
 moe_status moe_ffn_mx4(const void *x, int64_t ldx, const void *w_gate, const void *w_up, int32_t type,
-                       int32_t T, int32_t d, int32_t f, void *h, void *stream) {
+                       int32_t T, int32_t d, int32_t f, void *h, void *workspace, size_t workspace_bytes,
+                       void *stream) {
   const char *fn = "moe_ffn_mx4";
   moe_status s = check_types(fn, type, type);
-  if (s) return s;
-  if (d < 32 || d % 32 || d > MOE_MAX_HIDDEN || f < 32 || f % 32 || f > MOE_MAX_FFN)
-    return fail_status(MOE_ERR_SHAPE, "%s: d=%d, f=%d must be multiples of 32 in [32, %d] and [32, %d]",
-                       fn, d, f, MOE_MAX_HIDDEN, MOE_MAX_FFN);
-  if ((s = check_rows(fn, T, ldx, d, 2))) return s;
+  if (s || (s = check_block(fn, d, f)) || (s = check_rows(fn, T, ldx, d, 2))) return s;
   if (T == 0) return ok_status();
   if (!x || !w_gate || !w_up || !h)
     return fail_status(MOE_ERR_NULL, "%s: x, w_gate, w_up and h are required", fn);
   if (!all_aligned({x, w_gate, w_up, h}, 16))
     return fail_status(MOE_ERR_ALIGN, "%s: every array must be 16-byte aligned", fn);
   const int64_t wb = Mx4Layout(f, d).bytes();
-  const Span out[] = {{h, (int64_t)T * f * 2}};
+  const size_t need = mx4_product_workspace(T, d, f, true);
+  if ((s = need_workspace(fn, workspace, workspace_bytes, need))) return s;
+  const Span out[] = {{h, (int64_t)T * f * 2}, {workspace, (int64_t)need}};
   const Span in[] = {{x, span_rows(T, ldx, d, 2)}, {w_gate, wb}, {w_up, wb}};
-  if (clash(out, in)) return fail_status(MOE_ERR_SHAPE, "%s: h overlaps an input", fn);
+  if (clash(out, in))
+    return fail_status(MOE_ERR_SHAPE, "%s: h or the workspace overlaps an input or the other", fn);
   const Mx4Product p{x, ldx, (const uint8_t *)w_gate, (const uint8_t *)w_up, nullptr, T, d, f, type,
-                     type, h};
+                     type, h, workspace};
   return finish(launch_mx4_product(p, as_stream(stream)), fn);
 }
 

@@ -52,7 +52,9 @@ struct Mx4Product {
   const float *bias;
   int32_t T, K, N, type, out_type;
   void *y;
+  void *workspace;  // mx4_product_workspace bytes
 };
+size_t mx4_product_workspace(int32_t T, int32_t K, int32_t N, bool gated);
 hipError_t launch_mx4_product(const Mx4Product &p, hipStream_t stream);
 
 // A whole MoE layer of up to kMx4MaxTokens tokens.  Expert e's matrices follow

@@ -128,13 +128,46 @@ struct Mx4Ring {
   }
 };
 
+// The same with activations that are somewhere else (in LDS) when a tile is
+// multiplied: x(j, m) as load_x above.
+template <class Op, int NR, int D>
+struct Mx4Weights {
+  v4i w[D][NR];
+  uint32_t s[D][NR];
+  __device__ __forceinline__ void load(int c, const uint8_t *const (&block)[NR], const Mx4Layout &l,
+                                       int kt, int lane) {
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      w[c][r] = load16_nt(block[r] + (int64_t)kt * 1024 + lane * 16);
+      s[c][r] = *reinterpret_cast<const uint32_t *>(block[r] + l.scales + kt * 64 + (lane & 15) * 4);
+    }
+  }
+  template <int XT, class X>
+  __device__ __forceinline__ void multiply(int c, X x, v4f (&acc)[NR][XT]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      typename Op::X xs[XT];
+#pragma unroll
+      for (int m = 0; m < XT; ++m) xs[m] = x(j, m);
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const v4i a = mx4_operand<Op>(w[c][r][j], mx4_scale<Op>(s[c][r], j));
+#pragma unroll
+        for (int m = 0; m < XT; ++m) acc[r][m] = Op::mfma(a, xs[m], acc[r][m]);
+      }
+    }
+  }
+};
+
 // Runs n tiles through a ring of D: load(c, i) asks for tile i into slot c,
-// use(c, i) multiplies it.
-template <int D, class Load, class Use>
-__device__ __forceinline__ void run_ring(int n, Load load, Use use) {
+// use(c, i) multiplies it; ready() comes between the first D loads and the first
+// use.
+template <int D, class Load, class Use, class Ready>
+__device__ __forceinline__ void run_ring(int n, Load load, Use use, Ready ready) {
 #pragma unroll
   for (int c = 0; c < D; ++c)
     if (c < n) load(c, c);
+  ready();
   int i = 0;
   // no branches between the loads: the compiler's waits then leave D - 1 tiles in flight
   for (; i + 2 * D <= n; i += D)

@@ -418,7 +418,13 @@ moe_status moe_gated_ffn_backward(const void *dh, int64_t lddh, const void *x, i
  * products by moe_pack_mx4 (an opaque order in which a wave's loads are whole
  * pieces of 1 KB).  Activations are bf16 or fp16 rows, not quantised; row
  * strides are as for the dense operators.  Inputs are finite; the sums
- * sum_k |x[k]| too, in fp32. */
+ * sum_k |x[k]| too, in fp32.
+ *
+ * Workspaces: where a product's K is cut for more workgroups, the parts' sums
+ * need room: the *_workspace_bytes functions give it (0 where the product is not
+ * cut, and, with a text in moe_last_error(), for sizes that the call refuses).
+ * The workspace is a device buffer of at least that size, 256-byte aligned, not
+ * touched by anything else while the work is in flight; it need not be cleared. */
 #define MOE_MX4_GROUP 32
 #define MOE_MAX_MX4_K 65536 /* longest row */
 
@@ -455,15 +461,19 @@ moe_status moe_pack_mx4(const uint8_t *codes, const uint8_t *scales, int32_t row
  * 2^-35 of the largest scale of their channel are rounded to steps of 2^-36 of
  * it.  Sums in fp32, rounded once.  K: a multiple of 32 up to MOE_MAX_MX4_K; T
  * and N: any up to MOE_MAX_TOKENS. */
+size_t moe_matmul_mx4_workspace_bytes(int32_t T, int32_t K, int32_t N);
 moe_status moe_matmul_mx4(const void *x, int64_t ldx, const void *w, const float *bias, int32_t x_type,
-                          int32_t T, int32_t K, int32_t N, int32_t y_type, void *y, void *stream);
+                          int32_t T, int32_t K, int32_t N, int32_t y_type, void *y, void *workspace,
+                          size_t workspace_bytes, void *stream);
 
 /* The gated block on packed weights of f channels by d inputs, in one kernel:
  *   g = x w_gate^T, u = x w_up^T (fp32 sums), h = SiLU(g) * u, rounded once
  * x [T][d], h [T][f] in `type`.  d, f: multiples of 32 up to MOE_MAX_HIDDEN /
  * MOE_MAX_FFN.  (moe_matmul_mx4 on h is the down projection.) */
+size_t moe_ffn_mx4_workspace_bytes(int32_t T, int32_t d, int32_t f);
 moe_status moe_ffn_mx4(const void *x, int64_t ldx, const void *w_gate, const void *w_up, int32_t type,
-                       int32_t T, int32_t d, int32_t f, void *h, void *stream);
+                       int32_t T, int32_t d, int32_t f, void *h, void *workspace,
+                       size_t workspace_bytes, void *stream);
 
 /* Forward pass of a whole mixture-of-experts layer of a few tokens with 4-bit
  * experts, in three launches: router logits (or logits_override), top-k and

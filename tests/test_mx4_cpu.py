@@ -87,8 +87,8 @@ def test_packed_size():
     assert fp8.packed_mx4_bytes(1 << 40, 32) == fp8.packed_mx4_bytes(4, 1 << 40) == 0
 
 
-def matmul(x=P[0], ldx=64, w=P[1], bias=None, x_type=BF16, T=4, K=64, N=40, y_type=F32, y=P[2]):
-    return fp8._matmul_mx4(x, ldx, w, bias, x_type, T, K, N, y_type, y, None)
+def matmul(x=P[0], ldx=64, w=P[1], bias=None, x_type=BF16, T=4, K=64, N=40, y_type=F32, y=P[2], ws=None, wsb=0):
+    return fp8._matmul_mx4(x, ldx, w, bias, x_type, T, K, N, y_type, y, ws, wsb, None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -106,8 +106,8 @@ def test_matmul_refuses(kw, code):
     assert fp8._last_error().startswith(b"moe_matmul_mx4")
 
 
-def gated(x=P[0], ldx=64, wg=P[1], wu=P[2], kind=F16, T=4, d=64, f=96, h=P[3]):
-    return fp8._ffn_mx4(x, ldx, wg, wu, kind, T, d, f, h, None)
+def gated(x=P[0], ldx=64, wg=P[1], wu=P[2], kind=F16, T=4, d=64, f=96, h=P[3], ws=None, wsb=0):
+    return fp8._ffn_mx4(x, ldx, wg, wu, kind, T, d, f, h, ws, wsb, None)
 
 
 @pytest.mark.parametrize("kw,code", [
