@@ -168,19 +168,23 @@ struct Mx4Out {
   const float *bias;
   OUT *y;
   int32_t T, N;
-  // four channels of token t
-  __device__ __forceinline__ void store(int t, int ch, v4f v, const float (&f)[4]) const {
-    float o[4];
+  // 4 P consecutive channels of token t
+  template <int P>
+  __device__ __forceinline__ void store(int t, int ch, const v4f (&v)[P], const float (&f)[P][4]) const {
+    float o[4 * P];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = fmaf(v[i], f[i], bias && ch + i < N ? bias[ch + i] : 0.0f);
-    store_run<OUT, 4>(y + (int64_t)t * N + ch, o, N - ch);
+    for (int i = 0; i < 4 * P; ++i)
+      o[i] = fmaf(v[i / 4][i % 4], f[i / 4][i % 4], bias && ch + i < N ? bias[ch + i] : 0.0f);
+    store_run<OUT, 4 * P>(y + (int64_t)t * N + ch, o, N - ch);
   }
-  __device__ __forceinline__ void store(int t, int ch, v4f g, const float (&fg)[4], v4f u,
-                                        const float (&fu)[4]) const {
-    float o[4];
+  template <int P>
+  __device__ __forceinline__ void store(int t, int ch, const v4f (&g)[P], const float (&fg)[P][4],
+                                        const v4f (&u)[P], const float (&fu)[P][4]) const {
+    float o[4 * P];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = silu_mul(g[i] * fg[i], u[i] * fu[i]);
-    store_run<OUT, 4>(y + (int64_t)t * N + ch, o, N - ch);
+    for (int i = 0; i < 4 * P; ++i)
+      o[i] = silu_mul(g[i / 4][i % 4] * fg[i / 4][i % 4], u[i / 4][i % 4] * fu[i / 4][i % 4]);
+    store_run<OUT, 4 * P>(y + (int64_t)t * N + ch, o, N - ch);
   }
 };
 
@@ -192,7 +196,7 @@ __device__ __forceinline__ void load_factors(const uint8_t *block, const Mx4Layo
 }
 
 // ---------------------------------------------------------------- few tokens
-// Up to 64 tokens the product is a stream of the weights, each byte used once,
+// Up to 32 tokens the product is a stream of the weights, each byte used once,
 // and what costs beside them is the activations, which every workgroup needs
 // whole: at 16 tokens a tile's are four times its weights.  So a workgroup takes a
 // part of K (`slices` of them, joined by a second launch where there is more than
@@ -201,7 +205,7 @@ __device__ __forceinline__ void load_factors(const uint8_t *block, const Mx4Layo
 // barrier stands in the stream of the weights, which go from memory to the
 // registers of the one wave that uses them.
 struct FewPlan {
-  int xt;      // 16-token sub-tiles: 1, 2, 4
+  int xt;      // 16-token sub-tiles: 1, 2
   int wr, wk;  // waves
   int nb;      // blocks of channels of a wave
   int slices, tiles;  // parts of K, and tiles of one
@@ -209,6 +213,7 @@ struct FewPlan {
   size_t lds;
 };
 
+constexpr int kFewTokens = 32;
 constexpr int kFewWaves = 8;
 constexpr int kFewLds = 128 * 1024;  // of activations
 constexpr int kFewGroups = 224;      // workgroups that fill the 256 compute units well enough
@@ -227,7 +232,7 @@ constexpr int kFewGroups = 224;      // workgroups that fill the 256 compute uni
 FewPlan few_plan(int32_t T, int32_t K, int32_t N, bool gated) {
   FewPlan f{};
   const Mx4Layout l(N, K);
-  f.xt = T <= 16 ? 1 : T <= 32 ? 2 : 4;
+  f.xt = T <= 16 ? 1 : 2;
   f.nb = gated || f.xt == 1 ? 1 : 2;
   for (f.rows = 1; f.rows < T; f.rows *= 2) {
   }
@@ -254,18 +259,20 @@ FewPlan few_plan(int32_t T, int32_t K, int32_t N, bool gated) {
 // y's four channels of one token from their sums; the types of few tokens' outputs
 // are told apart here, at run time.
 template <class Op>
-__device__ __forceinline__ void few_store(const Mx4Product &p, int t, int ch, v4f v, const float (&f)[4]) {
+__device__ __forceinline__ void few_store(const Mx4Product &p, int t, int ch, v4f v, const float (&f)[1][4]) {
   if (t >= p.T || ch >= p.N) return;
+  const v4f a[1] = {v};
   if (p.out_type == kTypeF32)
-    Mx4Out<float>{p.bias, static_cast<float *>(p.y), p.T, p.N}.store(t, ch, v, f);
+    Mx4Out<float>{p.bias, static_cast<float *>(p.y), p.T, p.N}.store(t, ch, a, f);
   else
-    Mx4Out<typename Op::E>{p.bias, static_cast<typename Op::E *>(p.y), p.T, p.N}.store(t, ch, v, f);
+    Mx4Out<typename Op::E>{p.bias, static_cast<typename Op::E *>(p.y), p.T, p.N}.store(t, ch, a, f);
 }
 template <class Op>
-__device__ __forceinline__ void few_store(const Mx4Product &p, int t, int ch, v4f g, const float (&fg)[4],
-                                          v4f u, const float (&fu)[4]) {
+__device__ __forceinline__ void few_store(const Mx4Product &p, int t, int ch, v4f g, const float (&fg)[1][4],
+                                          v4f u, const float (&fu)[1][4]) {
   if (t >= p.T || ch >= p.N) return;
-  Mx4Out<typename Op::E>{nullptr, static_cast<typename Op::E *>(p.y), p.T, p.N}.store(t, ch, g, fg, u, fu);
+  const v4f a[1] = {g}, b[1] = {u};
+  Mx4Out<typename Op::E>{nullptr, static_cast<typename Op::E *>(p.y), p.T, p.N}.store(t, ch, a, fg, b, fu);
 }
 
 template <class Op, int XT, int NB, bool GATED, int WR, int WK, int D>
@@ -347,11 +354,11 @@ __global__ __launch_bounds__(WR *WK *kWave) void mx4_few_kernel(Mx4Product p, in
       if constexpr (GATED) to[XT * kWave] = u;
       continue;
     }
-    float f[4], fu[4];
-    load_factors<Op>(p.w0 + b * l.block_bytes, l, q, f);
+    float f[1][4], fu[1][4];
+    load_factors<Op>(p.w0 + b * l.block_bytes, l, q, f[0]);
     const int t = m * 16 + c16, ch = mx4_channel(b, q * 4);
     if constexpr (GATED) {
-      load_factors<Op>(p.w1 + b * l.block_bytes, l, q, fu);
+      load_factors<Op>(p.w1 + b * l.block_bytes, l, q, fu[0]);
       few_store<Op>(p, t, ch, a, f, u, fu);
     } else {
       few_store<Op>(p, t, ch, a, f);
@@ -374,11 +381,11 @@ __global__ __launch_bounds__(256) void mx4_join_kernel(Mx4Product p, int slices,
     a += at[s * step];
     if constexpr (GATED) u += at[s * step + xt * kWave];
   }
-  float f[4], fu[4];
+  float f[1][4], fu[1][4];
   const int q = lane >> 4, t = m * 16 + (lane & 15), ch = mx4_channel(b, q * 4);
-  load_factors<Op>(p.w0 + b * l.block_bytes, l, q, f);
+  load_factors<Op>(p.w0 + b * l.block_bytes, l, q, f[0]);
   if constexpr (GATED) {
-    load_factors<Op>(p.w1 + b * l.block_bytes, l, q, fu);
+    load_factors<Op>(p.w1 + b * l.block_bytes, l, q, fu[0]);
     few_store<Op>(p, t, ch, a, f, u, fu);
   } else {
     few_store<Op>(p, t, ch, a, f);
@@ -410,146 +417,331 @@ hipError_t launch_few_rows(const Mx4Product &p, const FewPlan &f, hipStream_t st
 template <class Op, bool GATED>
 hipError_t launch_few(const Mx4Product &p, hipStream_t stream) {
   const FewPlan f = few_plan(p.T, p.K, p.N, GATED);
-  if (f.xt == 1) return launch_few_rows<Op, GATED, 1>(p, f, stream);
-  if (f.xt == 2) return launch_few_rows<Op, GATED, 2>(p, f, stream);
-  return launch_few_rows<Op, GATED, 4>(p, f, stream);
+  return f.xt == 1 ? launch_few_rows<Op, GATED, 1>(p, f, stream) : launch_few_rows<Op, GATED, 2>(p, f, stream);
 }
 
 // ---------------------------------------------------------------- tiles
-// BM tokens by BN rows (gated: half of them from each matrix).  The activations
-// of a tile's 128 inputs go to LDS (256 bytes a token, 16-byte piece i of token r
-// at position i ^ r%16, so that 16 lanes that read one piece of 16 tokens touch
-// all banks), the weights straight to the registers of the waves that use them.
-template <int BM, int W>
-struct Mx4Tokens {
-  static constexpr int kPieces = BM / 4 / W;  // of four tokens, a wave's
-  v4u rsrc;
-  uint32_t off[kPieces];
-  int pos[kPieces];
-  __device__ __forceinline__ Mx4Tokens(const uint8_t *x, int64_t ld, int M, int64_t kbytes, int t0,
-                                       int wave, int lane) {
-    const int rows = M - t0 < BM ? M - t0 : BM;
-    rsrc = buffer_of(x + (int64_t)t0 * ld, (int64_t)(rows - 1) * ld + kbytes);
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int r = (i * W + wave) * 4 + (lane >> 4);
-      pos[i] = ((lane & 15) ^ (r & 15)) * 16;
-      off[i] = r < rows ? (uint32_t)(r * ld) + pos[i] : kPastEnd;
-    }
-  }
-  // tile kt, `left` bytes of K from its start on
-  __device__ __forceinline__ void fetch(int kt, int left, uint32_t lds, int wave) const {
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-      dma16(rsrc, pos[i] < left ? off[i] + kt * 256 : kPastEnd, lds + (i * W + wave) * 1024);
-  }
+// BM tokens by BN rows of weights (gated: of each wave's WN rows half come from
+// each matrix), TM x TN waves, KG groups of them that share the tile, each with
+// LDS of its own and its part of the steps; their sums meet in LDS at the end.
+//
+// A step is 128 inputs.  It comes to LDS directly, ST steps deep: the activations
+// (256 bytes a token, 16-byte piece i of token r at position i ^ r%16, so that 16
+// lanes that read one piece of 16 tokens touch all banks), the codes as they lie
+// in memory, a block's 1 KB after the other, and their scales, 64 bytes a block.  A
+// quarter of a step is a
+// group of 32 inputs: while its products run, the next quarter's activations are
+// read from LDS, and the codes turn into 16-bit operands just before their use.
+// One barrier a step, before the last quarter's products: there every wave has
+// read all of the step, whose stage is filled again, and the next one has landed.
+template <int BM, int BN, int TM, int TN, int ST, int KG, bool GATED>
+struct Mx4Shape {
+  static constexpr int kWaves = TM * TN, kThreads = KG * kWaves * kWave;
+  static constexpr int WM = BM / TM, WN = BN / TN, MS = WM / 16, NR = WN / 16;
+  static constexpr int NC = GATED ? NR / 2 : NR;           // blocks of channels of a wave
+  static constexpr int kChannels = GATED ? BN / 2 : BN;    // of a tile
+  static constexpr int kCodes = BM * 256, kScales = kCodes + BN * 64;
+  static constexpr int kStage = kScales + BN * 4;
+  static constexpr int kRing = ST * kStage;
+  static constexpr int kLds = KG * kRing;
+  static constexpr int kX = BM / 4 / kWaves, kW = BN / 16 / kWaves;  // a wave's 1 KB pieces of a step
+  static constexpr int kPieces = kX + kW + 1;
+  static_assert(NC >= 1 && BM % (4 * kWaves) == 0 && BN % (16 * kWaves) == 0 && BN % 64 == 0, "tile shape");
+  static_assert(KG == 1 || kRing >= BM * BN * 4, "the sums of a group fit its ring");
 };
 
-template <class Op, class OUT, int BM, int BN, int TM, int TN, bool GATED>
-__global__ __launch_bounds__(TM *TN *kWave) void mx4_tile_kernel(Mx4Product p, int tiles_m, int tiles_n) {
-  constexpr int W = TM * TN, WM = BM / TM, WN = BN / TN, MS = WM / 16, NR = WN / 16;
-  constexpr int NC = GATED ? NR / 2 : NR;  // blocks of channels of a wave
-  static_assert(NC >= 1 && BM % (4 * W) == 0, "tile shape");
-  __shared__ uint8_t lds[2 * BM * 256];
+// 4 bytes a lane from memory to LDS at lds + 4 * lane; see dma16.
+__device__ __forceinline__ void dma4_from(const uint8_t *p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+               :
+               : "s"(lds), "v"(p)
+               : "memory");
+}
+
+template <class Op, class OUT, int BM, int BN, int TM, int TN, int ST, int KG, bool GATED>
+__global__ __launch_bounds__(KG *TM *TN *kWave) void mx4_tile_kernel(Mx4Product p, int tiles_m, int tiles_n, int slices, v4f *partial) {
+  typedef Mx4Shape<BM, BN, TM, TN, ST, KG, GATED> S;
+  constexpr int MS = S::MS, NR = S::NR, NC = S::NC, W = S::kWaves;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
   const Mx4Layout l(p.N, p.K);
-  const int lane = threadIdx.x & 63, q = lane >> 4, c = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / TN, wn = wave % TN;
+  const int lane = threadIdx.x & 63, q = lane >> 4, c16 = lane & 15;
+  const int all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kg = all / W, wave = all % W, wm = wave / TN, wn = wave % TN;
   int tm, tn;
-  tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
-  const int t0 = tm * BM, b0 = (tn * TN + wn) * NC;
-  const Mx4Tokens<BM, W> xs(static_cast<const uint8_t *>(p.x), p.ldx * 2, p.T, (int64_t)p.K * 2, t0,
-                            wave, lane);
+  const int slice = blockIdx.x % slices;
+  tile_of(blockIdx.x / slices, tiles_m, tiles_n, tm, tn);
+  const int t0 = tm * BM, tile_b = tn * (S::kChannels / 16), b0 = tile_b + wn * NC;
+  // this group's steps: nk from k0 on (those behind the end take zeros for activations)
+  const int nk = (l.kt + KG * slices - 1) / (KG * slices), k0 = (slice * KG + kg) * nk;
+  const LdsPtr ring = (LdsPtr)lds + kg * S::kRing;
+  const uint32_t ring_at = lds_address(ring);
+
+  // sources
+  const int rows = p.T - t0 < BM ? p.T - t0 : BM;
+  const int64_t ldx = p.ldx * 2, kbytes = (int64_t)p.K * 2;
+  const v4u rx = buffer_of(static_cast<const uint8_t *>(p.x) + (int64_t)t0 * ldx, (int64_t)(rows - 1) * ldx + kbytes);
+  // piece i: tokens i * 4 W + r, whose r%16 is the same (a token behind the last: its
+  // offset is behind the descriptor's end)
+  static_assert(W % 4 == 0, "pieces of a wave have one key");
+  const int r = wave * 4 + q, xpos = (c16 ^ (r & 15)) * 16;
+  const uint32_t xoff = (uint32_t)(r * ldx) + xpos, xstep = (uint32_t)(4 * W * ldx);
+  // block i of the tile, in the order of the waves' rows
+  auto source = [&](int i) {
+    const int r = i % NR, b = tile_b + i / NR * NC + r % NC;  // behind the last: not stored
+    return (GATED && r >= NC ? p.w1 : p.w0) + (int64_t)(b < l.blocks ? b : l.blocks - 1) * l.block_bytes;
+  };
+  const uint8_t *wsrc[S::kW];
+#pragma unroll
+  for (int i = 0; i < S::kW; ++i) wsrc[i] = source(wave * S::kW + i);
+  // scales: 256 bytes, four blocks, to an instruction; a wave behind the last repeats one
+  const int spiece = wave % (BN / 64);
+  static_assert(BN / 64 <= W, "a scale piece to a wave");
+  const uint8_t *ssrc = source(spiece * 4 + q) + l.scales + c16 * 4;
   const uint8_t *block[NR];
 #pragma unroll
-  for (int r = 0; r < NR; ++r) {
-    const int b = b0 + r % NC;  // a block behind the last repeats it, and is not stored
-    block[r] = (r < NC ? p.w0 : p.w1) + (b < l.blocks ? b : l.blocks - 1) * l.block_bytes;
-  }
+  for (int r = 0; r < NR; ++r) block[r] = source(wn * NR + r);
+
+  auto piece = [&](int i, int k, uint32_t stage) {
+    const int kt = k < l.kt ? k : l.kt - 1;
+    if (i < S::kX) {
+      const int64_t left = kbytes - (int64_t)k * 256;
+      dma16(rx, (xpos < left ? xoff + k * 256 : kPastEnd) + i * xstep, ring_at + stage + (i * W + wave) * 1024);
+    } else if (i < S::kX + S::kW) {
+      const int j = i - S::kX;
+      dma16(buffer_of(wsrc[j] + (int64_t)kt * 1024, 1024), lane * 16,
+            ring_at + stage + S::kCodes + (wave * S::kW + j) * 1024);
+    } else if (i < S::kPieces) {
+      dma4_from(ssrc + kt * 64, ring_at + stage + S::kScales + spiece * 256);
+    }
+  };
+  auto fetch = [&](int k, uint32_t stage) {
+#pragma unroll
+    for (int i = 0; i < S::kPieces; ++i) piece(i, k, stage);
+  };
   v4f acc[NR][MS];
 #pragma unroll
   for (int r = 0; r < NR; ++r)
 #pragma unroll
     for (int m = 0; m < MS; ++m) acc[r][m] = v4f{0.f, 0.f, 0.f, 0.f};
-  const LdsPtr base = (LdsPtr)lds;
-  const int64_t kbytes = (int64_t)p.K * 2;
-  auto left = [&](int kt) {
-    const int64_t n = kbytes - (int64_t)kt * 256;
-    return n < 256 ? (int)n : 256;
+
+  v4i fx[MS];
+  v2i cw[NR];  // the codes of half a step
+  uint32_t cs[NR];  // a step's scales
+  v4i a[NR];        // the operands of a quarter
+  auto read_x = [&](int m, int j, uint32_t stage) {
+    fx[m] = lds_read16(ring + stage + (wm * S::WM + m * 16 + c16) * 256 + (((j * 4 + q) ^ c16) * 16));
   };
-  v4i w[NR];
-  uint32_t s[NR];
-  auto fetch_w = [&](int kt) {
+  auto read_codes = [&](int half, uint32_t stage) {
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      w[r] = load16(block[r] + (int64_t)kt * 1024 + lane * 16);
-      s[r] = *reinterpret_cast<const uint32_t *>(block[r] + l.scales + kt * 64 + c * 4);
-    }
+    for (int r = 0; r < NR; ++r)
+      cw[r] = *(const __attribute__((address_space(3))) v2i *)(ring + stage + S::kCodes +
+                                                                     (wn * NR + r) * 1024 + lane * 16 + half * 8);
   };
-  xs.fetch(0, left(0), lds_address(base), wave);
-  fetch_w(0);
-  for (int kt = 0; kt < l.kt; ++kt) {
-    const uint32_t stage = (kt & 1) * BM * 256;
-    wait_dma<0>();
-    barrier_reads();
-    v4i cw[NR];
-    uint32_t cs[NR];
+  auto read_scales = [&](uint32_t stage) {
 #pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      cw[r] = w[r];
-      cs[r] = s[r];
-    }
-    if (kt + 1 < l.kt) {
-      xs.fetch(kt + 1, left(kt + 1), lds_address(base) + (BM * 256 - stage), wave);
-      fetch_w(kt + 1);
-    }
+    for (int r = 0; r < NR; ++r)
+      cs[r] = *(const __attribute__((address_space(3))) uint32_t *)(ring + stage + S::kScales +
+                                                                    (wn * NR + r) * 64 + c16 * 4);
+  };
+  auto convert = [&](int j) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v4i fx[MS];
-#pragma unroll
-      for (int m = 0; m < MS; ++m)
-        fx[m] = lds_read16(base + stage + (wm * WM + m * 16 + c) * 256 + (((j * 4 + q) ^ c) * 16));
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const v4i a = mx4_operand<Op>(cw[r][j], mx4_scale<Op>(cs[r], j));
-#pragma unroll
-        for (int m = 0; m < MS; ++m) acc[r][m] = Op::mfma(a, fx[m], acc[r][m]);
-      }
-    }
-  }
-  const Mx4Out<OUT> out{p.bias, static_cast<OUT *>(p.y), p.T, p.N};
-#pragma unroll
-  for (int r = 0; r < NC; ++r) {
-    const int ch = mx4_channel(b0 + r, q * 4);
-    if (ch >= p.N) continue;
-    float f[4], fu[4];
-    load_factors<Op>(block[r], l, q, f);
-    if constexpr (GATED) load_factors<Op>(block[NC + r], l, q, fu);
+    for (int r = 0; r < NR; ++r) a[r] = mx4_operand<Op>(cw[r][j & 1], mx4_scale<Op>(cs[r], j));
+  };
+  // the products of quarter j; a sub-tile's activations of the next quarter (stage
+  // `next`) are read into the place of this one's as soon as they are used, and
+  // (fetch_k >= 0) a later step is fetched in between
+  auto quarter = [&](int j, uint32_t next, bool reads, int fetch_k, uint32_t into) {
 #pragma unroll
     for (int m = 0; m < MS; ++m) {
-      const int t = t0 + wm * WM + m * 16 + c;
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int r = 0; r < NR; ++r) acc[r][m] = Op::mfma(a[r], fx[m], acc[r][m]);
+      __builtin_amdgcn_s_setprio(0);
+      if (reads) read_x(m, (j + 1) & 3, next);
+      if (fetch_k >= 0) {
+#pragma unroll
+        for (int i = m * S::kPieces / MS; i < (m + 1) * S::kPieces / MS; ++i) piece(i, fetch_k, into);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+#pragma unroll
+  for (int k = 0; k < ST; ++k)
+    if (k < nk) fetch(k0 + k, k * S::kStage);
+  if (nk >= ST)
+    wait_dma<(ST - 1) * S::kPieces>();
+  else
+    wait_dma<0>();
+  barrier_reads();
+  uint32_t stage = 0;
+  auto after = [&](uint32_t s) -> uint32_t { return s + S::kStage == S::kRing ? 0 : s + S::kStage; };
+  read_codes(0, 0);
+  read_scales(0);
+#pragma unroll
+  for (int m = 0; m < MS; ++m) read_x(m, 0, 0);
+  // a step up to its last quarter's operands, and the next one's start
+  auto three = [&]() {
+    convert(0);
+    quarter(0, stage, true, -1, 0);
+    convert(1);
+    read_codes(1, stage);
+    quarter(1, stage, true, -1, 0);
+    convert(2);
+    quarter(2, stage, true, -1, 0);
+    convert(3);
+  };
+  auto enter = [&]() {
+    barrier_reads();
+    stage = after(stage);
+    read_codes(0, stage);
+    read_scales(stage);
+  };
+  int k = 0;
+  for (; k + ST < nk; ++k) {
+    three();
+    wait_dma<(ST - 2) * S::kPieces>();
+    const uint32_t into = stage;
+    enter();
+    quarter(3, stage, true, k0 + k + ST, into);
+  }
+  for (; k + 1 < nk; ++k) {
+    three();
+    wait_dma<0>();
+    enter();
+    quarter(3, stage, true, -1, 0);
+  }
+  three();
+  quarter(3, stage, false, -1, 0);
+
+  if constexpr (KG > 1) {
+    // every wave has read its last operands and no load is in flight
+    barrier_reads();
+    uint8_t *mine = lds + kg * S::kRing + wave * (S::WM * S::WN * 4) + lane * 16;
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+#pragma unroll
+      for (int m = 0; m < MS; ++m)
+        if (kg > 0) *reinterpret_cast<v4f *>(mine + (r * MS + m) * 1024) = acc[r][m];
+    barrier_reads();
+    if (kg > 0) return;
+#pragma unroll
+    for (int g = 1; g < KG; ++g)
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
+#pragma unroll
+        for (int m = 0; m < MS; ++m)
+          acc[r][m] += *reinterpret_cast<const v4f *>(mine + g * S::kRing + (r * MS + m) * 1024);
+  }
+  const int tb = t0 + wm * S::WM;
+  if (slices > 1) {
+    const int xt = (p.T + 15) / 16;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const int b = b0 + r % NC;
+      if (b >= l.blocks) continue;
+      const int64_t at = ((int64_t)slice * l.blocks + b) * (GATED ? 2 : 1) + r / NC;
+#pragma unroll
+      for (int m = 0; m < MS; ++m)
+        if (tb / 16 + m < xt) partial[(at * xt + tb / 16 + m) * kWave + lane] = acc[r][m];
+    }
+    return;
+  }
+  const Mx4Out<OUT> out{p.bias, static_cast<OUT *>(p.y), p.T, p.N};
+  // pairs of blocks: eight consecutive channels a lane
+  constexpr int P = NC % 2 == 0 ? 2 : 1;
+#pragma unroll
+  for (int r = 0; r < NC; r += P) {
+    const int ch = mx4_channel(b0 + r, q * 4);
+    if (ch >= p.N) continue;
+    float f[P][4], fu[P][4];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      load_factors<Op>(block[r + i], l, q, f[i]);
+      if constexpr (GATED) load_factors<Op>(block[NC + r + i], l, q, fu[i]);
+    }
+#pragma unroll
+    for (int m = 0; m < MS; ++m) {
+      const int t = tb + m * 16 + c16;
       if (t >= p.T) continue;
+      v4f a[P], u[P];
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        a[i] = acc[r + i][m];
+        if constexpr (GATED) u[i] = acc[NC + r + i][m];
+      }
       if constexpr (GATED)
-        out.store(t, ch, acc[r][m], f, acc[NC + r][m], fu);
+        out.template store<P>(t, ch, a, f, u, fu);
       else
-        out.store(t, ch, acc[r][m], f);
+        out.template store<P>(t, ch, a, f);
     }
   }
 }
 
 // ---------------------------------------------------------------- launch
+// The tiles, and what a step of 128 inputs of one takes with a workgroup on every
+// compute unit (us; measured at 256 and 512 workgroups).  What bounds the largest is
+// LDS, whose reads and fills take four fifths of the matrix instructions' cycles,
+// and power; the small ones the loads from the L2, 10-12 TB/s in all.
+struct TileKind {
+  int bm, bn, kg;
+  float step;
+};
+constexpr TileKind kTiles[] = {{64, 64, 2, 0.67f}, {64, 128, 2, 1.1f}, {128, 128, 1, 0.98f}, {128, 256, 1, 1.56f}};
+constexpr int kTileCuts[] = {1, 2, 3, 4, 6, 8};  // parts of K
+
+struct TilePlan {
+  int tile, slices;
+};
+// The tile and the cut of K with the least estimated time: rounds of workgroups, one
+// to a compute unit, of 1.3 us and their steps each, and for a cut the joining
+// launch, 2 us and the sums' way through memory.  (Measured against every tile with
+// 1, 2, 4 and 8 parts at 20 sizes from 33 x 14336 x 4096 to 8192 x 4096 x 2*14336.)
+TilePlan tile_plan(int32_t T, int32_t K, int32_t N, bool gated) {
+  const Mx4Layout l(N, K);
+  const double outputs = (double)T * l.blocks * 16 * (gated ? 2 : 1);
+  TilePlan best{0, 1};
+  double least = 1e30;
+  for (int i = 0; i < 4; ++i) {
+    const TileKind &k = kTiles[i];
+    const int channels = gated ? k.bn / 2 : k.bn;
+    const int64_t tiles = (int64_t)((T + k.bm - 1) / k.bm) * ((l.blocks * 16 + channels - 1) / channels);
+    for (int s : kTileCuts) {
+      if (s > 1 && s * k.kg > l.kt) break;
+      const int64_t rounds = (tiles * s + 255) / 256;
+      const int steps = (l.kt + k.kg * s - 1) / (k.kg * s);
+      const double us = rounds * (1.3 + steps * (double)k.step) + (s > 1 ? 2.0 + s * outputs * 8 / 5e6 : 0.0);
+      if (us < least) least = us, best = TilePlan{i, s};
+    }
+  }
+  return best;
+}
+
+template <class Op, class OUT, bool GATED, int BM, int BN, int TM, int TN, int ST, int KG>
+hipError_t launch_tile(const Mx4Product &p, int slices, hipStream_t stream) {
+  typedef Mx4Shape<BM, BN, TM, TN, ST, KG, GATED> S;
+  const Mx4Layout l(p.N, p.K);
+  const int tm = (p.T + BM - 1) / BM, tn = (l.blocks * 16 + S::kChannels - 1) / S::kChannels;
+  v4f *partial = static_cast<v4f *>(p.workspace);
+  mx4_tile_kernel<Op, OUT, BM, BN, TM, TN, ST, KG, GATED>
+      <<<tm * tn * slices, S::kThreads, 0, stream>>>(p, tm, tn, slices, partial);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || slices == 1) return e;
+  const int xt = (p.T + 15) / 16;
+  mx4_join_kernel<Op, GATED><<<(l.blocks * xt + 3) / 4, 256, 0, stream>>>(p, slices, xt, partial);
+  return hipGetLastError();
+}
+
 template <class Op, class OUT, bool GATED>
 hipError_t launch_product(const Mx4Product &p, hipStream_t stream) {
-  const Mx4Layout l(p.N, p.K);
-  if (p.T <= 64) {
-    return launch_few<Op, GATED>(p, stream);
-  } else {
-    constexpr int BM = 128, BN = 128;
-    const int channels = GATED ? BN / 2 : BN;
-    const int tm = (p.T + BM - 1) / BM, tn = (l.blocks * 16 + channels - 1) / channels;
-    mx4_tile_kernel<Op, OUT, BM, BN, 2, 2, GATED><<<tm * tn, 4 * kWave, 0, stream>>>(p, tm, tn);
+  if (p.T <= kFewTokens) return launch_few<Op, GATED>(p, stream);
+  const TilePlan t = tile_plan(p.T, p.K, p.N, GATED);
+  switch (t.tile) {
+    case 0: return launch_tile<Op, OUT, GATED, 64, 64, 2, 2, 3, 2>(p, t.slices, stream);
+    case 1: return launch_tile<Op, OUT, GATED, 64, 128, 2, 2, 3, 2>(p, t.slices, stream);
+    case 2: return launch_tile<Op, OUT, GATED, 128, 128, 2, 4, 3, 1>(p, t.slices, stream);
+    default: return launch_tile<Op, OUT, GATED, 128, 256, 2, 4, 3, 1>(p, t.slices, stream);
   }
-  return hipGetLastError();
 }
 
 template <class Op, class T>
@@ -592,10 +784,10 @@ hipError_t launch_pack_mx4(const uint8_t *codes, const uint8_t *scales, int32_t 
 }
 
 size_t mx4_product_workspace(int32_t T, int32_t K, int32_t N, bool gated) {
-  if (T == 0 || T > 64) return 0;
-  const FewPlan f = few_plan(T, K, N, gated);
-  if (f.slices == 1) return 0;
-  return (size_t)f.slices * Mx4Layout(N, K).blocks * (gated ? 2 : 1) * f.xt * 1024;
+  if (T == 0) return 0;
+  const int slices = T <= kFewTokens ? few_plan(T, K, N, gated).slices : tile_plan(T, K, N, gated).slices;
+  const int xt = T <= kFewTokens ? few_plan(T, K, N, gated).xt : (T + 15) / 16;
+  return slices == 1 ? 0 : (size_t)slices * Mx4Layout(N, K).blocks * (gated ? 2 : 1) * xt * 1024;
 }
 
 hipError_t launch_mx4_product(const Mx4Product &p, hipStream_t stream) {
