@@ -1,13 +1,14 @@
 // kernels_mx4_moe.hip -- a whole mixture-of-experts layer of a few tokens with
-// 4-bit experts, in three launches:
+// 4-bit experts, in three launches, four for more than four tokens:
 //
 //   logits   every expert's score of every token, summed in 64 bits
 //   gate/up  each workgroup picks every token's experts by itself (that is
-//            quicker than waiting for one to do it), then takes (expert, 16
-//            channels) pairs: h = p * SiLU(g) * u, p the routing weight
-//   down     a workgroup takes 16 outputs and every expert in use: with p inside h
-//            the layer's sum over experts is one product whose K runs through
-//            them all, a token's activations zero where it did not pick one
+//            quicker than waiting for one to do it), then its waves take (expert,
+//            up to 16 of its tokens, 16 channels): h = p * SiLU(g) * u, p the
+//            routing weight
+//   down     a workgroup takes 16 or 32 outputs and, in parts of K, the experts in
+//            use; with p inside h the sum over experts is a plain sum, kept in LDS
+//            by token (join: of several workgroups, for the same outputs)
 //
 // The weights of the experts in use are what bounds it.
 #include "dense.hpp"
@@ -19,65 +20,67 @@ namespace fp8moe {
 
 namespace {
 
-constexpr int kMaxRows = kMx4MaxTokens * kMaxK + kMx4MaxTokens * kMx4MaxShared;
-constexpr int kMaxUsed = kMaxExperts + kMx4MaxShared;
+constexpr int kWaves = 8;
+constexpr int kMaxRows = kMx4MaxTokens * (kMaxK + kMx4MaxShared);
+// entries of the list below: one to an expert in use, and one more for each 16 tokens
+// past the first 16
+constexpr int kMaxUsed = kMaxExperts + 2 * kMx4MaxShared + kMx4MaxTokens * kMaxK / 16;
 
-// An expert in use: the tokens that picked it (bit t), and the first of their
-// rows of h, which follow in token order.
+// Up to 16 tokens of an expert in use: their rows of h, which follow each other.
 struct Used {
-  int32_t expert;
-  uint32_t tokens;
-  int32_t row;
+  int32_t expert, row, count;
 };
 
 struct Space {
-  size_t logits, used, hi, lo, bytes;
-  Space(int32_t T, int32_t f, int32_t E, int32_t S, int32_t k_max) {
+  size_t logits, list, tokens, hi, lo, partial, bytes;
+  Space(int32_t T, int32_t d, int32_t f, int32_t E, int32_t S, int32_t k_max, int32_t slices) {
     auto round = [](size_t n) { return (n + 255) / 256 * 256; };
     const size_t rows = (size_t)T * (k_max + S);
     logits = 0;
-    used = logits + round((size_t)T * E * 4);
-    hi = used + round(16 + (size_t)(E + S) * sizeof(Used));
+    list = logits + round((size_t)T * E * 4);
+    tokens = list + round(16 + kMaxUsed * sizeof(Used));
+    hi = tokens + round(rows);
     lo = hi + round(rows * f * 2);
-    bytes = lo + round(rows * f * 2);
+    partial = lo + round(rows * f * 2);
+    bytes = partial + (slices > 1 ? round((size_t)slices * T * d * 4) : 0);
   }
 };
 
 // ---------------------------------------------------------------- logits
-// A workgroup takes an expert and eight tokens; its threads four inputs at a
-// time, summed in 64 bits, so that two experts' order hardly ever hangs on
-// rounding: logit = fl32(sum + bias).
-constexpr int kLogitTokens = 8, kLogitThreads = 256;
+// A workgroup takes an expert and four tokens; its threads four inputs at a time,
+// summed in 64 bits, so that two experts' order hardly ever hangs on rounding:
+// logit = fl32(sum + bias).
+constexpr int kLogitTokens = 4, kLogitThreads = 256;
 template <class E>
 __global__ __launch_bounds__(kLogitThreads) void mx4_logits_kernel(Mx4Moe p, float *logits) {
   __shared__ double part[kLogitTokens][kLogitThreads];
   typedef E Vec __attribute__((ext_vector_type(4)));
   const int e = blockIdx.x, t0 = blockIdx.y * kLogitTokens, tid = threadIdx.x;
-  const int n = p.T - t0 < kLogitTokens ? p.T - t0 : kLogitTokens;
   const float *w = p.w_router + (int64_t)e * p.d;
-  const E *x = static_cast<const E *>(p.x) + (int64_t)t0 * p.ldx;
+  const E *x[kLogitTokens];  // tokens behind the last repeat it
+#pragma unroll
+  for (int t = 0; t < kLogitTokens; ++t)
+    x[t] = static_cast<const E *>(p.x) + (int64_t)(t0 + t < p.T ? t0 + t : p.T - 1) * p.ldx;
   double acc[kLogitTokens] = {};
   for (int i = tid * 4; i < p.d; i += kLogitThreads * 4) {
     const v4f wv = *reinterpret_cast<const v4f *>(w + i);
+    Vec xv[kLogitTokens];
+#pragma unroll
+    for (int t = 0; t < kLogitTokens; ++t) xv[t] = *reinterpret_cast<const Vec *>(x[t] + i);
 #pragma unroll
     for (int t = 0; t < kLogitTokens; ++t)
-      if (t < n) {
-        const Vec xv = *reinterpret_cast<const Vec *>(x + t * p.ldx + i);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[t] = fma((double)wv[j], (double)(float)xv[j], acc[t]);
-      }
+      for (int j = 0; j < 4; ++j) acc[t] = fma((double)wv[j], (double)(float)xv[t][j], acc[t]);
   }
 #pragma unroll
   for (int t = 0; t < kLogitTokens; ++t) part[t][tid] = acc[t];
   __syncthreads();
-  // 32 threads add a token's sums
-  const int t = tid >> 5, i = tid & 31;
-  double v = 0.0;
+  // a wave adds a token's sums
+  const int t = tid >> 6, i = tid & 63;
+  double v = (part[t][i] + part[t][i + 64]) + (part[t][i + 128] + part[t][i + 192]);
 #pragma unroll
-  for (int j = 0; j < kLogitThreads / 32; ++j) v += part[t][i + 32 * j];
-#pragma unroll
-  for (int m = 16; m; m >>= 1) v += __shfl_xor(v, m);
-  if (i == 0 && t < n)
+  for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
+  if (i == 0 && t0 + t < p.T)
     logits[(int64_t)(t0 + t) * p.E + e] = (float)(v + (p.bias ? (double)p.bias[e] : 0.0));
 }
 
@@ -85,60 +88,61 @@ __global__ __launch_bounds__(kLogitThreads) void mx4_logits_kernel(Mx4Moe p, flo
 struct Routing {
   int32_t ids[kMx4MaxTokens * kMaxK];
   float weight[kMx4MaxTokens * kMaxK];
-  uint32_t tokens[kMaxExperts];  // by expert
-  int32_t place[kMaxExperts];    // in used, of those in use
+  uint32_t tokens[kMaxExperts];  // by expert: bit t for token t
+  int32_t row[kMaxExperts];      // by expert: its first row of h
   Used used[kMaxUsed];
   uint8_t row_token[kMaxRows];
   float row_weight[kMaxRows];
-  int32_t n_used;
+  int32_t n_used, n_rows;
 };
 
 __device__ __forceinline__ uint32_t below(int bit) { return (1u << bit) - 1; }
 
-// By the whole workgroup of `threads`, the same in each.
-__device__ __forceinline__ void route_tokens(const Mx4Moe &p, const float *logits, Routing &r, int threads) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = threads >> 6;
-  for (int e = tid; e < p.E; e += threads) r.tokens[e] = 0;
-  for (int t = wave; t < p.T; t += waves)
+// By the whole workgroup, the same in each.
+__device__ __forceinline__ void route_tokens(const Mx4Moe &p, const float *logits, Routing &r) {
+  constexpr int kThreads = kWaves * kWave;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int e = tid; e < p.E; e += kThreads) r.tokens[e] = 0;
+  for (int t = wave; t < p.T; t += kWaves)
     topk_token_wave(logits, p.T, p.E, p.k_max, p.kpt, r.ids, r.weight, t, lane);
   __syncthreads();
   const int pairs = p.T * p.k_max;
-  for (int i = tid; i < pairs; i += threads) {
-    const int e = r.ids[i];
-    // (an id past E - 1 only for logits that are no numbers)
-    if (e >= 0) atomicOr(&r.tokens[e < p.E ? e : p.E - 1], 1u << (i / p.k_max));
+  for (int i = tid; i < pairs; i += kThreads) {
+    // an id past E - 1: only for logits that are no numbers
+    const int e = r.ids[i] < p.E ? r.ids[i] : p.E - 1;
+    if (e >= 0) atomicOr(&r.tokens[e], 1u << (i / p.k_max));
   }
   __syncthreads();
   if (wave == 0) {
     int n = 0, rows = 0;
-    for (int e0 = 0; e0 < p.E; e0 += kWave) {
-      const uint32_t m = e0 + lane < p.E ? r.tokens[e0 + lane] : 0;
-      const uint64_t in = __ballot(m != 0);
-      const int count = __popc(m), upto = wave_incl_scan(count, lane);
-      if (m) {
-        const int at = n + __popcll(in & ((1ull << lane) - 1));
-        r.used[at] = Used{e0 + lane, m, rows + upto - count};
-        r.place[e0 + lane] = at;
-      }
-      n += __popcll(in);
+    const int all = p.E + p.S;  // the shared experts behind the others
+    for (int e0 = 0; e0 < all; e0 += kWave) {
+      const int e = e0 + lane;
+      const int count = e < p.E ? __popc(r.tokens[e]) : e < all ? p.T : 0;
+      const int entries = (count + 15) / 16;
+      const int upto = wave_incl_scan(count, lane), place = wave_incl_scan(entries, lane);
+      const int row = rows + upto - count;
+      for (int i = 0; i < entries; ++i)
+        r.used[n + place - entries + i] = Used{e, row + i * 16, count - i * 16 < 16 ? count - i * 16 : 16};
+      if (e < p.E) r.row[e] = row;
+      if (e >= p.E)
+        for (int t = 0; t < count; ++t) {
+          r.row_token[row + t] = (uint8_t)t;
+          r.row_weight[row + t] = 1.0f;
+        }
+      n += __builtin_amdgcn_readlane(place, 63);
       rows += __builtin_amdgcn_readlane(upto, 63);
     }
-    if (lane < p.S) r.used[n + lane] = Used{p.E + lane, p.T == 32 ? ~0u : below(p.T), rows + lane * p.T};
-    if (lane == 0) r.n_used = n + p.S;
-    // the shared experts' rows: weight 1
-    for (int i = lane; i < p.S * p.T; i += kWave) {
-      r.row_token[rows + i] = (uint8_t)(i % p.T);
-      r.row_weight[rows + i] = 1.0f;
+    if (lane == 0) {
+      r.n_used = n;
+      r.n_rows = rows;
     }
   }
   __syncthreads();
-  for (int i = tid; i < pairs; i += threads) {
-    int e = r.ids[i];
+  for (int i = tid; i < pairs; i += kThreads) {
+    const int e = r.ids[i] < p.E ? r.ids[i] : p.E - 1;
     if (e < 0) continue;
-    e = e < p.E ? e : p.E - 1;
-    const int t = i / p.k_max;
-    const Used u = r.used[r.place[e]];
-    const int row = u.row + __popc(u.tokens & below(t));
+    const int t = i / p.k_max, row = r.row[e] + __popc(r.tokens[e] & below(t));
     r.row_token[row] = (uint8_t)t;
     r.row_weight[row] = r.weight[i];
   }
@@ -151,78 +155,102 @@ __device__ __forceinline__ const uint8_t *expert_matrix(const uint8_t *routed, c
 }
 
 // ---------------------------------------------------------------- gate/up
-// Teams of kTeamWaves waves share a pair's K.
-constexpr int kTeamWaves = 4;
-template <class Op, int XT, int TEAMS, int D>
-__global__ __launch_bounds__(TEAMS *kTeamWaves *kWave) void mx4_gate_up_kernel(Mx4Moe p, const float *logits,
-                                                                            char *used_out, __bf16 *hi,
-                                                                            __bf16 *lo) {
-  constexpr int kThreads = TEAMS * kTeamWaves * kWave;
+// An item is 16 channels of an entry.  TW waves share its K (one, where there are
+// items enough for all waves: then nothing waits for another).  rows > 0: the
+// activations of all tokens are in LDS, `rows` (a power of two) to a tile, laid out as
+// the few-token products lay theirs; 0: a wave asks for them with its weights.
+constexpr int kMoeLds = 96 * 1024;
+
+template <class Op, int TW, bool LDS, int D>
+__global__ __launch_bounds__(kWaves *kWave) void mx4_gate_up_kernel(Mx4Moe p, const float *logits, char *list,
+                                                                    uint8_t *tokens, __bf16 *hi, __bf16 *lo,
+                                                                    int rows) {
+  constexpr int TEAMS = kWaves / TW;
   __shared__ Routing r;
-  __shared__ v4f part[TEAMS][kTeamWaves][2][XT][kWave];
-  route_tokens(p, logits, r, kThreads);
+  __shared__ v4f part[TW > 1 ? kWaves : 1][2][kWave];
+  extern __shared__ __attribute__((aligned(1024))) uint8_t moe_lds[];
   const int lane = threadIdx.x & 63, q = lane >> 4, c16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Mx4Layout l(p.f, p.d);
+  const LdsPtr xs = (LdsPtr)moe_lds;
+  if constexpr (LDS) {
+    // under way while the tokens are routed
+    const v4u rsrc = buffer_of(static_cast<const uint8_t *>(p.x), (int64_t)(p.T - 1) * p.ldx * 2 + p.d * 2);
+    const int shift = 31 - __builtin_clz(rows), pieces = (l.kt * rows + 3) / 4;
+    for (int i = wave; i < pieces; i += kWaves) {
+      const int at = i * 4 + q, t = at & (rows - 1), kt = at >> shift, byte = kt * 256 + (c16 ^ (t & 15)) * 16;
+      dma16(rsrc, t < p.T && byte < p.d * 2 ? (uint32_t)(t * p.ldx * 2 + byte) : kPastEnd,
+            lds_address(xs) + i * 1024);
+    }
+  }
+  route_tokens(p, logits, r);
+  if constexpr (LDS) {
+    wait_dma<0>();
+    barrier_reads();
+  }
   const int n_used = __builtin_amdgcn_readfirstlane(r.n_used);
   if (blockIdx.x == 0) {
-    int32_t *head = reinterpret_cast<int32_t *>(used_out);
-    if (threadIdx.x == 0) head[0] = n_used;
-    Used *list = reinterpret_cast<Used *>(used_out + 16);
-    for (int i = threadIdx.x; i < n_used; i += kThreads) list[i] = r.used[i];
+    constexpr int kThreads = kWaves * kWave;
+    if (threadIdx.x == 0) *reinterpret_cast<int32_t *>(list) = n_used;
+    Used *to = reinterpret_cast<Used *>(list + 16);
+    for (int i = threadIdx.x; i < n_used; i += kThreads) to[i] = r.used[i];
+    for (int i = threadIdx.x; i < r.n_rows; i += kThreads) tokens[i] = r.row_token[i];
     for (int i = threadIdx.x; i < p.T * p.k_max; i += kThreads) {
       if (p.ids_out) p.ids_out[i] = r.ids[i];
       if (p.w_out) p.w_out[i] = r.weight[i];
     }
   }
-  const int team = wave / kTeamWaves, tw = wave % kTeamWaves;
-  const Mx4Layout l(p.f, p.d);
+  const int team = wave / TW, tw = wave % TW;
   const int64_t bytes = l.block_bytes * l.blocks;
   const int per = p.f / 16, groups = p.d / kMxGroup;
-  const int items = n_used * per, stride = TEAMS * gridDim.x;
-  const int first = team * gridDim.x + blockIdx.x;
-  const int rounds = (items + stride - 1) / stride;  // the same for every team
-  const int tiles = (l.kt + kTeamWaves - 1) / kTeamWaves;  // of a wave, per pair
+  const int items = n_used * per, stride = TEAMS * gridDim.x, first = team * gridDim.x + blockIdx.x;
+  // the waves of a team, and where they wait for each other all teams, take as many rounds
+  const int rounds = TW > 1 ? (items + stride - 1) / stride : items > first ? (items - first + stride - 1) / stride : 0;
+  const int tiles = (l.kt + TW - 1) / TW;  // of a wave, per item
 
-  // the load cursor
-  int item = first, at = 0;
+  int item = first, at = 0;  // the load cursor
   const uint8_t *block[2] = {nullptr, nullptr};
-  const typename Op::E *row[XT];
-  bool there[XT] = {};
+  const typename Op::E *row = nullptr;
   auto enter = [&]() {
     if (item >= items) return;
     const int a = item / per, b = item - a * per;
     const int e = __builtin_amdgcn_readfirstlane(r.used[a].expert);
-    const int row0 = __builtin_amdgcn_readfirstlane(r.used[a].row);
-    const int count = __popc(__builtin_amdgcn_readfirstlane(r.used[a].tokens));
     block[0] = expert_matrix(p.w_gate, p.ws_gate, e, p.E, bytes) + b * l.block_bytes;
     block[1] = expert_matrix(p.w_up, p.ws_up, e, p.E, bytes) + b * l.block_bytes;
-#pragma unroll
-    for (int m = 0; m < XT; ++m) {
-      const int c = m * 16 + c16;
-      there[m] = c < count;
-      const int t = there[m] ? r.row_token[row0 + c] : 0;
-      row[m] = static_cast<const typename Op::E *>(p.x) + (int64_t)t * p.ldx + q * 8;
+    if constexpr (!LDS) {
+      const Used u = r.used[a];  // columns behind the last token repeat the first
+      const int t = r.row_token[u.row + (c16 < u.count ? c16 : 0)];
+      row = static_cast<const typename Op::E *>(p.x) + (int64_t)t * p.ldx + q * 8;
     }
   };
   enter();
-  v4f acc[2][XT];
-  auto clear = [&]() {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int m = 0; m < XT; ++m) acc[i][m] = v4f{0.f, 0.f, 0.f, 0.f};
+  v4f acc[2][1] = {};
+  Mx4Weights<Op, 2, D> weights;
+  typename Op::X x[LDS ? 1 : D][4];
+  int done = first, step = 0;  // the item that is multiplied, and its tiles so far
+  LdsPtr xrow = xs;
+  int xkey = 0;
+  auto begin = [&]() {
+    if constexpr (LDS) {
+      if (done >= items) return;
+      const Used u = r.used[done / per];
+      const int t = r.row_token[u.row + (c16 < u.count ? c16 : 0)];
+      xrow = xs + t * 256;
+      xkey = t & 15;
+    }
   };
-  clear();
-  Mx4Ring<Op, XT, 2, D> ring;
-  int done = first, step = 0;  // the pair that is multiplied, and its tiles so far
+  begin();
   run_ring<D>(
       rounds * tiles,
       [&](int c, int) {
-        const int kt = tw + at * kTeamWaves;
-        if (item < items && kt < l.kt) {
-          ring.load(c, block, l, kt, lane, [&](int j, int m) {
-            return kt * 4 + j < groups && there[m] ? load16(row[m] + kt * 128 + j * 32) : v4i{0, 0, 0, 0};
-          });
+        const int kt = tw + at * TW;
+        if (TW == 1 || (item < items && kt < l.kt)) {
+          if constexpr (!LDS) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              x[c][j] = kt * 4 + j < groups ? load16(row + kt * 128 + j * 32) : v4i{0, 0, 0, 0};
+          }
+          weights.load(c, block, l, kt, lane);
         }
         if (++at == tiles) {
           at = 0;
@@ -231,37 +259,44 @@ __global__ __launch_bounds__(TEAMS *kTeamWaves *kWave) void mx4_gate_up_kernel(M
         }
       },
       [&](int c, int) {
-        if (done < items && tw + step * kTeamWaves < l.kt) ring.multiply(c, acc);
+        const int kt = tw + step * TW;
+        if (TW == 1 || (done < items && kt < l.kt)) {
+          const LdsPtr from = xrow + kt * rows * 256;
+          weights.template multiply<1>(
+              c, [&](int j, int) { return LDS ? lds_read16(from + (((j * 4 + q) ^ xkey) * 16)) : x[LDS ? 0 : c][j]; },
+              acc);
+        }
         if (++step < tiles) return;
         step = 0;
+        v4f g = acc[0][0], u = acc[1][0];
+        acc[0][0] = acc[1][0] = v4f{0.f, 0.f, 0.f, 0.f};
+        if constexpr (TW > 1) {
+          part[wave][0][lane] = g;
+          part[wave][1][lane] = u;
+          barrier_reads();
+          g = part[team * TW][0][lane], u = part[team * TW][1][lane];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int m = 0; m < XT; ++m) part[team][tw][i][m][lane] = acc[i][m];
-        clear();
-        barrier_reads();
-        if (done < items && tw < XT) {
-          const int a = done / per, b = done - a * per, m = tw;
-          const Used u = r.used[a];
-          const int e = __builtin_amdgcn_readfirstlane(u.expert);
-          const int col = m * 16 + c16;
-          v4f g = part[team][0][0][m][lane], up = part[team][0][1][m][lane];
-#pragma unroll
-          for (int w = 1; w < kTeamWaves; ++w) {
-            g += part[team][w][0][m][lane];
-            up += part[team][w][1][m][lane];
+          for (int w = 1; w < TW; ++w) {
+            g += part[team * TW + w][0][lane];
+            u += part[team * TW + w][1][lane];
           }
-          if (col < __popc(u.tokens)) {
+          barrier_reads();  // the sums are read: they can be written again
+        }
+        if (done < items && tw == 0) {
+          const int a = done / per, b = done - a * per;
+          const Used us = r.used[a];
+          const int e = __builtin_amdgcn_readfirstlane(us.expert);
+          if (c16 < us.count) {
             const uint8_t *bg = expert_matrix(p.w_gate, p.ws_gate, e, p.E, bytes) + b * l.block_bytes;
             const uint8_t *bu = expert_matrix(p.w_up, p.ws_up, e, p.E, bytes) + b * l.block_bytes;
-            const float weight = r.row_weight[u.row + col];
-            const int64_t to = (int64_t)(u.row + col) * p.f + mx4_channel(b, q * 4);
+            const float weight = r.row_weight[us.row + c16];
+            const int64_t to = (int64_t)(us.row + c16) * p.f + mx4_channel(b, q * 4);
             typedef __bf16 v4b __attribute__((ext_vector_type(4)));
             v4b vh, vl;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float h = weight * silu_mul(g[i] * mx4_factor<Op>(bg, l, q * 4 + i),
-                                                up[i] * mx4_factor<Op>(bu, l, q * 4 + i));
+                                                u[i] * mx4_factor<Op>(bu, l, q * 4 + i));
               vh[i] = (__bf16)h;
               vl[i] = (__bf16)(h - (float)vh[i]);  // 16 bits of h's 24 in all
             }
@@ -269,121 +304,200 @@ __global__ __launch_bounds__(TEAMS *kTeamWaves *kWave) void mx4_gate_up_kernel(M
             *reinterpret_cast<v4b *>(lo + to) = vl;
           }
         }
-        barrier_reads();  // the sums are read: they can be written again
         done += stride;
+        begin();
       },
       [] {});
 }
 
 // ---------------------------------------------------------------- down
-template <class OUT, int XT, int W, int D>
-__global__ __launch_bounds__(W *kWave) void mx4_down_kernel(Mx4Moe p, const char *used_in, const __bf16 *hi,
-                                                            const __bf16 *lo) {
+// A workgroup takes NB blocks of outputs; its waves and those of the `slices`
+// workgroups with the same outputs take units in turn, a unit being a part of an
+// entry's K.  A wave adds a unit's sums to its own copy of the outputs in LDS, by
+// token; in the end the copies are added in wave order.
+template <class OUT, int NB, int D>
+__global__ __launch_bounds__(kWaves *kWave) void mx4_down_kernel(Mx4Moe p, const char *list_in,
+                                                                 const uint8_t *tokens, const __bf16 *hi,
+                                                                 const __bf16 *lo, int slices, float *partial) {
+  constexpr int kOut = NB * 16;  // outputs
   __shared__ Used used[kMaxUsed];
-  __shared__ v4f part[W][XT][kWave];
+  __shared__ uint8_t row_token[kMaxRows];
+  extern __shared__ __attribute__((aligned(16))) uint8_t down_lds[];
+  float *mine = reinterpret_cast<float *>(down_lds);  // [wave][token][kOut]
   const int lane = threadIdx.x & 63, q = lane >> 4, c16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n_used = *reinterpret_cast<const int32_t *>(used_in);
-  const Used *list = reinterpret_cast<const Used *>(used_in + 16);
-  for (int i = threadIdx.x; i < n_used; i += W * kWave) used[i] = list[i];
+  const int n_used = __builtin_amdgcn_readfirstlane(*reinterpret_cast<const int32_t *>(list_in));
+  const Used *list = reinterpret_cast<const Used *>(list_in + 16);
+  for (int i = threadIdx.x; i < n_used; i += kWaves * kWave) used[i] = list[i];
+  for (int i = threadIdx.x; i < p.T * (p.k_max + p.S); i += kWaves * kWave) row_token[i] = tokens[i];
+  for (int i = threadIdx.x; i < kWaves * p.T * kOut / 4; i += kWaves * kWave)
+    reinterpret_cast<v4f *>(mine)[i] = v4f{0.f, 0.f, 0.f, 0.f};
+  mine += wave * p.T * kOut;
   __syncthreads();
   const Mx4Layout l(p.d, p.f);
   const int64_t bytes = l.block_bytes * l.blocks;
-  const int b = blockIdx.x, groups = p.f / kMxGroup;
-  const int total = n_used * l.kt;
+  const int slice = blockIdx.x % slices, b0 = blockIdx.x / slices * NB, groups = p.f / kMxGroup;
+  // parts of an entry's K, at least two tiles each: two units and more to a wave
+  const int want = (2 * kWaves * slices + n_used - 1) / n_used, most = (l.kt + 1) / 2;
+  const int tiles = (l.kt + (want < most ? want : most) - 1) / (want < most ? want : most);
+  const int parts = (l.kt + tiles - 1) / tiles, units = n_used * parts;
+  const int first = slice * kWaves + wave, stride = slices * kWaves;
+  int total = 0;
+  for (int u = first; u < units; u += stride) total += u % parts == parts - 1 ? l.kt - (parts - 1) * tiles : tiles;
 
-  // the load cursor: expert a's tile kt
-  int a = wave / l.kt, kt = wave - a * l.kt;
-  int entered = -1;
-  const uint8_t *block[1] = {nullptr};
-  int64_t from[XT];
-  bool there[XT] = {};
-  v4f acc[1][XT];
+  struct Cursor {
+    int unit, kt, end;
+  };
+  auto set = [&](Cursor &c, int u) {
+    c.unit = u;
+    c.kt = u % parts * tiles;
+    c.end = c.kt + tiles < l.kt ? c.kt + tiles : l.kt;
+  };
+  Cursor in, out;
+  set(in, first);
+  set(out, first);
+  const uint8_t *block[NB];
+  int64_t from = 0;
+  auto enter = [&]() {
+    if (in.unit >= units) return;
+    const Used u = used[in.unit / parts];
+    const int e = __builtin_amdgcn_readfirstlane(u.expert);
 #pragma unroll
-  for (int m = 0; m < XT; ++m) acc[0][m] = v4f{0.f, 0.f, 0.f, 0.f};
-  Mx4Ring<Mx4Pair, XT, 1, D, true> ring;  // each expert has factors of its own
+    for (int r = 0; r < NB; ++r)
+      block[r] = expert_matrix(p.w_down, p.ws_down, e, p.E, bytes) + (b0 + r) * l.block_bytes;
+    // columns behind the last token repeat the first
+    from = (int64_t)(u.row + (c16 < u.count ? c16 : 0)) * p.f + q * 8;
+  };
+  enter();
+  v4f acc[NB][1] = {};
+  Mx4Ring<Mx4Pair, 1, NB, D, true> ring;  // each expert has factors of its own
   run_ring<D>(
-      total > wave ? (total - wave + W - 1) / W : 0,
+      total,
       [&](int c, int) {
-        if (a != entered) {
-          entered = a;
-          const int e = __builtin_amdgcn_readfirstlane(used[a].expert);
-          const uint32_t tokens = __builtin_amdgcn_readfirstlane(used[a].tokens);
-          const int row0 = __builtin_amdgcn_readfirstlane(used[a].row);
-          block[0] = expert_matrix(p.w_down, p.ws_down, e, p.E, bytes) + b * l.block_bytes;
-#pragma unroll
-          for (int m = 0; m < XT; ++m) {
-            const int t = m * 16 + c16;
-            there[m] = (tokens >> t) & 1u;
-            from[m] = (int64_t)(row0 + __popc(tokens & below(t))) * p.f + q * 8;
-          }
-        }
-        ring.load(c, block, l, kt, lane, [&](int j, int m) {
+        const int kt = in.kt;
+        ring.load(c, block, l, kt, lane, [&](int j, int) {
           Mx4Pair::X x{{0, 0, 0, 0}, {0, 0, 0, 0}};
-          if (kt * 4 + j < groups && there[m]) {
-            x.hi = load16(hi + from[m] + kt * 128 + j * 32);
-            x.lo = load16(lo + from[m] + kt * 128 + j * 32);
+          if (kt * 4 + j < groups) {
+            x.hi = load16(hi + from + kt * 128 + j * 32);
+            x.lo = load16(lo + from + kt * 128 + j * 32);
           }
           return x;
         });
-        for (kt += W; kt >= l.kt; kt -= l.kt) ++a;
+        if (++in.kt == in.end) {
+          set(in, in.unit + stride);
+          enter();
+        }
       },
-      [&](int c, int) { ring.multiply(c, acc); }, [] {});
+      [&](int c, int) {
+        ring.multiply(c, acc);
+        if (++out.kt < out.end) return;
+        const Used u = used[out.unit / parts];
+        if (c16 < u.count) {
+          v4f *to = reinterpret_cast<v4f *>(mine + row_token[u.row + c16] * kOut + q * 4);
 #pragma unroll
-  for (int m = 0; m < XT; ++m) part[wave][m][lane] = acc[0][m];
+          for (int r = 0; r < NB; ++r) to[r * 4] += acc[r][0];
+        }
+#pragma unroll
+        for (int r = 0; r < NB; ++r) acc[r][0] = v4f{0.f, 0.f, 0.f, 0.f};
+        set(out, out.unit + stride);
+      },
+      [] {});
   __syncthreads();
-  if (wave < XT) {
-    const int m = wave, t = m * 16 + c16, ch = mx4_channel(b, q * 4);
-    v4f v = part[0][m][lane];
+  // four outputs of a token to a thread
+  mine = reinterpret_cast<float *>(down_lds);
+  for (int i = threadIdx.x; i < p.T * kOut / 4; i += kWaves * kWave) {
+    v4f v = reinterpret_cast<const v4f *>(mine)[i];
 #pragma unroll
-    for (int w = 1; w < W; ++w) v += part[w][m][lane];
-    const float o[4] = {v.x, v.y, v.z, v.w};
-    if (t < p.T) store_run<OUT, 4>(static_cast<OUT *>(p.out) + (int64_t)t * p.d + ch, o, 4);
+    for (int w = 1; w < kWaves; ++w) v += reinterpret_cast<const v4f *>(mine)[w * p.T * kOut / 4 + i];
+    const int t = i / (kOut / 4), o = i % (kOut / 4), ch = mx4_channel(b0 + o / 4, o % 4 * 4);
+    const float f[4] = {v.x, v.y, v.z, v.w};
+    if (slices > 1)
+      store_run<float, 4>(partial + ((int64_t)slice * p.T + t) * p.d + ch, f, 4);
+    else
+      store_run<OUT, 4>(static_cast<OUT *>(p.out) + (int64_t)t * p.d + ch, f, 4);
   }
+}
+
+// The slices' sums, in order.
+template <class OUT>
+__global__ __launch_bounds__(256) void mx4_moe_join_kernel(Mx4Moe p, int slices, const float *partial) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, n = (int64_t)p.T * p.d;
+  if (i >= n) return;
+  v4f v = *reinterpret_cast<const v4f *>(partial + i);
+  for (int s = 1; s < slices; ++s) v += *reinterpret_cast<const v4f *>(partial + s * n + i);
+  const float f[4] = {v.x, v.y, v.z, v.w};
+  store_run<OUT, 4>(static_cast<OUT *>(p.out) + i, f, 4);
+}
+
+// ---------------------------------------------------------------- launch
+constexpr int kCus = 256;
+
+// Up to four tokens h is little and a fourth launch (2 us) not worth it: 16 outputs to
+// a workgroup.  Above, what every workgroup reads of h costs as much as its
+// weights: 32 outputs, and as many slices as fill the compute units twice.
+struct DownPlan {
+  int nb, slices;
+};
+DownPlan down_plan(int32_t T, int32_t d) {
+  if (T <= 4) return {1, 1};
+  const int groups = d / 32, slices = (2 * kCus + groups - 1) / groups;
+  return {2, slices < 8 ? slices : 8};
+}
+
+template <class Op, int TW>
+void launch_gate_up(const Mx4Moe &p, const float *scores, char *list, uint8_t *tokens, __bf16 *hi, __bf16 *lo,
+                    int grid, hipStream_t stream) {
+  int rows = 1;
+  while (rows < p.T) rows *= 2;
+  const size_t lds = ((size_t)(p.d + 127) / 128 * rows * 256 + 1023) / 1024 * 1024;
+  if (lds <= kMoeLds)
+    mx4_gate_up_kernel<Op, TW, true, 4><<<grid, kWaves * kWave, lds, stream>>>(p, scores, list, tokens, hi, lo, rows);
+  else
+    mx4_gate_up_kernel<Op, TW, false, 3><<<grid, kWaves * kWave, 0, stream>>>(p, scores, list, tokens, hi, lo, 0);
+}
+
+template <class Op>
+hipError_t launch_layer(const Mx4Moe &p, hipStream_t stream) {
+  typedef typename Op::E E;
+  const DownPlan down = down_plan(p.T, p.d);
+  const Space at(p.T, p.d, p.f, p.E, p.S, p.k_max, down.slices);
+  float *logits = reinterpret_cast<float *>(p.workspace + at.logits);
+  char *list = p.workspace + at.list;
+  uint8_t *tokens = reinterpret_cast<uint8_t *>(p.workspace + at.tokens);
+  __bf16 *hi = reinterpret_cast<__bf16 *>(p.workspace + at.hi), *lo = reinterpret_cast<__bf16 *>(p.workspace + at.lo);
+  float *partial = reinterpret_cast<float *>(p.workspace + at.partial);
+  hipError_t e;
+  if (!p.logits_override) {
+    const dim3 grid(p.E, (p.T + kLogitTokens - 1) / kLogitTokens);
+    mx4_logits_kernel<E><<<grid, kLogitThreads, 0, stream>>>(p, logits);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  const float *scores = p.logits_override ? p.logits_override : logits;
+  const int experts = (p.T * p.k_max < p.E ? p.T * p.k_max : p.E) + p.S;
+  const int most = experts * (p.f / 16);  // items, at least that many where picks spread
+  if (most >= 2048)
+    launch_gate_up<Op, 1>(p, scores, list, tokens, hi, lo, 2 * kCus, stream);
+  else
+    launch_gate_up<Op, 4>(p, scores, list, tokens, hi, lo, most < 2 * kCus ? most : 2 * kCus, stream);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const size_t lds = (size_t)kWaves * p.T * down.nb * 16 * 4;
+  const int grid = p.d / (16 * down.nb) * down.slices;
+  if (down.nb == 1)
+    mx4_down_kernel<E, 1, 4><<<grid, kWaves * kWave, lds, stream>>>(p, list, tokens, hi, lo, down.slices, partial);
+  else
+    mx4_down_kernel<E, 2, 3><<<grid, kWaves * kWave, lds, stream>>>(p, list, tokens, hi, lo, down.slices, partial);
+  if ((e = hipGetLastError()) != hipSuccess || down.slices == 1) return e;
+  mx4_moe_join_kernel<E><<<(p.T * p.d / 4 + 255) / 256, 256, 0, stream>>>(p, down.slices, partial);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 FP8MOE_DEBUG_TAKE(mx4)
 
-size_t mx4_moe_workspace(int32_t T, int32_t f, int32_t E, int32_t S, int32_t k_max) {
-  return Space(T, f, E, S, k_max).bytes;
+size_t mx4_moe_workspace(int32_t T, int32_t d, int32_t f, int32_t E, int32_t S, int32_t k_max) {
+  return Space(T, d, f, E, S, k_max, down_plan(T, d).slices).bytes;
 }
-
-namespace {
-
-constexpr int kCus = 256;
-
-template <class Op>
-hipError_t launch_layer(const Mx4Moe &p, hipStream_t stream) {
-  typedef typename Op::E E;
-  const Space at(p.T, p.f, p.E, p.S, p.k_max);
-  float *logits = reinterpret_cast<float *>(p.workspace + at.logits);
-  char *used = p.workspace + at.used;
-  __bf16 *hi = reinterpret_cast<__bf16 *>(p.workspace + at.hi), *lo = reinterpret_cast<__bf16 *>(p.workspace + at.lo);
-  if (!p.logits_override) {
-    const dim3 grid(p.E, (p.T + kLogitTokens - 1) / kLogitTokens);
-    mx4_logits_kernel<E><<<grid, kLogitThreads, 0, stream>>>(p, logits);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  const float *scores = p.logits_override ? p.logits_override : logits;
-  const int experts = (p.T * p.k_max < p.E ? p.T * p.k_max : p.E) + p.S;
-  const int most = experts * (p.f / 16), grid = most < kCus ? most : kCus;
-  if (p.T <= 16)
-    mx4_gate_up_kernel<Op, 1, 4, 3><<<grid, 4 * kTeamWaves * kWave, 0, stream>>>(p, scores, used, hi, lo);
-  else
-    mx4_gate_up_kernel<Op, 2, 2, 3><<<grid, 2 * kTeamWaves * kWave, 0, stream>>>(p, scores, used, hi, lo);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if (p.T <= 16)
-    mx4_down_kernel<E, 1, 16, 2><<<p.d / 16, 16 * kWave, 0, stream>>>(p, used, hi, lo);
-  else
-    mx4_down_kernel<E, 2, 8, 2><<<p.d / 16, 8 * kWave, 0, stream>>>(p, used, hi, lo);
-  return hipGetLastError();
-}
-
-}  // namespace
 
 hipError_t launch_mx4_moe(const Mx4Moe &p, hipStream_t stream) {
   return p.type == kTypeBf16 ? launch_layer<Mx4Bf16>(p, stream) : launch_layer<Mx4F16>(p, stream);

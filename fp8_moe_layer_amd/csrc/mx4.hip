@@ -202,7 +202,7 @@ moe_status moe_ffn_mx4(const void *x, int64_t ldx, const void *w_gate, const voi
 size_t moe_mx4_workspace_bytes(const moe_dims *dims) {
   if (check_layer("moe_mx4_workspace_bytes", dims)) return 0;
   (void)ok_status();
-  return mx4_moe_workspace(dims->T, dims->f, dims->E, dims->n_shared, dims->k_max);
+  return mx4_moe_workspace(dims->T, dims->d, dims->f, dims->E, dims->n_shared, dims->k_max);
 }
 
 moe_status moe_mx4_forward(const moe_dims *dims, int32_t type, const void *x, int64_t ldx,
@@ -224,7 +224,7 @@ moe_status moe_mx4_forward(const moe_dims *dims, int32_t type, const void *x, in
       !all_aligned({router_bias, k_per_token, logits_override, topk_ids_out, topk_w_out}, 4))
     return fail_status(MOE_ERR_ALIGN, "%s: x, out, w_router and the matrices must be 16-byte, the other "
                        "arrays 4-byte aligned", fn);
-  const size_t need = mx4_moe_workspace(m.T, m.f, m.E, m.n_shared, m.k_max);
+  const size_t need = mx4_moe_workspace(m.T, m.d, m.f, m.E, m.n_shared, m.k_max);
   if (!workspace || workspace_bytes < need)
     return fail_status(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn,
                        workspace ? workspace_bytes : (size_t)0, need);
