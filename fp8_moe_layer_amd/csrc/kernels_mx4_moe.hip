@@ -1,14 +1,15 @@
 // kernels_mx4_moe.hip -- a whole mixture-of-experts layer of a few tokens with
-// 4-bit experts, in three launches, four for more than four tokens:
+// 4-bit experts, in three to five launches:
 //
 //   logits   every expert's score of every token, summed in 64 bits
-//   gate/up  each workgroup picks every token's experts by itself (that is
-//            quicker than waiting for one to do it), then its waves take (expert,
-//            up to 16 of its tokens, 16 channels): h = p * SiLU(g) * u, p the
-//            routing weight
-//   down     a workgroup takes 16 or 32 outputs and, in parts of K, the experts in
+//   plan     every token's experts, and the list of experts in use with their
+//            tokens (up to four tokens: by each gate/up workgroup for itself)
+//   gate/up  waves take (expert, up to 16 of its tokens, 16 channels):
+//            h = p * SiLU(g) * u, p the routing weight
+//   down     a workgroup takes 16 or 64 outputs and, in parts of K, the experts in
 //            use; with p inside h the sum over experts is a plain sum, kept in LDS
-//            by token (join: of several workgroups, for the same outputs)
+//            by token
+//   join     of the workgroups with the same outputs, where there are several
 //
 // The weights of the experts in use are what bounds it.
 #include "dense.hpp"
@@ -29,21 +30,6 @@ constexpr int kMaxUsed = kMaxExperts + 2 * kMx4MaxShared + kMx4MaxTokens * kMaxK
 // Up to 16 tokens of an expert in use: their rows of h, which follow each other.
 struct Used {
   int32_t expert, row, count;
-};
-
-struct Space {
-  size_t logits, list, tokens, hi, lo, partial, bytes;
-  Space(int32_t T, int32_t d, int32_t f, int32_t E, int32_t S, int32_t k_max, int32_t slices) {
-    auto round = [](size_t n) { return (n + 255) / 256 * 256; };
-    const size_t rows = (size_t)T * (k_max + S);
-    logits = 0;
-    list = logits + round((size_t)T * E * 4);
-    tokens = list + round(16 + kMaxUsed * sizeof(Used));
-    hi = tokens + round(rows);
-    lo = hi + round(rows * f * 2);
-    partial = lo + round(rows * f * 2);
-    bytes = partial + (slices > 1 ? round((size_t)slices * T * d * 4) : 0);
-  }
 };
 
 // ---------------------------------------------------------------- logits
@@ -85,25 +71,30 @@ __global__ __launch_bounds__(kLogitThreads) void mx4_logits_kernel(Mx4Moe p, flo
 }
 
 // ---------------------------------------------------------------- routing
+// What the experts in use are given: in LDS, and in the workspace for the launches
+// behind the one that made it.
+struct Plan {
+  int32_t n_used, n_rows, unused[2];
+  Used used[kMaxUsed];
+  uint8_t row_token[kMaxRows];  // by row of h
+  float row_weight[kMaxRows];
+};
 struct Routing {
   int32_t ids[kMx4MaxTokens * kMaxK];
   float weight[kMx4MaxTokens * kMaxK];
   uint32_t tokens[kMaxExperts];  // by expert: bit t for token t
   int32_t row[kMaxExperts];      // by expert: its first row of h
-  Used used[kMaxUsed];
-  uint8_t row_token[kMaxRows];
-  float row_weight[kMaxRows];
-  int32_t n_used, n_rows;
 };
 
 __device__ __forceinline__ uint32_t below(int bit) { return (1u << bit) - 1; }
 
-// By the whole workgroup, the same in each.
-__device__ __forceinline__ void route_tokens(const Mx4Moe &p, const float *logits, Routing &r) {
-  constexpr int kThreads = kWaves * kWave;
+// By the whole workgroup of W waves.
+template <int W>
+__device__ __forceinline__ void route_tokens(const Mx4Moe &p, const float *logits, Routing &r, Plan &plan) {
+  constexpr int kThreads = W * kWave;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int e = tid; e < p.E; e += kThreads) r.tokens[e] = 0;
-  for (int t = wave; t < p.T; t += kWaves)
+  for (int t = wave; t < p.T; t += W)
     topk_token_wave(logits, p.T, p.E, p.k_max, p.kpt, r.ids, r.weight, t, lane);
   __syncthreads();
   const int pairs = p.T * p.k_max;
@@ -123,19 +114,19 @@ __device__ __forceinline__ void route_tokens(const Mx4Moe &p, const float *logit
       const int upto = wave_incl_scan(count, lane), place = wave_incl_scan(entries, lane);
       const int row = rows + upto - count;
       for (int i = 0; i < entries; ++i)
-        r.used[n + place - entries + i] = Used{e, row + i * 16, count - i * 16 < 16 ? count - i * 16 : 16};
+        plan.used[n + place - entries + i] = Used{e, row + i * 16, count - i * 16 < 16 ? count - i * 16 : 16};
       if (e < p.E) r.row[e] = row;
       if (e >= p.E)
         for (int t = 0; t < count; ++t) {
-          r.row_token[row + t] = (uint8_t)t;
-          r.row_weight[row + t] = 1.0f;
+          plan.row_token[row + t] = (uint8_t)t;
+          plan.row_weight[row + t] = 1.0f;
         }
       n += __builtin_amdgcn_readlane(place, 63);
       rows += __builtin_amdgcn_readlane(upto, 63);
     }
     if (lane == 0) {
-      r.n_used = n;
-      r.n_rows = rows;
+      plan.n_used = n;
+      plan.n_rows = rows;
     }
   }
   __syncthreads();
@@ -143,9 +134,50 @@ __device__ __forceinline__ void route_tokens(const Mx4Moe &p, const float *logit
     const int e = r.ids[i] < p.E ? r.ids[i] : p.E - 1;
     if (e < 0) continue;
     const int t = i / p.k_max, row = r.row[e] + __popc(r.tokens[e] & below(t));
-    r.row_token[row] = (uint8_t)t;
-    r.row_weight[row] = r.weight[i];
+    plan.row_token[row] = (uint8_t)t;
+    plan.row_weight[row] = r.weight[i];
   }
+  __syncthreads();
+}
+
+// The plan, and the picks where the caller wants them, to memory.
+template <int W>
+__device__ __forceinline__ void publish(const Mx4Moe &p, const Routing &r, const Plan &plan, Plan *to) {
+  for (int i = threadIdx.x; i < plan.n_used; i += W * kWave) to->used[i] = plan.used[i];
+  for (int i = threadIdx.x; i < plan.n_rows; i += W * kWave) {
+    to->row_token[i] = plan.row_token[i];
+    to->row_weight[i] = plan.row_weight[i];
+  }
+  if (threadIdx.x == 0) {
+    to->n_used = plan.n_used;
+    to->n_rows = plan.n_rows;
+  }
+  for (int i = threadIdx.x; i < p.T * p.k_max; i += W * kWave) {
+    if (p.ids_out) p.ids_out[i] = r.ids[i];
+    if (p.w_out) p.w_out[i] = r.weight[i];
+  }
+}
+
+constexpr int kPlanWaves = 16;
+__global__ __launch_bounds__(kPlanWaves *kWave) void mx4_plan_kernel(Mx4Moe p, const float *logits, Plan *to) {
+  __shared__ Routing r;
+  __shared__ Plan plan;
+  route_tokens<kPlanWaves>(p, logits, r, plan);
+  publish<kPlanWaves>(p, r, plan, to);
+}
+
+// A plan from memory, by W waves, and a barrier.  What the sizes allow at most is read
+// at once, without waiting for how much there is.
+template <int W>
+__device__ __forceinline__ void read_plan(const Mx4Moe &p, const Plan *from, Plan &plan, bool weights) {
+  const int rows = p.T * (p.k_max + p.S), pairs = p.T * p.k_max;
+  const int used = (pairs < p.E ? pairs : p.E) + pairs / 16 + 2 * p.S;
+  for (int i = threadIdx.x; i < used; i += W * kWave) plan.used[i] = from->used[i];
+  for (int i = threadIdx.x; i < rows; i += W * kWave) {
+    plan.row_token[i] = from->row_token[i];
+    if (weights) plan.row_weight[i] = from->row_weight[i];
+  }
+  if (threadIdx.x == 0) plan.n_used = from->n_used;
   __syncthreads();
 }
 
@@ -161,12 +193,12 @@ __device__ __forceinline__ const uint8_t *expert_matrix(const uint8_t *routed, c
 // the few-token products lay theirs; 0: a wave asks for them with its weights.
 constexpr int kMoeLds = 96 * 1024;
 
-template <class Op, int TW, bool LDS, int D>
-__global__ __launch_bounds__(kWaves *kWave) void mx4_gate_up_kernel(Mx4Moe p, const float *logits, char *list,
-                                                                    uint8_t *tokens, __bf16 *hi, __bf16 *lo,
-                                                                    int rows) {
+// logits: the tokens are routed here (ROUTE); else their plan is in memory.
+template <class Op, int TW, bool LDS, bool ROUTE, int D>
+__global__ __launch_bounds__(kWaves *kWave) void mx4_gate_up_kernel(Mx4Moe p, const float *logits, Plan *to_plan,
+                                                                    __bf16 *hi, __bf16 *lo, int rows) {
   constexpr int TEAMS = kWaves / TW;
-  __shared__ Routing r;
+  __shared__ Plan r;
   __shared__ v4f part[TW > 1 ? kWaves : 1][2][kWave];
   extern __shared__ __attribute__((aligned(1024))) uint8_t moe_lds[];
   const int lane = threadIdx.x & 63, q = lane >> 4, c16 = lane & 15;
@@ -174,7 +206,7 @@ __global__ __launch_bounds__(kWaves *kWave) void mx4_gate_up_kernel(Mx4Moe p, co
   const Mx4Layout l(p.f, p.d);
   const LdsPtr xs = (LdsPtr)moe_lds;
   if constexpr (LDS) {
-    // under way while the tokens are routed
+    // under way while the plan is made or read
     const v4u rsrc = buffer_of(static_cast<const uint8_t *>(p.x), (int64_t)(p.T - 1) * p.ldx * 2 + p.d * 2);
     const int shift = 31 - __builtin_clz(rows), pieces = (l.kt * rows + 3) / 4;
     for (int i = wave; i < pieces; i += kWaves) {
@@ -183,23 +215,18 @@ __global__ __launch_bounds__(kWaves *kWave) void mx4_gate_up_kernel(Mx4Moe p, co
             lds_address(xs) + i * 1024);
     }
   }
-  route_tokens(p, logits, r);
+  if constexpr (ROUTE) {
+    __shared__ Routing routing;
+    route_tokens<kWaves>(p, logits, routing, r);
+    if (blockIdx.x == 0) publish<kWaves>(p, routing, r, to_plan);
+  } else {
+    read_plan<kWaves>(p, to_plan, r, true);
+  }
   if constexpr (LDS) {
     wait_dma<0>();
     barrier_reads();
   }
   const int n_used = __builtin_amdgcn_readfirstlane(r.n_used);
-  if (blockIdx.x == 0) {
-    constexpr int kThreads = kWaves * kWave;
-    if (threadIdx.x == 0) *reinterpret_cast<int32_t *>(list) = n_used;
-    Used *to = reinterpret_cast<Used *>(list + 16);
-    for (int i = threadIdx.x; i < n_used; i += kThreads) to[i] = r.used[i];
-    for (int i = threadIdx.x; i < r.n_rows; i += kThreads) tokens[i] = r.row_token[i];
-    for (int i = threadIdx.x; i < p.T * p.k_max; i += kThreads) {
-      if (p.ids_out) p.ids_out[i] = r.ids[i];
-      if (p.w_out) p.w_out[i] = r.weight[i];
-    }
-  }
   const int team = wave / TW, tw = wave % TW;
   const int64_t bytes = l.block_bytes * l.blocks;
   const int per = p.f / 16, groups = p.d / kMxGroup;
@@ -311,37 +338,33 @@ __global__ __launch_bounds__(kWaves *kWave) void mx4_gate_up_kernel(Mx4Moe p, co
 }
 
 // ---------------------------------------------------------------- down
-// A workgroup takes NB blocks of outputs; its waves and those of the `slices`
+// A workgroup takes NB blocks of outputs; its W waves and those of the `slices`
 // workgroups with the same outputs take units in turn, a unit being a part of an
 // entry's K.  A wave adds a unit's sums to its own copy of the outputs in LDS, by
 // token; in the end the copies are added in wave order.
-template <class OUT, int NB, int D>
-__global__ __launch_bounds__(kWaves *kWave) void mx4_down_kernel(Mx4Moe p, const char *list_in,
-                                                                 const uint8_t *tokens, const __bf16 *hi,
-                                                                 const __bf16 *lo, int slices, float *partial) {
+template <class OUT, int NB, int W, int D>
+__global__ __launch_bounds__(W *kWave) void mx4_down_kernel(Mx4Moe p, const Plan *from_plan,
+                                                                 const __bf16 *hi, const __bf16 *lo, int slices,
+                                                                 float *partial) {
   constexpr int kOut = NB * 16;  // outputs
-  __shared__ Used used[kMaxUsed];
-  __shared__ uint8_t row_token[kMaxRows];
+  __shared__ Plan plan;
   extern __shared__ __attribute__((aligned(16))) uint8_t down_lds[];
   float *mine = reinterpret_cast<float *>(down_lds);  // [wave][token][kOut]
   const int lane = threadIdx.x & 63, q = lane >> 4, c16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n_used = __builtin_amdgcn_readfirstlane(*reinterpret_cast<const int32_t *>(list_in));
-  const Used *list = reinterpret_cast<const Used *>(list_in + 16);
-  for (int i = threadIdx.x; i < n_used; i += kWaves * kWave) used[i] = list[i];
-  for (int i = threadIdx.x; i < p.T * (p.k_max + p.S); i += kWaves * kWave) row_token[i] = tokens[i];
-  for (int i = threadIdx.x; i < kWaves * p.T * kOut / 4; i += kWaves * kWave)
+  for (int i = threadIdx.x; i < W * p.T * kOut / 4; i += W * kWave)
     reinterpret_cast<v4f *>(mine)[i] = v4f{0.f, 0.f, 0.f, 0.f};
   mine += wave * p.T * kOut;
-  __syncthreads();
+  read_plan<W>(p, from_plan, plan, false);
+  const int n_used = __builtin_amdgcn_readfirstlane(plan.n_used);
   const Mx4Layout l(p.d, p.f);
   const int64_t bytes = l.block_bytes * l.blocks;
   const int slice = blockIdx.x % slices, b0 = blockIdx.x / slices * NB, groups = p.f / kMxGroup;
   // parts of an entry's K, at least two tiles each: two units and more to a wave
-  const int want = (2 * kWaves * slices + n_used - 1) / n_used, most = (l.kt + 1) / 2;
+  const int want = (2 * W * slices + n_used - 1) / n_used, most = (l.kt + 1) / 2;
   const int tiles = (l.kt + (want < most ? want : most) - 1) / (want < most ? want : most);
   const int parts = (l.kt + tiles - 1) / tiles, units = n_used * parts;
-  const int first = slice * kWaves + wave, stride = slices * kWaves;
+  const int first = slice * W + wave, stride = slices * W;
   int total = 0;
   for (int u = first; u < units; u += stride) total += u % parts == parts - 1 ? l.kt - (parts - 1) * tiles : tiles;
 
@@ -360,11 +383,13 @@ __global__ __launch_bounds__(kWaves *kWave) void mx4_down_kernel(Mx4Moe p, const
   int64_t from = 0;
   auto enter = [&]() {
     if (in.unit >= units) return;
-    const Used u = used[in.unit / parts];
+    const Used u = plan.used[in.unit / parts];
     const int e = __builtin_amdgcn_readfirstlane(u.expert);
 #pragma unroll
     for (int r = 0; r < NB; ++r)
-      block[r] = expert_matrix(p.w_down, p.ws_down, e, p.E, bytes) + (b0 + r) * l.block_bytes;
+      // (a block behind the last is read again, and not stored)
+      block[r] = expert_matrix(p.w_down, p.ws_down, e, p.E, bytes) +
+                 (b0 + r < l.blocks ? b0 + r : l.blocks - 1) * l.block_bytes;
     // columns behind the last token repeat the first
     from = (int64_t)(u.row + (c16 < u.count ? c16 : 0)) * p.f + q * 8;
   };
@@ -391,9 +416,9 @@ __global__ __launch_bounds__(kWaves *kWave) void mx4_down_kernel(Mx4Moe p, const
       [&](int c, int) {
         ring.multiply(c, acc);
         if (++out.kt < out.end) return;
-        const Used u = used[out.unit / parts];
+        const Used u = plan.used[out.unit / parts];
         if (c16 < u.count) {
-          v4f *to = reinterpret_cast<v4f *>(mine + row_token[u.row + c16] * kOut + q * 4);
+          v4f *to = reinterpret_cast<v4f *>(mine + plan.row_token[u.row + c16] * kOut + q * 4);
 #pragma unroll
           for (int r = 0; r < NB; ++r) to[r * 4] += acc[r][0];
         }
@@ -405,12 +430,13 @@ __global__ __launch_bounds__(kWaves *kWave) void mx4_down_kernel(Mx4Moe p, const
   __syncthreads();
   // four outputs of a token to a thread
   mine = reinterpret_cast<float *>(down_lds);
-  for (int i = threadIdx.x; i < p.T * kOut / 4; i += kWaves * kWave) {
+  for (int i = threadIdx.x; i < p.T * kOut / 4; i += W * kWave) {
     v4f v = reinterpret_cast<const v4f *>(mine)[i];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) v += reinterpret_cast<const v4f *>(mine)[w * p.T * kOut / 4 + i];
+    for (int w = 1; w < W; ++w) v += reinterpret_cast<const v4f *>(mine)[w * p.T * kOut / 4 + i];
     const int t = i / (kOut / 4), o = i % (kOut / 4), ch = mx4_channel(b0 + o / 4, o % 4 * 4);
     const float f[4] = {v.x, v.y, v.z, v.w};
+    if (ch >= p.d) continue;
     if (slices > 1)
       store_run<float, 4>(partial + ((int64_t)slice * p.T + t) * p.d + ch, f, 4);
     else
@@ -432,38 +458,63 @@ __global__ __launch_bounds__(256) void mx4_moe_join_kernel(Mx4Moe p, int slices,
 // ---------------------------------------------------------------- launch
 constexpr int kCus = 256;
 
-// Up to four tokens h is little and a fourth launch (2 us) not worth it: 16 outputs to
-// a workgroup.  Above, what every workgroup reads of h costs as much as its
-// weights: 32 outputs, and as many slices as fill the compute units twice.
+// The workspace.
+struct Space {
+  size_t logits, plan, hi, lo, partial, bytes;
+  Space(const Mx4Moe &p, int slices) {
+    auto round = [](size_t n) { return (n + 255) / 256 * 256; };
+    const size_t rows = (size_t)p.T * (p.k_max + p.S);
+    logits = 0;
+    plan = logits + round((size_t)p.T * p.E * 4);
+    hi = plan + round(sizeof(Plan));
+    lo = hi + round(rows * p.f * 2);
+    partial = lo + round(rows * p.f * 2);
+    bytes = partial + (slices > 1 ? round((size_t)slices * p.T * p.d * 4) : 0);
+  }
+};
+
+// Up to here every gate/up workgroup routes for itself (one token 1 us); above, that
+// takes longer (13 tokens 8 us, 32 tokens 12) than a launch for it.
+constexpr int kRouteTokens = 4;
+// Gate/up items from which on a wave takes one alone: below, four waves share it
+// (one token of the 128-expert layer, 384 items: 6.1 us with four, 7.5 with one; of the
+// 8-expert one, 1792: 22.3 and 20.9).
+constexpr int kWaveItems = 1024;
+
+// What a wave reads of h for a tile is 8 KB whatever the entry's tokens, for 1 KB of
+// weights to a block: 64 outputs to a workgroup, in as many slices as fill the compute
+// units (twice as many: 13 tokens of the 64-expert layer 24 -> 30 us; 32 outputs 26),
+// and a launch to join them (2 us and more).  Where the weights are little that is not
+// worth it: 16 outputs to a workgroup.
 struct DownPlan {
   int nb, slices;
 };
-DownPlan down_plan(int32_t T, int32_t d) {
-  if (T <= 4) return {1, 1};
-  const int groups = d / 32, slices = (2 * kCus + groups - 1) / groups;
-  return {2, slices < 8 ? slices : 8};
+DownPlan down_plan(const Mx4Moe &p) {
+  const int experts = (p.T * p.k_max < p.E ? p.T * p.k_max : p.E) + p.S;
+  if ((int64_t)experts * p.d * p.f < (int64_t)24 << 20) return {1, 1};
+  const int groups = (p.d + 63) / 64, slices = (kCus + groups - 1) / groups;
+  return {4, slices < 16 ? slices : 16};
 }
 
-template <class Op, int TW>
-void launch_gate_up(const Mx4Moe &p, const float *scores, char *list, uint8_t *tokens, __bf16 *hi, __bf16 *lo,
-                    int grid, hipStream_t stream) {
+template <class Op, int TW, bool ROUTE>
+void launch_gate_up(const Mx4Moe &p, const float *scores, Plan *plan, __bf16 *hi, __bf16 *lo, int grid,
+                    hipStream_t stream) {
   int rows = 1;
   while (rows < p.T) rows *= 2;
   const size_t lds = ((size_t)(p.d + 127) / 128 * rows * 256 + 1023) / 1024 * 1024;
   if (lds <= kMoeLds)
-    mx4_gate_up_kernel<Op, TW, true, 4><<<grid, kWaves * kWave, lds, stream>>>(p, scores, list, tokens, hi, lo, rows);
+    mx4_gate_up_kernel<Op, TW, true, ROUTE, 4><<<grid, kWaves * kWave, lds, stream>>>(p, scores, plan, hi, lo, rows);
   else
-    mx4_gate_up_kernel<Op, TW, false, 3><<<grid, kWaves * kWave, 0, stream>>>(p, scores, list, tokens, hi, lo, 0);
+    mx4_gate_up_kernel<Op, TW, false, ROUTE, 3><<<grid, kWaves * kWave, 0, stream>>>(p, scores, plan, hi, lo, 0);
 }
 
 template <class Op>
 hipError_t launch_layer(const Mx4Moe &p, hipStream_t stream) {
   typedef typename Op::E E;
-  const DownPlan down = down_plan(p.T, p.d);
-  const Space at(p.T, p.d, p.f, p.E, p.S, p.k_max, down.slices);
+  const DownPlan down = down_plan(p);
+  const Space at(p, down.slices);
   float *logits = reinterpret_cast<float *>(p.workspace + at.logits);
-  char *list = p.workspace + at.list;
-  uint8_t *tokens = reinterpret_cast<uint8_t *>(p.workspace + at.tokens);
+  Plan *plan = reinterpret_cast<Plan *>(p.workspace + at.plan);
   __bf16 *hi = reinterpret_cast<__bf16 *>(p.workspace + at.hi), *lo = reinterpret_cast<__bf16 *>(p.workspace + at.lo);
   float *partial = reinterpret_cast<float *>(p.workspace + at.partial);
   hipError_t e;
@@ -474,18 +525,29 @@ hipError_t launch_layer(const Mx4Moe &p, hipStream_t stream) {
   }
   const float *scores = p.logits_override ? p.logits_override : logits;
   const int experts = (p.T * p.k_max < p.E ? p.T * p.k_max : p.E) + p.S;
-  const int most = experts * (p.f / 16);  // items, at least that many where picks spread
-  if (most >= 2048)
-    launch_gate_up<Op, 1>(p, scores, list, tokens, hi, lo, 2 * kCus, stream);
-  else
-    launch_gate_up<Op, 4>(p, scores, list, tokens, hi, lo, most < 2 * kCus ? most : 2 * kCus, stream);
+  const int most = experts * (p.f / 16);  // items, where picks spread
+  const int grid = most < 2 * kCus ? most : 2 * kCus;
+  if (p.T <= kRouteTokens) {
+    if (most >= kWaveItems)
+      launch_gate_up<Op, 1, true>(p, scores, plan, hi, lo, grid, stream);
+    else
+      launch_gate_up<Op, 4, true>(p, scores, plan, hi, lo, grid, stream);
+  } else {
+    mx4_plan_kernel<<<1, kPlanWaves * kWave, 0, stream>>>(p, scores, plan);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (most >= kWaveItems)
+      launch_gate_up<Op, 1, false>(p, scores, plan, hi, lo, grid, stream);
+    else
+      launch_gate_up<Op, 4, false>(p, scores, plan, hi, lo, grid, stream);
+  }
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  const size_t lds = (size_t)kWaves * p.T * down.nb * 16 * 4;
-  const int grid = p.d / (16 * down.nb) * down.slices;
+  const int blocks = (p.d / 16 + down.nb - 1) / down.nb * down.slices;
   if (down.nb == 1)
-    mx4_down_kernel<E, 1, 4><<<grid, kWaves * kWave, lds, stream>>>(p, list, tokens, hi, lo, down.slices, partial);
+    mx4_down_kernel<E, 1, 16, 2>
+        <<<blocks, 16 * kWave, (size_t)16 * p.T * 16 * 4, stream>>>(p, plan, hi, lo, down.slices, partial);
   else
-    mx4_down_kernel<E, 2, 3><<<grid, kWaves * kWave, lds, stream>>>(p, list, tokens, hi, lo, down.slices, partial);
+    mx4_down_kernel<E, 4, 8, 3>
+        <<<blocks, 8 * kWave, (size_t)8 * p.T * 64 * 4, stream>>>(p, plan, hi, lo, down.slices, partial);
   if ((e = hipGetLastError()) != hipSuccess || down.slices == 1) return e;
   mx4_moe_join_kernel<E><<<(p.T * p.d / 4 + 255) / 256, 256, 0, stream>>>(p, down.slices, partial);
   return hipGetLastError();
@@ -495,9 +557,7 @@ hipError_t launch_layer(const Mx4Moe &p, hipStream_t stream) {
 
 FP8MOE_DEBUG_TAKE(mx4)
 
-size_t mx4_moe_workspace(int32_t T, int32_t d, int32_t f, int32_t E, int32_t S, int32_t k_max) {
-  return Space(T, d, f, E, S, k_max, down_plan(T, d).slices).bytes;
-}
+size_t mx4_moe_workspace(const Mx4Moe &p) { return Space(p, down_plan(p).slices).bytes; }
 
 hipError_t launch_mx4_moe(const Mx4Moe &p, hipStream_t stream) {
   return p.type == kTypeBf16 ? launch_layer<Mx4Bf16>(p, stream) : launch_layer<Mx4F16>(p, stream);

@@ -75,6 +75,12 @@ moe_status check_layer(const char *fn, const moe_dims *m) {
   return MOE_OK;
 }
 
+size_t layer_workspace(const moe_dims &m) {
+  Mx4Moe p{};
+  p.T = m.T, p.d = m.d, p.f = m.f, p.E = m.E, p.S = m.n_shared, p.k_max = m.k_max;
+  return mx4_moe_workspace(p);
+}
+
 int64_t code_bytes(int32_t rows, int32_t cols) { return (int64_t)rows * (cols / 2); }
 int64_t scale_bytes(int32_t rows, int32_t cols) { return (int64_t)rows * (cols / MOE_MX4_GROUP); }
 
@@ -202,7 +208,7 @@ moe_status moe_ffn_mx4(const void *x, int64_t ldx, const void *w_gate, const voi
 size_t moe_mx4_workspace_bytes(const moe_dims *dims) {
   if (check_layer("moe_mx4_workspace_bytes", dims)) return 0;
   (void)ok_status();
-  return mx4_moe_workspace(dims->T, dims->d, dims->f, dims->E, dims->n_shared, dims->k_max);
+  return layer_workspace(*dims);
 }
 
 moe_status moe_mx4_forward(const moe_dims *dims, int32_t type, const void *x, int64_t ldx,
@@ -224,7 +230,7 @@ moe_status moe_mx4_forward(const moe_dims *dims, int32_t type, const void *x, in
       !all_aligned({router_bias, k_per_token, logits_override, topk_ids_out, topk_w_out}, 4))
     return fail_status(MOE_ERR_ALIGN, "%s: x, out, w_router and the matrices must be 16-byte, the other "
                        "arrays 4-byte aligned", fn);
-  const size_t need = mx4_moe_workspace(m.T, m.d, m.f, m.E, m.n_shared, m.k_max);
+  const size_t need = layer_workspace(m);
   if (!workspace || workspace_bytes < need)
     return fail_status(MOE_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", fn,
                        workspace ? workspace_bytes : (size_t)0, need);

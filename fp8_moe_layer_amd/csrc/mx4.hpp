@@ -73,7 +73,7 @@ struct Mx4Moe {
   float *w_out;
   char *workspace;
 };
-size_t mx4_moe_workspace(int32_t T, int32_t d, int32_t f, int32_t E, int32_t S, int32_t k_max);
+size_t mx4_moe_workspace(const Mx4Moe &p);  // by the sizes alone
 hipError_t launch_mx4_moe(const Mx4Moe &p, hipStream_t stream);
 uint32_t debug_take_mx4();
 
