@@ -168,13 +168,14 @@ __global__ __launch_bounds__(NT > 256 ? NT : 256) void norm_forward_kernel(NormF
 }
 
 // ---------------------------------------------------------------- backward
-// The rows are cut into chunks, one to a workgroup, which sums its rows' shares
-// of the vectors' gradients in registers and leaves them in the workspace; a
-// second launch adds the chunks in order (no atomics: equal calls, equal bits).
+// The rows are cut into chunks, one to a workgroup, whose teams sum their rows' shares
+// of the vectors' gradients in registers and add them in LDS, in team order; the chunk's
+// sums go to the workspace, and a second launch adds the chunks in order (no atomics:
+// equal calls, equal bits).
 //
 // A gate row's tokens are next to each other.  Where there are few gate rows,
 // each is cut into `parts` chunks; where there are many, a chunk is `whole` of
-// them, and their gradients need no second launch.
+// them, a team takes whole ones, and their gradients need no second launch.
 struct Chunks {
   int32_t count;  // of chunks
   int32_t parts;  // chunks of one gate row, or 0
@@ -183,7 +184,10 @@ struct Chunks {
   int32_t rows;   // tokens of a chunk, at most
 };
 
+// Workgroups of a pass.  With few rows a chunk is one, for the least latency; more of
+// them make the second launch's work less.
 constexpr int kMaxChunks = 512;
+int32_t least_rows(int32_t T) { return T <= 256 ? 1 : T <= 512 ? 2 : T <= 768 ? 3 : 4; }
 
 Chunks chunks_of(int32_t T, int32_t gate_rows) {
   Chunks c{};
@@ -193,8 +197,8 @@ Chunks chunks_of(int32_t T, int32_t gate_rows) {
   const int32_t G = gate_rows > 0 ? gate_rows : 1;
   c.rep = T / G;
   if (G <= kMaxChunks / 2) {
-    const int32_t most = kMaxChunks / G;
-    c.parts = c.rep < most ? c.rep : most;
+    const int32_t most = kMaxChunks / G, fit = (c.rep + least_rows(T) - 1) / least_rows(T);
+    c.parts = fit < most ? fit : most;
     c.rows = (c.rep + c.parts - 1) / c.parts;
     c.parts = (c.rep + c.rows - 1) / c.rows;
     c.count = G * c.parts;
@@ -206,29 +210,81 @@ Chunks chunks_of(int32_t T, int32_t gate_rows) {
   return c;
 }
 
+// Teams of a workgroup: waves that take rows by themselves, or one.
+constexpr int teams_of(int nt) { return nt == kWave ? 8 : 1; }
+
+// What there is not counts as ones (weights, gate, rstd_y) or zeros (dr, dn, rstd_r), so
+// that no value's arithmetic asks.
 template <class E, class W, int NT, int V>
-__global__ __launch_bounds__(NT) void norm_backward_kernel(NormBackward p, Chunks c) {
-  constexpr int N = Run<E>::N;
+__global__ __launch_bounds__(NT *teams_of(NT)) void norm_backward_kernel(NormBackward p, Chunks c) {
+  constexpr int N = Run<E>::N, TEAMS = teams_of(NT);
+  // rows past 8192 values: registers do not hold three sums a value, LDS takes two of
+  // them, and what the first pass over a row finds is found again in the second
+  constexpr bool kLong = NT * V * N > 8192;
   __shared__ float red[2 * (NT / kWave)];
-  const int tid = threadIdx.x;
+  __shared__ float joined[TEAMS > 1 ? TEAMS * NT * V * N : 1];
+  __shared__ v4f lds_sums[2][kLong ? V * N / 4 : 1][kLong ? NT : 1];
+  const int tid = TEAMS > 1 ? threadIdx.x & 63 : threadIdx.x;
+  const int team = TEAMS > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
   TeamSum<NT> sum{red};
   const float inv_d = 1.0f / (float)p.d;
-  int64_t t0, t1;
+  // the team's rows: t, t + step, ... up to t1 of gate row `grow`, then (whole gate rows)
+  // the same of the gate rows TEAMS further on, up to last_grow
+  int grow, last_grow, t, t1, step;
   if (c.parts) {
-    const int g = blockIdx.x / c.parts, part = blockIdx.x % c.parts;
-    t0 = (int64_t)g * c.rep + (int64_t)part * c.rows;
-    t1 = t0 + c.rows < (int64_t)(g + 1) * c.rep ? t0 + c.rows : (int64_t)(g + 1) * c.rep;
+    grow = blockIdx.x / c.parts;
+    const int part = blockIdx.x - grow * c.parts;
+    last_grow = grow + 1;
+    t = grow * c.rep + part * c.rows;
+    t1 = t + c.rows < (grow + 1) * c.rep ? t + c.rows : (grow + 1) * c.rep;
+    t += team;
+    step = TEAMS;
   } else {
-    t0 = (int64_t)blockIdx.x * c.rows;
-    t1 = t0 + c.rows < p.T ? t0 + c.rows : p.T;
+    grow = blockIdx.x * c.whole + team;
+    last_grow = (blockIdx.x + 1) * c.whole < p.gate_rows ? (blockIdx.x + 1) * c.whole : p.gate_rows;
+    t = grow * c.rep;
+    t1 = grow < last_grow ? t + c.rep : t;
+    step = 1;
   }
-  float a_post[V][N], a_gate[V][N], a_next[V][N];
+  float a_post[kLong ? 1 : V][N], a_gate[kLong ? 1 : V][N], a_next[V][N];
 #pragma unroll
   for (int j = 0; j < V; ++j)
 #pragma unroll
-    for (int i = 0; i < N; ++i) a_post[j][i] = a_gate[j][i] = a_next[j][i] = 0.0f;
+    for (int i = 0; i < N; ++i) {
+      a_next[j][i] = 0.0f;
+      if constexpr (kLong)
+        lds_sums[i & 1][j * (N / 4) + i / 4][tid] = v4f{0.f, 0.f, 0.f, 0.f};  // (a thread's own)
+      else
+        a_post[j][i] = a_gate[j][i] = 0.0f;
+    }
+  // a thread's sums of a_post (0) or a_gate (1), run j
+  auto take = [&](auto &a, int which, int j, float (&v)[N], bool clear) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if constexpr (kLong) {
+        v[i] = lds_sums[which][j * (N / 4) + i / 4][tid][i & 3];
+      } else {
+        v[i] = a[j][i];
+        if (clear) a[j][i] = 0.0f;
+      }
+    }
+    if constexpr (kLong)
+      if (clear)
+#pragma unroll
+        for (int i = 0; i < N; i += 4) lds_sums[which][j * (N / 4) + i / 4][tid] = v4f{0.f, 0.f, 0.f, 0.f};
+  };
+  auto weights = [&](const void *w, float offset, int at, float none, float (&v)[N]) {
+    if (w && at < p.d) {
+      load_weights<W, N>(w, at, v);
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += offset;
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = none;
+    }
+  };
 
-  for (int64_t t = t0; t < t1; ++t) {
+  for (; t < t1;) {
     Run<E> xr[V], yr[V], dr[V], dn[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -242,58 +298,71 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormBackward p, Chunk
     }
     const float sy = p.w_post ? p.rstd_y[t] : 1.0f;
     const float sr = p.w_next ? p.rstd_r[t] : 0.0f;
-    const int64_t grow = p.gate ? t / c.rep : 0;
     const W *gate = p.gate ? row_of<W>(p.gate, p.ldg, grow) : nullptr;
-    // the gradient of r: dr, and what comes back through the next norm
-    float total[V][N], z[V][N];
-    float dot = 0.0f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int at = (j * NT + tid) * N;
-      const bool in = at < p.d;
-      float wp[N] = {}, g[N] = {}, wn[N] = {};
-      if (in && p.w_post) load_weights<W, N>(p.w_post, at, wp);
-      if (in && gate) load_weights<W, N>(gate, at, g);
-      if (in && p.w_next) load_weights<W, N>(p.w_next, at, wn);
+    // z, and r^ (the residual sum before it is rounded, times its rstd)
+    auto first = [&](int j, const float (&wp)[N], const float (&g)[N], float (&z)[N], float (&rh)[N]) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        z[j][i] = yr[j][i];
-        if (p.w_post) z[j][i] = z[j][i] * sy * (p.offset + wp[i]);
-        const float r = fmaf(p.scale, gate ? z[j][i] * g[i] : z[j][i], xr[j][i]);
-        const float rh = r * sr, a = dn[j][i] * (p.offset + wn[i]);
-        a_next[j][i] = fmaf(dn[j][i], rh, a_next[j][i]);
-        dot = fmaf(a, rh, dot);
+        z[i] = yr[j][i] * sy * wp[i];
+        rh[i] = fmaf(p.scale, z[i] * g[i], xr[j][i]) * sr;
       }
+    };
+    float z[kLong ? 1 : V][N], rh[kLong ? 1 : V][N];
+    float dot = 0.0f;
+    if (p.w_next || !kLong) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int at = (j * NT + tid) * N, k = kLong ? 0 : j;
+        float wp[N], g[N], wn[N];
+        weights(p.w_post, p.offset, at, 1.0f, wp);
+        weights(gate, 0.0f, at, 1.0f, g);
+        weights(p.w_next, p.offset, at, 0.0f, wn);
+        first(j, wp, g, z[k], rh[k]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          a_next[j][i] = fmaf(dn[j][i], rh[k][i], a_next[j][i]);
+          dot = fmaf(dn[j][i] * wn[i], rh[k][i], dot);
+        }
+      }
+      if (p.w_next) dot = sum(dot) * inv_d;
     }
-    const float m = p.w_next ? sum(dot) * inv_d : 0.0f;
+    // the gradient of r: dr, and what comes back through the next norm
+    float b[V][N];
     float dot_y = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int at = (j * NT + tid) * N;
-      const bool in = at < p.d;
-      float wp[N] = {}, g[N] = {}, wn[N] = {};
-      if (in && p.w_post) load_weights<W, N>(p.w_post, at, wp);
-      if (in && gate) load_weights<W, N>(gate, at, g);
-      if (in && p.w_next) load_weights<W, N>(p.w_next, at, wn);
+      const int at = (j * NT + tid) * N, k = kLong ? 0 : j;
+      float wp[N], g[N], wn[N];
+      weights(p.w_post, p.offset, at, 1.0f, wp);
+      weights(gate, 0.0f, at, 1.0f, g);
+      weights(p.w_next, p.offset, at, 0.0f, wn);
+      if constexpr (kLong) first(j, wp, g, z[k], rh[k]);
+#pragma unroll
+      for (int i = 0; i < N; ++i) b[j][i] = fmaf(sr, fmaf(-rh[k][i], dot, dn[j][i] * wn[i]), dr[j][i]);
+      if (at < p.d) store_values<E, N>(static_cast<E *>(p.dx) + (int64_t)t * p.d, at, b[j]);
+      float s_gate[N], s_post[N];
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float gi = gate ? g[i] : 1.0f;
-        const float r = fmaf(p.scale, gate ? z[j][i] * gi : z[j][i], xr[j][i]);
-        const float rh = r * sr, a = dn[j][i] * (p.offset + wn[i]);
-        total[j][i] = dr[j][i];
-        if (p.w_next) total[j][i] = fmaf(sr, fmaf(-rh, m, a), total[j][i]);
+        const float e = p.scale * b[j][i], cg = e * g[i], yh = yr[j][i] * sy;
+        s_gate[i] = e * z[k][i];
+        s_post[i] = cg * yh;
+        b[j][i] = cg * wp[i];
+        dot_y = fmaf(b[j][i], yh, dot_y);
       }
-      if (in) store_values<E, N>(static_cast<E *>(p.dx) + t * p.d, at, total[j]);
+      if constexpr (kLong) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float e = p.scale * total[j][i];
-        a_gate[j][i] = fmaf(e, z[j][i], a_gate[j][i]);
-        const float cg = gate ? e * g[i] : e;
-        const float yh = yr[j][i] * sy;
-        a_post[j][i] = fmaf(cg, yh, a_post[j][i]);
-        const float b = p.w_post ? cg * (p.offset + wp[i]) : cg;
-        dot_y = fmaf(b, yh, dot_y);
-        total[j][i] = b;
+        for (int i = 0; i < N; i += 4) {
+          v4f *to = &lds_sums[0][j * (N / 4) + i / 4][tid];
+          if (p.w_post) *to += v4f{s_post[i], s_post[i + 1], s_post[i + 2], s_post[i + 3]};
+          to = &lds_sums[1][j * (N / 4) + i / 4][tid];
+          if (gate) *to += v4f{s_gate[i], s_gate[i + 1], s_gate[i + 2], s_gate[i + 3]};
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          a_gate[j][i] += s_gate[i];
+          a_post[j][i] += s_post[i];
+        }
       }
     }
     if (p.y) {
@@ -302,36 +371,58 @@ __global__ __launch_bounds__(NT) void norm_backward_kernel(NormBackward p, Chunk
       for (int j = 0; j < V; ++j) {
         const int at = (j * NT + tid) * N;
         if (at >= p.d) continue;
-        if (p.w_post) {
 #pragma unroll
-          for (int i = 0; i < N; ++i)
-            total[j][i] = sy * fmaf(-yr[j][i] * sy, my, total[j][i]);
-        }
-        store_values<E, N>(static_cast<E *>(p.dy) + t * p.d, at, total[j]);
+        for (int i = 0; i < N; ++i) b[j][i] = sy * fmaf(-yr[j][i] * sy, my, b[j][i]);
+        store_values<E, N>(static_cast<E *>(p.dy) + (int64_t)t * p.d, at, b[j]);
       }
     }
-    // a whole gate row ends here
-    if (p.gate && !c.parts && (t + 1) % c.rep == 0) {
+    t += step;
+    if (!c.parts && t == t1) {  // a whole gate row ends here
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const int at = (j * NT + tid) * N;
-        if (at < p.d) store_values<W, N>(static_cast<W *>(p.dgate) + grow * p.d, at, a_gate[j]);
-#pragma unroll
-        for (int i = 0; i < N; ++i) a_gate[j][i] = 0.0f;
+        float v[N];
+        take(a_gate, 1, j, v, true);
+        if (at < p.d) store_values<W, N>(static_cast<W *>(p.dgate) + (int64_t)grow * p.d, at, v);
       }
+      grow += TEAMS;
+      if (grow < last_grow) t = grow * c.rep, t1 = t + c.rep;
     }
   }
   // the chunk's sums: [next, post, gate][chunk][d]
-  const int64_t slab = (int64_t)c.count * p.d;
-  float *mine = p.workspace + (int64_t)blockIdx.x * p.d;
+  auto leave = [&](int which, auto value) {
+    float v[V][N];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int at = (j * NT + tid) * N;
-    if (at >= p.d) continue;
-    if (p.w_next) store_run<float, N>(mine + at, a_next[j], N);
-    if (p.w_post) store_run<float, N>(mine + slab + at, a_post[j], N);
-    if (p.gate && c.parts) store_run<float, N>(mine + 2 * slab + at, a_gate[j], N);
-  }
+    for (int j = 0; j < V; ++j) value(j, v[j]);
+    if constexpr (TEAMS > 1) {
+      __syncthreads();  // the last vector's are read
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+#pragma unroll
+        for (int i = 0; i < N; ++i) joined[((team * V + j) * N + i) * NT + tid] = v[j][i];
+      __syncthreads();
+      if (team > 0) return;
+#pragma unroll
+      for (int w = 1; w < TEAMS; ++w)
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+#pragma unroll
+          for (int i = 0; i < N; ++i) v[j][i] += joined[((w * V + j) * N + i) * NT + tid];
+    }
+    float *mine = p.workspace + ((int64_t)which * c.count + blockIdx.x) * p.d;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int at = (j * NT + tid) * N;
+      if (at < p.d) store_run<float, N>(mine + at, v[j], N);
+    }
+  };
+  if (p.w_next)
+    leave(0, [&](int j, float (&v)[N]) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = a_next[j][i];
+    });
+  if (p.w_post) leave(1, [&](int j, float (&v)[N]) { take(a_post, 0, j, v, false); });
+  if (p.gate && c.parts) leave(2, [&](int j, float (&v)[N]) { take(a_gate, 1, j, v, false); });
 }
 
 // Adds the chunks' sums: 64 columns to a workgroup, whose 16 waves take the
@@ -364,8 +455,18 @@ __global__ __launch_bounds__(kSumWaves * kWave) void norm_sum_kernel(NormBackwar
     last = c.count > 0 ? first + c.parts : first;
   }
   float v = 0.0f;
-  if (col < p.d)
-    for (int k = first + wave; k < last; k += kSumWaves) v += in[(int64_t)k * p.d + col];
+  if (col < p.d) {
+    int k = first + wave;
+    constexpr int kAtOnce = 8;
+    for (; k + (kAtOnce - 1) * kSumWaves < last; k += kAtOnce * kSumWaves) {
+      float w[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) w[i] = in[(int64_t)(k + i * kSumWaves) * p.d + col];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) v += w[i];
+    }
+    for (; k < last; k += kSumWaves) v += in[(int64_t)k * p.d + col];
+  }
   part[wave][lane] = v;
   __syncthreads();
   if (wave == 0 && col < p.d) {
@@ -384,8 +485,9 @@ hipError_t with_team(int32_t d, Fn fn) {
   if (runs <= 256) return fn.template operator()<E, W, 256, 1>();
   if (runs <= 512) return fn.template operator()<E, W, 512, 1>();
   if (runs <= 1024) return fn.template operator()<E, W, 1024, 1>();
-  if (runs <= 2048) return fn.template operator()<E, W, 1024, 2>();
-  return fn.template operator()<E, W, 1024, 4>();
+  if constexpr (Run<E>::N == 4)
+    if (runs > 2048) return fn.template operator()<E, W, 1024, 4>();
+  return fn.template operator()<E, W, 1024, 2>();
 }
 
 template <class Fn>
@@ -414,7 +516,7 @@ struct Backward {
   template <class E, class W, int NT, int V>
   hipError_t operator()() const {
     if (c.count > 0) {
-      norm_backward_kernel<E, W, NT, V><<<c.count, NT, 0, stream>>>(p, c);
+      norm_backward_kernel<E, W, NT, V><<<c.count, NT * teams_of(NT), 0, stream>>>(p, c);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
