@@ -481,6 +481,12 @@ class _Call:
         with _on(self.alloc):
             return torch.empty(shape, dtype=dtype, device=self.dev)
 
+    def like(self, t: torch.Tensor):
+        """A new contiguous tensor of t's shape and type (half the time of empty)."""
+        if self.alloc is None and t.is_contiguous():
+            return torch.empty_like(t)
+        return self.empty(t.shape, t.dtype)
+
     def workspace(self, size, T: int, inner: int, outputs: int):
         """(tensor, address, bytes) of the workspace that the call can use:
         size(T, inner, outputs) bytes, most often none."""
@@ -673,31 +679,30 @@ def dense_form(op: str, T: int, inner: int, outputs: int):
 # --------------------------------------------------------------------------- norms around a block
 # Plain calls like the dense operators above.
 
-class _Norm:
-    """The arguments that a norm's forward and backward calls share, checked: the
-    dims, and pointers to the vectors.  Vectors are of one type, fp32 or x's."""
-    __slots__ = ("call", "dims", "shape", "w_type", "w_post", "gate", "ldg", "w_next")
+@functools.lru_cache(maxsize=4096)
+def _norm_dims(T: int, d: int, dtype, w_type, gate_rows: int, scale: float, offset: float, eps: float):
+    """The dims argument of the norms' calls, kept: building one takes 1 us."""
+    return C.byref(_NormDims(T, d, _type(dtype), _type(w_type), gate_rows, scale, offset, eps))
 
-    def __init__(self, first, T, d, w_post, gate, w_next, scale, offset, eps, stream):
-        c = self.call = _Call(first, stream)
-        vectors = [v for v in (w_post, gate, w_next) if v is not None]
-        self.w_type = vectors[0].dtype if vectors else first.dtype
-        if self.w_type is not torch.float32 and self.w_type is not first.dtype:
-            raise TypeError(f"weights and gate are {first.dtype} or torch.float32, got {self.w_type}")
-        self.shape = (T, d)
-        self.w_post = None if w_post is None else c.ptr(w_post, (d,), self.w_type, "w_post")
-        self.w_next = None if w_next is None else c.ptr(w_next, (d,), self.w_type, "w_next")
-        self.gate, self.ldg, rows = None, 0, 0
-        if gate is not None:
-            rows = _shape2(gate, "gate")[0]
-            if rows < 1 and T > 0 or rows > 1 and T % rows:
-                raise ValueError(f"gate: {rows} rows for {T} tokens")
-            if rows:
-                self.gate, self.ldg = c.rows(gate, (rows, d), self.w_type, "gate")
-        self.dims = _NormDims(T, d, _type(first.dtype), _TYPES[self.w_type], rows, scale, offset, eps)
 
-    def rows(self, t, dtype, name):
-        return (None, 0) if t is None else self.call.rows(t, self.shape, dtype, name)
+def _norm_vectors(c: _Call, T: int, d: int, dtype, w_post, gate, w_next):
+    """(their type, address of w_post, of the gate, its row stride and rows, address
+    of w_next), checked: one type, fp32 or the rows'."""
+    first = w_post if w_post is not None else gate if gate is not None else w_next
+    if first is None:
+        return dtype, None, None, 0, 0, None
+    w_type = first.dtype
+    if w_type is not torch.float32 and w_type is not dtype:
+        raise TypeError(f"weights and gate are {dtype} or torch.float32, got {w_type}")
+    wp = None if w_post is None else c.ptr(w_post, (d,), w_type, "w_post")
+    np_ = None if w_next is None else c.ptr(w_next, (d,), w_type, "w_next")
+    if gate is None:
+        return w_type, wp, None, 0, 0, np_
+    rows = _shape2(gate, "gate")[0]
+    if rows < 1 and T > 0 or rows > 1 and T % rows:
+        raise ValueError(f"gate: {rows} rows for {T} tokens")
+    gp, ldg = c.rows(gate, (rows, d), w_type, "gate") if rows else (None, 0)
+    return w_type, wp, gp, ldg, rows, np_
 
 
 def _out(c, t, shape, dtype, name):
@@ -708,20 +713,29 @@ def _out(c, t, shape, dtype, name):
     return t, c.ptr(t, shape, dtype, name)
 
 
+def _out_like(c, t, x, name):
+    """The same for an output of x's shape and type."""
+    if t is None:
+        t = c.like(x)
+        return t, t.data_ptr()
+    return t, c.ptr(t, x.shape, x.dtype, name)
+
+
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, offset: float = 0.0,
              out: Optional[torch.Tensor] = None, save: bool = False, stream=None):
     """x * rstd * (offset + weight) with rstd = 1 / sqrt(mean(x^2) + eps), row by
     row (moe_norm_residual without a sum): x [T, d] fp32, bf16 or fp16 (rows may
     be strided), weight [d] fp32 or x's type.  With save=True (n, rstd), rstd
     [T] fp32 as rms_norm_backward takes it."""
-    T, d = _shape2(x, "x")
+    T, d = shape = _shape2(x, "x")
     _no_autograd("rms_norm", x, weight)
-    m = _Norm(x, T, d, None, None, weight, 1.0, offset, eps, stream)
-    xp, ldx = m.rows(x, x.dtype, "x")
-    n, at = _out(m.call, out, (T, d), x.dtype, "out")
-    rstd = m.call.empty((T,), torch.float32) if save else None
-    m.call.run(_norm_residual, C.byref(m.dims), xp, ldx, None, 0, None, None, 0, m.w_next, None, at,
-               None, rstd.data_ptr() if save else None)
+    c = _Call(x, stream)
+    w_type, _, _, _, _, wp = _norm_vectors(c, T, d, x.dtype, None, None, weight)
+    xp, ldx = c.rows(x, shape, x.dtype, "x")
+    n, at = _out_like(c, out, x, "out")
+    rstd = c.empty((T,), torch.float32) if save else None
+    c.run(_norm_residual, _norm_dims(T, d, x.dtype, w_type, 0, 1.0, offset, eps), xp, ldx, None, 0, None,
+          None, 0, wp, None, at, None, rstd.data_ptr() if save else None)
     return (n, rstd) if save else n
 
 
@@ -737,54 +751,74 @@ def norm_residual(x: torch.Tensor, y: torch.Tensor, w_post: Optional[torch.Tenso
     x's type.  Returns r, with w_next (r, n); with save=True always
     (r, n, rstd_y, rstd_r), None for what there is not, the rstd fp32 [T] as
     norm_residual_backward takes them."""
-    T, d = _shape2(x, "x")
+    T, d = shape = _shape2(x, "x")
     _no_autograd("norm_residual", x, y, w_post, gate, w_next)
-    m = _Norm(x, T, d, w_post, gate, w_next, scale, offset, eps, stream)
-    c = m.call
-    xp, ldx = m.rows(x, x.dtype, "x")
-    yp, ldy = m.rows(y, x.dtype, "y")
-    r, rp = _out(c, r, (T, d), x.dtype, "r")
-    np_ = None
+    c, t = _Call(x, stream), x.dtype
+    w_type, wp, gp, ldg, rows, wn = _norm_vectors(c, T, d, t, w_post, gate, w_next)
+    xp, ldx = c.rows(x, shape, t, "x")
+    yp, ldy = c.rows(y, shape, t, "y")
+    r, rp = _out_like(c, r, x, "r")
+    np_ = rstd_y = rstd_r = syp = srp = None
     if w_next is not None:
-        n, np_ = _out(c, n, (T, d), x.dtype, "n")
+        n, np_ = _out_like(c, n, x, "n")
     elif n is not None:
         raise ValueError("n needs w_next")
-    rstd_y = c.empty((T,), torch.float32) if save and w_post is not None else None
-    rstd_r = c.empty((T,), torch.float32) if save and w_next is not None else None
-    c.run(_norm_residual, C.byref(m.dims), xp, ldx, yp, ldy, m.w_post, m.gate, m.ldg, m.w_next, rp, np_,
-          None if rstd_y is None else rstd_y.data_ptr(), None if rstd_r is None else rstd_r.data_ptr())
+    if save:
+        if w_post is not None:
+            rstd_y = c.empty((T,), torch.float32)
+            syp = rstd_y.data_ptr()
+        if w_next is not None:
+            rstd_r = c.empty((T,), torch.float32)
+            srp = rstd_r.data_ptr()
+    c.run(_norm_residual, _norm_dims(T, d, t, w_type, rows, scale, offset, eps), xp, ldx, yp, ldy, wp, gp,
+          ldg, wn, rp, np_, syp, srp)
     if save:
         return r, n, rstd_y, rstd_r
     return r if w_next is None else (r, n)
 
 
-def _norm_backward(m, dr, dn, x, y, rstd_y, rstd_r, has, dx, dy, workspace):
-    """The library's backward call; has: which of w_post, gate, w_next there are
-    (the gate's shape for the gate).  (dx, dy, dw_post, dgate, dw_next)."""
-    c, (T, d), t = m.call, m.shape, x.dtype
-    post, gate, nxt = has
-    drp, lddr = m.rows(dr, t, "dr")
-    dnp, lddn = m.rows(dn, t, "dn")
-    xp, ldx = m.rows(x, t, "x")
-    yp, ldy = m.rows(y, t, "y")
-    dx, dxp = _out(c, dx, (T, d), t, "dx")
-    dyp = None
+@_by_sizes
+def _norm_bwd_size(T: int, d: int, gate_rows: int) -> int:
+    return _norm_bwd_ws(_norm_dims(T, d, torch.float32, torch.float32, gate_rows, 1.0, 0.0, 1.0))
+
+
+def _norm_backward(c, shape, dr, dn, x, y, rstd_y, rstd_r, w_post, gate, w_next, scale, offset, dx, dy,
+                   workspace):
+    """The library's backward call, y None without a sum: (dx, dy, dw_post, dgate,
+    dw_next)."""
+    (T, d), t = shape, x.dtype
+    w_type, wp, gp, ldg, rows, wn = _norm_vectors(c, T, d, t, w_post, gate, w_next)
+    drp, lddr = c.rows(dr, shape, t, "dr") if dr is not None else (None, 0)
+    dnp, lddn = c.rows(dn, shape, t, "dn") if dn is not None else (None, 0)
+    xp, ldx = c.rows(x, shape, t, "x")
+    dx, dxp = _out_like(c, dx, x, "dx")
+    yp, ldy, dyp, syp, srp, pp, pg, pn = None, 0, None, None, None, None, None, None
+    dw_post = dgate = dw_next = None
     if y is not None:
-        dy, dyp = _out(c, dy, (T, d), t, "dy")
-    dw_post = c.empty((d,), m.w_type) if post else None
-    dgate = c.empty(gate, m.w_type) if gate else None
-    dw_next = c.empty((d,), m.w_type) if nxt else None
-    at = lambda v: None if v is None or v.numel() == 0 else v.data_ptr()
-    need = int(_norm_bwd_ws(C.byref(m.dims)))
-    if workspace is None and need:
-        workspace = c.empty((need,), torch.uint8)
-    elif workspace is not None:
-        c.ptr(workspace, workspace.shape, torch.uint8, "workspace")
-    c.run(_norm_bwd, C.byref(m.dims), drp, lddr, dnp, lddn, xp, ldx, yp, ldy,
-          c.ptr(rstd_y, (T,), torch.float32, "rstd_y") if post else None,
-          c.ptr(rstd_r, (T,), torch.float32, "rstd_r") if nxt else None, m.w_post, m.gate, m.ldg,
-          m.w_next, dxp, dyp, at(dw_post), at(dgate), at(dw_next), at(workspace),
-          0 if workspace is None else workspace.numel())
+        yp, ldy = c.rows(y, shape, t, "y")
+        dy, dyp = _out_like(c, dy, x, "dy")
+    if w_post is not None:
+        syp = c.ptr(rstd_y, (T,), torch.float32, "rstd_y")
+        dw_post = c.like(w_post)
+        pp = dw_post.data_ptr()
+    if gate is not None:
+        dgate = c.like(gate)
+        pg = dgate.data_ptr() if rows else None
+    if w_next is not None:
+        srp = c.ptr(rstd_r, (T,), torch.float32, "rstd_r")
+        dw_next = c.like(w_next)
+        pn = dw_next.data_ptr()
+    dims = _norm_dims(T, d, t, w_type, rows, scale, offset, 1.0)
+    at, size = None, 0
+    if workspace is not None:
+        at, size = c.ptr(workspace, workspace.shape, torch.uint8, "workspace"), workspace.numel()
+    else:
+        size = _norm_bwd_size(T, d, rows)
+        if size:
+            workspace = c.empty((size,), torch.uint8)
+            at = workspace.data_ptr()
+    c.run(_norm_bwd, dims, drp, lddr, dnp, lddn, xp, ldx, yp, ldy, syp, srp, wp, gp, ldg, wn, dxp, dyp, pp,
+          pg, pn, at, size)
     return dx, dy, dw_post, dgate, dw_next
 
 
@@ -794,11 +828,10 @@ def rms_norm_backward(dn: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, r
                       stream=None):
     """Gradients of rms_norm from dn and its saved rstd: (dx, dweight).  dr [T,
     d]: x's gradient from elsewhere (the residual stream), added to dx."""
-    T, d = _shape2(x, "x")
+    shape = _shape2(x, "x")
     _no_autograd("rms_norm_backward", dn, x, weight, rstd, dr)
-    m = _Norm(x, T, d, None, None, weight, 1.0, offset, 1.0, stream)
-    dx, _, _, _, dw = _norm_backward(m, dr, dn, x, None, None, rstd, (False, None, True), dx, None,
-                                     workspace)
+    dx, _, _, _, dw = _norm_backward(_Call(x, stream), shape, dr, dn, x, None, None, rstd, None, None,
+                                     weight, 1.0, offset, dx, None, workspace)
     return dx, dw
 
 
@@ -816,20 +849,18 @@ def norm_residual_backward(dr: Optional[torch.Tensor], dn: Optional[torch.Tensor
     there is not, written over whatever dx and dy held.  workspace: uint8,
     256-byte aligned, norm_backward_workspace_bytes(T, d, gate rows) or more;
     allocated here when not given."""
-    T, d = _shape2(x, "x")
+    shape = _shape2(x, "x")
     _no_autograd("norm_residual_backward", dr, dn, x, y, rstd_y, rstd_r, w_post, gate, w_next)
     if (dn is None) != (w_next is None):
         raise ValueError("dn and w_next go together")
     if dr is None and dn is None:
         raise ValueError("dr or dn is required")
-    m = _Norm(x, T, d, w_post, gate, w_next, scale, offset, 1.0, stream)
-    return _norm_backward(m, dr, dn, x, y, rstd_y, rstd_r,
-                          (w_post is not None, None if gate is None else tuple(gate.shape),
-                           w_next is not None), dx, dy, workspace)
+    return _norm_backward(_Call(x, stream), shape, dr, dn, x, y, rstd_y, rstd_r, w_post, gate, w_next,
+                          scale, offset, dx, dy, workspace)
 
 
 def norm_backward_workspace_bytes(T: int, d: int, gate_rows: int = 0) -> int:
-    return int(_norm_bwd_ws(C.byref(_NormDims(T, d, 0, 0, gate_rows, 1.0, 0.0, 1.0))))
+    return int(_norm_bwd_size(T, d, gate_rows))
 
 
 # --------------------------------------------------------------------------- 4-bit weights
@@ -1033,7 +1064,9 @@ class Mx4MoELayer:
         return step
 
     def _workspace(self, c: _Call, n: int):
-        if torch.cuda.is_current_stream_capturing():
+        with _on(c.alloc):
+            capturing = torch.cuda.is_current_stream_capturing()
+        if capturing:
             return c.empty((n,), torch.uint8)
         ws = self._ws.get(c.stream)
         if ws is None or ws.numel() < n:
@@ -1055,7 +1088,7 @@ class Mx4MoELayer:
         kind = _type(x.dtype, _TYPES16)
         xp, ldx = c.rows(x, (T, self.w.d), x.dtype, "x")
         dm, need = self._step(T)
-        out, at = _out(c, out, (T, d), x.dtype, "out")
+        out, at = _out_like(c, out, x, "out")
         i32, f32, K = torch.int32, torch.float32, self.k_max
         opt = lambda t, shape, dtype, name: None if t is None else c.ptr(t, shape, dtype, name)
         ws = self._workspace(c, need)
