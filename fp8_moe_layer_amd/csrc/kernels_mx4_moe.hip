@@ -187,19 +187,21 @@ __device__ __forceinline__ const uint8_t *expert_matrix(const uint8_t *routed, c
 }
 
 // ---------------------------------------------------------------- gate/up
-// An item is 16 channels of an entry.  TW waves share its K (one, where there are
-// items enough for all waves: then nothing waits for another).  rows > 0: the
+// An item is 16 or (NB == 2) 32 channels of an entry.  TW waves share its K (one, where
+// there are items enough for all waves: then nothing waits for another).  LDS: the
 // activations of all tokens are in LDS, `rows` (a power of two) to a tile, laid out as
-// the few-token products lay theirs; 0: a wave asks for them with its weights.
+// the few-token products lay theirs.  Else a wave asks for them with its weights, and
+// what the L2 gives of them is the bound: hence 32 channels (32 tokens of the 8-expert
+// layer: 16 channels 120 us).
 constexpr int kMoeLds = 96 * 1024;
 
 // logits: the tokens are routed here (ROUTE); else their plan is in memory.
-template <class Op, int TW, bool LDS, bool ROUTE, int D>
+template <class Op, int TW, int NB, bool LDS, bool ROUTE, int D>
 __global__ __launch_bounds__(kWaves *kWave) void mx4_gate_up_kernel(Mx4Moe p, const float *logits, Plan *to_plan,
                                                                     __bf16 *hi, __bf16 *lo, int rows) {
   constexpr int TEAMS = kWaves / TW;
   __shared__ Plan r;
-  __shared__ v4f part[TW > 1 ? kWaves : 1][2][kWave];
+  __shared__ v4f part[TW > 1 ? kWaves : 1][2 * NB][kWave];
   extern __shared__ __attribute__((aligned(1024))) uint8_t moe_lds[];
   const int lane = threadIdx.x & 63, q = lane >> 4, c16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -229,21 +231,24 @@ __global__ __launch_bounds__(kWaves *kWave) void mx4_gate_up_kernel(Mx4Moe p, co
   const int n_used = __builtin_amdgcn_readfirstlane(r.n_used);
   const int team = wave / TW, tw = wave % TW;
   const int64_t bytes = l.block_bytes * l.blocks;
-  const int per = p.f / 16, groups = p.d / kMxGroup;
+  const int per = p.f / (16 * NB), groups = p.d / kMxGroup;
   const int items = n_used * per, stride = TEAMS * gridDim.x, first = team * gridDim.x + blockIdx.x;
   // the waves of a team, and where they wait for each other all teams, take as many rounds
   const int rounds = TW > 1 ? (items + stride - 1) / stride : items > first ? (items - first + stride - 1) / stride : 0;
   const int tiles = (l.kt + TW - 1) / TW;  // of a wave, per item
 
   int item = first, at = 0;  // the load cursor
-  const uint8_t *block[2] = {nullptr, nullptr};
+  const uint8_t *block[2 * NB] = {};  // gate, then up
   const typename Op::E *row = nullptr;
   auto enter = [&]() {
     if (item >= items) return;
     const int a = item / per, b = item - a * per;
     const int e = __builtin_amdgcn_readfirstlane(r.used[a].expert);
-    block[0] = expert_matrix(p.w_gate, p.ws_gate, e, p.E, bytes) + b * l.block_bytes;
-    block[1] = expert_matrix(p.w_up, p.ws_up, e, p.E, bytes) + b * l.block_bytes;
+#pragma unroll
+    for (int r = 0; r < NB; ++r) {
+      block[r] = expert_matrix(p.w_gate, p.ws_gate, e, p.E, bytes) + (b * NB + r) * l.block_bytes;
+      block[NB + r] = expert_matrix(p.w_up, p.ws_up, e, p.E, bytes) + (b * NB + r) * l.block_bytes;
+    }
     if constexpr (!LDS) {
       const Used u = r.used[a];  // columns behind the last token repeat the first
       const int t = r.row_token[u.row + (c16 < u.count ? c16 : 0)];
@@ -251,8 +256,8 @@ __global__ __launch_bounds__(kWaves *kWave) void mx4_gate_up_kernel(Mx4Moe p, co
     }
   };
   enter();
-  v4f acc[2][1] = {};
-  Mx4Weights<Op, 2, D> weights;
+  v4f acc[2 * NB][1] = {};
+  Mx4Weights<Op, 2 * NB, D> weights;
   typename Op::X x[LDS ? 1 : D][4];
   int done = first, step = 0;  // the item that is multiplied, and its tiles so far
   LdsPtr xrow = xs;
@@ -295,17 +300,21 @@ __global__ __launch_bounds__(kWaves *kWave) void mx4_gate_up_kernel(Mx4Moe p, co
         }
         if (++step < tiles) return;
         step = 0;
-        v4f g = acc[0][0], u = acc[1][0];
-        acc[0][0] = acc[1][0] = v4f{0.f, 0.f, 0.f, 0.f};
-        if constexpr (TW > 1) {
-          part[wave][0][lane] = g;
-          part[wave][1][lane] = u;
-          barrier_reads();
-          g = part[team * TW][0][lane], u = part[team * TW][1][lane];
+        v4f sums[2 * NB];
 #pragma unroll
-          for (int w = 1; w < TW; ++w) {
-            g += part[team * TW + w][0][lane];
-            u += part[team * TW + w][1][lane];
+        for (int r = 0; r < 2 * NB; ++r) {
+          sums[r] = acc[r][0];
+          acc[r][0] = v4f{0.f, 0.f, 0.f, 0.f};
+        }
+        if constexpr (TW > 1) {
+#pragma unroll
+          for (int r = 0; r < 2 * NB; ++r) part[wave][r][lane] = sums[r];
+          barrier_reads();
+#pragma unroll
+          for (int r = 0; r < 2 * NB; ++r) {
+            sums[r] = part[team * TW][r][lane];
+#pragma unroll
+            for (int w = 1; w < TW; ++w) sums[r] += part[team * TW + w][r][lane];
           }
           barrier_reads();  // the sums are read: they can be written again
         }
@@ -314,21 +323,25 @@ __global__ __launch_bounds__(kWaves *kWave) void mx4_gate_up_kernel(Mx4Moe p, co
           const Used us = r.used[a];
           const int e = __builtin_amdgcn_readfirstlane(us.expert);
           if (c16 < us.count) {
-            const uint8_t *bg = expert_matrix(p.w_gate, p.ws_gate, e, p.E, bytes) + b * l.block_bytes;
-            const uint8_t *bu = expert_matrix(p.w_up, p.ws_up, e, p.E, bytes) + b * l.block_bytes;
             const float weight = r.row_weight[us.row + c16];
-            const int64_t to = (int64_t)(us.row + c16) * p.f + mx4_channel(b, q * 4);
-            typedef __bf16 v4b __attribute__((ext_vector_type(4)));
-            v4b vh, vl;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float h = weight * silu_mul(g[i] * mx4_factor<Op>(bg, l, q * 4 + i),
-                                                u[i] * mx4_factor<Op>(bu, l, q * 4 + i));
-              vh[i] = (__bf16)h;
-              vl[i] = (__bf16)(h - (float)vh[i]);  // 16 bits of h's 24 in all
+            for (int k = 0; k < NB; ++k) {
+              const int at_b = b * NB + k;
+              const uint8_t *bg = expert_matrix(p.w_gate, p.ws_gate, e, p.E, bytes) + at_b * l.block_bytes;
+              const uint8_t *bu = expert_matrix(p.w_up, p.ws_up, e, p.E, bytes) + at_b * l.block_bytes;
+              const int64_t to = (int64_t)(us.row + c16) * p.f + mx4_channel(at_b, q * 4);
+              typedef __bf16 v4b __attribute__((ext_vector_type(4)));
+              v4b vh, vl;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float h = weight * silu_mul(sums[k][i] * mx4_factor<Op>(bg, l, q * 4 + i),
+                                                  sums[NB + k][i] * mx4_factor<Op>(bu, l, q * 4 + i));
+                vh[i] = (__bf16)h;
+                vl[i] = (__bf16)(h - (float)vh[i]);  // 16 bits of h's 24 in all
+              }
+              *reinterpret_cast<v4b *>(hi + to) = vh;
+              *reinterpret_cast<v4b *>(lo + to) = vl;
             }
-            *reinterpret_cast<v4b *>(hi + to) = vh;
-            *reinterpret_cast<v4b *>(lo + to) = vl;
           }
         }
         done += stride;
@@ -360,11 +373,16 @@ __global__ __launch_bounds__(W *kWave) void mx4_down_kernel(Mx4Moe p, const Plan
   const Mx4Layout l(p.d, p.f);
   const int64_t bytes = l.block_bytes * l.blocks;
   const int slice = blockIdx.x % slices, b0 = blockIdx.x / slices * NB, groups = p.f / kMxGroup;
-  // parts of an entry's K, at least two tiles each: two units and more to a wave
-  const int want = (2 * W * slices + n_used - 1) / n_used, most = (l.kt + 1) / 2;
-  const int tiles = (l.kt + (want < most ? want : most) - 1) / (want < most ? want : most);
-  const int parts = (l.kt + tiles - 1) / tiles, units = n_used * parts;
+  // A unit's tiles: of 1 .. 64, those that give the busiest wave the least to do, a unit's
+  // start and end counted as half a tile.  (Lane i looks at i + 1; the same in every wave.)
   const int first = slice * W + wave, stride = slices * W;
+  int tiles;
+  {
+    const int tl = lane + 1, n = n_used * ((l.kt + tl - 1) / tl);
+    const int cost = ((n + stride - 1) / stride) * (2 * (tl < l.kt ? tl : l.kt) + 1);
+    tiles = (wave_reduce(cost << 6 | lane, [](int a, int b) { return a < b ? a : b; }) & 63) + 1;
+  }
+  const int parts = (l.kt + tiles - 1) / tiles, units = n_used * parts;
   int total = 0;
   for (int u = first; u < units; u += stride) total += u % parts == parts - 1 ? l.kt - (parts - 1) * tiles : tiles;
 
@@ -496,16 +514,24 @@ DownPlan down_plan(const Mx4Moe &p) {
   return {4, slices < 16 ? slices : 16};
 }
 
-template <class Op, int TW, bool ROUTE>
-void launch_gate_up(const Mx4Moe &p, const float *scores, Plan *plan, __bf16 *hi, __bf16 *lo, int grid,
-                    hipStream_t stream) {
+template <class Op, bool ROUTE>
+void launch_gate_up(const Mx4Moe &p, const float *scores, Plan *plan, __bf16 *hi, __bf16 *lo, hipStream_t stream) {
   int rows = 1;
   while (rows < p.T) rows *= 2;
   const size_t lds = ((size_t)(p.d + 127) / 128 * rows * 256 + 1023) / 1024 * 1024;
-  if (lds <= kMoeLds)
-    mx4_gate_up_kernel<Op, TW, true, ROUTE, 4><<<grid, kWaves * kWave, lds, stream>>>(p, scores, plan, hi, lo, rows);
+  const bool in_lds = lds <= kMoeLds;
+  const int experts = (p.T * p.k_max < p.E ? p.T * p.k_max : p.E) + p.S;
+  const int most = experts * (p.f / (in_lds ? 16 : 32));  // items, where picks spread
+  const int grid = most < 2 * kCus ? most : 2 * kCus;
+  constexpr int kThreads = kWaves * kWave;
+  if (in_lds && most < kWaveItems)
+    mx4_gate_up_kernel<Op, 4, 1, true, ROUTE, 4><<<grid, kThreads, lds, stream>>>(p, scores, plan, hi, lo, rows);
+  else if (in_lds)
+    mx4_gate_up_kernel<Op, 1, 1, true, ROUTE, 4><<<grid, kThreads, lds, stream>>>(p, scores, plan, hi, lo, rows);
+  else if (most < kWaveItems)
+    mx4_gate_up_kernel<Op, 4, 2, false, ROUTE, 3><<<grid, kThreads, 0, stream>>>(p, scores, plan, hi, lo, 0);
   else
-    mx4_gate_up_kernel<Op, TW, false, ROUTE, 3><<<grid, kWaves * kWave, 0, stream>>>(p, scores, plan, hi, lo, 0);
+    mx4_gate_up_kernel<Op, 1, 2, false, ROUTE, 3><<<grid, kThreads, 0, stream>>>(p, scores, plan, hi, lo, 0);
 }
 
 template <class Op>
@@ -524,21 +550,12 @@ hipError_t launch_layer(const Mx4Moe &p, hipStream_t stream) {
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   const float *scores = p.logits_override ? p.logits_override : logits;
-  const int experts = (p.T * p.k_max < p.E ? p.T * p.k_max : p.E) + p.S;
-  const int most = experts * (p.f / 16);  // items, where picks spread
-  const int grid = most < 2 * kCus ? most : 2 * kCus;
   if (p.T <= kRouteTokens) {
-    if (most >= kWaveItems)
-      launch_gate_up<Op, 1, true>(p, scores, plan, hi, lo, grid, stream);
-    else
-      launch_gate_up<Op, 4, true>(p, scores, plan, hi, lo, grid, stream);
+    launch_gate_up<Op, true>(p, scores, plan, hi, lo, stream);
   } else {
     mx4_plan_kernel<<<1, kPlanWaves * kWave, 0, stream>>>(p, scores, plan);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    if (most >= kWaveItems)
-      launch_gate_up<Op, 1, false>(p, scores, plan, hi, lo, grid, stream);
-    else
-      launch_gate_up<Op, 4, false>(p, scores, plan, hi, lo, grid, stream);
+    launch_gate_up<Op, false>(p, scores, plan, hi, lo, stream);
   }
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int blocks = (p.d / 16 + down.nb - 1) / down.nb * down.slices;
