@@ -135,6 +135,87 @@ def test_streams_and_graphs():
         assert all(torch.equal(o, e) for (_, o), e in zip(graphs, eager)), k
 
 
+def test_a_decode_step_as_it_is_served():
+    """Norm, layer, norms and residual sum of a step on the same stream, eager and as a
+    replayed graph: each step against its own formula on what the step before gave."""
+    import norm_ref
+    layer = Layer(512, 256, 16, 4, 1)
+    g, t = layer.g, torch.bfloat16
+    w = [(1 + 0.2 * normal(g, (512,))).to(t) for _ in range(3)]
+    for T in (1, 7, 32):
+        x = normal(g, (T, 512), 1, t)
+
+        def step():
+            n = lib().rms_norm(x, w[0])
+            y = layer.op.forward(n)
+            return (n, y) + lib().norm_residual(x, y, w[1], None, w[2], scale=0.5)
+
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        for k in range(3):
+            x.copy_(normal(gen(k + T), (T, 512), 1, t))
+            graph.replay()
+            eager = step()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, eager)), k
+        n, y, r, m = eager
+        ref, err = norm_ref.forward(x, None, None, None, w[0], 1.0, 1e-6, 0.0)
+        within(n, ref[1], err[1], "n")
+        ids, p = mx4_ref.routing(layer.logits(n), layer.k)
+        within(y, *mx4_ref.layer(n, ids, p, layer.values[:16], layer.values[16:]), "y")
+        ref, err = norm_ref.forward(x, y, w[1], None, w[2], 0.5, 1e-6, 0.0)
+        within(r, ref[0], err[0], "r")
+        within(m, ref[1], err[1], "m")
+
+
+def debug_calls(monkeypatch):
+    """The package's new calls go to the device-checked build."""
+    import ctypes as C
+    m = lib()
+    if not m.DEBUG_LIB_PATH.exists():
+        pytest.fail("libfp8moe_debug.so is not built (fp8_moe_layer_amd/build.py --debug)")
+    dbg = C.CDLL(str(m.DEBUG_LIB_PATH))
+    for name, symbol in (("_mx4_forward", "moe_mx4_forward"), ("_matmul_mx4", "moe_matmul_mx4"),
+                         ("_ffn_mx4", "moe_ffn_mx4"), ("_norm_residual", "moe_norm_residual"),
+                         ("_norm_bwd", "moe_norm_residual_backward")):
+        fn, old = getattr(dbg, symbol), getattr(m, name)
+        fn.restype, fn.argtypes = old.restype, old.argtypes
+        monkeypatch.setattr(m, name, fn)
+
+
+@pytest.mark.parametrize("T", [2, 20])
+def test_debug_build(T, monkeypatch):
+    """The same bits as the release library on valid inputs; a budget outside its range
+    and a logit that is no number are named, and stay within bounds (the kernels clamp
+    the one and give the other's token some experts)."""
+    layer = Layer(256, 128, 8, 4, 1)
+    x = normal(layer.g, (T, 256), 1, torch.bfloat16)
+    w = torch.ones(256, device=dev(), dtype=torch.bfloat16)
+
+    def outputs():
+        y = layer.op.forward(x)
+        r, n, sy, sr = lib().norm_residual(x, y, w, None, w, save=True)
+        return (y, r, n) + lib().norm_residual_backward(r, n, x, y, sy, sr, w, None, w)
+
+    want = [o for o in outputs() if o is not None]
+    debug_calls(monkeypatch)
+    got = [o for o in outputs() if o is not None]
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    kpt = torch.full((T,), 4, dtype=torch.int32, device=dev())
+    kpt[1] = 9
+    with pytest.raises(lib().MoEError) as e:
+        layer.op.forward(x, k_per_token=kpt)
+    assert e.value.status == 7
+    logits = torch.zeros((T, 8), device=dev())
+    logits[0, 3] = torch.nan
+    with pytest.raises(lib().MoEError) as e:
+        layer.op.forward(x, logits_override=logits)
+    assert e.value.status == 7
+
+
 def test_refusals_on_the_device():
     f = lib()
     layer = Layer(64, 32, 4, 2)
