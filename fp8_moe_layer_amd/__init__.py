@@ -122,6 +122,7 @@ _matmul_mx4 = _sig("moe_matmul_mx4", _i32, _vp, _i64, _vp, _vp, _i32, _i32, _i32
 _matmul_mx4_ws = _sig("moe_matmul_mx4_workspace_bytes", C.c_size_t, _i32, _i32, _i32)
 _ffn_mx4 = _sig("moe_ffn_mx4", _i32, _vp, _i64, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, C.c_size_t, _vp)
 _ffn_mx4_ws = _sig("moe_ffn_mx4_workspace_bytes", C.c_size_t, _i32, _i32, _i32)
+_mx4_form = _sig("moe_mx4_form", _i32, _i32, _i32, _i32, _i32, C.POINTER(_i32))
 _mx4_workspace_bytes = _sig("moe_mx4_workspace_bytes", C.c_size_t, _DP)
 _mx4_forward = _sig("moe_mx4_forward", _i32, _DP, _i32, _vp, _i64, _vp, _vp, _vp, C.POINTER(_Mx4Weights),
                     _vp, _vp, _vp, _vp, _vp, C.c_size_t, _vp)
@@ -978,6 +979,19 @@ def gated_ffn_mx4(x: torch.Tensor, w_gate: Mx4Matrix, w_up: Mx4Matrix,
     ws, wsp, size = c.workspace(_ffn_mx4_size, T, d, f)
     c.run(_ffn_mx4, xp, ldx, gp, up, kind, T, d, f, at, wsp, size)
     return h
+
+
+_MX4_FORMS = {0: "none", 1: "stream 16", 2: "stream 32",
+              **{16 + i: f"tile {n}" for i, n in enumerate(("64x64", "64x128", "128x128", "128x256"))}}
+
+
+def mx4_form(op: str, T: int, inner: int, outputs: int):
+    """Which kernel matmul_mx4 or gated_ffn_mx4 takes for its sizes (moe_mx4_form):
+    (name, parts that K is cut into, waves along the channels of a stream).  A host
+    call."""
+    forms = (_i32 * 3)()
+    _check(_mx4_form(("matmul_mx4", "gated_ffn_mx4").index(op), T, inner, outputs, forms))
+    return _MX4_FORMS[forms[0]], forms[1], forms[2]
 
 
 @dataclass

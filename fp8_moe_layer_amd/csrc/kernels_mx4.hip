@@ -783,6 +783,18 @@ hipError_t launch_pack_mx4(const uint8_t *codes, const uint8_t *scales, int32_t 
   return hipGetLastError();
 }
 
+void mx4_form(int32_t T, int32_t K, int32_t N, bool gated, int32_t (&form)[3]) {
+  form[0] = form[1] = form[2] = 0;
+  if (T == 0) return;
+  if (T <= kFewTokens) {
+    const FewPlan f = few_plan(T, K, N, gated);
+    form[0] = kMx4Stream + f.xt - 1, form[1] = f.slices, form[2] = f.wr;
+  } else {
+    const TilePlan t = tile_plan(T, K, N, gated);
+    form[0] = kMx4Tile + t.tile, form[1] = t.slices, form[2] = 0;
+  }
+}
+
 size_t mx4_product_workspace(int32_t T, int32_t K, int32_t N, bool gated) {
   if (T == 0) return 0;
   const int slices = T <= kFewTokens ? few_plan(T, K, N, gated).slices : tile_plan(T, K, N, gated).slices;

@@ -10,7 +10,8 @@ using namespace fp8moe;
 
 static_assert(MOE_MX4_GROUP == kMxGroup && MOE_MX4_MAX_TOKENS == kMx4MaxTokens &&
                   MOE_MX4_MAX_SHARED == kMx4MaxShared && MOE_MAX_EXPERTS == kMaxExperts &&
-                  MOE_MAX_K == kMaxK, "limits");
+                  MOE_MAX_K == kMaxK && MOE_MX4_FORM_STREAM == kMx4Stream &&
+                  MOE_MX4_FORM_TILE == kMx4Tile, "limits and forms");
 
 namespace {
 
@@ -203,6 +204,17 @@ moe_status moe_ffn_mx4(const void *x, int64_t ldx, const void *w_gate, const voi
   const Mx4Product p{x, ldx, (const uint8_t *)w_gate, (const uint8_t *)w_up, nullptr, T, d, f, type,
                      type, h, workspace};
   return finish(launch_mx4_product(p, as_stream(stream)), fn);
+}
+
+moe_status moe_mx4_form(int32_t gated, int32_t T, int32_t inner, int32_t outputs, int32_t *forms) {
+  const char *fn = "moe_mx4_form";
+  moe_status s = gated ? check_block(fn, inner, outputs) : check_matrix(fn, outputs < 1 ? -1 : outputs, inner);
+  if (s || (s = check_rows(fn, T, inner, inner, 2))) return s;
+  if (!forms) return fail_status(MOE_ERR_NULL, "%s: forms is required", fn);
+  int32_t form[3];
+  mx4_form(T, inner, outputs, gated != 0, form);
+  for (int i = 0; i < 3; ++i) forms[i] = form[i];
+  return ok_status();
 }
 
 size_t moe_mx4_workspace_bytes(const moe_dims *dims) {

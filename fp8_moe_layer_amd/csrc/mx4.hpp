@@ -56,6 +56,10 @@ struct Mx4Product {
 };
 size_t mx4_product_workspace(int32_t T, int32_t K, int32_t N, bool gated);
 hipError_t launch_mx4_product(const Mx4Product &p, hipStream_t stream);
+// Which kernel the sizes take (MOE_MX4_FORM_* of the C ABI), in how many parts of K, with
+// how many waves along the channels (of a stream).
+enum : int32_t { kMx4Stream = 1 /* + 0, 1 */, kMx4Tile = 16 /* + 0..3 */ };
+void mx4_form(int32_t T, int32_t K, int32_t N, bool gated, int32_t (&form)[3]);
 
 // A whole MoE layer of up to kMx4MaxTokens tokens.  Expert e's matrices follow
 // each other by the packed size of one.

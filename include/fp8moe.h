@@ -661,6 +661,15 @@ enum {
 moe_status moe_dense_form(int32_t op, int32_t T, int32_t inner, int32_t outputs, int32_t workspace,
                           int32_t *forms /*host*/);
 
+/* The same of moe_ffn_mx4 (gated != 0) and moe_matmul_mx4 for T, d or K, f or N.
+ * forms [3], HOST memory: the kernel, the parts that K is cut into, and of a stream
+ * the waves along the channels.
+ *   MOE_MX4_FORM_STREAM + i   up to 16, 32 tokens
+ *   MOE_MX4_FORM_TILE + i     tiles of 64x64, 64x128, 128x128, 128x256
+ * Errors: MOE_ERR_SHAPE (sizes the operator refuses), MOE_ERR_NULL. */
+enum { MOE_MX4_FORM_NONE = 0, MOE_MX4_FORM_STREAM = 1, MOE_MX4_FORM_TILE = 16 };
+moe_status moe_mx4_form(int32_t gated, int32_t T, int32_t inner, int32_t outputs, int32_t *forms /*host*/);
+
 const char *moe_status_str(moe_status s);
 const char *moe_last_error(void); /* thread-local detail of this thread's last failing call */
 int32_t moe_abi_version(void);

@@ -123,6 +123,52 @@ def test_gated(T, d, f, dtype):
     within(h, ref, tol, f"{T}x{d}x{f}")
 
 
+# every kernel, cut along K and not, with every count of waves along the channels (mx4_form)
+FORMS = [
+    ("stream 16", False, 1, [(3, 544, 33), (1, 288, 96)]), ("stream 16", False, 2, [(2, 96, 8190), (2, 96, 8192)]),
+    ("stream 16", False, 4, [(9, 160, 14335), (9, 160, 14336)]), ("stream 16", True, 4, [(13, 6176, 65), (13, 6176, 96)]),
+    ("stream 32", False, 1, [(31, 544, 70), (17, 800, 64)]), ("stream 32", False, 2, [(19, 160, 14336), (19, 160, 8192)]),
+    ("stream 32", False, 4, [None, (32, 96, 14336)]), ("stream 32", True, 4, [(17, 4128, 100), None]),
+    ("stream 32", True, 8, [None, (27, 4128, 96)]),
+    ("tile 64x64", False, 0, [(45, 160, 67), (45, 160, 96)]), ("tile 64x64", True, 0, [(65, 2080, 35), (70, 1440, 64)]),
+    ("tile 64x128", False, 0, [(200, 160, 4097), (500, 160, 1056)]),
+    ("tile 64x128", True, 0, [(1500, 8192, 95), (130, 4096, 1024)]),
+    ("tile 128x128", False, 0, [(200, 96, 4097), (500, 96, 1056)]),
+    ("tile 128x128", True, 0, [(200, 4096, 4097), (500, 6176, 1056)]),
+    ("tile 128x256", False, 0, [(1000, 96, 4097), (2047, 96, 1056)]),
+    ("tile 128x256", True, 0, [(200, 8192, 4097), (1000, 4096, 1056)]),
+]
+
+
+@pytest.mark.parametrize("dtype", F16S)
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("name,cut,along,sizes", FORMS)
+def test_every_form(name, cut, along, sizes, gated, dtype):
+    if sizes[gated] is None:
+        pytest.skip("the rule does not give this form")
+    T, K, N = sizes[gated]
+    form = lib().mx4_form("gated_ffn_mx4" if gated else "matmul_mx4", T, K, N)
+    assert (form[0], form[1] > 1, form[2]) == (name, cut, along), form
+    g = gen(T + K + N)
+    x = strided(normal(g, (T, K), 1, dtype), 8)
+    (cg, sg), (cu, su) = matrix(g, N, K, 0.5), matrix(g, N, K, 0.5)
+    w = lib().pack_mx4(cg, sg)
+    if gated:
+        h, ok = guarded((T, N), dtype)
+        lib().gated_ffn_mx4(x, w, lib().pack_mx4(cu, su), out=h)
+        ok()
+        within(h, *mx4_ref.gated(x, mx4_ref.values(cg, sg), mx4_ref.values(cu, su)), str(form))
+        return
+    bias = normal(g, (N,))
+    ref, tol = mx4_ref.product(x, mx4_ref.values(cg, sg))
+    ref += bias.double()
+    for out in (dtype, torch.float32):
+        y, ok = guarded((T, N), out)
+        lib().matmul_mx4(x, w, bias=bias, out=y)
+        ok()
+        within(y, ref, tol + 2 * mx4_ref.U * ref.abs(), str(form))
+
+
 @pytest.mark.parametrize("dtype", F16S)
 @pytest.mark.parametrize("T", [1, 20, 70])
 def test_uneven_scales(T, dtype):

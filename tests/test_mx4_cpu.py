@@ -122,6 +122,24 @@ def test_gated_refuses(kw, code):
     assert fp8._last_error().startswith(b"moe_ffn_mx4")
 
 
+def test_forms_and_workspaces():
+    form = fp8.mx4_form
+    assert form("matmul_mx4", 1, 14336, 4096) == ("stream 16", 1, 1)
+    assert form("gated_ffn_mx4", 32, 2048, 768)[0] == "stream 32" and form("gated_ffn_mx4", 33, 2048, 768)[0][:4] == "tile"
+    assert form("gated_ffn_mx4", 8192, 4096, 14336) == ("tile 128x256", 1, 0)
+    assert form("matmul_mx4", 0, 64, 64) == ("none", 0, 0)
+    for T in (1, 5, 16, 17, 32, 33, 64, 300, 5000):
+        for K, N in ((32, 1), (1408, 2051), (14336, 4096), (65536, 96)):
+            parts = form("matmul_mx4", T, K, N)[1]
+            size = fp8._matmul_mx4_ws(T, K, N)
+            # a part's fp32 sums, tokens in sixteens and channels in 32s, or nothing
+            assert (size == 0) == (parts == 1)
+            assert size == 0 or size == parts * -(-T // 16) * 16 * -(-N // 32) * 32 * 4
+    for bad in (("matmul_mx4", 1, 40, 64), ("gated_ffn_mx4", 1, 64, 40), ("matmul_mx4", -1, 64, 64)):
+        with pytest.raises(fp8.MoEError, match="moe_mx4_form"):
+            form(*bad)
+
+
 def test_no_tokens_is_valid():
     assert quantize(rows=0, x=None, codes=None, scales=None) == OK
     assert dequantize(rows=0, codes=None, scales=None, y=None) == OK
