@@ -163,23 +163,24 @@ __global__ __launch_bounds__(256) void pack_mx4_kernel(const uint8_t *codes, con
 }
 
 // ---------------------------------------------------------------- epilogues
+// A lane's 4 P consecutive channels of token t, from their sums v, their rows' factors f
+// and the bias b.  (Factors and bias are asked for at a kernel's start: at its end they
+// would come from memory while nothing else does, 1.5 us.)
 template <class OUT>
 struct Mx4Out {
-  const float *bias;
   OUT *y;
   int32_t T, N;
-  // 4 P consecutive channels of token t
   template <int P>
-  __device__ __forceinline__ void store(int t, int ch, const v4f (&v)[P], const float (&f)[P][4]) const {
+  __device__ __forceinline__ void store(int t, int ch, const v4f (&v)[P], const v4f (&f)[P],
+                                        const v4f (&b)[P]) const {
     float o[4 * P];
 #pragma unroll
-    for (int i = 0; i < 4 * P; ++i)
-      o[i] = fmaf(v[i / 4][i % 4], f[i / 4][i % 4], bias && ch + i < N ? bias[ch + i] : 0.0f);
+    for (int i = 0; i < 4 * P; ++i) o[i] = fmaf(v[i / 4][i % 4], f[i / 4][i % 4], b[i / 4][i % 4]);
     store_run<OUT, 4 * P>(y + (int64_t)t * N + ch, o, N - ch);
   }
   template <int P>
-  __device__ __forceinline__ void store(int t, int ch, const v4f (&g)[P], const float (&fg)[P][4],
-                                        const v4f (&u)[P], const float (&fu)[P][4]) const {
+  __device__ __forceinline__ void store_gated(int t, int ch, const v4f (&g)[P], const v4f (&fg)[P],
+                                              const v4f (&u)[P], const v4f (&fu)[P]) const {
     float o[4 * P];
 #pragma unroll
     for (int i = 0; i < 4 * P; ++i)
@@ -188,11 +189,14 @@ struct Mx4Out {
   }
 };
 
+// Four rows' factors as they lie in memory, from row q*4 on.
+__device__ __forceinline__ v4f block_factors(const uint8_t *block, const Mx4Layout &l, int q) {
+  return reinterpret_cast<const v4f *>(block + l.factors)[q];
+}
+// A factor of the operand type's, from memory's.
 template <class Op>
-__device__ __forceinline__ void load_factors(const uint8_t *block, const Mx4Layout &l, int q,
-                                             float (&f)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = mx4_factor<Op>(block, l, q * 4 + i);
+__device__ __forceinline__ v4f op_factor(v4f f) {
+  return Op::kShift ? f * 0x1p-15f : f;
 }
 
 // ---------------------------------------------------------------- few tokens
@@ -256,23 +260,22 @@ FewPlan few_plan(int32_t T, int32_t K, int32_t N, bool gated) {
   return f;
 }
 
-// y's four channels of one token from their sums; the types of few tokens' outputs
-// are told apart here, at run time.
+// The same, four channels; the types of few tokens' outputs are told apart here, at run
+// time.
 template <class Op>
-__device__ __forceinline__ void few_store(const Mx4Product &p, int t, int ch, v4f v, const float (&f)[1][4]) {
+__device__ __forceinline__ void few_store(const Mx4Product &p, int t, int ch, v4f v, v4f f, v4f b) {
   if (t >= p.T || ch >= p.N) return;
-  const v4f a[1] = {v};
+  const v4f v1[1] = {v}, f1[1] = {op_factor<Op>(f)}, b1[1] = {b};
   if (p.out_type == kTypeF32)
-    Mx4Out<float>{p.bias, static_cast<float *>(p.y), p.T, p.N}.store(t, ch, a, f);
+    Mx4Out<float>{static_cast<float *>(p.y), p.T, p.N}.store(t, ch, v1, f1, b1);
   else
-    Mx4Out<typename Op::E>{p.bias, static_cast<typename Op::E *>(p.y), p.T, p.N}.store(t, ch, a, f);
+    Mx4Out<typename Op::E>{static_cast<typename Op::E *>(p.y), p.T, p.N}.store(t, ch, v1, f1, b1);
 }
 template <class Op>
-__device__ __forceinline__ void few_store(const Mx4Product &p, int t, int ch, v4f g, const float (&fg)[1][4],
-                                          v4f u, const float (&fu)[1][4]) {
+__device__ __forceinline__ void few_store_gated(const Mx4Product &p, int t, int ch, v4f g, v4f fg, v4f u, v4f fu) {
   if (t >= p.T || ch >= p.N) return;
-  const v4f a[1] = {g}, b[1] = {u};
-  Mx4Out<typename Op::E>{nullptr, static_cast<typename Op::E *>(p.y), p.T, p.N}.store(t, ch, a, fg, b, fu);
+  const v4f g1[1] = {g}, fg1[1] = {op_factor<Op>(fg)}, u1[1] = {u}, fu1[1] = {op_factor<Op>(fu)};
+  Mx4Out<typename Op::E>{static_cast<typename Op::E *>(p.y), p.T, p.N}.store_gated(t, ch, g1, fg1, u1, fu1);
 }
 
 template <class Op, int XT, int NB, bool GATED, int WR, int WK, int D>
@@ -280,6 +283,8 @@ __global__ __launch_bounds__(WR *WK *kWave) void mx4_few_kernel(Mx4Product p, in
                                                             int rows, v4f *partial) {
   constexpr int NR = GATED ? 2 * NB : NB, W = WR * WK;
   extern __shared__ __attribute__((aligned(1024))) uint8_t few_lds[];
+  // the factors of the workgroup's blocks [WR][NR][16], and its bias [WR][NB][16]
+  __shared__ __attribute__((aligned(256))) float factors[(WR * NR + 3) / 4 * 64], bias[(WR * NB + 3) / 4 * 64];
   const Mx4Layout l(p.N, p.K);
   const int lane = threadIdx.x & 63, q = lane >> 4, c16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -311,6 +316,21 @@ __global__ __launch_bounds__(WR *WK *kWave) void mx4_few_kernel(Mx4Product p, in
       const int byte = kt * 256 + (c16 ^ (t & 15)) * 16;
       dma16(rsrc, t < p.T && kt < n && byte < kbytes ? (uint32_t)(t * p.ldx * 2 + byte) : kPastEnd,
             lds_address(xs) + i * 1024);
+    }
+    if (slices == 1) {
+      // four blocks to an instruction; those behind the last repeat it
+      const int first = (blockIdx.x * WR) * NB;
+      if (wave < (WR * NR + 3) / 4) {
+        const int i = wave * 4 + q < WR * NR ? wave * 4 + q : WR * NR - 1, r = i % NR, b = first + i / NR * NB + r % NB;
+        dma4_from((GATED && r >= NB ? p.w1 : p.w0) + (int64_t)(b < l.blocks ? b : l.blocks - 1) * l.block_bytes +
+                      l.factors + c16 * 4,
+                  lds_address((LdsPtr)factors) + wave * 256);
+      }
+      if (p.bias && wave < (WR * NB + 3) / 4) {
+        const int ch = mx4_channel(first + wave * 4 + q, c16);
+        dma4_from(reinterpret_cast<const uint8_t *>(p.bias + (ch < p.N ? ch : p.N - 1)),
+                  lds_address((LdsPtr)bias) + wave * 256);
+      }
     }
     wait_dma<0>();
     barrier_reads();
@@ -354,15 +374,13 @@ __global__ __launch_bounds__(WR *WK *kWave) void mx4_few_kernel(Mx4Product p, in
       if constexpr (GATED) to[XT * kWave] = u;
       continue;
     }
-    float f[1][4], fu[1][4];
-    load_factors<Op>(p.w0 + b * l.block_bytes, l, q, f[0]);
     const int t = m * 16 + c16, ch = mx4_channel(b, q * 4);
-    if constexpr (GATED) {
-      load_factors<Op>(p.w1 + b * l.block_bytes, l, q, fu[0]);
-      few_store<Op>(p, t, ch, a, f, u, fu);
-    } else {
-      few_store<Op>(p, t, ch, a, f);
-    }
+    auto four = [&](const float *from, int i) { return *reinterpret_cast<const v4f *>(from + i * 16 + q * 4); };
+    if constexpr (GATED)
+      few_store_gated<Op>(p, t, ch, a, four(factors, g * NR + r), u, four(factors, g * NR + NB + r));
+    else
+      few_store<Op>(p, t, ch, a, four(factors, g * NR + r),
+                    p.bias ? four(bias, g * NB + r) : v4f{0.f, 0.f, 0.f, 0.f});
   }
 }
 
@@ -373,6 +391,15 @@ __global__ __launch_bounds__(256) void mx4_join_kernel(Mx4Product p, int slices,
   const int lane = threadIdx.x & 63, i = blockIdx.x * 4 + (threadIdx.x >> 6);
   const int b = i / xt, m = i % xt;
   if (b >= l.blocks) return;
+  const int q = lane >> 4, t = m * 16 + (lane & 15), ch = mx4_channel(b, q * 4);
+  const v4f f = block_factors(p.w0 + b * l.block_bytes, l, q);
+  v4f other{0.f, 0.f, 0.f, 0.f};  // the up matrix's factors, or the bias
+  if constexpr (GATED) {
+    other = block_factors(p.w1 + b * l.block_bytes, l, q);
+  } else if (p.bias) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) other[j] = p.bias[ch + j < p.N ? ch + j : p.N - 1];
+  }
   const int64_t step = (int64_t)l.blocks * (GATED ? 2 : 1) * xt * kWave;
   const v4f *at = partial + ((int64_t)b * (GATED ? 2 : 1) * xt + m) * kWave + lane;
   v4f a = at[0], u = a;
@@ -381,15 +408,10 @@ __global__ __launch_bounds__(256) void mx4_join_kernel(Mx4Product p, int slices,
     a += at[s * step];
     if constexpr (GATED) u += at[s * step + xt * kWave];
   }
-  float f[1][4], fu[1][4];
-  const int q = lane >> 4, t = m * 16 + (lane & 15), ch = mx4_channel(b, q * 4);
-  load_factors<Op>(p.w0 + b * l.block_bytes, l, q, f[0]);
-  if constexpr (GATED) {
-    load_factors<Op>(p.w1 + b * l.block_bytes, l, q, fu[0]);
-    few_store<Op>(p, t, ch, a, f, u, fu);
-  } else {
-    few_store<Op>(p, t, ch, a, f);
-  }
+  if constexpr (GATED)
+    few_store_gated<Op>(p, t, ch, a, f, u, other);
+  else
+    few_store<Op>(p, t, ch, a, f, other);
 }
 
 template <class Op, bool GATED, int XT, int NB, int WR, int WK, int D>
@@ -429,11 +451,10 @@ hipError_t launch_few(const Mx4Product &p, hipStream_t stream) {
 // (256 bytes a token, 16-byte piece i of token r at position i ^ r%16, so that 16
 // lanes that read one piece of 16 tokens touch all banks), the codes as they lie
 // in memory, a block's 1 KB after the other, and their scales, 64 bytes a block.  A
-// quarter of a step is a
-// group of 32 inputs: while its products run, the next quarter's activations are
-// read from LDS, and the codes turn into 16-bit operands just before their use.
-// One barrier a step, before the last quarter's products: there every wave has
-// read all of the step, whose stage is filled again, and the next one has landed.
+// quarter of a step is a group of 32 inputs: while its products run, the next quarter's
+// activations are read from LDS, and the codes turn into 16-bit operands just before
+// their use.  One barrier a step, before the last quarter's products: there every wave
+// has read all of the step, whose stage is filled again, and the next one has landed.
 template <int BM, int BN, int TM, int TN, int ST, int KG, bool GATED>
 struct Mx4Shape {
   static constexpr int kWaves = TM * TN, kThreads = KG * kWaves * kWave;
@@ -450,19 +471,12 @@ struct Mx4Shape {
   static_assert(KG == 1 || kRing >= BM * BN * 4, "the sums of a group fit its ring");
 };
 
-// 4 bytes a lane from memory to LDS at lds + 4 * lane; see dma16.
-__device__ __forceinline__ void dma4_from(const uint8_t *p, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
-               :
-               : "s"(lds), "v"(p)
-               : "memory");
-}
-
 template <class Op, class OUT, int BM, int BN, int TM, int TN, int ST, int KG, bool GATED>
 __global__ __launch_bounds__(KG *TM *TN *kWave) void mx4_tile_kernel(Mx4Product p, int tiles_m, int tiles_n, int slices, v4f *partial) {
   typedef Mx4Shape<BM, BN, TM, TN, ST, KG, GATED> S;
   constexpr int MS = S::MS, NR = S::NR, NC = S::NC, W = S::kWaves;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
+  __shared__ __attribute__((aligned(256))) float factors[BN], bias[S::kChannels < 64 ? 64 : S::kChannels];
   const Mx4Layout l(p.N, p.K);
   const int lane = threadIdx.x & 63, q = lane >> 4, c16 = lane & 15;
   const int all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -497,9 +511,6 @@ __global__ __launch_bounds__(KG *TM *TN *kWave) void mx4_tile_kernel(Mx4Product 
   const int spiece = wave % (BN / 64);
   static_assert(BN / 64 <= W, "a scale piece to a wave");
   const uint8_t *ssrc = source(spiece * 4 + q) + l.scales + c16 * 4;
-  const uint8_t *block[NR];
-#pragma unroll
-  for (int r = 0; r < NR; ++r) block[r] = source(wn * NR + r);
 
   auto piece = [&](int i, int k, uint32_t stage) {
     const int kt = k < l.kt ? k : l.kt - 1;
@@ -569,6 +580,16 @@ __global__ __launch_bounds__(KG *TM *TN *kWave) void mx4_tile_kernel(Mx4Product 
 #pragma unroll
   for (int k = 0; k < ST; ++k)
     if (k < nk) fetch(k0 + k, k * S::kStage);
+  // behind the ring's, whose counts of loads in flight hold with them all the more
+  if (slices == 1 && kg == 0) {
+    if (wave < BN / 64)
+      dma4_from(source(wave * 4 + q) + l.factors + c16 * 4, lds_address((LdsPtr)factors) + wave * 256);
+    if (!GATED && p.bias && wave < S::kChannels / 64) {
+      const int ch = mx4_channel(tile_b + wave * 4 + q, c16);
+      dma4_from(reinterpret_cast<const uint8_t *>(p.bias + (ch < p.N ? ch : p.N - 1)),
+                lds_address((LdsPtr)bias) + wave * 256);
+    }
+  }
   if (nk >= ST)
     wait_dma<(ST - 1) * S::kPieces>();
   else
@@ -647,18 +668,23 @@ __global__ __launch_bounds__(KG *TM *TN *kWave) void mx4_tile_kernel(Mx4Product 
     }
     return;
   }
-  const Mx4Out<OUT> out{p.bias, static_cast<OUT *>(p.y), p.T, p.N};
+  const Mx4Out<OUT> out{static_cast<OUT *>(p.y), p.T, p.N};
+  auto four = [&](const float *from, int i) { return *reinterpret_cast<const v4f *>(from + i * 16 + q * 4); };
   // pairs of blocks: eight consecutive channels a lane
   constexpr int P = NC % 2 == 0 ? 2 : 1;
 #pragma unroll
   for (int r = 0; r < NC; r += P) {
     const int ch = mx4_channel(b0 + r, q * 4);
     if (ch >= p.N) continue;
-    float f[P][4], fu[P][4];
+    v4f f[P], other[P];  // the up matrix's factors, or the bias
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      load_factors<Op>(block[r + i], l, q, f[i]);
-      if constexpr (GATED) load_factors<Op>(block[NC + r + i], l, q, fu[i]);
+      f[i] = op_factor<Op>(four(factors, wn * NR + r + i));
+      other[i] = v4f{0.f, 0.f, 0.f, 0.f};
+      if constexpr (GATED)
+        other[i] = op_factor<Op>(four(factors, wn * NR + NC + r + i));
+      else if (p.bias)
+        other[i] = four(bias, wn * NC + r + i);
     }
 #pragma unroll
     for (int m = 0; m < MS; ++m) {
@@ -671,9 +697,9 @@ __global__ __launch_bounds__(KG *TM *TN *kWave) void mx4_tile_kernel(Mx4Product 
         if constexpr (GATED) u[i] = acc[NC + r + i][m];
       }
       if constexpr (GATED)
-        out.template store<P>(t, ch, a, f, u, fu);
+        out.store_gated(t, ch, a, f, u, other);
       else
-        out.template store<P>(t, ch, a, f);
+        out.store(t, ch, a, f, other);
     }
   }
 }

@@ -262,10 +262,19 @@ __global__ __launch_bounds__(kWaves *kWave) void mx4_gate_up_kernel(Mx4Moe p, co
   int done = first, step = 0;  // the item that is multiplied, and its tiles so far
   LdsPtr xrow = xs;
   int xkey = 0;
+  v4f factor[2 * NB];  // asked for at an item's start: at its end they would hold it up
   auto begin = [&]() {
+    if (done >= items) return;
+    const Used u = r.used[done / per];
+    const int e = __builtin_amdgcn_readfirstlane(u.expert), b = done % per * NB;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const uint8_t *bg = expert_matrix(p.w_gate, p.ws_gate, e, p.E, bytes) + (b + k) * l.block_bytes;
+      const uint8_t *bu = expert_matrix(p.w_up, p.ws_up, e, p.E, bytes) + (b + k) * l.block_bytes;
+      factor[k] = reinterpret_cast<const v4f *>(bg + l.factors)[q];
+      factor[NB + k] = reinterpret_cast<const v4f *>(bu + l.factors)[q];
+    }
     if constexpr (LDS) {
-      if (done >= items) return;
-      const Used u = r.used[done / per];
       const int t = r.row_token[u.row + (c16 < u.count ? c16 : 0)];
       xrow = xs + t * 256;
       xkey = t & 15;
@@ -321,21 +330,19 @@ __global__ __launch_bounds__(kWaves *kWave) void mx4_gate_up_kernel(Mx4Moe p, co
         if (done < items && tw == 0) {
           const int a = done / per, b = done - a * per;
           const Used us = r.used[a];
-          const int e = __builtin_amdgcn_readfirstlane(us.expert);
+          constexpr float kUnit = Op::kShift ? 0x1p-15f : 1.0f;
           if (c16 < us.count) {
             const float weight = r.row_weight[us.row + c16];
 #pragma unroll
             for (int k = 0; k < NB; ++k) {
               const int at_b = b * NB + k;
-              const uint8_t *bg = expert_matrix(p.w_gate, p.ws_gate, e, p.E, bytes) + at_b * l.block_bytes;
-              const uint8_t *bu = expert_matrix(p.w_up, p.ws_up, e, p.E, bytes) + at_b * l.block_bytes;
               const int64_t to = (int64_t)(us.row + c16) * p.f + mx4_channel(at_b, q * 4);
               typedef __bf16 v4b __attribute__((ext_vector_type(4)));
               v4b vh, vl;
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const float h = weight * silu_mul(sums[k][i] * mx4_factor<Op>(bg, l, q * 4 + i),
-                                                  sums[NB + k][i] * mx4_factor<Op>(bu, l, q * 4 + i));
+                const float h = weight * silu_mul(sums[k][i] * (factor[k][i] * kUnit),
+                                                  sums[NB + k][i] * (factor[NB + k][i] * kUnit));
                 vh[i] = (__bf16)h;
                 vl[i] = (__bf16)(h - (float)vh[i]);  // 16 bits of h's 24 in all
               }

@@ -79,10 +79,6 @@ template <class Op>
 __device__ __forceinline__ float mx4_scale(uint32_t bytes, int j) {
   return __uint_as_float((((bytes >> (8 * j)) & 0xffu) << 23) + ((uint32_t)Op::kShift << 23));
 }
-template <class Op>
-__device__ __forceinline__ float mx4_factor(const uint8_t *block, const Mx4Layout &l, int row) {
-  return reinterpret_cast<const float *>(block + l.factors)[row] * (Op::kShift ? 0x1p-15f : 1.0f);
-}
 
 // Few tokens: what a wave has in flight of the stream of tiles of NR blocks of 16
 // rows against XT x 16 tokens, D tiles deep.  Loads return in the order of their
@@ -183,6 +179,14 @@ __device__ __forceinline__ void run_ring(int n, Load load, Use use, Ready ready)
         use(c, i + c);
         if (i + c + D < n) load(c, i + c + D);
       }
+}
+
+// 4 bytes a lane from memory to LDS at lds + 4 * lane; see dma16.
+__device__ __forceinline__ void dma4_from(const uint8_t *p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+               :
+               : "s"(lds), "v"(p)
+               : "memory");
 }
 
 // channel of row p of block b
