@@ -432,8 +432,10 @@ hipError_t launch_few_rows(const Mx4Product &p, const FewPlan &f, hipStream_t st
   constexpr int NB = GATED || XT == 1 ? 1 : 2, W = kFewWaves, D = XT == 1 ? 4 : 3;
   if (f.wr == 1) return launch_few_form<Op, GATED, XT, NB, 1, W, D>(p, f, stream);
   if (f.wr == 2) return launch_few_form<Op, GATED, XT, NB, 2, W / 2, D>(p, f, stream);
-  if (f.wr == 4) return launch_few_form<Op, GATED, XT, NB, 4, W / 4, D>(p, f, stream);
-  return launch_few_form<Op, GATED, XT, NB, 8, W / 8, D>(p, f, stream);
+  if constexpr (GATED && XT == 2) {  // no other has eight
+    if (f.wr == 8) return launch_few_form<Op, GATED, XT, NB, 8, W / 8, D>(p, f, stream);
+  }
+  return launch_few_form<Op, GATED, XT, NB, 4, W / 4, D>(p, f, stream);
 }
 
 template <class Op, bool GATED>

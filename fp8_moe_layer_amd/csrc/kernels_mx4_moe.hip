@@ -74,7 +74,7 @@ __global__ __launch_bounds__(kLogitThreads) void mx4_logits_kernel(Mx4Moe p, flo
 // What the experts in use are given: in LDS, and in the workspace for the launches
 // behind the one that made it.
 struct Plan {
-  int32_t n_used, n_rows, unused[2];
+  int32_t n_used, n_rows;
   Used used[kMaxUsed];
   uint8_t row_token[kMaxRows];  // by row of h
   float row_weight[kMaxRows];
@@ -258,7 +258,7 @@ __global__ __launch_bounds__(kWaves *kWave) void mx4_gate_up_kernel(Mx4Moe p, co
   enter();
   v4f acc[2 * NB][1] = {};
   Mx4Weights<Op, 2 * NB, D> weights;
-  typename Op::X x[LDS ? 1 : D][4];
+  v4i x[LDS ? 1 : D][4];
   int done = first, step = 0;  // the item that is multiplied, and its tiles so far
   LdsPtr xrow = xs;
   int xkey = 0;
@@ -358,6 +358,41 @@ __global__ __launch_bounds__(kWaves *kWave) void mx4_gate_up_kernel(Mx4Moe p, co
 }
 
 // ---------------------------------------------------------------- down
+// What a wave has in flight: D tiles of NB blocks, their rows' factors, and h.  Loads
+// return in the order of their issue, so h is asked for with its weights: asked for when
+// it is needed, it would come behind every weight in flight.  The factors go into the
+// groups' scales, so that the sums of several experts add up.
+template <int NB, int D>
+struct DownRing {
+  v4i w[D][NB];
+  uint32_t s[D][NB];
+  float f[D][NB];
+  v4i hi[D][4], lo[D][4];
+
+  // h(j, hi, lo): the lane's h of group j
+  template <class H>
+  __device__ __forceinline__ void load(int c, const uint8_t *const (&block)[NB], const Mx4Layout &l, int kt,
+                                       int lane, H h) {
+#pragma unroll
+    for (int r = 0; r < NB; ++r) {
+      w[c][r] = load16_nt(block[r] + (int64_t)kt * 1024 + lane * 16);
+      s[c][r] = *reinterpret_cast<const uint32_t *>(block[r] + l.scales + kt * 64 + (lane & 15) * 4);
+      f[c][r] = reinterpret_cast<const float *>(block[r] + l.factors)[lane & 15];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h(j, hi[c][j], lo[c][j]);
+  }
+  __device__ __forceinline__ void multiply(int c, v4f (&acc)[NB]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int r = 0; r < NB; ++r) {
+        const v4i a = mx4_operand<Mx4Bf16>(w[c][r][j], mx4_scale<Mx4Bf16>(s[c][r], j) * f[c][r]);
+        acc[r] = Mx4Bf16::mfma(a, lo[c][j], Mx4Bf16::mfma(a, hi[c][j], acc[r]));
+      }
+  }
+};
+
 // A workgroup takes NB blocks of outputs; its W waves and those of the `slices`
 // workgroups with the same outputs take units in turn, a unit being a part of an
 // entry's K.  A wave adds a unit's sums to its own copy of the outputs in LDS, by
@@ -419,19 +454,18 @@ __global__ __launch_bounds__(W *kWave) void mx4_down_kernel(Mx4Moe p, const Plan
     from = (int64_t)(u.row + (c16 < u.count ? c16 : 0)) * p.f + q * 8;
   };
   enter();
-  v4f acc[NB][1] = {};
-  Mx4Ring<Mx4Pair, 1, NB, D, true> ring;  // each expert has factors of its own
+  v4f acc[NB] = {};
+  DownRing<NB, D> ring;
   run_ring<D>(
       total,
       [&](int c, int) {
         const int kt = in.kt;
-        ring.load(c, block, l, kt, lane, [&](int j, int) {
-          Mx4Pair::X x{{0, 0, 0, 0}, {0, 0, 0, 0}};
+        ring.load(c, block, l, kt, lane, [&](int j, v4i &h, v4i &rest) {
+          h = rest = v4i{0, 0, 0, 0};
           if (kt * 4 + j < groups) {
-            x.hi = load16(hi + from + kt * 128 + j * 32);
-            x.lo = load16(lo + from + kt * 128 + j * 32);
+            h = load16(hi + from + kt * 128 + j * 32);
+            rest = load16(lo + from + kt * 128 + j * 32);
           }
-          return x;
         });
         if (++in.kt == in.end) {
           set(in, in.unit + stride);
@@ -445,10 +479,10 @@ __global__ __launch_bounds__(W *kWave) void mx4_down_kernel(Mx4Moe p, const Plan
         if (c16 < u.count) {
           v4f *to = reinterpret_cast<v4f *>(mine + plan.row_token[u.row + c16] * kOut + q * 4);
 #pragma unroll
-          for (int r = 0; r < NB; ++r) to[r * 4] += acc[r][0];
+          for (int r = 0; r < NB; ++r) to[r * 4] += acc[r];
         }
 #pragma unroll
-        for (int r = 0; r < NB; ++r) acc[r][0] = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < NB; ++r) acc[r] = v4f{0.f, 0.f, 0.f, 0.f};
         set(out, out.unit + stride);
       },
       [] {});

@@ -22,7 +22,6 @@ typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 // The matrix operand types.  kShift: what the scale bytes' exponents are raised
 // by, and the row factors lowered.
 struct Mx4Bf16 {
-  typedef v4i X;
   typedef __bf16 E;
   static constexpr int kShift = 0;
   template <int B>
@@ -34,7 +33,6 @@ struct Mx4Bf16 {
 // fp16: the values are exact where the group's scale is at least 2^-35 of the
 // row's largest, and rounded to steps of 2^-24 (of 24576 for the largest) below.
 struct Mx4F16 {
-  typedef v4i X;
   typedef _Float16 E;
   static constexpr int kShift = 15;
   template <int B>
@@ -42,30 +40,6 @@ struct Mx4F16 {
     return __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, scale, B));
   }
   static __device__ __forceinline__ v4f mfma(v4i w, v4i x, v4f c) { return OpF16::mfma(w, x, c); }
-};
-// fp32 activations as two bf16 each, 16 bits of their 24.
-struct Mx4Pair {
-  struct X {
-    v4i hi, lo;
-  };
-  static constexpr int kShift = 0;
-  template <int B>
-  static __device__ __forceinline__ int pair(uint32_t codes, float scale) {
-    return Mx4Bf16::pair<B>(codes, scale);
-  }
-  static __device__ __forceinline__ v4f mfma(v4i w, const X &x, v4f c) {
-    return OpBf16::mfma(w, x.lo, OpBf16::mfma(w, x.hi, c));
-  }
-  static __device__ __forceinline__ X split(const float (&v)[8]) {
-    typedef __bf16 v8 __attribute__((ext_vector_type(8)));
-    v8 hi, lo;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      hi[i] = (__bf16)v[i];
-      lo[i] = (__bf16)(v[i] - (float)hi[i]);
-    }
-    return X{__builtin_bit_cast(v4i, hi), __builtin_bit_cast(v4i, lo)};
-  }
 };
 
 // The operand of a group from the lane's dword of its codes.
@@ -81,55 +55,12 @@ __device__ __forceinline__ float mx4_scale(uint32_t bytes, int j) {
 }
 
 // Few tokens: what a wave has in flight of the stream of tiles of NR blocks of 16
-// rows against XT x 16 tokens, D tiles deep.  Loads return in the order of their
-// issue, so a tile's activations are asked for with its weights, D tiles ahead:
-// asked for when they are needed, they would come behind every weight in flight.
-// ABS: the rows' factors go into the scales (bf16 operands only), so that one
-// accumulator can take blocks of several matrices.
-template <class Op, int XT, int NR, int D, bool ABS = false>
-struct Mx4Ring {
-  v4i w[D][NR];
-  uint32_t s[D][NR];
-  float f[D][NR];
-  typename Op::X x[D][4][XT];
-
-  // Tile kt of the blocks into slot c.  load_x(j, m): the lane's activations of
-  // group j, tokens m*16 ...
-  template <class LoadX>
-  __device__ __forceinline__ void load(int c, const uint8_t *const (&block)[NR], const Mx4Layout &l,
-                                       int kt, int lane, LoadX load_x) {
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      w[c][r] = load16_nt(block[r] + (int64_t)kt * 1024 + lane * 16);
-      s[c][r] = *reinterpret_cast<const uint32_t *>(block[r] + l.scales + kt * 64 + (lane & 15) * 4);
-      if (ABS) f[c][r] = reinterpret_cast<const float *>(block[r] + l.factors)[lane & 15];
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int m = 0; m < XT; ++m) x[c][j][m] = load_x(j, m);
-  }
-  // acc[r][m] += the slot's products: element i of lane l is row (l/16)*4 + i,
-  // token m*16 + l%16
-  __device__ __forceinline__ void multiply(int c, v4f (&acc)[NR][XT]) const {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        const float sc = mx4_scale<Op>(s[c][r], j);
-        const v4i a = mx4_operand<Op>(w[c][r][j], ABS ? sc * f[c][r] : sc);
-#pragma unroll
-        for (int m = 0; m < XT; ++m) acc[r][m] = Op::mfma(a, x[c][j][m], acc[r][m]);
-      }
-  }
-};
-
-// The same with activations that are somewhere else (in LDS) when a tile is
-// multiplied: x(j, m) as load_x above.
+// rows, D tiles deep.
 template <class Op, int NR, int D>
 struct Mx4Weights {
   v4i w[D][NR];
   uint32_t s[D][NR];
+  // Tile kt of the blocks into slot c.
   __device__ __forceinline__ void load(int c, const uint8_t *const (&block)[NR], const Mx4Layout &l,
                                        int kt, int lane) {
 #pragma unroll
@@ -138,11 +69,13 @@ struct Mx4Weights {
       s[c][r] = *reinterpret_cast<const uint32_t *>(block[r] + l.scales + kt * 64 + (lane & 15) * 4);
     }
   }
+  // acc[r][m] += the slot's products: element i of lane l is row (l/16)*4 + i, token
+  // m*16 + l%16.  x(j, m): the lane's activations of group j, tokens m*16 ...
   template <int XT, class X>
   __device__ __forceinline__ void multiply(int c, X x, v4f (&acc)[NR][XT]) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      typename Op::X xs[XT];
+      v4i xs[XT];
 #pragma unroll
       for (int m = 0; m < XT; ++m) xs[m] = x(j, m);
 #pragma unroll
