@@ -538,17 +538,16 @@ __global__ __launch_bounds__(KG *TM *TN *kWave) void mx4_tile_kernel(Mx4Product 
     for (int m = 0; m < MS; ++m) acc[r][m] = v4f{0.f, 0.f, 0.f, 0.f};
 
   v4i fx[MS];
-  v2i cw[NR];  // the codes of half a step
+  v4i cw[NR];       // a step's codes
   uint32_t cs[NR];  // a step's scales
   v4i a[NR];        // the operands of a quarter
   auto read_x = [&](int m, int j, uint32_t stage) {
     fx[m] = lds_read16(ring + stage + (wm * S::WM + m * 16 + c16) * 256 + (((j * 4 + q) ^ c16) * 16));
   };
-  auto read_codes = [&](int half, uint32_t stage) {
+  auto read_codes = [&](uint32_t stage) {
 #pragma unroll
     for (int r = 0; r < NR; ++r)
-      cw[r] = *(const __attribute__((address_space(3))) v2i *)(ring + stage + S::kCodes +
-                                                                     (wn * NR + r) * 1024 + lane * 16 + half * 8);
+      cw[r] = lds_read16(ring + stage + S::kCodes + (wn * NR + r) * 1024 + lane * 16);
   };
   auto read_scales = [&](uint32_t stage) {
 #pragma unroll
@@ -558,7 +557,7 @@ __global__ __launch_bounds__(KG *TM *TN *kWave) void mx4_tile_kernel(Mx4Product 
   };
   auto convert = [&](int j) {
 #pragma unroll
-    for (int r = 0; r < NR; ++r) a[r] = mx4_operand<Op>(cw[r][j & 1], mx4_scale<Op>(cs[r], j));
+    for (int r = 0; r < NR; ++r) a[r] = mx4_operand<Op>(cw[r][j], mx4_scale<Op>(cs[r], j));
   };
   // the products of quarter j; a sub-tile's activations of the next quarter (stage
   // `next`) are read into the place of this one's as soon as they are used, and
@@ -599,7 +598,7 @@ __global__ __launch_bounds__(KG *TM *TN *kWave) void mx4_tile_kernel(Mx4Product 
   barrier_reads();
   uint32_t stage = 0;
   auto after = [&](uint32_t s) -> uint32_t { return s + S::kStage == S::kRing ? 0 : s + S::kStage; };
-  read_codes(0, 0);
+  read_codes(0);
   read_scales(0);
 #pragma unroll
   for (int m = 0; m < MS; ++m) read_x(m, 0, 0);
@@ -608,7 +607,6 @@ __global__ __launch_bounds__(KG *TM *TN *kWave) void mx4_tile_kernel(Mx4Product 
     convert(0);
     quarter(0, stage, true, -1, 0);
     convert(1);
-    read_codes(1, stage);
     quarter(1, stage, true, -1, 0);
     convert(2);
     quarter(2, stage, true, -1, 0);
@@ -617,7 +615,7 @@ __global__ __launch_bounds__(KG *TM *TN *kWave) void mx4_tile_kernel(Mx4Product 
   auto enter = [&]() {
     barrier_reads();
     stage = after(stage);
-    read_codes(0, stage);
+    read_codes(stage);
     read_scales(stage);
   };
   int k = 0;

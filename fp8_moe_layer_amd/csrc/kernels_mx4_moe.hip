@@ -387,7 +387,8 @@ struct DownRing {
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int r = 0; r < NB; ++r) {
-        const v4i a = mx4_operand<Mx4Bf16>(w[c][r][j], mx4_scale<Mx4Bf16>(s[c][r], j) * f[c][r]);
+        const float scale = __uint_as_float((s[c][r] >> (8 * j) & 0xffu) << 23);
+        const v4i a = mx4_operand<Mx4Bf16>(w[c][r][j], scale * f[c][r]);
         acc[r] = Mx4Bf16::mfma(a, lo[c][j], Mx4Bf16::mfma(a, hi[c][j], acc[r]));
       }
   }
