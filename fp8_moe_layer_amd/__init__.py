@@ -1043,8 +1043,8 @@ class Mx4Experts:
 class Mx4MoELayer:
     """One mixture-of-experts layer with 4-bit experts, for steps of up to
     MX4_MAX_TOKENS tokens (moe_mx4_forward): router, top-k, the picked and the
-    shared experts and their weighted sum in three launches on the current
-    stream.  w_router [E, d] and router_bias [E] fp32.  A workspace per stream is
+    shared experts and their weighted sum in three to five launches on the
+    current stream.  w_router [E, d] and router_bias [E] fp32.  A workspace per stream is
     allocated for the largest step so far and kept; a captured call has one of
     its own, which the graph keeps."""
 

@@ -3,7 +3,7 @@
 //
 //   logits   every expert's score of every token, summed in 64 bits
 //   plan     every token's experts, and the list of experts in use with their
-//            tokens (up to four tokens: by each gate/up workgroup for itself)
+//            tokens (up to eight tokens: by each gate/up workgroup for itself)
 //   gate/up  waves take (expert, up to 16 of its tokens, 16 channels):
 //            h = p * SiLU(g) * u, p the routing weight
 //   down     a workgroup takes 16 or 64 outputs and, in parts of K, the experts in
@@ -11,7 +11,11 @@
 //            by token
 //   join     of the workgroups with the same outputs, where there are several
 //
-// The weights of the experts in use are what bounds it.
+// The weights of the experts in use are what bounds it where there are many: 32 tokens of
+// 8 experts, 4096 x 14336, 169 us, 4.4 TB/s; 13 tokens of 64 experts, 2048 x 1408, 66 us,
+// 3.4 TB/s.  Where there are few it is the launches, each of which waits for the one
+// before: one token of 128 experts, 2048 x 768, 22 us (logits 3, gate/up and
+// the routing 11, down 8) where 21 MB would take 4.
 #include "dense.hpp"
 #include "elem_dev.hpp"
 #include "mx4_dev.hpp"
@@ -35,7 +39,7 @@ struct Used {
 // ---------------------------------------------------------------- logits
 // A workgroup takes an expert and four tokens; its threads four inputs at a time,
 // summed in 64 bits, so that two experts' order hardly ever hangs on rounding:
-// logit = fl32(sum + bias).
+// logit = fl32(sum + bias).  128 experts of 2048 inputs, one token: 3.2 us, a launch.
 constexpr int kLogitTokens = 4, kLogitThreads = 256;
 template <class E>
 __global__ __launch_bounds__(kLogitThreads) void mx4_logits_kernel(Mx4Moe p, float *logits) {
@@ -533,19 +537,22 @@ struct Space {
   }
 };
 
-// Up to here every gate/up workgroup routes for itself (one token 1 us); above, that
-// takes longer (13 tokens 8 us, 32 tokens 12) than a launch for it.
-constexpr int kRouteTokens = 4;
+// Up to here every gate/up workgroup routes for itself; above, that takes longer than a
+// launch for it.  (The layer of 128 experts, us, with and without that launch: one token
+// 23.5 and 22.2, eight 46.7 and 44.8; 13 tokens of 64 experts 65.9 and 69.2.)
+constexpr int kRouteTokens = 8;
 // Gate/up items from which on a wave takes one alone: below, four waves share it
-// (one token of the 128-expert layer, 384 items: 6.1 us with four, 7.5 with one; of the
-// 8-expert one, 1792: 22.3 and 20.9).
+// (one token of the 128-expert layer, 384 items: 22.0 us with four, 23.7 with one; of the
+// 8-expert one, 1792: 48.9 and 47.4).
 constexpr int kWaveItems = 1024;
 
 // What a wave reads of h for a tile is 8 KB whatever the entry's tokens, for 1 KB of
 // weights to a block: 64 outputs to a workgroup, in as many slices as fill the compute
-// units (twice as many: 13 tokens of the 64-expert layer 24 -> 30 us; 32 outputs 26),
-// and a launch to join them (2 us and more).  Where the weights are little that is not
-// worth it: 16 outputs to a workgroup.
+// units (twice as many: 13 tokens of the 64-expert layer 66 -> 74 us), and a launch to
+// join them (2 us and more).  Where the weights are little that is not worth it: 16
+// outputs to a workgroup.  (The layer with 16 and with 64: one token of 128 experts, 12.6
+// million weights, 22.0 and 22.9; four of them, up to 50 million, 40.0 and 33.4; one of
+// the 8-expert layer, 117 million, 54.9 and 47.4.)
 struct DownPlan {
   int nb, slices;
 };

@@ -476,9 +476,9 @@ moe_status moe_ffn_mx4(const void *x, int64_t ldx, const void *w_gate, const voi
                        size_t workspace_bytes, void *stream);
 
 /* Forward pass of a whole mixture-of-experts layer of a few tokens with 4-bit
- * experts, in three launches: router logits (or logits_override), top-k and
- * softmax weights, the picked experts' gated blocks, their down projections and
- * the weighted sum, and the shared experts.  Against moe_fused_forward: nothing
+ * experts, in three to five launches: router logits (or logits_override), top-k
+ * and softmax weights, the picked experts' gated blocks, their down projections
+ * and the weighted sum, and the shared experts.  Against moe_fused_forward: nothing
  * is permuted, activations are not quantised (bf16 or fp16 rows in and out,
  * `type`), and the logits are summed in 64 bits, then rounded to fp32; ids and
  * weights are moe_route_topk's of those.  SiLU(g) * u times the routing weight is
