@@ -12,8 +12,8 @@
 //   join     of the workgroups with the same outputs, where there are several
 //
 // The weights of the experts in use are what bounds it where there are many: 32 tokens of
-// 8 experts, 4096 x 14336, 169 us, 4.4 TB/s; 13 tokens of 64 experts, 2048 x 1408, 66 us,
-// 3.4 TB/s.  Where there are few it is the launches, each of which waits for the one
+// 8 experts, 4096 x 14336, 169 us, 4.4 TB/s; 13 tokens of 64 experts, 2048 x 1408, 61 us,
+// 3.6 TB/s.  Where there are few it is the launches, each of which waits for the one
 // before: one token of 128 experts, 2048 x 768, 22 us (logits 3, gate/up and
 // the routing 11, down 8) where 21 MB would take 4.
 #include "dense.hpp"
@@ -25,7 +25,6 @@ namespace fp8moe {
 
 namespace {
 
-constexpr int kWaves = 8;
 constexpr int kMaxRows = kMx4MaxTokens * (kMaxK + kMx4MaxShared);
 // entries of the list below: one to an expert in use, and one more for each 16 tokens
 // past the first 16
@@ -197,15 +196,14 @@ __device__ __forceinline__ const uint8_t *expert_matrix(const uint8_t *routed, c
 // the few-token products lay theirs.  Else a wave asks for them with its weights, and
 // what the L2 gives of them is the bound: hence 32 channels (32 tokens of the 8-expert
 // layer: 16 channels 120 us).
-constexpr int kMoeLds = 96 * 1024;
-
+//
 // logits: the tokens are routed here (ROUTE); else their plan is in memory.
-template <class Op, int TW, int NB, bool LDS, bool ROUTE, int D>
-__global__ __launch_bounds__(kWaves *kWave) void mx4_gate_up_kernel(Mx4Moe p, const float *logits, Plan *to_plan,
+template <class Op, int W, int TW, int NB, bool LDS, bool ROUTE, int D>
+__global__ __launch_bounds__(W *kWave) void mx4_gate_up_kernel(Mx4Moe p, const float *logits, Plan *to_plan,
                                                                     __bf16 *hi, __bf16 *lo, int rows) {
-  constexpr int TEAMS = kWaves / TW;
+  constexpr int TEAMS = W / TW;
   __shared__ Plan r;
-  __shared__ v4f part[TW > 1 ? kWaves : 1][2 * NB][kWave];
+  __shared__ v4f part[TW > 1 ? W : 1][2 * NB][kWave];
   extern __shared__ __attribute__((aligned(1024))) uint8_t moe_lds[];
   const int lane = threadIdx.x & 63, q = lane >> 4, c16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -215,7 +213,7 @@ __global__ __launch_bounds__(kWaves *kWave) void mx4_gate_up_kernel(Mx4Moe p, co
     // under way while the plan is made or read
     const v4u rsrc = buffer_of(static_cast<const uint8_t *>(p.x), (int64_t)(p.T - 1) * p.ldx * 2 + p.d * 2);
     const int shift = 31 - __builtin_clz(rows), pieces = (l.kt * rows + 3) / 4;
-    for (int i = wave; i < pieces; i += kWaves) {
+    for (int i = wave; i < pieces; i += W) {
       const int at = i * 4 + q, t = at & (rows - 1), kt = at >> shift, byte = kt * 256 + (c16 ^ (t & 15)) * 16;
       dma16(rsrc, t < p.T && byte < p.d * 2 ? (uint32_t)(t * p.ldx * 2 + byte) : kPastEnd,
             lds_address(xs) + i * 1024);
@@ -223,10 +221,10 @@ __global__ __launch_bounds__(kWaves *kWave) void mx4_gate_up_kernel(Mx4Moe p, co
   }
   if constexpr (ROUTE) {
     __shared__ Routing routing;
-    route_tokens<kWaves>(p, logits, routing, r);
-    if (blockIdx.x == 0) publish<kWaves>(p, routing, r, to_plan);
+    route_tokens<W>(p, logits, routing, r);
+    if (blockIdx.x == 0) publish<W>(p, routing, r, to_plan);
   } else {
-    read_plan<kWaves>(p, to_plan, r, true);
+    read_plan<W>(p, to_plan, r, true);
   }
   if constexpr (LDS) {
     wait_dma<0>();
@@ -362,12 +360,15 @@ __global__ __launch_bounds__(kWaves *kWave) void mx4_gate_up_kernel(Mx4Moe p, co
 }
 
 // ---------------------------------------------------------------- down
-// What a wave has in flight: D tiles of NB blocks, their rows' factors, and h.  Loads
+// What a wave has in flight: two tiles of NB blocks (three: 61 -> 61.5 us at 13 tokens of
+// the 64-expert layer), their rows' factors, and h.  Loads
 // return in the order of their issue, so h is asked for with its weights: asked for when
 // it is needed, it would come behind every weight in flight.  The factors go into the
 // groups' scales, so that the sums of several experts add up.
-template <int NB, int D>
+constexpr int kDownDepth = 2;
+template <int NB>
 struct DownRing {
+  static constexpr int D = kDownDepth;
   v4i w[D][NB];
   uint32_t s[D][NB];
   float f[D][NB];
@@ -402,7 +403,7 @@ struct DownRing {
 // workgroups with the same outputs take units in turn, a unit being a part of an
 // entry's K.  A wave adds a unit's sums to its own copy of the outputs in LDS, by
 // token; in the end the copies are added in wave order.
-template <class OUT, int NB, int W, int D>
+template <class OUT, int NB, int W>
 __global__ __launch_bounds__(W *kWave) void mx4_down_kernel(Mx4Moe p, const Plan *from_plan,
                                                                  const __bf16 *hi, const __bf16 *lo, int slices,
                                                                  float *partial) {
@@ -460,8 +461,8 @@ __global__ __launch_bounds__(W *kWave) void mx4_down_kernel(Mx4Moe p, const Plan
   };
   enter();
   v4f acc[NB] = {};
-  DownRing<NB, D> ring;
-  run_ring<D>(
+  DownRing<NB> ring;
+  run_ring<kDownDepth>(
       total,
       [&](int c, int) {
         const int kt = in.kt;
@@ -548,7 +549,7 @@ constexpr int kWaveItems = 1024;
 
 // What a wave reads of h for a tile is 8 KB whatever the entry's tokens, for 1 KB of
 // weights to a block: 64 outputs to a workgroup, in as many slices as fill the compute
-// units (twice as many: 13 tokens of the 64-expert layer 66 -> 74 us), and a launch to
+// units (twice as many: 13 tokens of the 64-expert layer 12 % more), and a launch to
 // join them (2 us and more).  Where the weights are little that is not worth it: 16
 // outputs to a workgroup.  (The layer with 16 and with 64: one token of 128 experts, 12.6
 // million weights, 22.0 and 22.9; four of them, up to 50 million, 40.0 and 33.4; one of
@@ -568,19 +569,24 @@ void launch_gate_up(const Mx4Moe &p, const float *scores, Plan *plan, __bf16 *hi
   int rows = 1;
   while (rows < p.T) rows *= 2;
   const size_t lds = ((size_t)(p.d + 127) / 128 * rows * 256 + 1023) / 1024 * 1024;
-  const bool in_lds = lds <= kMoeLds;
   const int experts = (p.T * p.k_max < p.E ? p.T * p.k_max : p.E) + p.S;
-  const int most = experts * (p.f / (in_lds ? 16 : 32));  // items, where picks spread
-  const int grid = most < 2 * kCus ? most : 2 * kCus;
-  constexpr int kThreads = kWaves * kWave;
-  if (in_lds && most < kWaveItems)
-    mx4_gate_up_kernel<Op, 4, 1, true, ROUTE, 4><<<grid, kThreads, lds, stream>>>(p, scores, plan, hi, lo, rows);
-  else if (in_lds)
-    mx4_gate_up_kernel<Op, 1, 1, true, ROUTE, 4><<<grid, kThreads, lds, stream>>>(p, scores, plan, hi, lo, rows);
-  else if (most < kWaveItems)
-    mx4_gate_up_kernel<Op, 4, 2, false, ROUTE, 3><<<grid, kThreads, 0, stream>>>(p, scores, plan, hi, lo, 0);
+  const int half = experts * (p.f / 32), items = 2 * half;  // where picks spread
+  auto grid = [](int n) { return n < 2 * kCus ? n : 2 * kCus; };
+  // Beside the activations LDS holds the plan, and what routing and shared items need (up
+  // to 46 KB with four waves to an item, 30 with one).  Where a wave takes an item alone,
+  // one workgroup of 16 waves to a compute unit: two of eight hardly fit, and each would
+  // fetch all activations (13 tokens of the 64-expert layer 67 -> 61 us, 8 of the 8-expert
+  // layer 137 -> 128).
+  if (items < kWaveItems && lds <= 96 * 1024)
+    mx4_gate_up_kernel<Op, 8, 4, 1, true, ROUTE, 4>
+        <<<grid(items), 8 * kWave, lds, stream>>>(p, scores, plan, hi, lo, rows);
+  else if (items >= kWaveItems && lds <= 128 * 1024)
+    mx4_gate_up_kernel<Op, 16, 1, 1, true, ROUTE, 4><<<kCus, 16 * kWave, lds, stream>>>(p, scores, plan, hi, lo, rows);
+  else if (half < kWaveItems)
+    mx4_gate_up_kernel<Op, 8, 4, 2, false, ROUTE, 3>
+        <<<grid(half), 8 * kWave, 0, stream>>>(p, scores, plan, hi, lo, 0);
   else
-    mx4_gate_up_kernel<Op, 1, 2, false, ROUTE, 3><<<grid, kThreads, 0, stream>>>(p, scores, plan, hi, lo, 0);
+    mx4_gate_up_kernel<Op, 8, 1, 2, false, ROUTE, 3><<<grid(half), 8 * kWave, 0, stream>>>(p, scores, plan, hi, lo, 0);
 }
 
 template <class Op>
@@ -609,10 +615,10 @@ hipError_t launch_layer(const Mx4Moe &p, hipStream_t stream) {
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int blocks = (p.d / 16 + down.nb - 1) / down.nb * down.slices;
   if (down.nb == 1)
-    mx4_down_kernel<E, 1, 16, 2>
+    mx4_down_kernel<E, 1, 16>
         <<<blocks, 16 * kWave, (size_t)16 * p.T * 16 * 4, stream>>>(p, plan, hi, lo, down.slices, partial);
   else
-    mx4_down_kernel<E, 4, 8, 3>
+    mx4_down_kernel<E, 4, 8>
         <<<blocks, 8 * kWave, (size_t)8 * p.T * 64 * 4, stream>>>(p, plan, hi, lo, down.slices, partial);
   if ((e = hipGetLastError()) != hipSuccess || down.slices == 1) return e;
   mx4_moe_join_kernel<E><<<(p.T * p.d / 4 + 255) / 256, 256, 0, stream>>>(p, down.slices, partial);
