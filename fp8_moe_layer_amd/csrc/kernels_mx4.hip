@@ -467,7 +467,7 @@ hipError_t launch_few(const Mx4Product &p, hipStream_t stream) {
 //
 // 8192 x 4096 x 2 x 14336 gated takes 1470 us (1.31 PFLOP/s; 1312 us on zeros, which run
 // the same instructions at less power), 4096 x 14336 x 4096 355 (1.35 PFLOP/s).  Matrix
-// instructions are busy 59 % of the time at 2.1 GHz; beside them each wave turns codes
+// instructions are busy 59 % of the cycles; beside them each wave turns codes
 // into operands, 5 instructions to 4 products of a 64 x 64 wave tile, twice in all (both
 // rows of waves).  Tiles of 256 x 256 and 128 x 512 were slower: their accumulators leave
 // too few registers.
