@@ -435,11 +435,12 @@ class _Call:
     runs with that device current.  A small product takes the GPU 3 us, so the
     checks are kept cheap: torch.cuda.current_stream alone builds an object in
     1.9 us, the raw handle comes in 0.1."""
-    __slots__ = ("dev", "index", "stream", "alloc")
+    __slots__ = ("first", "dev", "index", "stream", "alloc")
 
     def __init__(self, first: torch.Tensor, stream):
         if not first.is_cuda:
             raise ValueError("fp8_moe_layer_amd works on device tensors only")
+        self.first = first
         dev = self.dev = first.device
         self.index = first.get_device()
         self.alloc = stream
@@ -478,7 +479,7 @@ class _Call:
 
     def empty(self, shape, dtype):
         if self.alloc is None:
-            return torch.empty(shape, dtype=dtype, device=self.dev)
+            return self.first.new_empty(shape, dtype=dtype)  # (0.2 us less than torch.empty)
         with _on(self.alloc):
             return torch.empty(shape, dtype=dtype, device=self.dev)
 
@@ -1044,9 +1045,9 @@ class Mx4MoELayer:
     """One mixture-of-experts layer with 4-bit experts, for steps of up to
     MX4_MAX_TOKENS tokens (moe_mx4_forward): router, top-k, the picked and the
     shared experts and their weighted sum in three to five launches on the
-    current stream.  w_router [E, d] and router_bias [E] fp32.  A workspace per stream is
-    allocated for the largest step so far and kept; a captured call has one of
-    its own, which the graph keeps."""
+    current stream.  w_router [E, d] and router_bias [E] fp32.  A workspace per
+    stream is allocated for the largest step so far and kept; a captured call has
+    one of its own, which the graph keeps."""
 
     def __init__(self, weights: Mx4Experts, w_router: Optional[torch.Tensor], k_max: int,
                  router_bias: Optional[torch.Tensor] = None):
@@ -1078,6 +1079,9 @@ class Mx4MoELayer:
         return step
 
     def _workspace(self, c: _Call, n: int):
+        if torch.cuda.current_device() != c.index:  # the stream that counts is the layer's device's
+            with torch.cuda.device(c.dev):
+                return self._workspace(c, n)
         with _on(c.alloc):
             capturing = torch.cuda.is_current_stream_capturing()
         if capturing:
@@ -1095,7 +1099,7 @@ class Mx4MoELayer:
         k_per_token int32 [T]; logits_override fp32 [T, E]; topk_ids int32 and
         topk_w fp32 [T, k_max]: where the picks are written, if given."""
         T, d = _shape2(x, "x")
-        _no_autograd("Mx4MoELayer.forward", x, logits_override)
+        _no_autograd("Mx4MoELayer.forward", x, logits_override, self.w_router, self.router_bias)
         c = _Call(x, stream)
         if c.index != self._index:
             raise ValueError(f"x is on {c.dev}, the weights are on cuda:{self._index}")

@@ -246,3 +246,36 @@ def test_refusals_on_the_device():
         f.Mx4MoELayer(layer.op.w, layer.router[:2], 2)
     with pytest.raises(ValueError, match="codes: expected shape"):
         layer.op.w.set_expert("gate", 0, *f.quantize_rows_mx4(torch.ones((64, 32), device=dev())))
+
+
+def test_inputs_that_autograd_records_are_refused():
+    """Every call of the set, for each tensor whose gradient would be lost; under
+    no_grad they pass, and forward-mode tangents are refused too."""
+    f = lib()
+    new = lambda *shape, dtype=torch.bfloat16: torch.ones(shape, dtype=dtype, device=dev())
+    layer = Layer(64, 32, 4, 2, bias=True)
+    w = f.pack_mx4(*f.quantize_rows_mx4(new(32, 64)))
+    x, y, v, rstd = new(2, 64), new(2, 64), new(64), new(2, dtype=torch.float32)
+    calls = [
+        (f.quantize_rows_mx4, [x]), (lambda a, b: f.matmul_mx4(a, w, b), [x, new(32, dtype=torch.float32)]),
+        (lambda a: f.gated_ffn_mx4(a, w, w), [x]), (f.rms_norm, [x, v]),
+        (f.norm_residual, [x, y, v, new(1, 64), v]),
+        (lambda a, b, c, d: f.rms_norm_backward(a, b, c, rstd, dr=d), [x, y, v, x]),
+        (lambda a, b, c, d, e, g, h: f.norm_residual_backward(a, b, c, d, rstd, rstd, e, g, h),
+         [x, x, y, y, v, new(1, 64), v]),
+        (layer.op.forward, [x]),
+        (lambda a, b: f.Mx4MoELayer(layer.op.w, a, 2, b).forward(x), [layer.router, layer.bias]),
+    ]
+    for call, tensors in calls:
+        call(*tensors)
+        for i in range(len(tensors)):
+            one = [t.clone().requires_grad_(j == i) for j, t in enumerate(tensors)]
+            with pytest.raises(RuntimeError, match="not recorded by autograd"):
+                call(*one)
+            with torch.no_grad():
+                call(*one)
+            with torch.autograd.forward_ad.dual_level():
+                dual = [torch.autograd.forward_ad.make_dual(t, t) if j == i else t
+                        for j, t in enumerate(tensors)]
+                with pytest.raises(RuntimeError):
+                    call(*dual)

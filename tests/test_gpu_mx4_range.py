@@ -85,3 +85,30 @@ def test_longest_rows_and_strides(T):
     within(lib().matmul_mx4(x, lib().pack_mx4(codes, scales), out_dtype=torch.float32), ref, tol, "y")
     with pytest.raises(lib().MoEError, match="row stride"):
         lib().matmul_mx4(torch.empty((2, ld + 8), dtype=BF, device=dev())[:, :K], lib().pack_mx4(codes, scales))
+
+
+@pytest.mark.parametrize("T", [2, 30])
+def test_experts_past_4_gib(T):
+    """The last experts of matrices of more than 4 GiB give what they give alone."""
+    d, f, E = 4096, 8192, 256
+    g = gen(6)
+    two = lib().Mx4Experts.empty(2, d, f, 1)
+    many = lib().Mx4Experts.empty(E, d, f, 1)
+    assert many.w_gate.numel() > 1 << 32 and many.w_down.numel() > 1 << 32
+    for i, e in enumerate((E - 2, E - 1)):
+        for which, shape in (("gate", (f, d)), ("up", (f, d)), ("down", (d, f))):
+            codes, scales = lib().quantize_rows_mx4(normal(g, shape, shape[1] ** -0.5))
+            two.set_expert(which, i, codes, scales)
+            many.set_expert(which, e, codes, scales)
+            if i == 0:
+                for w in (two, many):
+                    w.set_expert(which, 0, codes, scales, shared=True)
+    x = normal(g, (T, d), 1, BF)
+    logits = torch.zeros((T, E), device=dev())
+    logits[:, -2:] = normal(g, (T, 2)) + 50
+    ids = torch.empty((T, 2), dtype=torch.int32, device=dev())
+    y = lib().Mx4MoELayer(many, None, 2).forward(x, logits_override=logits, topk_ids=ids)
+    assert bool((ids >= E - 2).all()) and bool(y.isfinite().all())
+    want = lib().Mx4MoELayer(two, None, 2).forward(x, logits_override=logits[:, -2:].contiguous())
+    # both round once to bf16 (half a step each); the sums are the same products in another order
+    within(y, want.double(), 2.0 ** -8 * want.double().abs() + 2.0 ** -14 * want.double().abs().max(), "y")
