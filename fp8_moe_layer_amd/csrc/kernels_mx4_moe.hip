@@ -14,7 +14,7 @@
 // The weights of the experts in use are what bounds it where there are many: 32 tokens of
 // 8 experts, 4096 x 14336, 169 us, 4.4 TB/s; 13 tokens of 64 experts, 2048 x 1408, 61 us,
 // 3.6 TB/s.  Where there are few it is the launches, each of which waits for the one
-// before: one token of 128 experts, 2048 x 768, 22 us (logits 3, gate/up and
+// before: one token of 128 experts, 2048 x 768, 21.6 us (logits 3, gate/up and
 // the routing 11, down 8) where 21 MB would take 4.
 #include "dense.hpp"
 #include "elem_dev.hpp"
@@ -546,6 +546,10 @@ constexpr int kRouteTokens = 8;
 // (one token of the 128-expert layer, 384 items: 22.0 us with four, 23.7 with one; of the
 // 8-expert one, 1792: 48.9 and 47.4).
 constexpr int kWaveItems = 1024;
+// Up to here all eight waves of a workgroup share one (one token of two experts of 4096 x
+// 1536, 192 items: 18.1 us, with four waves 20.4; of the 128-expert layer 21.6 and 22.1;
+// 704 items 27.3 and 26.9).
+constexpr int kTeamItems = 2 * kCus;
 
 // What a wave reads of h for a tile is 8 KB whatever the entry's tokens, for 1 KB of
 // weights to a block: 64 outputs to a workgroup, in as many slices as fill the compute
@@ -573,11 +577,14 @@ void launch_gate_up(const Mx4Moe &p, const float *scores, Plan *plan, __bf16 *hi
   const int half = experts * (p.f / 32), items = 2 * half;  // where picks spread
   auto grid = [](int n) { return n < 2 * kCus ? n : 2 * kCus; };
   // Beside the activations LDS holds the plan, and what routing and shared items need (up
-  // to 46 KB with four waves to an item, 30 with one).  Where a wave takes an item alone,
+  // to 46 KB with several waves to an item, 30 with one).  Where a wave takes an item alone,
   // one workgroup of 16 waves to a compute unit: two of eight hardly fit, and each would
   // fetch all activations (13 tokens of the 64-expert layer 67 -> 61 us, 8 of the 8-expert
   // layer 137 -> 128).
-  if (items < kWaveItems && lds <= 96 * 1024)
+  if (items <= kTeamItems && lds <= 96 * 1024)
+    mx4_gate_up_kernel<Op, 8, 8, 1, true, ROUTE, 2>
+        <<<items, 8 * kWave, lds, stream>>>(p, scores, plan, hi, lo, rows);
+  else if (items < kWaveItems && lds <= 96 * 1024)
     mx4_gate_up_kernel<Op, 8, 4, 1, true, ROUTE, 4>
         <<<grid(items), 8 * kWave, lds, stream>>>(p, scores, plan, hi, lo, rows);
   else if (items >= kWaveItems && lds <= 128 * 1024)

@@ -57,9 +57,10 @@ def test_tokens_and_shapes(d, f, E, k, S, dtype):
         layer.check(strided(normal(layer.g, (T, d), 1, dtype), 8 if T % 2 else 0), what=f"T {T}")
 
 
-@pytest.mark.parametrize("T,d,f,E,k", [(8, 6144, 32, 3, 2), (8, 6176, 32, 3, 2), (8, 8192, 256, 64, 8), (8, 8224, 256, 64, 8),
-                                       (16, 3200, 32, 5, 4), (32, 2048, 512, 40, 8), (32, 2080, 512, 40, 8),
-                                       (9, 4096, 1056, 16, 16)])
+@pytest.mark.parametrize("T,d,f,E,k", [
+    (8, 6144, 32, 3, 2), (8, 6176, 32, 3, 2), (8, 8192, 256, 64, 8), (8, 8224, 256, 64, 8),
+    (8, 8224, 512, 64, 8), (16, 3200, 32, 5, 4), (32, 2048, 512, 40, 8), (32, 2080, 512, 40, 8),
+    (32, 2080, 512, 64, 8), (9, 4096, 1056, 16, 16)])
 def test_activations_at_the_ends_of_what_lds_holds(T, d, f, E, k):
     """The most that fits beside the plan, with items for a wave each and for several
     waves together, and a little more than that."""
