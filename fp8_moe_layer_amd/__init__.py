@@ -982,7 +982,7 @@ def gated_ffn_mx4(x: torch.Tensor, w_gate: Mx4Matrix, w_up: Mx4Matrix,
 
 
 _MX4_FORMS = {0: "none", 1: "stream 16", 2: "stream 32",
-              **{16 + i: f"tile {n}" for i, n in enumerate(("64x64", "64x128", "128x128", "128x256"))}}
+              **{16 + i: f"tile {n}" for i, n in enumerate(("32x128", "64x128", "64x256", "128x256"))}}
 
 
 def mx4_form(op: str, T: int, inner: int, outputs: int):

@@ -465,12 +465,12 @@ hipError_t launch_few(const Mx4Product &p, hipStream_t stream) {
 // their use.  One barrier a step, before the last quarter's products: there every wave
 // has read all of the step, whose stage is filled again, and the next one has landed.
 //
-// 8192 x 4096 x 2 x 14336 gated takes 1470 us (1.31 PFLOP/s; 1312 us on zeros, which run
-// the same instructions at less power), 4096 x 14336 x 4096 355 (1.35 PFLOP/s).  Matrix
-// instructions are busy 59 % of the cycles; beside them each wave turns codes
-// into operands, 5 instructions to 4 products of a 64 x 64 wave tile, twice in all (both
-// rows of waves).  Tiles of 256 x 256 and 128 x 512 were slower: their accumulators leave
-// too few registers.
+// The waves stand side by side along the channels (TM is 1): each code is turned into an
+// operand once, 5 instructions to a group of 16 rows and 2 to 8 products.  With two rows of
+// waves every code is turned twice, with half the reads of activations from LDS: 128 x 256
+// tiles took 1474 us instead of 1400 at 8192 x 4096 x 2*14336, 115 instead of 106 at 512 x
+// 8192 x 16384.  Now 1.37 PFLOP/s; 4096 x 14336 x 4096 338 us, 1.42 PFLOP/s.  Tiles of 256 x
+// 256 and 128 x 512 were slower: their accumulators leave too few registers.
 template <int BM, int BN, int TM, int TN, int ST, int KG, bool GATED>
 struct Mx4Shape {
   static constexpr int kWaves = TM * TN, kThreads = KG * kWaves * kWave;
@@ -721,12 +721,14 @@ __global__ __launch_bounds__(KG *TM *TN *kWave) void mx4_tile_kernel(Mx4Product 
 // ---------------------------------------------------------------- launch
 // The tiles, and what a step of 128 inputs of one takes with a workgroup on every
 // compute unit (us; measured at 256 and 512 workgroups).  The small tiles are bound by
-// the loads from the L2, 10-12 TB/s in all.
+// the loads from the L2, 10-15 TB/s in all: a token's activations are 256 bytes a step, a
+// channel's codes 68, hence wide ones (64 x 64 for 32 x 128: 256 x 4096 x 4096 16.4 us
+// instead of 14.6; 128 x 128 for 64 x 256: 512 x 8192 x 8192 69.6 instead of 63.8).
 struct TileKind {
   int bm, bn, kg;
   float step;
 };
-constexpr TileKind kTiles[] = {{64, 64, 2, 0.67f}, {64, 128, 2, 1.1f}, {128, 128, 1, 0.98f}, {128, 256, 1, 1.56f}};
+constexpr TileKind kTiles[] = {{32, 128, 2, 0.68f}, {64, 128, 2, 1.05f}, {64, 256, 1, 0.88f}, {128, 256, 1, 1.43f}};
 constexpr int kTileCuts[] = {1, 2, 3, 4, 6, 8};  // parts of K
 
 struct TilePlan {
@@ -734,8 +736,8 @@ struct TilePlan {
 };
 // The tile and the cut of K with the least estimated time: rounds of workgroups, one
 // to a compute unit, of 1.3 us and their steps each, and for a cut the joining
-// launch, 2 us and the sums' way through memory.  (Measured against every tile with
-// 1, 2, 4 and 8 parts at 20 sizes from 33 x 14336 x 4096 to 8192 x 4096 x 2*14336.)
+// launch, 4 us and the sums' way through memory (with 2 us for it, 64 x 2048 x 2*768 takes
+// 9.1 us instead of 8.1, 128 x 14336 x 4096 26.0 instead of 24.2).
 TilePlan tile_plan(int32_t T, int32_t K, int32_t N, bool gated) {
   const Mx4Layout l(N, K);
   const double outputs = (double)T * l.blocks * 16 * (gated ? 2 : 1);
@@ -749,7 +751,7 @@ TilePlan tile_plan(int32_t T, int32_t K, int32_t N, bool gated) {
       if (s > 1 && s * k.kg > l.kt) break;
       const int64_t rounds = (tiles * s + 255) / 256;
       const int steps = (l.kt + k.kg * s - 1) / (k.kg * s);
-      const double us = rounds * (1.3 + steps * (double)k.step) + (s > 1 ? 2.0 + s * outputs * 8 / 5e6 : 0.0);
+      const double us = rounds * (1.3 + steps * (double)k.step) + (s > 1 ? 4.0 + s * outputs * 8 / 5e6 : 0.0);
       if (us < least) least = us, best = TilePlan{i, s};
     }
   }
@@ -776,10 +778,10 @@ hipError_t launch_product(const Mx4Product &p, hipStream_t stream) {
   if (p.T <= kFewTokens) return launch_few<Op, GATED>(p, stream);
   const TilePlan t = tile_plan(p.T, p.K, p.N, GATED);
   switch (t.tile) {
-    case 0: return launch_tile<Op, OUT, GATED, 64, 64, 2, 2, 3, 2>(p, t.slices, stream);
-    case 1: return launch_tile<Op, OUT, GATED, 64, 128, 2, 2, 3, 2>(p, t.slices, stream);
-    case 2: return launch_tile<Op, OUT, GATED, 128, 128, 2, 4, 3, 1>(p, t.slices, stream);
-    default: return launch_tile<Op, OUT, GATED, 128, 256, 2, 4, 3, 1>(p, t.slices, stream);
+    case 0: return launch_tile<Op, OUT, GATED, 32, 128, 1, 4, 3, 2>(p, t.slices, stream);
+    case 1: return launch_tile<Op, OUT, GATED, 64, 128, 1, 4, 3, 2>(p, t.slices, stream);
+    case 2: return launch_tile<Op, OUT, GATED, 64, 256, 1, 8, 3, 1>(p, t.slices, stream);
+    default: return launch_tile<Op, OUT, GATED, 128, 256, 1, 8, 3, 1>(p, t.slices, stream);
   }
 }
 

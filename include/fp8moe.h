@@ -665,7 +665,7 @@ moe_status moe_dense_form(int32_t op, int32_t T, int32_t inner, int32_t outputs,
  * forms [3], HOST memory: the kernel, the parts that K is cut into, and of a stream
  * the waves along the channels.
  *   MOE_MX4_FORM_STREAM + i   up to 16, 32 tokens
- *   MOE_MX4_FORM_TILE + i     tiles of 64x64, 64x128, 128x128, 128x256
+ *   MOE_MX4_FORM_TILE + i     tiles of 32x128, 64x128, 64x256, 128x256
  * Errors: MOE_ERR_SHAPE (sizes the operator refuses), MOE_ERR_NULL. */
 enum { MOE_MX4_FORM_NONE = 0, MOE_MX4_FORM_STREAM = 1, MOE_MX4_FORM_TILE = 16 };
 moe_status moe_mx4_form(int32_t gated, int32_t T, int32_t inner, int32_t outputs, int32_t *forms /*host*/);

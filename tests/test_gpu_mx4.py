@@ -130,13 +130,13 @@ FORMS = [
     ("stream 32", False, 1, [(31, 544, 70), (17, 800, 64)]), ("stream 32", False, 2, [(19, 160, 14336), (19, 160, 8192)]),
     ("stream 32", False, 4, [None, (32, 96, 14336)]), ("stream 32", True, 4, [(17, 4128, 100), None]),
     ("stream 32", True, 8, [None, (27, 4128, 96)]),
-    ("tile 64x64", False, 0, [(45, 160, 67), (45, 160, 96)]), ("tile 64x64", True, 0, [(65, 2080, 35), (70, 1440, 64)]),
-    ("tile 64x128", False, 0, [(200, 160, 4097), (500, 160, 1056)]),
-    ("tile 64x128", True, 0, [(1500, 8192, 95), (130, 4096, 1024)]),
-    ("tile 128x128", False, 0, [(200, 96, 4097), (500, 96, 1056)]),
-    ("tile 128x128", True, 0, [(200, 4096, 4097), (500, 6176, 1056)]),
+    ("tile 32x128", False, 0, [(45, 160, 67), (45, 160, 96)]), ("tile 32x128", True, 0, [(65, 2080, 35), (33, 2080, 32)]),
+    ("tile 64x128", False, 0, [(500, 160, 2051), (500, 160, 1056)]),
+    ("tile 64x128", True, 0, [(1500, 8192, 95), (1500, 3200, 32)]),
+    ("tile 64x256", False, 0, [(500, 96, 2051), (500, 96, 1056)]),
+    ("tile 64x256", True, 0, [(500, 6176, 2051), (500, 6176, 1056)]),
     ("tile 128x256", False, 0, [(1000, 96, 4097), (2047, 96, 1056)]),
-    ("tile 128x256", True, 0, [(200, 8192, 4097), (1000, 4096, 1056)]),
+    ("tile 128x256", True, 0, [(500, 6176, 4097), (500, 6176, 2080)]),
 ]
 
 
