@@ -684,12 +684,9 @@ def _numbers(fn: str, *values):
     """A call's scalars as plain floats, converted as ctypes would: what is kept by them
     (_norm_dims) goes by their values, where a tensor hashes by identity and can change
     in place.  Tensors that autograd would have to record are refused."""
-    for v in values:
-        if type(v) is not float:
-            _no_autograd(fn, *(v for v in values if isinstance(v, torch.Tensor)))
-            with torch.no_grad():
-                return [C.c_double(v).value for v in values]
-    return values
+    _no_autograd(fn, *(v for v in values if isinstance(v, torch.Tensor)))
+    with torch.no_grad():
+        return [C.c_double(v).value for v in values]
 
 
 @functools.lru_cache(maxsize=4096)
@@ -743,7 +740,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, offset: f
     [T] fp32 as rms_norm_backward takes it."""
     T, d = shape = _shape2(x, "x")
     _no_autograd("rms_norm", x, weight)
-    eps, offset = _numbers("rms_norm", eps, offset)
+    if not (type(eps) is type(offset) is float):
+        eps, offset = _numbers("rms_norm", eps, offset)
     c = _Call(x, stream)
     w_type, _, _, _, _, wp = _norm_vectors(c, T, d, x.dtype, None, None, weight)
     xp, ldx = c.rows(x, shape, x.dtype, "x")
@@ -768,7 +766,8 @@ def norm_residual(x: torch.Tensor, y: torch.Tensor, w_post: Optional[torch.Tenso
     norm_residual_backward takes them."""
     T, d = shape = _shape2(x, "x")
     _no_autograd("norm_residual", x, y, w_post, gate, w_next)
-    scale, eps, offset = _numbers("norm_residual", scale, eps, offset)
+    if not (type(scale) is type(eps) is type(offset) is float):
+        scale, eps, offset = _numbers("norm_residual", scale, eps, offset)
     c, t = _Call(x, stream), x.dtype
     w_type, wp, gp, ldg, rows, wn = _norm_vectors(c, T, d, t, w_post, gate, w_next)
     xp, ldx = c.rows(x, shape, t, "x")
@@ -846,7 +845,8 @@ def rms_norm_backward(dn: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, r
     d]: x's gradient from elsewhere (the residual stream), added to dx."""
     shape = _shape2(x, "x")
     _no_autograd("rms_norm_backward", dn, x, weight, rstd, dr)
-    offset, = _numbers("rms_norm_backward", offset)
+    if type(offset) is not float:
+        offset, = _numbers("rms_norm_backward", offset)
     dx, _, _, _, dw = _norm_backward(_Call(x, stream), shape, dr, dn, x, None, None, rstd, None, None,
                                      weight, 1.0, offset, dx, None, workspace)
     return dx, dw
@@ -868,7 +868,8 @@ def norm_residual_backward(dr: Optional[torch.Tensor], dn: Optional[torch.Tensor
     allocated here when not given."""
     shape = _shape2(x, "x")
     _no_autograd("norm_residual_backward", dr, dn, x, y, rstd_y, rstd_r, w_post, gate, w_next)
-    scale, offset = _numbers("norm_residual_backward", scale, offset)
+    if not (type(scale) is type(offset) is float):
+        scale, offset = _numbers("norm_residual_backward", scale, offset)
     if (dn is None) != (w_next is None):
         raise ValueError("dn and w_next go together")
     if dr is None and dn is None:
