@@ -1050,21 +1050,26 @@ class Mx4Experts:
             raise ValueError(f"codes: expected shape {(rows, cols // 2)}, got {tuple(codes.shape)}")
         pack_mx4(codes, scales, out=getattr(self, ("ws_" if shared else "w_") + which)[e])
 
-    def struct(self, c: _Call) -> _Mx4Weights:
-        gu, dn = packed_mx4_bytes(self.f, self.d), packed_mx4_bytes(self.d, self.f)
-        E, S = self.E, self.n_shared
-        at = lambda name, n, size: c.ptr(getattr(self, name), (n, size), torch.uint8, name)
-        shared = [at("ws_gate", S, gu), at("ws_up", S, gu), at("ws_down", S, dn)] if S else [None] * 3
-        return _Mx4Weights(at("w_gate", E, gu), at("w_up", E, gu), at("w_down", E, dn), *shared)
+    def struct(self, c: _Call, E: int, S: int) -> _Mx4Weights:
+        """The matrices of E experts and S shared ones, checked."""
+        gu, dn, u8 = _mx4_shape(self.f, self.d)[0], _mx4_shape(self.d, self.f)[0], torch.uint8
+        w = _Mx4Weights(c.ptr(self.w_gate, (E, gu), u8, "w_gate"), c.ptr(self.w_up, (E, gu), u8, "w_up"),
+                        c.ptr(self.w_down, (E, dn), u8, "w_down"))
+        if S:
+            w.ws_gate = c.ptr(self.ws_gate, (S, gu), u8, "ws_gate")
+            w.ws_up = c.ptr(self.ws_up, (S, gu), u8, "ws_up")
+            w.ws_down = c.ptr(self.ws_down, (S, dn), u8, "ws_down")
+        return w
 
 
 class Mx4MoELayer:
     """One mixture-of-experts layer with 4-bit experts, for steps of up to
     MX4_MAX_TOKENS tokens (moe_mx4_forward): router, top-k, the picked and the
     shared experts and their weighted sum in three to five launches on the
-    current stream.  w_router [E, d] and router_bias [E] fp32.  A workspace per
-    stream is allocated for the largest step so far and kept; a captured call has
-    one of its own, which the graph keeps."""
+    current stream.  w_router [E, d] and router_bias [E] fp32.  Its tensors and k_max
+    can be replaced between steps.  A workspace per stream is allocated for the
+    largest step so far and kept; a captured call has one of its own, which the
+    graph keeps."""
 
     def __init__(self, weights: Mx4Experts, w_router: Optional[torch.Tensor], k_max: int,
                  router_bias: Optional[torch.Tensor] = None):
@@ -1073,34 +1078,40 @@ class Mx4MoELayer:
         self.router_bias = router_bias
         self.k_max = k_max
         self._ws = {}
-        c = _Call(weights.w_gate, None)
-        self._index = c.index
-        self._wstruct = weights.struct(c)
-        E, d = weights.E, weights.d
-        self._router = None if w_router is None else c.ptr(w_router, (E, d), torch.float32, "w_router")
-        self._bias = None if router_bias is None else c.ptr(router_bias, (E,), torch.float32, "router_bias")
         self._need = {}
+        self._tensors(_Call(weights.w_gate, None), weights, weights.E, weights.n_shared)
+
+    def _tensors(self, c: _Call, w: Mx4Experts, E: int, S: int):
+        """(the experts' matrices, addresses of the router and of its bias) as they are
+        now, checked: the layer's tensors can be replaced between two steps."""
+        router, bias = self.w_router, self.router_bias
+        return (w.struct(c, E, S),
+                None if router is None else c.ptr(router, (E, w.d), torch.float32, "w_router"),
+                None if bias is None else c.ptr(bias, (E,), torch.float32, "router_bias"))
 
     def dims(self, T: int) -> Dims:
         return dims(T, self.w.d, self.w.f, self.w.E, self.k_max, self.w.n_shared)
 
-    def _step(self, T: int):
-        """(dims, workspace bytes) of a step of T tokens."""
-        step = self._need.get(T)
+    def _step(self, *sizes):
+        """(the dims argument, workspace bytes) of a step of those sizes, kept."""
+        step = self._need.get(sizes)
         if step is None:
-            dm = self.dims(T)
+            dm = dims(*sizes)
             n = int(_mx4_workspace_bytes(C.byref(dm)))
             if n == 0:
                 raise MoEError(int(2))
-            step = self._need[T] = (dm, n)
+            step = self._need[sizes] = (C.byref(dm), n)
         return step
 
     def _workspace(self, c: _Call, n: int):
         if torch.cuda.current_device() != c.index:  # the stream that counts is the layer's device's
             with torch.cuda.device(c.dev):
                 return self._workspace(c, n)
-        with _on(c.alloc):
+        if c.alloc is None:
             capturing = torch.cuda.is_current_stream_capturing()
+        else:
+            with torch.cuda.stream(c.alloc):
+                capturing = torch.cuda.is_current_stream_capturing()
         if capturing:
             return c.empty((n,), torch.uint8)
         ws = self._ws.get(c.stream)
@@ -1118,20 +1129,28 @@ class Mx4MoELayer:
         T, d = _shape2(x, "x")
         _no_autograd("Mx4MoELayer.forward", x, logits_override, self.w_router, self.router_bias)
         c = _Call(x, stream)
-        if c.index != self._index:
-            raise ValueError(f"x is on {c.dev}, the weights are on cuda:{self._index}")
+        w = self.w
+        if w.w_gate.get_device() != c.index:
+            raise ValueError(f"x is on {c.dev}, the weights are on {w.w_gate.device}")
         kind = _type(x.dtype, _TYPES16)
-        xp, ldx = c.rows(x, (T, self.w.d), x.dtype, "x")
-        dm, need = self._step(T)
+        xp, ldx = c.rows(x, (T, w.d), x.dtype, "x")
+        E, k, shared = w.w_gate.shape[0], self.k_max, w.ws_gate
+        S = 0 if shared is None else shared.shape[0]
+        weights, router, bias = self._tensors(c, w, E, S)
+        dm, need = self._step(T, d, w.f, E, k, S)
         out, at = _out_like(c, out, x, "out")
-        i32, f32, K = torch.int32, torch.float32, self.k_max
-        opt = lambda t, shape, dtype, name: None if t is None else c.ptr(t, shape, dtype, name)
+        kpt = over = ids_at = w_at = None
+        if k_per_token is not None:
+            kpt = c.ptr(k_per_token, (T,), torch.int32, "k_per_token")
+        if logits_override is not None:
+            over = c.ptr(logits_override, (T, E), torch.float32, "logits_override")
+        if topk_ids is not None:
+            ids_at = c.ptr(topk_ids, (T, k), torch.int32, "topk_ids")
+        if topk_w is not None:
+            w_at = c.ptr(topk_w, (T, k), torch.float32, "topk_w")
         ws = self._workspace(c, need)
-        c.run(_mx4_forward, C.byref(dm), kind, xp, ldx, self._router, self._bias,
-              opt(k_per_token, (T,), i32, "k_per_token"), C.byref(self._wstruct),
-              opt(logits_override, (T, self.w.E), f32, "logits_override"), at,
-              opt(topk_ids, (T, K), i32, "topk_ids"), opt(topk_w, (T, K), f32, "topk_w"),
-              ws.data_ptr(), ws.numel())
+        c.run(_mx4_forward, dm, kind, xp, ldx, router, bias, kpt, C.byref(weights), over, at, ids_at,
+              w_at, ws.data_ptr(), ws.numel())
         return out
 
     __call__ = forward

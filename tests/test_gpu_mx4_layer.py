@@ -1,0 +1,49 @@
+"""The 4-bit mixture-of-experts layer as an object that a server keeps: its tensors
+replaced between steps."""
+import pytest
+import torch
+
+from gpu_common import dev, lib
+from test_gpu_dense import normal
+from test_gpu_mx4_moe import Layer
+
+pytestmark = pytest.mark.gpu
+
+
+def matrices(w):
+    return [n for n in ("w_gate", "w_up", "w_down", "ws_gate", "ws_up", "ws_down") if getattr(w, n) is not None]
+
+
+@pytest.mark.parametrize("T", [3, 20])
+def test_replaced_tensors(T):
+    """After each replacement a step gives the bits of a layer made from the same tensors."""
+    f, a, b = lib(), Layer(256, 128, 8, 2, 1, bias=True, seed=1), Layer(256, 128, 8, 2, 1, bias=True, seed=2)
+    x = normal(a.g, (T, 256), 1, torch.bfloat16)
+    first = a.op.forward(x)
+
+    def step():
+        y = a.op.forward(x)
+        torch.cuda.synchronize()
+        assert torch.equal(y, f.Mx4MoELayer(a.op.w, a.op.w_router, a.op.k_max, a.op.router_bias).forward(x))
+        return y
+
+    last = step()
+    assert torch.equal(last, first)
+    for name in ("w_router", "router_bias"):
+        setattr(a.op, name, getattr(b.op, name))
+        y = step()
+        assert not torch.equal(y, last), name
+        last = y
+    for name in matrices(b.op.w):
+        setattr(a.op.w, name, getattr(b.op.w, name))
+        y = step()
+        assert not torch.equal(y, last), name
+        last = y
+    assert torch.equal(last, b.op.forward(x))
+    a.op.k_max = 3
+    assert not torch.equal(step(), last)
+    a.op.w = Layer(256, 512, 8, 2, 0, seed=3).op.w  # other sizes, a larger workspace
+    step()
+    a.op.w_router = torch.zeros((7, 256), device=dev())
+    with pytest.raises(ValueError, match="w_router"):
+        a.op.forward(x)
