@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes as C
 import functools
 import pathlib
+import threading
 from dataclasses import dataclass
 from typing import Optional
 
@@ -1069,7 +1070,8 @@ class Mx4MoELayer:
     current stream.  w_router [E, d] and router_bias [E] fp32.  Its tensors and k_max
     can be replaced between steps.  A workspace per stream is allocated for the
     largest step so far and kept; a captured call has one of its own, which the
-    graph keeps."""
+    graph keeps.  Threads can share a layer, and a stream: what a step enqueues is
+    not mixed with another's."""
 
     def __init__(self, weights: Mx4Experts, w_router: Optional[torch.Tensor], k_max: int,
                  router_bias: Optional[torch.Tensor] = None):
@@ -1079,6 +1081,8 @@ class Mx4MoELayer:
         self.k_max = k_max
         self._ws = {}
         self._need = {}
+        # held from the choice of a workspace until all of a step's launches are enqueued
+        self._lock = threading.Lock()
         self._tensors(_Call(weights.w_gate, None), weights, weights.E, weights.n_shared)
 
     def _tensors(self, c: _Call, w: Mx4Experts, E: int, S: int):
@@ -1148,9 +1152,10 @@ class Mx4MoELayer:
             ids_at = c.ptr(topk_ids, (T, k), torch.int32, "topk_ids")
         if topk_w is not None:
             w_at = c.ptr(topk_w, (T, k), torch.float32, "topk_w")
-        ws = self._workspace(c, need)
-        c.run(_mx4_forward, dm, kind, xp, ldx, router, bias, kpt, C.byref(weights), over, at, ids_at,
-              w_at, ws.data_ptr(), ws.numel())
+        with self._lock:
+            ws = self._workspace(c, need)
+            c.run(_mx4_forward, dm, kind, xp, ldx, router, bias, kpt, C.byref(weights), over, at, ids_at,
+                  w_at, ws.data_ptr(), ws.numel())
         return out
 
     __call__ = forward

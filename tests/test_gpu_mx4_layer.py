@@ -1,5 +1,5 @@
 """The 4-bit mixture-of-experts layer as an object that a server keeps: its tensors
-replaced between steps."""
+replaced between steps, and threads that share it."""
 import pytest
 import torch
 
@@ -47,3 +47,35 @@ def test_replaced_tensors(T):
     a.op.w_router = torch.zeros((7, 256), device=dev())
     with pytest.raises(ValueError, match="w_router"):
         a.op.forward(x)
+
+
+@pytest.mark.parametrize("streams", [1, 2])
+def test_threads_share_a_layer(streams):
+    """Four threads' steps of several sizes at once, on one stream or on two: the bits
+    that a thread alone gets."""
+    import threading
+    layer = Layer(512, 1056, 16, 4, 1, bias=True)
+    sizes = (1, 7, 13, 32)
+    xs = {T: [normal(layer.g, (T, 512), 1, torch.bfloat16) for _ in range(5)] for T in sizes}
+    fresh = lib().Mx4MoELayer(layer.op.w, layer.op.w_router, layer.op.k_max, layer.op.router_bias)
+    want = {T: [layer.op.forward(x) for x in xs[T]] for T in sizes}
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in range(streams)] if streams > 1 else [None]
+    got, failed, start = {}, [], threading.Barrier(len(sizes))
+
+    def work(i, T):
+        try:
+            start.wait(timeout=30)
+            got[T] = [fresh.forward(xs[T][k % 5], stream=side[i % streams]) for k in range(60)]
+        except Exception as e:  # noqa: BLE001 -- told by the test's own thread
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i, T)) for i, T in enumerate(sizes)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=60)
+    torch.cuda.synchronize()
+    assert not failed, failed
+    for T in sizes:
+        assert all(torch.equal(y, want[T][k % 5]) for k, y in enumerate(got[T])), T

@@ -96,3 +96,43 @@ def test_a_replaced_tensor_that_does_not_fit_is_refused(monkeypatch):
         change(layer)
         with pytest.raises(error, match=text):
             layer.forward(x)
+
+
+def test_threads_do_not_meet_in_a_workspace(monkeypatch):
+    """A step's launches write and read its workspace one after the other; a second
+    thread's step on the same stream must not come between them."""
+    import threading
+    import time
+    inside, met, steps = {}, [], []
+
+    def run(fn, args):
+        ws = args[-2]
+        met.append(inside.get(ws, 0))
+        inside[ws] = inside.get(ws, 0) + 1
+        time.sleep(0.01)  # as ctypes does, the others are let on
+        inside[ws] -= 1
+        steps.append(args[-1])
+
+    host_calls(monkeypatch, fp8, run)
+    layer = make()
+    # steps of several sizes: a larger workspace takes the place of a smaller one
+    work = lambda T: [layer.forward(torch.zeros(T, 64, dtype=torch.bfloat16)) for _ in range(4)]
+    threads = [threading.Thread(target=work, args=(T,)) for T in (1, 3, 20, 32)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(steps) == 16 and met == [0] * 16
+
+
+def test_a_refused_step_leaves_the_layer_usable(monkeypatch):
+    def run(fn, args):
+        if not calls[1:]:
+            raise fp8.MoEError(2)
+
+    calls = host_calls(monkeypatch, fp8, run)
+    layer, x = make(), torch.zeros(3, 64, dtype=torch.bfloat16)
+    with pytest.raises(fp8.MoEError):
+        layer.forward(x)
+    layer.forward(x)
+    assert len(calls) == 2
