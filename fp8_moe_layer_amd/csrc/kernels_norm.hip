@@ -219,13 +219,17 @@ Chunks chunks_of(int32_t T, int32_t gate_rows) {
 // Teams of a workgroup: waves that take rows by themselves, or one.
 constexpr int teams_of(int nt) { return nt == kWave ? 8 : 1; }
 
-// What there is not counts as ones (weights, gate, rstd_y) or zeros (dr, dn, rstd_r), so
-// that no value's arithmetic asks.
+// What there is not counts as ones (weights, gate, rstd_y) or zeros (dr, dn, r^), so that
+// hardly any value's arithmetic asks.  But nothing that is there is multiplied by a zero for
+// what is not: y can hold infinities (a training step that overflowed), and the product would
+// be a NaN where the formula has no such factor.  NORMS: both are there, and nothing asks
+// (asked there too: 1024 x 16384 fp32 184 -> 191 us, 8192 x 1024 bf16 with 512 gate rows 92.5
+// -> 95.5).
 //
 // 4096 x 4096 bf16 with both norms and a gate: 49 us, 4.1 TB/s read and written (six
 // arrays; three sums a value and two dot products a row between the loads and the
 // stores), and 6 us for the second launch; 333 x 2048 fp16 with 37 gate rows: 9 and 6 us.
-template <class E, class W, int NT, int V>
+template <class E, class W, int NT, int V, bool NORMS>
 __global__ __launch_bounds__(NT *teams_of(NT)) void norm_backward_kernel(NormBackward p, Chunks c) {
   constexpr int N = Run<E>::N, TEAMS = teams_of(NT);
   // rows past 8192 values: registers do not hold three sums a value, LDS takes two of
@@ -314,7 +318,7 @@ __global__ __launch_bounds__(NT *teams_of(NT)) void norm_backward_kernel(NormBac
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         z[i] = yr[j][i] * sy * wp[i];
-        rh[i] = fmaf(p.scale, z[i] * g[i], xr[j][i]) * sr;
+        rh[i] = NORMS || p.w_next ? fmaf(p.scale, z[i] * g[i], xr[j][i]) * sr : 0.0f;
       }
     };
     float z[kLong ? 1 : V][N], rh[kLong ? 1 : V][N];
@@ -382,7 +386,8 @@ __global__ __launch_bounds__(NT *teams_of(NT)) void norm_backward_kernel(NormBac
         const int at = (j * NT + tid) * N;
         if (at >= p.d) continue;
 #pragma unroll
-        for (int i = 0; i < N; ++i) b[j][i] = sy * fmaf(-yr[j][i] * sy, my, b[j][i]);
+        for (int i = 0; i < N; ++i)
+          if (NORMS || p.w_post) b[j][i] = sy * fmaf(-yr[j][i] * sy, my, b[j][i]);
         store_values<E, N>(static_cast<E *>(p.dy) + (int64_t)t * p.d, at, b[j]);
       }
     }
@@ -526,7 +531,10 @@ struct Backward {
   template <class E, class W, int NT, int V>
   hipError_t operator()() const {
     if (c.count > 0) {
-      norm_backward_kernel<E, W, NT, V><<<c.count, NT * teams_of(NT), 0, stream>>>(p, c);
+      if (p.w_post && p.w_next)
+        norm_backward_kernel<E, W, NT, V, true><<<c.count, NT * teams_of(NT), 0, stream>>>(p, c);
+      else
+        norm_backward_kernel<E, W, NT, V, false><<<c.count, NT * teams_of(NT), 0, stream>>>(p, c);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
