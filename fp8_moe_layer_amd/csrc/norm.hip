@@ -146,7 +146,9 @@ moe_status moe_norm_residual_backward(const moe_norm_dims *dims, const void *dr,
   if (clash(out, in))
     return fail_status(MOE_ERR_SHAPE,
                        "%s: an output or the workspace overlaps an input or another output", fn);
-  const NormBackward p{m.T, m.d, m.type, m.w_type, m.gate_rows, m.scale, m.offset, dr, lddr, dn, lddn,
+  // without a sum its scale is not read (the kernel multiplies it with zeros for y)
+  const float scale = y ? m.scale : 1.0f;
+  const NormBackward p{m.T, m.d, m.type, m.w_type, m.gate_rows, scale, m.offset, dr, lddr, dn, lddn,
                        x, ldx, y, ldy, rstd_y, rstd_r, w_post, gate, ldg, w_next, dx, dy, dw_post,
                        dgate, dw_next, static_cast<float *>(workspace)};
   return finish(launch_norm_backward(p, as_stream(stream)), fn);

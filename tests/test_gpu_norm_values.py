@@ -90,3 +90,24 @@ def test_a_next_norm_alone(d):
     assert bool(got[0][2].isnan().all()) and bool(got[1][2].isnan().all())
     ok = torch.arange(d, device=dev()) != 5
     assert bool(got[4][ok].isfinite().all()) and bool(got[4][5].isnan())
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), 0.0, -3.0])
+def test_scale_does_not_count_without_a_sum(scale):
+    """The C entry points with y NULL: dims.scale belongs to the sum, and a caller may
+    leave it unset."""
+    import ctypes as C
+    f, g, T, d = lib(), gen(7), 5, 96
+    x, dn, w = normal(g, (T, d)), normal(g, (T, d)), 1 + 0.2 * normal(g, (d,))
+    n, rstd = f.rms_norm(x, w, save=True)
+    dx, dw = f.rms_norm_backward(dn, x, w, rstd)
+    dims = f._NormDims(T, d, 0, 0, 0, scale, 0.0, 1e-6)
+    n2, dx2, dw2 = (torch.empty_like(t) for t in (n, dx, dw))
+    ws = torch.empty(f.norm_backward_workspace_bytes(T, d), dtype=torch.uint8, device=dev())
+    stream = torch.cuda.current_stream().cuda_stream
+    at = lambda t: t.data_ptr()
+    f._check(f._norm_residual(C.byref(dims), at(x), d, None, 0, None, None, 0, at(w), None, at(n2), None, None, stream))
+    f._check(f._norm_bwd(C.byref(dims), None, 0, at(dn), d, at(x), d, None, 0, None, at(rstd), None, None, 0, at(w),
+                         at(dx2), None, None, None, at(dw2), at(ws), ws.numel(), stream))
+    torch.cuda.synchronize()
+    assert torch.equal(n, n2) and torch.equal(dx, dx2) and torch.equal(dw, dw2)
