@@ -346,7 +346,9 @@ __global__ __launch_bounds__(W *kWave) void mx4_gate_up_kernel(Mx4Moe p, const f
                 const float h = weight * silu_mul(sums[k][i] * (factor[k][i] * kUnit),
                                                   sums[NB + k][i] * (factor[NB + k][i] * kUnit));
                 vh[i] = (__bf16)h;
-                vl[i] = (__bf16)(h - (float)vh[i]);  // 16 bits of h's 24 in all
+                const float top = (float)vh[i];
+                // 16 bits of h's 24 in all; an infinity has no rest
+                vl[i] = (__bf16)(fabsf(top) == __builtin_inff() ? 0.0f : h - top);
               }
               *reinterpret_cast<v4b *>(hi + to) = vh;
               *reinterpret_cast<v4b *>(lo + to) = vl;

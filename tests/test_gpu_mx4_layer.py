@@ -79,3 +79,33 @@ def test_threads_share_a_layer(streams):
     assert not failed, failed
     for T in sizes:
         assert all(torch.equal(y, want[T][k % 5]) for k, y in enumerate(got[T])), T
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T", [4, 20])
+@pytest.mark.parametrize("d,f", [(64, 96), (2048, 1056)])
+def test_an_infinite_activation_stays_an_infinity(d, f, T, dtype):
+    """All weights of one sign to an output: a token whose gate and up are infinite gets
+    infinities of those signs, as the formula has them, and the others their own values."""
+    m, E = lib(), 4
+    w = m.Mx4Experts.empty(E, d, f, 1)
+    one = torch.ones((f, d), device=dev()) / d
+    sign = torch.where(torch.arange(d, device=dev()) % 3 == 0, -1.0, 1.0)
+    for e in range(E + 1):
+        for which, v in (("gate", one), ("up", one), ("down", sign[:, None] * torch.ones((d, f), device=dev()) / f)):
+            w.set_expert(which, e % E, *m.quantize_rows_mx4(v), shared=e == E)
+    layer = m.Mx4MoELayer(w, None, 2)
+    logits = torch.zeros((T, E), device=dev())
+    x = torch.ones((T, d), device=dev(), dtype=dtype)
+    clean = layer.forward(x, logits_override=logits)
+    assert bool(clean.isfinite().all())
+    x[1, 5] = torch.inf
+    if dtype == torch.bfloat16:
+        x[3] = 3e38  # g and u are finite, their product is not
+    got = layer.forward(x, logits_override=logits)
+    bad = [1, 3] if dtype == torch.bfloat16 else [1]
+    keep = torch.ones(T, dtype=torch.bool, device=dev())
+    keep[bad] = False
+    assert torch.equal(got[keep], clean[keep])
+    for t in bad:
+        assert torch.equal(got[t].float(), sign * torch.inf), t
