@@ -511,6 +511,12 @@ class _Call:
 _INT32_MAX = 0x7fffffff
 
 
+def _fit(v: int) -> int:
+    """A size as a 32-bit integer; those past it become -1 or the largest, which the
+    library refuses like all past its limits."""
+    return max(-1, min(v, _INT32_MAX))
+
+
 def _shape2(t: torch.Tensor, name: str):
     """A matrix's shape.  Both sizes reach the library as 32-bit integers, which
     ctypes cuts off without a word; its own limits are far below."""
@@ -621,8 +627,7 @@ def gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
 
 
 def gated_ffn_backward_workspace_bytes(T: int, d: int, f: int) -> int:
-    fit = lambda v: max(-1, min(v, _INT32_MAX))  # both refused, like all past the limits
-    return int(_gated_bwd_ws(fit(T), fit(d), fit(f)))
+    return int(_gated_bwd_ws(_fit(T), _fit(d), _fit(f)))
 
 
 def gated_ffn_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor,
@@ -793,9 +798,13 @@ def norm_residual(x: torch.Tensor, y: torch.Tensor, w_post: Optional[torch.Tenso
     return r if w_next is None else (r, n)
 
 
-@_by_sizes
-def _norm_bwd_size(T: int, d: int, gate_rows: int) -> int:
-    return _norm_bwd_ws(_norm_dims(T, d, torch.float32, torch.float32, gate_rows, 1.0, 0.0, 1.0))
+def norm_backward_workspace_bytes(T: int, d: int, gate_rows: int = 0) -> int:
+    """Bytes of the backward calls' workspace (0 for sizes that are refused)."""
+    return int(_norm_bwd_ws(_norm_dims(_fit(T), _fit(d), torch.float32, torch.float32, _fit(gate_rows),
+                                       1.0, 0.0, 1.0)))
+
+
+_norm_bwd_size = _by_sizes(norm_backward_workspace_bytes)
 
 
 def _norm_backward(c, shape, dr, dn, x, y, rstd_y, rstd_r, w_post, gate, w_next, scale, offset, dx, dy,
@@ -879,10 +888,6 @@ def norm_residual_backward(dr: Optional[torch.Tensor], dn: Optional[torch.Tensor
                           scale, offset, dx, dy, workspace)
 
 
-def norm_backward_workspace_bytes(T: int, d: int, gate_rows: int = 0) -> int:
-    return int(_norm_bwd_size(T, d, gate_rows))
-
-
 # --------------------------------------------------------------------------- 4-bit weights
 # Plain calls like the dense operators above.
 
@@ -936,8 +941,7 @@ class Mx4Matrix:
 
 def packed_mx4_bytes(rows: int, cols: int) -> int:
     """Bytes of a packed matrix (0 for sizes that are refused)."""
-    fit = lambda v: max(-1, min(v, _INT32_MAX))  # both refused, like all past the limits
-    return int(_packed_mx4_bytes(fit(rows), fit(cols)))
+    return int(_packed_mx4_bytes(_fit(rows), _fit(cols)))
 
 
 def pack_mx4(codes: torch.Tensor, scales: torch.Tensor, out: Optional[torch.Tensor] = None,
@@ -1009,7 +1013,7 @@ def mx4_form(op: str, T: int, inner: int, outputs: int):
     (name, parts that K is cut into, waves along the channels of a stream).  A host
     call."""
     forms = (_i32 * 3)()
-    _check(_mx4_form(("matmul_mx4", "gated_ffn_mx4").index(op), T, inner, outputs, forms))
+    _check(_mx4_form(("matmul_mx4", "gated_ffn_mx4").index(op), _fit(T), _fit(inner), _fit(outputs), forms))
     return _MX4_FORMS[forms[0]], forms[1], forms[2]
 
 
@@ -1100,7 +1104,7 @@ class Mx4MoELayer:
         """(the dims argument, workspace bytes) of a step of those sizes, kept."""
         step = self._need.get(sizes)
         if step is None:
-            dm = dims(*sizes)
+            dm = dims(*map(_fit, sizes))
             n = int(_mx4_workspace_bytes(C.byref(dm)))
             if n == 0:
                 raise MoEError(int(2))

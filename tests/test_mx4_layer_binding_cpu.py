@@ -136,3 +136,16 @@ def test_a_refused_step_leaves_the_layer_usable(monkeypatch):
         layer.forward(x)
     layer.forward(x)
     assert len(calls) == 2
+
+
+def test_sizes_past_32_bits_are_refused(monkeypatch):
+    host_calls(monkeypatch, fp8)
+    layer = make()
+    layer.k_max = 2 ** 32 + 2  # 2 in 32 bits
+    with pytest.raises(fp8.MoEError, match="k_max"):
+        layer.forward(torch.zeros(3, 64, dtype=torch.bfloat16))
+    for op in ("matmul_mx4", "gated_ffn_mx4"):
+        assert fp8.mx4_form(op, 1, 64, 64)[0] == "stream 16"
+        for bad in ((2 ** 32 + 1, 64, 64), (1, 2 ** 32 + 64, 64), (1, 64, 2 ** 32 + 64), (1 - 2 ** 32, 64, 64)):
+            with pytest.raises(fp8.MoEError, match="moe_mx4_form"):
+                fp8.mx4_form(op, *bad)

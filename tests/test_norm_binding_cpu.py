@@ -57,3 +57,16 @@ def test_a_scalar_that_autograd_would_record_is_refused(fn, name, monkeypatch):
     with torch.no_grad():
         CALLS[fn][0](**{name: s})
     assert len(calls) == 1
+
+
+def test_workspace_of_sizes_past_32_bits():
+    size = fp8.norm_backward_workspace_bytes
+    assert size(4, 64) > 0 and size(4, 64, 2) > 0
+    for bad in ((2 ** 32 + 4, 64), (4, 2 ** 32 + 64), (4, 64, 2 ** 32 + 2), (4 - 2 ** 32, 64), (4, 64, 2 - 2 ** 32)):
+        assert size(*bad) == 0
+        assert fp8._last_error().startswith(b"moe_norm_residual_backward_workspace_bytes")
+
+
+def test_a_refused_size_is_named_each_time():
+    for d in (20, 24, 20, 24):
+        assert fp8.norm_backward_workspace_bytes(4, d) == 0 and f"d={d}".encode() in fp8._last_error()
