@@ -453,7 +453,7 @@ hipError_t launch_few(const Mx4Product &p, hipStream_t stream) {
 
 // ---------------------------------------------------------------- tiles
 // BM tokens by BN rows of weights (gated: of each wave's WN rows half come from
-// each matrix), TM x TN waves, KG groups of them that share the tile, each with
+// each matrix), W waves, KG groups of them that share the tile, each with
 // LDS of its own and its part of the steps; their sums meet in LDS at the end.
 //
 // A step is 128 inputs.  It comes to LDS directly, ST steps deep: the activations
@@ -465,42 +465,43 @@ hipError_t launch_few(const Mx4Product &p, hipStream_t stream) {
 // their use.  One barrier a step, before the last quarter's products: there every wave
 // has read all of the step, whose stage is filled again, and the next one has landed.
 //
-// The waves stand side by side along the channels (TM is 1): each code is turned into an
+// The waves stand side by side along the channels: each code is turned into an
 // operand once, 5 instructions to a group of 16 rows and 2 to 8 products.  With two rows of
 // waves every code is turned twice, with half the reads of activations from LDS: 128 x 256
 // tiles took 1474 us instead of 1400 at 8192 x 4096 x 2*14336, 115 instead of 106 at 512 x
 // 8192 x 16384.  Now 1.37 PFLOP/s; 4096 x 14336 x 4096 338 us, 1.42 PFLOP/s.  Tiles of 256 x
 // 256 and 128 x 512 were slower: their accumulators leave too few registers.
-template <int BM, int BN, int TM, int TN, int ST, int KG, bool GATED>
+template <int BM, int BN, int W, int ST, int KG, bool GATED>
 struct Mx4Shape {
-  static constexpr int kWaves = TM * TN, kThreads = KG * kWaves * kWave;
-  static constexpr int WM = BM / TM, WN = BN / TN, MS = WM / 16, NR = WN / 16;
+  static constexpr int kThreads = KG * W * kWave;
+  static constexpr int WN = BN / W, MS = BM / 16, NR = WN / 16;
   static constexpr int NC = GATED ? NR / 2 : NR;           // blocks of channels of a wave
   static constexpr int kChannels = GATED ? BN / 2 : BN;    // of a tile
   static constexpr int kCodes = BM * 256, kScales = kCodes + BN * 64;
   static constexpr int kStage = kScales + BN * 4;
   static constexpr int kRing = ST * kStage;
   static constexpr int kLds = KG * kRing;
-  static constexpr int kX = BM / 4 / kWaves, kW = BN / 16 / kWaves;  // a wave's 1 KB pieces of a step
+  static constexpr int kX = BM / 4 / W, kW = BN / 16 / W;  // a wave's 1 KB pieces of a step
   static constexpr int kPieces = kX + kW + 1;
-  static_assert(NC >= 1 && BM % (4 * kWaves) == 0 && BN % (16 * kWaves) == 0 && BN % 64 == 0, "tile shape");
+  static_assert(NC >= 1 && BM % (4 * W) == 0 && BN % (16 * W) == 0 && BN % 64 == 0, "tile shape");
   static_assert(KG == 1 || kRing >= BM * BN * 4, "the sums of a group fit its ring");
 };
 
-template <class Op, class OUT, int BM, int BN, int TM, int TN, int ST, int KG, bool GATED>
-__global__ __launch_bounds__(KG *TM *TN *kWave) void mx4_tile_kernel(Mx4Product p, int tiles_m, int tiles_n, int slices, v4f *partial) {
-  typedef Mx4Shape<BM, BN, TM, TN, ST, KG, GATED> S;
-  constexpr int MS = S::MS, NR = S::NR, NC = S::NC, W = S::kWaves;
+template <class Op, class OUT, int BM, int BN, int W, int ST, int KG, bool GATED>
+__global__ __launch_bounds__(KG *W *kWave) void mx4_tile_kernel(Mx4Product p, int tiles_m, int tiles_n, int slices,
+                                                                v4f *partial) {
+  typedef Mx4Shape<BM, BN, W, ST, KG, GATED> S;
+  constexpr int MS = S::MS, NR = S::NR, NC = S::NC;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
   __shared__ __attribute__((aligned(256))) float factors[BN], bias[S::kChannels < 64 ? 64 : S::kChannels];
   const Mx4Layout l(p.N, p.K);
   const int lane = threadIdx.x & 63, q = lane >> 4, c16 = lane & 15;
   const int all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int kg = all / W, wave = all % W, wm = wave / TN, wn = wave % TN;
+  const int kg = KG > 1 ? all / W : 0, wave = KG > 1 ? all % W : all;
   int tm, tn;
   const int slice = blockIdx.x % slices;
   tile_of(blockIdx.x / slices, tiles_m, tiles_n, tm, tn);
-  const int t0 = tm * BM, tile_b = tn * (S::kChannels / 16), b0 = tile_b + wn * NC;
+  const int t0 = tm * BM, tile_b = tn * (S::kChannels / 16), b0 = tile_b + wave * NC;
   // this group's steps: nk from k0 on (those behind the end take zeros for activations)
   const int nk = (l.kt + KG * slices - 1) / (KG * slices), k0 = (slice * KG + kg) * nk;
   const LdsPtr ring = (LdsPtr)lds + kg * S::kRing;
@@ -556,18 +557,18 @@ __global__ __launch_bounds__(KG *TM *TN *kWave) void mx4_tile_kernel(Mx4Product 
   uint32_t cs[NR];  // a step's scales
   v4i a[NR];        // the operands of a quarter
   auto read_x = [&](int m, int j, uint32_t stage) {
-    fx[m] = lds_read16(ring + stage + (wm * S::WM + m * 16 + c16) * 256 + (((j * 4 + q) ^ c16) * 16));
+    fx[m] = lds_read16(ring + stage + (m * 16 + c16) * 256 + (((j * 4 + q) ^ c16) * 16));
   };
   auto read_codes = [&](uint32_t stage) {
 #pragma unroll
     for (int r = 0; r < NR; ++r)
-      cw[r] = lds_read16(ring + stage + S::kCodes + (wn * NR + r) * 1024 + lane * 16);
+      cw[r] = lds_read16(ring + stage + S::kCodes + (wave * NR + r) * 1024 + lane * 16);
   };
   auto read_scales = [&](uint32_t stage) {
 #pragma unroll
     for (int r = 0; r < NR; ++r)
       cs[r] = *(const __attribute__((address_space(3))) uint32_t *)(ring + stage + S::kScales +
-                                                                    (wn * NR + r) * 64 + c16 * 4);
+                                                                    (wave * NR + r) * 64 + c16 * 4);
   };
   auto convert = [&](int j) {
 #pragma unroll
@@ -652,7 +653,7 @@ __global__ __launch_bounds__(KG *TM *TN *kWave) void mx4_tile_kernel(Mx4Product 
   if constexpr (KG > 1) {
     // every wave has read its last operands and no load is in flight
     barrier_reads();
-    uint8_t *mine = lds + kg * S::kRing + wave * (S::WM * S::WN * 4) + lane * 16;
+    uint8_t *mine = lds + kg * S::kRing + wave * (BM * S::WN * 4) + lane * 16;
 #pragma unroll
     for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -668,7 +669,6 @@ __global__ __launch_bounds__(KG *TM *TN *kWave) void mx4_tile_kernel(Mx4Product 
         for (int m = 0; m < MS; ++m)
           acc[r][m] += *reinterpret_cast<const v4f *>(mine + g * S::kRing + (r * MS + m) * 1024);
   }
-  const int tb = t0 + wm * S::WM;
   if (slices > 1) {
     const int xt = (p.T + 15) / 16;
 #pragma unroll
@@ -678,7 +678,7 @@ __global__ __launch_bounds__(KG *TM *TN *kWave) void mx4_tile_kernel(Mx4Product 
       const int64_t at = ((int64_t)slice * l.blocks + b) * (GATED ? 2 : 1) + r / NC;
 #pragma unroll
       for (int m = 0; m < MS; ++m)
-        if (tb / 16 + m < xt) partial[(at * xt + tb / 16 + m) * kWave + lane] = acc[r][m];
+        if (t0 / 16 + m < xt) partial[(at * xt + t0 / 16 + m) * kWave + lane] = acc[r][m];
     }
     return;
   }
@@ -693,16 +693,16 @@ __global__ __launch_bounds__(KG *TM *TN *kWave) void mx4_tile_kernel(Mx4Product 
     v4f f[P], other[P];  // the up matrix's factors, or the bias
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      f[i] = op_factor<Op>(four(factors, wn * NR + r + i));
+      f[i] = op_factor<Op>(four(factors, wave * NR + r + i));
       other[i] = v4f{0.f, 0.f, 0.f, 0.f};
       if constexpr (GATED)
-        other[i] = op_factor<Op>(four(factors, wn * NR + NC + r + i));
+        other[i] = op_factor<Op>(four(factors, wave * NR + NC + r + i));
       else if (p.bias)
-        other[i] = four(bias, wn * NC + r + i);
+        other[i] = four(bias, wave * NC + r + i);
     }
 #pragma unroll
     for (int m = 0; m < MS; ++m) {
-      const int t = tb + m * 16 + c16;
+      const int t = t0 + m * 16 + c16;
       if (t >= p.T) continue;
       v4f a[P], u[P];
 #pragma unroll
@@ -758,13 +758,13 @@ TilePlan tile_plan(int32_t T, int32_t K, int32_t N, bool gated) {
   return best;
 }
 
-template <class Op, class OUT, bool GATED, int BM, int BN, int TM, int TN, int ST, int KG>
+template <class Op, class OUT, bool GATED, int BM, int BN, int W, int ST, int KG>
 hipError_t launch_tile(const Mx4Product &p, int slices, hipStream_t stream) {
-  typedef Mx4Shape<BM, BN, TM, TN, ST, KG, GATED> S;
+  typedef Mx4Shape<BM, BN, W, ST, KG, GATED> S;
   const Mx4Layout l(p.N, p.K);
   const int tm = (p.T + BM - 1) / BM, tn = (l.blocks * 16 + S::kChannels - 1) / S::kChannels;
   v4f *partial = static_cast<v4f *>(p.workspace);
-  mx4_tile_kernel<Op, OUT, BM, BN, TM, TN, ST, KG, GATED>
+  mx4_tile_kernel<Op, OUT, BM, BN, W, ST, KG, GATED>
       <<<tm * tn * slices, S::kThreads, 0, stream>>>(p, tm, tn, slices, partial);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || slices == 1) return e;
@@ -778,10 +778,10 @@ hipError_t launch_product(const Mx4Product &p, hipStream_t stream) {
   if (p.T <= kFewTokens) return launch_few<Op, GATED>(p, stream);
   const TilePlan t = tile_plan(p.T, p.K, p.N, GATED);
   switch (t.tile) {
-    case 0: return launch_tile<Op, OUT, GATED, 32, 128, 1, 4, 3, 2>(p, t.slices, stream);
-    case 1: return launch_tile<Op, OUT, GATED, 64, 128, 1, 4, 3, 2>(p, t.slices, stream);
-    case 2: return launch_tile<Op, OUT, GATED, 64, 256, 1, 8, 3, 1>(p, t.slices, stream);
-    default: return launch_tile<Op, OUT, GATED, 128, 256, 1, 8, 3, 1>(p, t.slices, stream);
+    case 0: return launch_tile<Op, OUT, GATED, 32, 128, 4, 3, 2>(p, t.slices, stream);
+    case 1: return launch_tile<Op, OUT, GATED, 64, 128, 4, 3, 2>(p, t.slices, stream);
+    case 2: return launch_tile<Op, OUT, GATED, 64, 256, 8, 3, 1>(p, t.slices, stream);
+    default: return launch_tile<Op, OUT, GATED, 128, 256, 8, 3, 1>(p, t.slices, stream);
   }
 }
 
