@@ -1122,9 +1122,10 @@ class Mx4MoELayer:
                 capturing = torch.cuda.is_current_stream_capturing()
         if capturing:
             return c.empty((n,), torch.uint8)
-        ws = self._ws.get(c.stream)
+        key = c.index, c.stream
+        ws = self._ws.get(key)
         if ws is None or ws.numel() < n:
-            ws = self._ws[c.stream] = c.empty((n,), torch.uint8)
+            ws = self._ws[key] = c.empty((n,), torch.uint8)
         return ws
 
     def forward(self, x: torch.Tensor, k_per_token: Optional[torch.Tensor] = None,

@@ -149,3 +149,15 @@ def test_sizes_past_32_bits_are_refused(monkeypatch):
         for bad in ((2 ** 32 + 1, 64, 64), (1, 2 ** 32 + 64, 64), (1, 64, 2 ** 32 + 64), (1 - 2 ** 32, 64, 64)):
             with pytest.raises(fp8.MoEError, match="moe_mx4_form"):
                 fp8.mx4_form(op, *bad)
+
+
+def test_workspaces_of_two_devices_are_two(monkeypatch):
+    """A layer whose tensors moved to another device: the default streams have one handle."""
+    host_calls(monkeypatch, fp8)
+    layer, kept = make(), []
+    for index in (0, 1, 0, 1):
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: index)
+        c = fp8._Call(layer.w_router, None)
+        c.index = index
+        kept.append(layer._workspace(c, 512).data_ptr())
+    assert kept[0] == kept[2] != kept[1] == kept[3]
