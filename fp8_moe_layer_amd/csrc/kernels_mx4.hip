@@ -468,9 +468,10 @@ hipError_t launch_few(const Mx4Product &p, hipStream_t stream) {
 // The waves stand side by side along the channels: each code is turned into an
 // operand once, 5 instructions to a group of 16 rows and 2 to 8 products.  With two rows of
 // waves every code is turned twice, with half the reads of activations from LDS: 128 x 256
-// tiles took 1474 us instead of 1400 at 8192 x 4096 x 2*14336, 115 instead of 106 at 512 x
-// 8192 x 16384.  Now 1.37 PFLOP/s; 4096 x 14336 x 4096 338 us, 1.42 PFLOP/s.  Tiles of 256 x
-// 256 and 128 x 512 were slower: their accumulators leave too few registers.
+// tiles took 1447 us instead of 1415 at 8192 x 4096 x 2*14336 (1.36 PFLOP/s), 348 instead of
+// 339 at 4096 x 14336 x 4096 (1.42), in turn on one card in bursts of fifty; after an idle
+// time the first twenty take up to 1650.  Tiles of 256 x 256 and 128 x 512 were slower: their
+// accumulators leave too few registers.
 template <int BM, int BN, int W, int ST, int KG, bool GATED>
 struct Mx4Shape {
   static constexpr int kThreads = KG * W * kWave;

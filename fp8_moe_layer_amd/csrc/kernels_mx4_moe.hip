@@ -12,8 +12,8 @@
 //   join     of the workgroups with the same outputs, where there are several
 //
 // The weights of the experts in use are what bounds it where there are many: 32 tokens of
-// 8 experts, 4096 x 14336, 169 us, 4.4 TB/s; 13 tokens of 64 experts, 2048 x 1408, 61 us,
-// 3.6 TB/s.  Where there are few it is the launches, each of which waits for the one
+// 8 experts, 4096 x 14336, 169 us, 4.4 TB/s; 13 tokens of 64 experts, 2048 x 1408, 63 us,
+// 3.5 TB/s.  Where there are few it is the launches, each of which waits for the one
 // before: one token of 128 experts, 2048 x 768, 21.6 us (logits 3, gate/up and
 // the routing 11, down 8) where 21 MB would take 4.
 #include "dense.hpp"

@@ -530,14 +530,16 @@ moe_status moe_mx4_forward(const moe_dims *dims /*host*/, int32_t type, const vo
  * rstd_r [T] fp32: kept for the backward pass, or NULL.
  * Row strides are in ELEMENTS, as for the dense operators; every array is
  * 16-byte aligned (rstd 4-byte), outputs overlap nothing.  Inputs are finite,
- * and so are the fp32 sums of squares. */
+ * and so are the fp32 sums of squares; where they are not, a row's values do
+ * not reach other rows. */
 typedef struct {
   int32_t T;         /* tokens, 0 .. MOE_MAX_TOKENS */
   int32_t d;         /* a multiple of 16 up to MOE_MAX_HIDDEN */
   int32_t type;      /* MOE_T_* of rows and their gradients */
   int32_t w_type;    /* of w_post, gate, w_next and their gradients: fp32 or `type` */
   int32_t gate_rows; /* 0 without a gate; divides T (T = 0: 0 or 1) */
-  float scale, offset;
+  float scale;       /* of the sum: not read where y is NULL */
+  float offset;
   float eps; /* a positive normal number; the backward pass does not use it */
 } moe_norm_dims;
 moe_status moe_norm_residual(const moe_norm_dims *dims /*host*/, const void *x, int64_t ldx,
@@ -553,7 +555,8 @@ moe_status moe_norm_residual(const moe_norm_dims *dims /*host*/, const void *x, 
  *   c = scale * D * gate,  dw_post = sum_t c * y^
  *   dy = rstd_y * (b - y^ * mean(b * y^)),  b = c * (offset + w_post)
  *                                           (dy = c where w_post is NULL)
- * r is formed again from x and y, as the forward pass had it before rounding.
+ * r is formed again from x and y, as the forward pass had it before rounding.  An
+ * infinite x or y does not reach a gradient whose formula does not have it.
  * Sums in fp32 in an order that depends on T, d and gate_rows alone; each output
  * is rounded once and overwritten (not added to).  A vector and its gradient are
  * given together or not at all; x, dn and rstd_r are read where there is w_next.
