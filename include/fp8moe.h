@@ -493,7 +493,7 @@ moe_status moe_ffn_mx4(const void *x, int64_t ldx, const void *w_gate, const voi
  * Weights: E (n_shared) packed matrices one after the other, gate and up of f
  * channels by d inputs, down of d by f.  The down projections' weights are bf16
  * numbers as they are: below 2^-125 they may count as zero, and a channel with a
- * scale byte above 251 in an expert in use is a NaN for every token.
+ * scale byte above 251 is a NaN for the expert's tokens.
  * workspace: moe_mx4_workspace_bytes(dims), 256-byte aligned, not touched by
  * anything else while the work is in flight; it need not be cleared. */
 #define MOE_MX4_MAX_TOKENS 32

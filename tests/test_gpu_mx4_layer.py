@@ -109,3 +109,24 @@ def test_an_infinite_activation_stays_an_infinity(d, f, T, dtype):
     assert torch.equal(got[keep], clean[keep])
     for t in bad:
         assert torch.equal(got[t].float(), sign * torch.inf), t
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T", [1, 4, 20, 32])
+def test_a_scale_that_is_none_stays_with_its_expert(T, dtype):
+    """A scale byte of 255 in one expert's down projection: that channel of its tokens."""
+    layer = Layer(64, 96, 4, 2, 1)
+    codes, scales = lib().quantize_rows_mx4(normal(layer.g, (64, 96), 0.1))
+    layer.op.w.set_expert("down", 0, codes, scales)
+    x = normal(layer.g, (T, 64), 1, dtype)
+    logits = torch.zeros((T, 4), device=dev())
+    logits[:, 0] = -9
+    logits[T // 2, 0] = 9  # one token alone is on expert 0
+    clean = layer.op.forward(x, logits_override=logits)
+    scales[7, 1] = 255
+    layer.op.w.set_expert("down", 0, codes, scales)
+    got = layer.op.forward(x, logits_override=logits)
+    want = clean.clone()
+    want[T // 2, 7] = torch.nan
+    assert bool(clean.isfinite().all()) and torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got.nan_to_num(), want.nan_to_num())
