@@ -686,13 +686,19 @@ def dense_form(op: str, T: int, inner: int, outputs: int):
 # --------------------------------------------------------------------------- norms around a block
 # Plain calls like the dense operators above.
 
+def _number(fn: str, v) -> float:
+    """A scalar as a plain float, converted as ctypes would.  A tensor that autograd
+    would have to record is refused."""
+    if isinstance(v, torch.Tensor):
+        _no_autograd(fn, v)
+        v = v.detach()
+    return C.c_double(v).value
+
+
 def _numbers(fn: str, *values):
-    """A call's scalars as plain floats, converted as ctypes would: what is kept by them
-    (_norm_dims) goes by their values, where a tensor hashes by identity and can change
-    in place.  Tensors that autograd would have to record are refused."""
-    _no_autograd(fn, *(v for v in values if isinstance(v, torch.Tensor)))
-    with torch.no_grad():
-        return [C.c_double(v).value for v in values]
+    """A call's scalars as plain floats: what is kept by them (_norm_dims) goes by their
+    values, where a tensor hashes by identity and can change in place."""
+    return [v if type(v) is float else float(v) if type(v) is int else _number(fn, v) for v in values]
 
 
 @functools.lru_cache(maxsize=4096)
